@@ -319,10 +319,10 @@ def _own_attention(s):
     if "workspace" not in s:  # kept with the sequence plan, as a serving loop keeps it
         if case["op"] == "decode":
             s["splits"] = c.decode_splits_fp8(B, hkv, table.shape[1], page)
-            s["workspace"] = c.workspace(B, hq, s["splits"])
+            s["workspace"] = c.workspace_fp8(B, hq, s["splits"])
         else:
             s["splits"] = c.prefill_splits_fp8(B, case["tq"], hq, hkv, table.shape[1], page)
-            s["workspace"] = c.workspace(B * case["tq"], hq, s["splits"])
+            s["workspace"] = c.workspace_fp8(B * case["tq"], hq, s["splits"])
         s["out"] = torch.empty_like(s["q"])
     call = c.decode_attention_fp8 if case["op"] == "decode" else c.prefill_attention_fp8
     return call(s["q"], s["k_pool"], s["v_pool"], s["k_scales"], s["v_scales"], table, s["seq_lens"], hkv, page,
