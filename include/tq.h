@@ -61,6 +61,9 @@ typedef enum {
 #define TQ_DEVERR_SLOT_RANGE  0x1u  /* compress: slot >= num_blocks * page_size (token skipped)   */
 #define TQ_DEVERR_BLOCK_RANGE 0x2u  /* decode/dequant: block id < 0 or >= num_blocks (page skipped) */
 #define TQ_DEVERR_SEQ_RANGE   0x4u  /* decode: seq_len > max_blocks_per_seq * page_size (clamped)  */
+#define TQ_DEVERR_POSITION    0x10u /* append: a position outside the rope table (token skipped)           */
+#define TQ_DEVERR_SLOT_ORDER  0x20u /* append, 8-bit pages: rows of one page in two places of the call (the
+                                       later ones are skipped)                                           */
 #define TQ_DEVERR_TIMEOUT     0x8u  /* a barrier wait ran past the handle's wait limit (tq_set_wait_limit):
                                        compress -- a tensor-core completion or hand-off wait; the CTA stops
                                        and the rows of its unfinished tiles are left unwritten;
@@ -282,6 +285,109 @@ tq_status tq_decode_attention_static(tq_handle h, const uint16_t *q, const uint8
  */
 tq_status tq_decode_attention_bf16(tq_handle h, const uint16_t *q, const uint16_t *k_pool, const uint16_t *v_pool,
                                    const int32_t *block_table, const int32_t *seq_lens, int batch, int num_q_heads,
+                                   int num_kv_heads, int page_size, int max_blocks_per_seq, int64_t num_blocks,
+                                   float sm_scale, int splits, void *workspace, size_t ws_bytes, uint16_t *out,
+                                   void *stream);
+
+/*
+ * tq_append_kv_bf16 -- put T tokens of keys and values into the plain bf16 pages
+ * that tq_decode_attention_bf16 reads, the keys (and, when q is given, the
+ * queries) rotated by their positions on the way.
+ *
+ * q, k, v: device bf16, token t / head h at ptr + t*stride_tok + h*head_dim
+ *       (strides in elements, multiples of 8, rows 16-byte aligned), so that
+ *       slices of one fused projection can be passed.  q may be NULL (then
+ *       num_q_heads and q_stride_tok are ignored and q_out must be NULL).
+ * q_out: device bf16 [T][num_q_heads][head_dim], contiguous; may be q itself
+ *       where q has that layout.
+ * rope: device fp32 [rope_rows][rot_dim], a row holding rot_dim/2 cosines and then
+ *       rot_dim/2 sines of one position; rot_dim is a multiple of 16 up to
+ *       head_dim.  (x, y) -> (x c - y s, y c + x s) in fp32, each product and sum
+ *       rounded once, the result to the nearest bf16.  style TQ_ROPE_HALF pairs
+ *       coordinates (j, j + rot_dim/2), TQ_ROPE_INTERLEAVED (2j, 2j + 1);
+ *       coordinates from rot_dim on pass through.  rot_dim 0: no rotation (rope and
+ *       positions may be NULL).
+ * positions: device int64 [T], the rope row of each token.  One outside
+ *       0 .. rope_rows - 1 skips the token and sets TQ_DEVERR_POSITION.
+ * slot_mapping: device int64 [T] as in tq_compress_kv: a negative slot skips the
+ *       token, one past the pool also sets TQ_DEVERR_SLOT_RANGE.  A skipped token
+ *       leaves its pool rows and its q_out row as they were.  Two tokens mapped to
+ *       one slot race (caller error).
+ * k_pool, v_pool: device bf16 [num_blocks][num_kv_heads][page_size][head_dim],
+ *       16-byte aligned, not overlapping the inputs.
+ * One launch on `stream`; T == 0 launches nothing.
+ */
+#define TQ_ROPE_HALF 0
+#define TQ_ROPE_INTERLEAVED 1
+tq_status tq_append_kv_bf16(tq_handle h, const uint16_t *q, const uint16_t *k, const uint16_t *v, int64_t T,
+                            int num_q_heads, int num_kv_heads, int64_t q_stride_tok, int64_t k_stride_tok,
+                            int64_t v_stride_tok, const int64_t *positions, const float *rope, int64_t rope_rows,
+                            int rot_dim, int style, const int64_t *slot_mapping, uint16_t *k_pool, uint16_t *v_pool,
+                            int page_size, int64_t num_blocks, uint16_t *q_out, void *stream);
+
+/*
+ * tq_append_kv_fp8 -- the same into 8-bit pages: a page holds e4m3 codes and, for
+ * its keys and its values apart, one fp32 scale per kv head; element = code * scale.
+ *
+ * k_pool, v_pool: device e4m3 [num_blocks][num_kv_heads][page_size][head_dim],
+ *       16-byte aligned; k_scales, v_scales: device fp32 [num_blocks][num_kv_heads].
+ * The scale that a page's rows x ask for is the least power of two 2^e, e >= -100,
+ * with max |x| <= 448 2^e over their finite elements (keys after the rotation, in
+ * fp32).  Tokens that begin a page (row 0) give it their scale and nothing of what
+ * it held counts; tokens that continue a page keep the larger of its scale and
+ * theirs, and where that grows, the page's earlier rows are coded anew by the ratio
+ * -- exact but for elements that become subnormal.  Codes round to nearest even;
+ * an infinity saturates to 448, a NaN stays one.  Rows behind the last one written
+ * keep their bytes.
+ * slot_mapping: as above, and the tokens of one page stand next to each other in the
+ *       call with ascending slots (as packed sequences have them): where another
+ *       token of the page, or the same slot again, stands up to 32 tokens before a
+ *       run of consecutive slots, that run is skipped and TQ_DEVERR_SLOT_ORDER set;
+ *       farther apart they race.  A token with a bad position inside a run keeps its
+ *       place but is not written.
+ * Everything else as in tq_append_kv_bf16.
+ */
+tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, const uint16_t *v, int64_t T,
+                           int num_q_heads, int num_kv_heads, int64_t q_stride_tok, int64_t k_stride_tok,
+                           int64_t v_stride_tok, const int64_t *positions, const float *rope, int64_t rope_rows,
+                           int rot_dim, int style, const int64_t *slot_mapping, uint8_t *k_pool, uint8_t *v_pool,
+                           float *k_scales, float *v_scales, int page_size, int64_t num_blocks, uint16_t *q_out,
+                           void *stream);
+
+/*
+ * tq_decode_attention_fp8 -- one query token per sequence over the 8-bit pages that
+ * tq_append_kv_fp8 writes: tq_decode_attention_bf16 with pools and scales as above
+ * (any non-negative finite scales; powers of two are what append writes).
+ *
+ * splits: split-K count, 0 = tq_decode_splits_fp8(...).  workspace: ws_bytes >=
+ *   tq_workspace_bytes_fp8(h, batch, num_q_heads, splits), 256-byte aligned; not
+ *   needed (may be NULL) where that is 0.  Its contents after the call are not
+ *   specified, and calls that may overlap need one each.
+ * The query enters the products exactly (two e4m3 terms of a power-of-two multiple;
+ * elements below 2^-9 of the head's largest lose bits below 2^-17 of it), the
+ * probabilities as two e4m3 terms (about 8 bits), sums are fp32.
+ * A page with a bad block id (TQ_DEVERR_BLOCK_RANGE) counts as hidden.
+ */
+int tq_decode_splits_fp8(tq_handle h, int batch, int num_kv_heads, int max_blocks_per_seq, int page_size);
+size_t tq_workspace_bytes_fp8(tq_handle h, int batch, int num_q_heads, int splits);
+tq_status tq_decode_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t *k_pool, const uint8_t *v_pool,
+                                  const float *k_scales, const float *v_scales, const int32_t *block_table,
+                                  const int32_t *seq_lens, int batch, int num_q_heads, int num_kv_heads,
+                                  int page_size, int max_blocks_per_seq, int64_t num_blocks, float sm_scale,
+                                  int splits, void *workspace, size_t ws_bytes, uint16_t *out, void *stream);
+
+/*
+ * tq_prefill_attention_fp8 -- the last q_tokens positions of every sequence attend
+ * causally to its 8-bit pages, their own rows included (tq_prefill_attention's
+ * contract over the pools above).  q, out: device bf16 [B][q_tokens][Hq][d].
+ * splits = 0 picks tq_prefill_splits_fp8(...); workspace: ws_bytes >=
+ * tq_workspace_bytes_fp8(h, batch * q_tokens, num_q_heads, splits).
+ */
+int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int num_q_heads, int num_kv_heads,
+                          int max_blocks_per_seq, int page_size);
+tq_status tq_prefill_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t *k_pool, const uint8_t *v_pool,
+                                   const float *k_scales, const float *v_scales, const int32_t *block_table,
+                                   const int32_t *seq_lens, int batch, int q_tokens, int num_q_heads,
                                    int num_kv_heads, int page_size, int max_blocks_per_seq, int64_t num_blocks,
                                    float sm_scale, int splits, void *workspace, size_t ws_bytes, uint16_t *out,
                                    void *stream);

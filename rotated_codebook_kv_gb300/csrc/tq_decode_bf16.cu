@@ -18,10 +18,7 @@
 // P.V: coordinates as M (V rows transposed by ldmatrix.trans), probabilities as
 // the B operand in two bf16 terms (high and low part, ~16 significant bits).
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
-
-#include <mutex>
 
 #include "tq.h"
 #include "tq_device.cuh"
@@ -372,41 +369,6 @@ __global__ void __launch_bounds__(kThreads) decode_bf16_kernel(const __grid_cons
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder(cudaError_t *err)
-{
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static cudaError_t e = cudaSuccess;
-    std::call_once(once, [] {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-        if (e == cudaSuccess && q != cudaDriverEntryPointSuccess) e = cudaErrorSymbolNotFound;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    *err = e;
-    return fn;
-}
-
-// A 2-D view [rows][d] of a bf16 pool, fetched in 16 x 64 boxes with the 128-byte swizzle.
-bool make_pool_map(CUtensorMap *tm, const void *pool, int d, int64_t rows, cudaError_t *err)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder(err);
-    if (!enc) return false;
-    const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(d) * 2};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBoxCols), static_cast<cuuint32_t>(kTile)};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), gdim, gstride, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        *err = cudaErrorInvalidValue;
-        return false;
-    }
-    return true;
-}
-
 template <int D>
 cudaError_t launch_bypass(const CUtensorMap &tk, const CUtensorMap &tv, const Codec &c, int P, const DecodeArgs &a,
                           cudaStream_t st)
@@ -464,7 +426,8 @@ extern "C" tq_status tq_decode_attention_bf16(tq_handle h, const uint16_t *q, co
                          need);
     CUtensorMap tk, tv;
     cudaError_t e = cudaSuccess;
-    if (!tq::make_pool_map(&tk, k_pool, c.d, rows, &e) || !tq::make_pool_map(&tv, v_pool, c.d, rows, &e))
+    if (!tq::encode_pool_map(&tk, k_pool, true, c.d, rows, tq::kBoxCols, tq::kTile, &e) ||
+        !tq::encode_pool_map(&tv, v_pool, true, c.d, rows, tq::kBoxCols, tq::kTile, &e))
         return api_error(TQ_ERR_CUDA, "tq_decode_attention_bf16: cuTensorMapEncodeTiled: %s", cudaGetErrorString(e));
     tq::DecodeArgs a{};
     a.q = q;

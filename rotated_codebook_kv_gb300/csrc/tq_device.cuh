@@ -10,6 +10,8 @@
 #define TQ_DEVERR_BLOCK_RANGE 0x2u
 #define TQ_DEVERR_SEQ_RANGE 0x4u
 #define TQ_DEVERR_TIMEOUT 0x8u
+#define TQ_DEVERR_POSITION 0x10u
+#define TQ_DEVERR_SLOT_ORDER 0x20u
 
 namespace tq {
 

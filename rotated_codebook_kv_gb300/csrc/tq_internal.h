@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <vector>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "tq.h"
@@ -137,6 +138,11 @@ cudaError_t static_scratch_lookup(void **out);
 void *handle_static_scratch(tq_handle h);
 // The codec constants of a (non-NULL) handle.
 const Codec &handle_codec(tq_handle h);
+
+// A 2-D tensor map of a page pool seen as [rows][cols] (16-bit or 8-bit elements, contiguous rows), fetched in
+// boxes of box_rows x box_cols (128 bytes wide) with the 128-byte swizzle; reads past the rows give zeros.
+bool encode_pool_map(CUtensorMap *tm, const void *pool, bool bf16, int cols, int64_t rows, int box_cols, int box_rows,
+                     cudaError_t *err);
 
 // Sets a kernel's dynamic shared-memory limit once per (function, device); thread safe.
 cudaError_t ensure_smem_attr(const void *func, size_t bytes);

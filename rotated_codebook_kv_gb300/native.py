@@ -16,6 +16,8 @@ from . import build as _build
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_OOM = range(5)
 TQ_ROTATION_DENSE, TQ_ROTATION_HADAMARD, TQ_VALUES_MSE = 0, 1, 2
 TQ_DEVERR_SLOT_RANGE, TQ_DEVERR_BLOCK_RANGE, TQ_DEVERR_SEQ_RANGE, TQ_DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+TQ_DEVERR_POSITION, TQ_DEVERR_SLOT_ORDER = 0x10, 0x20
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
 TQ_DEFAULT_WAIT_LIMIT = 2000000000
 
 # Every symbol include/tq.h declares, with (restype, argtypes).
@@ -40,6 +42,17 @@ SIGNATURES = {
                                         _i32, _vp, _sz, _vp, _vp]),
     "tq_decode_attention_static": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i64, _f32,
                                           _i32, _vp, _vp]),
+    "tq_append_kv_bf16": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _i32,
+                                 _vp, _vp, _vp, _i32, _i64, _vp, _vp]),
+    "tq_append_kv_fp8": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _i32,
+                                _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp]),
+    "tq_decode_splits_fp8": (_i32, [_vp, _i32, _i32, _i32, _i32]),
+    "tq_prefill_splits_fp8": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "tq_workspace_bytes_fp8": (_sz, [_vp, _i32, _i32, _i32]),
+    "tq_decode_attention_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i64,
+                                       _f32, _i32, _vp, _sz, _vp, _vp]),
+    "tq_prefill_attention_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                        _i64, _f32, _i32, _vp, _sz, _vp, _vp]),
     "tq_set_wait_limit": (_i32, [_vp, _i64]),
     "tq_get_status": (_i32, [_vp, _c.POINTER(_c.c_uint32), _vp]),
     "tq_export_params": (_i32, [_vp, _vp, _vp, _vp, _vp]),
@@ -166,6 +179,51 @@ def tq_decode_attention_static(h, q, k_cache, v_cache, block_table, seq_lens, ba
     _check("tq_decode_attention_static", load().tq_decode_attention_static(
         h, q, k_cache, v_cache, block_table, seq_lens, batch, num_q_heads, num_kv_heads, page_size,
         max_blocks_per_seq, num_blocks, sm_scale, splits, out, stream))
+
+
+def tq_append_kv_bf16(h, q, k, v, T, num_q_heads, num_kv_heads, q_stride_tok, k_stride_tok, v_stride_tok, positions,
+                      rope, rope_rows, rot_dim, style, slot_mapping, k_pool, v_pool, page_size, num_blocks, q_out,
+                      stream) -> None:
+    _check("tq_append_kv_bf16", load().tq_append_kv_bf16(
+        h, q, k, v, T, num_q_heads, num_kv_heads, q_stride_tok, k_stride_tok, v_stride_tok, positions, rope,
+        rope_rows, rot_dim, style, slot_mapping, k_pool, v_pool, page_size, num_blocks, q_out, stream))
+
+
+def tq_append_kv_fp8(h, q, k, v, T, num_q_heads, num_kv_heads, q_stride_tok, k_stride_tok, v_stride_tok, positions,
+                     rope, rope_rows, rot_dim, style, slot_mapping, k_pool, v_pool, k_scales, v_scales, page_size,
+                     num_blocks, q_out, stream) -> None:
+    _check("tq_append_kv_fp8", load().tq_append_kv_fp8(
+        h, q, k, v, T, num_q_heads, num_kv_heads, q_stride_tok, k_stride_tok, v_stride_tok, positions, rope,
+        rope_rows, rot_dim, style, slot_mapping, k_pool, v_pool, k_scales, v_scales, page_size, num_blocks, q_out,
+        stream))
+
+
+def tq_decode_splits_fp8(h, batch, num_kv_heads, max_blocks_per_seq, page_size) -> int:
+    return load().tq_decode_splits_fp8(h, batch, num_kv_heads, max_blocks_per_seq, page_size)
+
+
+def tq_prefill_splits_fp8(h, batch, q_tokens, num_q_heads, num_kv_heads, max_blocks_per_seq, page_size) -> int:
+    return load().tq_prefill_splits_fp8(h, batch, q_tokens, num_q_heads, num_kv_heads, max_blocks_per_seq, page_size)
+
+
+def tq_workspace_bytes_fp8(h, batch, num_q_heads, splits) -> int:
+    return load().tq_workspace_bytes_fp8(h, batch, num_q_heads, splits)
+
+
+def tq_decode_attention_fp8(h, q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, batch, num_q_heads,
+                            num_kv_heads, page_size, max_blocks_per_seq, num_blocks, sm_scale, splits, workspace,
+                            ws_bytes, out, stream) -> None:
+    _check("tq_decode_attention_fp8", load().tq_decode_attention_fp8(
+        h, q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, batch, num_q_heads, num_kv_heads, page_size,
+        max_blocks_per_seq, num_blocks, sm_scale, splits, workspace, ws_bytes, out, stream))
+
+
+def tq_prefill_attention_fp8(h, q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, batch, q_tokens,
+                             num_q_heads, num_kv_heads, page_size, max_blocks_per_seq, num_blocks, sm_scale, splits,
+                             workspace, ws_bytes, out, stream) -> None:
+    _check("tq_prefill_attention_fp8", load().tq_prefill_attention_fp8(
+        h, q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, batch, q_tokens, num_q_heads, num_kv_heads,
+        page_size, max_blocks_per_seq, num_blocks, sm_scale, splits, workspace, ws_bytes, out, stream))
 
 
 def tq_set_wait_limit(h, cycles: int) -> None:
