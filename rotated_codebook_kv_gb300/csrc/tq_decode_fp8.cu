@@ -16,24 +16,24 @@
 // two e4m3 terms (about 8 bits of the largest), the rest is fp32.
 //
 // Split partials (max, denominator, numerators) are merged by merge_kernel; with one
-// split the CTA writes the output itself.
+// split the CTA writes the output itself.  Up to eight (query token, head) columns of a
+// sequence and kv head go through this kernel, more through tq_prefill_fp8.cu.
 #include <cmath>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "tq.h"
-#include "tq_device.cuh"
-#include "tq_internal.h"
+#include "tq_fp8.cuh"
 
 namespace tq {
 namespace {
 
+using namespace fp8;
+
 constexpr int kTok = 32;                  // tokens of a warp's round
 constexpr int kStages = 2;
 constexpr int kBoxBytes = kTok * 128;     // one 128-byte-wide column block of a round
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 8.f;            // probabilities enter the product as 2^8 p <= 256
-constexpr float kLShift = 4.f;            // and the denominator as 2^4 p / vs: vs in 2^-100 .. 2^119 neither overflows it nor flushes
 
 template <int D>
 struct Fp8Smem {
@@ -75,42 +75,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
     return d;
 }
 
-__device__ __forceinline__ float fast_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// log2 of a page scale, exact for powers of two; below 2^-100 (an empty scale) as 2^-100.
-__device__ __forceinline__ float log2_scale(float s)
-{
-    const uint32_t b = __float_as_uint(fmaxf(s, 7.888609052210118e-31f));
-    float m;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(m) : "f"(__uint_as_float((b & 0x7fffffu) | 0x3f800000u)));
-    return static_cast<float>(static_cast<int>(b >> 23) - 127) + m;
-}
-
-// (x, y) to e4m3 (x in the low byte) and what is left of them.
-__device__ __forceinline__ uint32_t e4m3x2_rest(float &x, float &y)
-{
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-    x -= f.x;
-    y -= f.y;
-    return c;
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float x, float y)
-{
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
-    return c;
-}
-
 __device__ __forceinline__ bool mbar_test(uint32_t mb, uint32_t par)
 {
     uint32_t done;
@@ -127,26 +91,11 @@ __device__ __forceinline__ bool mbar_try(uint32_t mb, uint32_t par)
     return done != 0;
 }
 
-struct Fp8Args {
-    const uint16_t *q;
-    const float *k_scales, *v_scales;
-    const int32_t *block_table, *seq_lens;
-    int B, Hq, Hkv, G, P, pshift, max_blocks;
-    int64_t num_blocks;
-    float sm_scale;
-    int splits, pages_per_split;
-    int Tq, qpc, nqt;  // query tokens per sequence, per CTA, and CTAs over them
-    float *ml, *acc;   // [splits][B][Tq][Hq][2], [splits][B][Tq][Hq][D]; unused with one split
-    uint16_t *out;
-    unsigned *status;
-    long long wait_limit;
-};
-
 // The eight columns of a CTA are (query token, head of the group) pairs: with one query
 // token per sequence its G heads, else qpc = 8 / G tokens, each with its causal limit.
 template <int D>
 __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
-    attention_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Fp8Args A)
+    attention_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args A)
 {
     using SM = Fp8Smem<D>;
     constexpr int kWarps = SM::kWarps, kThreads = SM::kThreads;
@@ -577,13 +526,18 @@ size_t workspace_bytes(int d, int64_t rows, int splits)
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Fp8Args &a, cudaStream_t st)
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, bool tc, cudaStream_t st)
 {
-    const size_t smem = Fp8Smem<D>::kBytes;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_fp8_kernel<D>), smem);
-    if (e != cudaSuccess) return e;
-    attention_fp8_kernel<D><<<dim3(a.splits, a.Hkv, a.B * a.nqt), Fp8Smem<D>::kThreads, smem, st>>>(tk, tv, a);
-    e = cudaGetLastError();
+    cudaError_t e;
+    if (tc) {
+        e = launch_prefill_tc(tk, tv, D, a, st);
+    } else {
+        const size_t smem = Fp8Smem<D>::kBytes;
+        e = ensure_smem_attr(reinterpret_cast<const void *>(attention_fp8_kernel<D>), smem);
+        if (e != cudaSuccess) return e;
+        attention_fp8_kernel<D><<<dim3(a.splits, a.Hkv, a.B * a.nqt), Fp8Smem<D>::kThreads, smem, st>>>(tk, tv, a);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess || a.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.Tq * a.Hq;
     merge_fp8_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a.ml, a.acc, a.out, rows, a.splits);
@@ -618,13 +572,16 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint8_t 
     if (num_blocks >= (int64_t(1) << 31) / (static_cast<int64_t>(Hkv) * P))
         return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who, static_cast<long long>(num_blocks));
     if (batch == 0) return TQ_OK;
-    Fp8Args a{};
+    Args a{};
     a.G = Hq / Hkv;
     a.Tq = q_tokens;
-    a.qpc = q_tokens == 1 ? 1 : 8 / a.G;
+    // up to eight (query token, head) columns fit the mma.sync kernel of the decode; more go to the tcgen05 one
+    const bool tc = q_tokens * static_cast<int64_t>(a.G) > 8;
+    a.qpc = tc ? prefill_tc_columns(c.d) / a.G : q_tokens;
     a.nqt = (q_tokens + a.qpc - 1) / a.qpc;
     const int64_t rows = static_cast<int64_t>(batch) * q_tokens * Hq;
-    if (static_cast<int64_t>(batch) * a.nqt > 65535 || rows >= (int64_t(1) << 31))
+    if ((!tc && batch > 65535) || rows >= (int64_t(1) << 31) ||
+        static_cast<int64_t>(batch) * a.nqt * Hkv * (splits ? splits : 256) >= (int64_t(1) << 31))
         return api_error(TQ_ERR_UNSUPPORTED, "%s: too many sequences x query tokens in one call", who);
     if (!q || !k_pool || !v_pool || !k_scales || !v_scales || !block_table || !seq_lens || !out)
         return api_error(TQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -669,7 +626,7 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint8_t 
     a.status = c.status;
     a.wait_limit = c.wait_limit;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = c.d == 128 ? launch<128>(tk, tv, a, st) : launch<256>(tk, tv, a, st);
+    e = c.d == 128 ? launch<128>(tk, tv, a, tc, st) : launch<256>(tk, tv, a, tc, st);
     if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return TQ_OK;
 }
@@ -710,9 +667,14 @@ extern "C" int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int n
     if (!h || batch < 1 || q_tokens < 1 || num_kv_heads < 1 || num_q_heads < num_kv_heads || max_blocks_per_seq < 1 ||
         page_size < 1)
         return 1;
-    const int qpc = num_q_heads / num_kv_heads >= 8 ? 1 : 8 / (num_q_heads / num_kv_heads);
-    const long long z = static_cast<long long>(batch) * ((q_tokens + qpc - 1) / qpc);
-    return tq_decode_splits_fp8(h, static_cast<int>(z < 65535 ? z : 65535), num_kv_heads, max_blocks_per_seq, page_size);
+    const int G = num_q_heads / num_kv_heads;
+    if (static_cast<long long>(q_tokens) * G <= 8)  // the decode's kernel
+        return tq_decode_splits_fp8(h, batch, num_kv_heads, max_blocks_per_seq, page_size);
+    const int qpc = tq::fp8::prefill_tc_columns(tq::handle_codec(h).d) / G;
+    const long long units = static_cast<long long>(batch) * num_kv_heads * ((q_tokens + qpc - 1) / qpc);
+    // one CTA per SM: about two waves, each split at least 512 tokens
+    const long long most = (static_cast<long long>(max_blocks_per_seq) * page_size + 511) / 512;
+    return tq::clamp_splits((2LL * tq::handle_codec(h).num_sms + units - 1) / units, most);
 }
 
 extern "C" tq_status tq_prefill_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t *k_pool,

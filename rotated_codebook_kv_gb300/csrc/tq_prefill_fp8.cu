@@ -1,0 +1,637 @@
+// tq_prefill_fp8.cu -- causal attention of the last tokens of every sequence over 8-bit
+// pages, on the 5th-generation tensor cores.
+//
+//   S[c][t] = <q_c 2^e, kc_t>          kind::f8f6f4: the key codes as stored, q 2^e as two e4m3 terms (exact,
+//                                      see tq_decode_fp8.cu), M = 128 columns c, N = KT tokens t
+//   O[c][j] += sum_t P[c][t] vc_t[j]   kind::f16: P in fp16 from tensor memory, the value codes widened to fp16
+//                                      (exact) in shared memory, N = D coordinates j
+// with y = sm_scale log2(e) 2^-e ks[page] S + log2 vs[page], P = 2^(y - m), m a running maximum that is
+// only moved when it grows by more than 2^8 (P <= 2^8: fp16 keeps 11 bits of it down to 2^-14), and the
+// denominator the sum of P / vs in fp32.
+//
+// A CTA takes NQ tiles of 128 columns, (query token, head) pairs of one sequence and kv head, and the
+// KT-token tiles that they see in its split.  Two tiles at head dim 128: while one's scores are turned into
+// P, the tensor core works for the other.  At head dim 256 tensor memory holds one tile's O (256 columns)
+// and two score buffers.  P overwrites the scores that it came from.
+//
+// Warps (one CTA per SM):
+//   4 NQ      one thread per column: query operands, online softmax, output
+//   4         value codes of a tile to fp16 (rows of 64 coordinates, 128-byte swizzle, one row per token)
+//   1         tensor-memory allocation; lane 0 issues the MMAs as their operands become ready
+//   1         page copies (TMA boxes of a page x 128 bytes, 128-byte swizzle), scales
+// Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT, stops the CTA (its rows
+// then carry no weight), lets copies and MMAs in flight finish, and frees tensor memory.
+#include "tq_fp8.cuh"
+#include "tq_umma.cuh"
+
+namespace tq {
+namespace fp8 {
+namespace {
+
+template <int D>
+struct Tc {
+    static constexpr int NQ = D == 128 ? 2 : 1;         // column tiles
+    static constexpr int KT = D == 128 ? 128 : 64;      // tokens per tile
+    static constexpr int NB = D == 128 ? 1 : 2;         // score buffers per column tile
+    static constexpr int XB = D / 128;                  // 128-byte column blocks of a row of codes
+    static constexpr int kSoftWarps = 4 * NQ;
+    static constexpr int kConvWarps = 4;
+    static constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+    static constexpr int kLoadWarp = kMmaWarp + 1;
+    static constexpr int kThreads = 32 * (kLoadWarp + 1);
+    static constexpr int KS = 3, RS = 2, VS = 2;        // stages: keys, value codes, fp16 values
+    static constexpr int GR = KT / 16;                  // 16-token groups of a tile (a page holds one or two)
+    static constexpr int kRing = 8;                     // tiles whose scales are kept
+    static constexpr uint32_t kQBytes = 128u * D;       // one term of one column tile
+    static constexpr uint32_t kKBytes = static_cast<uint32_t>(KT) * D;
+    static constexpr uint32_t kQOff = 0;
+    static constexpr uint32_t kKOff = kQOff + 2 * NQ * kQBytes;
+    static constexpr uint32_t kROff = kKOff + KS * kKBytes;
+    static constexpr uint32_t kVOff = kROff + RS * kKBytes;
+    static constexpr uint32_t kInfoOff = kVOff + VS * 2 * kKBytes;  // [ring][GR] (ks, log2 vs, 2^4 / vs, -)
+    static constexpr uint32_t kOkOff = kInfoOff + kRing * GR * 16;  // [ring] bit g: group g's page is valid
+    static constexpr uint32_t kBarOff = kOkOff + kRing * 4;
+    // barriers
+    static constexpr int bQ = 0;                 // query operands in shared memory
+    static constexpr int bKFull = 1;             // [KS] keys landed (one arrival per page, and bytes)
+    static constexpr int bKFree = bKFull + KS;   // [KS] the score MMAs of every tile are done
+    static constexpr int bRFull = bKFree + KS;   // [RS] value codes landed
+    static constexpr int bRFree = bRFull + RS;   // [RS] widened
+    static constexpr int bVFull = bRFree + RS;   // [VS] fp16 values ready
+    static constexpr int bVFree = bVFull + VS;   // [VS] the P.V MMAs of every tile are done
+    static constexpr int bSFull = bVFree + VS;   // [NQ][NB] scores in tensor memory
+    static constexpr int bPFull = bSFull + NQ * NB;  // [NQ][NB] P in tensor memory, O rescaled
+    static constexpr int bPvDone = bPFull + NQ * NB;  // [NQ] O += P V done
+    static constexpr int bEnd = bPvDone + NQ;    // teardown: every MMA issued is done
+    static constexpr int kBars = bEnd + 1;
+    static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;  // tensor-memory base, abort flag
+    static constexpr size_t kSmem = 1024 + kMiscOff + 16;
+    // tensor-memory columns
+    static constexpr uint32_t kTmS = 0;                              // [NQ][NB] KT columns
+    static constexpr uint32_t kTmO = NQ * NB * KT;                   // [NQ] D columns
+    static constexpr uint32_t kTmCols = 512;
+    static_assert(kTmO + NQ * D <= kTmCols, "tensor memory");
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+constexpr float kLazy = 8.f;  // rescale O when the maximum grows by more than this (log2 units)
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void warp_arrive(uint64_t *mb)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(mb)) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t pair)
+{
+    uint32_t h;
+    const uint16_t c = static_cast<uint16_t>(pair);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Tc<D>::kThreads, 1)
+    prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args A)
+{
+    using T = Tc<D>;
+    constexpr int NQ = T::NQ, KT = T::KT, NB = T::NB, XB = T::XB, GR = T::GR;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // the CTAs over one sequence's query tokens are neighbours (they share its pages in L2), the longest first
+    int u = blockIdx.x;
+    const int qt = A.nqt - 1 - u % A.nqt;
+    u /= A.nqt;
+    const int split = u % A.splits;
+    u /= A.splits;
+    const int kvh = u % A.Hkv, b = u / A.Hkv;
+    const int G = A.G, P = A.P;
+    int L = A.seq_lens[b];
+    if (L < 0) L = 0;
+    if (L > A.max_blocks * P) {
+        if (split == 0 && kvh == 0 && qt == 0 && tid == 0) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
+        L = A.max_blocks * P;
+    }
+    const int q0 = qt * A.qpc;
+    const int ncol = min(A.qpc, A.Tq - q0) * G;
+    auto col_row = [&](int c) -> size_t {
+        return (static_cast<size_t>(b) * A.Tq + q0 + c / G) * A.Hq + static_cast<size_t>(kvh) * G + c % G;
+    };
+    auto col_lim = [&](int c) -> int { return max(0, L - A.Tq + q0 + c / G + 1); };
+    const size_t rows_total = static_cast<size_t>(A.B) * A.Tq * A.Hq;
+    const int tok0 = split * A.pages_per_split * P;
+    const int tok1 = min(col_lim(ncol - 1), tok0 + A.pages_per_split * P);
+    auto dead_row = [&](int c) {  // a row that this CTA has nothing for
+        const size_t rr = col_row(c);
+        if (A.splits == 1) {
+            uint4 *dst = reinterpret_cast<uint4 *>(A.out + rr * D);
+            for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            float *ml = A.ml + (static_cast<size_t>(split) * rows_total + rr) * 2;
+            ml[0] = -INFINITY;
+            ml[1] = 0.f;
+        }
+    };
+    if (tok0 >= tok1) {
+        for (int c = tid; c < ncol; c += T::kThreads) dead_row(c);
+        return;
+    }
+    int nt[NQ];  // token tiles that a column tile sees
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+        const int last = min(ncol, 128 * (q + 1)) - 1;
+        nt[q] = last < 128 * q ? 0 : max(0, (min(col_lim(last), tok1) - tok0 + KT - 1) / KT);
+    }
+    const int nt_all = (tok1 - tok0 + KT - 1) / KT;
+
+    uint64_t *mbar = reinterpret_cast<uint64_t *>(smem + T::kBarOff);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + T::kMiscOff);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + T::kMiscOff + 4);
+    const uint32_t sbase = saddr(smem);
+    const int ppt = KT / P;  // pages per tile
+
+    if (warp == T::kMmaWarp) umma::tmem_alloc(tmem_slot, T::kTmCols);
+    if (tid == 0) {
+        umma::mbar_init(&mbar[T::bQ], T::kSoftWarps);
+        for (int i = 0; i < T::KS; ++i) {
+            umma::mbar_init(&mbar[T::bKFull + i], ppt);
+            umma::mbar_init(&mbar[T::bKFree + i], 1);
+        }
+        for (int i = 0; i < T::RS; ++i) {
+            umma::mbar_init(&mbar[T::bRFull + i], ppt);
+            umma::mbar_init(&mbar[T::bRFree + i], T::kConvWarps);
+        }
+        for (int i = 0; i < T::VS; ++i) {
+            umma::mbar_init(&mbar[T::bVFull + i], T::kConvWarps);
+            umma::mbar_init(&mbar[T::bVFree + i], 1);
+        }
+        for (int i = 0; i < NQ * NB; ++i) {
+            umma::mbar_init(&mbar[T::bSFull + i], 1);
+            umma::mbar_init(&mbar[T::bPFull + i], 4);
+        }
+        for (int i = 0; i < NQ; ++i) umma::mbar_init(&mbar[T::bPvDone + i], 1);
+        umma::mbar_init(&mbar[T::bEnd], 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tbase = *tmem_slot;
+
+    // bounded wait: gives up on the CTA's abort flag or after the wait limit (then raising the flag and the
+    // status bit); a zero limit tests once
+    auto wait_bar = [&](int i, uint32_t par) -> bool {
+        uint64_t *mb = &mbar[i];
+        bool ok = false;
+        if (A.wait_limit <= 0) {
+            ok = umma::mbar_test_wait(mb, par);
+        } else {
+            const long long t0 = clock64();
+            while (!(ok = umma::mbar_try_wait(mb, par))) {
+                if (*abort_flag || clock64() - t0 > A.wait_limit) break;
+            }
+        }
+        if (!ok && !*abort_flag) {
+            *abort_flag = 1;
+            atomicOr(A.status, TQ_DEVERR_TIMEOUT);
+        }
+        return __all_sync(0xffffffffu, ok);  // the lanes poll separately: decide as a warp
+    };
+
+    if (warp < T::kSoftWarps) {
+        // ================= columns: query operands, softmax, output =================
+        const int q = warp >> 2, r = tid & 127, c = 128 * q + r;
+        const bool cv = c < ncol;
+        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        float fac;  // sm_scale log2(e) 2^-e >= 0: a negative scale goes into q's sign
+        {
+            const uint4 *src = reinterpret_cast<const uint4 *>(A.q + col_row(cv ? c : 0) * D);
+            float mx = 0.f;
+            bool nan = false;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 w = cv ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x0 = fabsf(__uint_as_float(v[k] << 16)), x1 = fabsf(__uint_as_float(v[k] & 0xffff0000u));
+                    nan |= !(x0 <= 3.4e38f) || !(x1 <= 3.4e38f);
+                    mx = fmaxf(mx, fmaxf(x0, x1));
+                }
+            }
+            int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // 2^(7 - ex) brings the largest into [2^7, 2^8)
+            ex = min(max(ex, -100), 120);
+            float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
+            fac = fabsf(A.sm_scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
+            if (nan) fac = __uint_as_float(0x7fc00000u);
+            if (A.sm_scale < 0.f) up = -up;
+            const uint32_t qs = sbase + T::kQOff + 2 * q * T::kQBytes;
+#pragma unroll 2
+            for (int i = 0; i < D / 16; ++i) {  // 16 coordinates: one 16-byte chunk of each term
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 w = cv ? __ldg(src + 2 * i + h) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t ph[4], pl[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float x0 = __uint_as_float(v[k] << 16) * up, x1 = __uint_as_float(v[k] & 0xffff0000u) * up;
+                        ph[k] = e4m3x2_rest(x0, x1);
+                        pl[k] = e4m3x2(x0, x1);
+                    }
+                    hi[2 * h] = ph[0] | (ph[1] << 16);
+                    hi[2 * h + 1] = ph[2] | (ph[3] << 16);
+                    lo[2 * h] = pl[0] | (pl[1] << 16);
+                    lo[2 * h + 1] = pl[2] | (pl[3] << 16);
+                }
+                const uint32_t at = qs + (i >> 3) * (128 * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4);
+                sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                sts128(at + T::kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            }
+            umma::fence_proxy_async();
+            warp_arrive(&mbar[T::bQ]);
+        }
+        const int lim = cv ? min(col_lim(c), tok1) : 0;
+        const int my_nt = q ? nt[NQ - 1] : nt[0];
+        float m_run = -INFINITY, l_run = 0.f;
+        bool ok = true;
+        for (int i = 0; i < my_nt; ++i) {
+            if (!(ok = wait_bar(T::bSFull + q * NB + i % NB, (i / NB) & 1))) break;
+            umma::fence_after_sync();
+            const uint32_t ts = lane_base + T::kTmS + (q * NB + i % NB) * KT;
+            const float4 *info = reinterpret_cast<const float4 *>(smem + T::kInfoOff) + (i % T::kRing) * GR;
+            const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
+            const int rem = lim - (tok0 + i * KT);  // tokens of the tile that this column sees
+            const bool whole = __all_sync(0xffffffffu, rem >= KT) && okm == (1u << GR) - 1u;
+            // ---- the tile's maximum ----
+            float top = -INFINITY;
+            uint32_t s[2][32];
+            umma::ld32_issue(ts, s[0]);
+#pragma unroll
+            for (int ch = 0; ch < KT / 32; ++ch) {
+                umma::wait_ld32(s[ch & 1]);
+                if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float4 f = info[2 * ch + g];
+                    float m0 = -INFINITY, m1 = -INFINITY;
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            m0 = fmaxf(m0, fmaxf(__uint_as_float(s[ch & 1][16 * g + k]), __uint_as_float(s[ch & 1][16 * g + k + 1])));
+                            m1 = fmaxf(m1, fmaxf(__uint_as_float(s[ch & 1][16 * g + k + 2]), __uint_as_float(s[ch & 1][16 * g + k + 3])));
+                        }
+                    } else if (okm >> (2 * ch + g) & 1u) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (32 * ch + 16 * g + k < rem) m0 = fmaxf(m0, __uint_as_float(s[ch & 1][16 * g + k]));
+                    }
+                    m0 = fmaxf(m0, m1);
+                    if (m0 != -INFINITY) top = fmaxf(top, fmaf(m0, fac * f.x, f.y));
+                }
+            }
+            // ---- lazy rescale ----
+            const float m_new = fmaxf(m_run, top);
+            const bool need = m_run != -INFINITY && m_new > m_run + kLazy;
+            if (m_run == -INFINITY) m_run = m_new;  // O's row is zero or unwritten so far
+            if (__any_sync(0xffffffffu, need)) {
+                // with one score buffer O += P V of the tile before is done when the scores are there
+                if (NB > 1 && !(ok = wait_bar(T::bPvDone + q, (i - 1) & 1))) break;
+                umma::fence_after_sync();
+                const float al = need ? fast_exp2(m_run - m_new) : 1.f;
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    const uint32_t to = lane_base + T::kTmO + q * D + 32 * ch;
+                    umma::ld32_issue(to, s[0]);
+                    umma::wait_ld32(s[0]);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[0][k] = __float_as_uint(__uint_as_float(s[0][k]) * al);
+                    umma::st32(to, s[0]);
+                }
+                umma::wait_st();
+                if (need) {
+                    l_run *= al;
+                    m_run = m_new;
+                }
+            }
+            // ---- P = 2^(y - m) over the scores ----
+            const float ref = m_run == -INFINITY ? 0.f : m_run;
+            umma::ld32_issue(ts, s[0]);
+#pragma unroll
+            for (int ch = 0; ch < KT / 32; ++ch) {
+                umma::wait_ld32(s[ch & 1]);
+                if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
+                uint32_t p[16];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float4 f = info[2 * ch + g];
+                    const float a = fac * f.x, sh = f.y - ref;
+                    const bool gok = whole || (okm >> (2 * ch + g) & 1u);
+                    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        float p0 = fast_exp2(fmaf(__uint_as_float(s[ch & 1][16 * g + k]), a, sh));
+                        float p1 = fast_exp2(fmaf(__uint_as_float(s[ch & 1][16 * g + k + 1]), a, sh));
+                        if (!whole) {
+                            if (!gok || 32 * ch + 16 * g + k >= rem) p0 = 0.f;
+                            if (!gok || 32 * ch + 16 * g + k + 1 >= rem) p1 = 0.f;
+                        }
+                        sum0 += p0;
+                        sum1 += p1;
+                        p[8 * g + k / 2] = half2_of(p0, p1);
+                    }
+                    if (gok) l_run = fmaf(sum0 + sum1, f.z, l_run);
+                }
+                umma::st16(ts + 16 * ch, p);
+            }
+            umma::wait_st();
+            umma::fence_before_sync();
+            warp_arrive(&mbar[T::bPFull + q * NB + i % NB]);
+        }
+        if (ok && my_nt > 0) ok = wait_bar(T::bPvDone + q, (my_nt - 1) & 1);
+        if (ok && my_nt > 0) {
+            umma::fence_after_sync();
+            const size_t rr = col_row(cv ? c : 0);
+            const float l = l_run * (1.f / 16.f);  // 2^-kLShift
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                umma::ld32_issue(lane_base + T::kTmO + q * D + 32 * ch, o);
+                umma::wait_ld32(o);
+                if (!cv) continue;
+                if (A.splits == 1) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + rr * D + 32 * ch);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float x0 = __uint_as_float(o[8 * k + 2 * m]) * inv, x1 = __uint_as_float(o[8 * k + 2 * m + 1]) * inv;
+                            w[m] = float_to_bf16_bits(l == 0.f ? 0.f : x0) |
+                                   (static_cast<uint32_t>(float_to_bf16_bits(l == 0.f ? 0.f : x1)) << 16);
+                        }
+                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(A.acc + (static_cast<size_t>(split) * rows_total + rr) * D + 32 * ch);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            if (cv && A.splits > 1) {
+                float *ml = A.ml + (static_cast<size_t>(split) * rows_total + rr) * 2;
+                ml[0] = m_run;
+                ml[1] = l;
+            }
+        } else if (cv && my_nt == 0) {
+            dead_row(c);
+        }
+        umma::fence_before_sync();
+    } else if (warp < T::kMmaWarp) {
+        // ================= value codes to fp16 =================
+        // item (token t, chunk of 16 codes): eight lanes take four chunks of tokens t and t ^ 5, whose reads
+        // and writes fall in eight different 16-byte bank groups
+        const int ct = tid - 32 * T::kSoftWarps;
+        for (int i = 0; i < nt_all; ++i) {
+            if (!wait_bar(T::bRFull + i % T::RS, (i / T::RS) & 1)) break;
+            if (i >= T::VS && !wait_bar(T::bVFree + i % T::VS, (i / T::VS - 1) & 1)) break;
+            const uint32_t raw = sbase + T::kROff + (i % T::RS) * T::kKBytes;
+            const uint32_t dst = sbase + T::kVOff + (i % T::VS) * 2 * T::kKBytes;
+            const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
+            const int rem = tok1 - (tok0 + i * KT);
+#pragma unroll 2
+            for (int e = ct; e < KT * D / 16; e += 32 * T::kConvWarps) {
+                const int cl = e & 3, pr = (e >> 2) & 1, hi = (e >> 3) % (2 * XB), tp = e / (16 * XB);  // tp: token pair
+                const int t8 = tp >> 2, k = tp & 3;
+                const int t = 8 * t8 + (pr ? k ^ 5 : k);
+                const int x = hi >> 1, ch = 4 * (hi & 1) + cl;  // column block of codes, chunk in it
+                uint4 w = lds128(raw + x * (KT * 128) + t * 128 + ((ch ^ (t & 7)) << 4));
+                if (t >= rem || !(okm >> (t >> 4) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);  // not a token: holds anything
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                uint32_t h[8];
+#pragma unroll
+                for (int k2 = 0; k2 < 4; ++k2) {
+                    h[2 * k2] = e4m3_to_half2(v[k2]);
+                    h[2 * k2 + 1] = e4m3_to_half2(v[k2] >> 16);
+                }
+                const uint32_t at = dst + (2 * x + (ch >> 2)) * (KT * 128) + t * 128;
+                sts128(at + (((2 * (ch & 3)) ^ (t & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                sts128(at + (((2 * (ch & 3) + 1) ^ (t & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+            }
+            umma::fence_proxy_async();
+            warp_arrive(&mbar[T::bRFree + i % T::RS]);
+            warp_arrive(&mbar[T::bVFull + i % T::VS]);
+        }
+    } else if (warp == T::kMmaWarp) {
+        // ================= MMA issue (lane 0) =================
+        if (lane == 0) {
+            constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
+            constexpr uint32_t id_o = umma::idesc_f16(128, D) | (1u << 16);                             // B along N
+            int total = 0, ns[NQ], npv[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                ns[q] = npv[q] = 0;
+                total += 2 * nt[q];
+            }
+            bool have_q = false;
+            long long t_last = clock64();
+            while (total > 0) {
+                bool moved = false;
+                if (!have_q) {
+                    have_q = umma::mbar_test_wait(&mbar[T::bQ], 0);
+                    if (have_q) umma::fence_after_sync();
+                    moved = have_q;
+                }
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    // O += P V of tile i, as soon as P is there
+                    int i = npv[q];
+                    if (i < ns[q] && umma::mbar_test_wait(&mbar[T::bPFull + q * NB + i % NB], (i / NB) & 1) &&
+                        umma::mbar_test_wait(&mbar[T::bVFull + i % T::VS], (i / T::VS) & 1) &&
+                        (NB == 1 || i == 0 || umma::mbar_test_wait(&mbar[T::bPvDone + q], (i - 1) & 1))) {
+                        umma::fence_after_sync();
+                        const uint32_t va = sbase + T::kVOff + (i % T::VS) * 2 * T::kKBytes;
+                        const uint32_t tp = tbase + T::kTmS + (q * NB + i % NB) * KT;
+#pragma unroll
+                        for (int k = 0; k < KT / 16; ++k) {
+                            const uint64_t dv = umma::make_desc_sw128(va + 2048 * k, KT * 128, 1024);
+                            umma::mma_f16_tmem_a(tbase + T::kTmO + q * D, tp + 8 * k, static_cast<uint32_t>(dv),
+                                                 static_cast<uint32_t>(dv >> 32), id_o, (i > 0 || k > 0) ? 1 : 0);
+                        }
+                        umma::commit(&mbar[T::bPvDone + q]);
+                        ++npv[q];
+                        bool all = true;
+#pragma unroll
+                        for (int p = 0; p < NQ; ++p) all = all && (nt[p] <= i || npv[p] > i);
+                        if (all) umma::commit(&mbar[T::bVFree + i % T::VS]);
+                        --total;
+                        moved = true;
+                    }
+                    // scores of tile i, as soon as its keys are there and its score buffer is free
+                    i = ns[q];
+                    if (have_q && i < nt[q] && umma::mbar_test_wait(&mbar[T::bKFull + i % T::KS], (i / T::KS) & 1) &&
+                        (i < NB || npv[q] > i - NB) &&
+                        (i < NB || (NB > 1 && npv[q] > i - 1) || umma::mbar_test_wait(&mbar[T::bPvDone + q], (i - NB) & 1))) {
+                        umma::fence_after_sync();
+                        const uint32_t ka = sbase + T::kKOff + (i % T::KS) * T::kKBytes;
+                        const uint32_t qa = sbase + T::kQOff + 2 * q * T::kQBytes;
+                        const uint32_t ds = tbase + T::kTmS + (q * NB + i % NB) * KT;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            const uint32_t step = 32 * (k & 3);
+                            const uint64_t dk = umma::make_desc_sw128(ka + (k >> 2) * (KT * 128) + step, 16, 1024);
+                            const uint64_t dh = umma::make_desc_sw128(qa + (k >> 2) * (128 * 128) + step, 16, 1024);
+                            const uint64_t dl = umma::make_desc_sw128(qa + T::kQBytes + (k >> 2) * (128 * 128) + step, 16, 1024);
+                            umma::mma_e4m3(ds, dh, dk, id_s, k > 0 ? 1 : 0);
+                            umma::mma_e4m3(ds, dl, dk, id_s, 1);
+                        }
+                        umma::commit(&mbar[T::bSFull + q * NB + i % NB]);
+                        ++ns[q];
+                        bool all = true;
+#pragma unroll
+                        for (int p = 0; p < NQ; ++p) all = all && (nt[p] <= i || ns[p] > i);
+                        if (all) umma::commit(&mbar[T::bKFree + i % T::KS]);
+                        --total;
+                        moved = true;
+                    }
+                }
+                if (moved) {
+                    t_last = clock64();
+                    continue;
+                }
+                if (*abort_flag) break;
+                if (A.wait_limit <= 0 || clock64() - t_last > A.wait_limit) {
+                    *abort_flag = 1;
+                    atomicOr(A.status, TQ_DEVERR_TIMEOUT);
+                    break;
+                }
+            }
+            // every MMA issued must be done before tensor memory is freed
+            umma::commit(&mbar[T::bEnd]);
+            const long long t0 = clock64();
+            while (!umma::mbar_try_wait(&mbar[T::bEnd], 0) && clock64() - t0 < kDrainLimit) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================= page copies and scales =================
+        int k_issued = 0, r_issued = 0;
+        for (int i = 0; i < nt_all; ++i) {
+            const int pos = tok0 + (i * ppt + lane) * P;  // lane p: the tile's page p
+            const bool in = lane < ppt && pos < tok1;
+            int blk = in ? __ldg(A.block_table + static_cast<int64_t>(b) * A.max_blocks + (pos >> A.pshift)) : -1;
+            const bool good = in && blk >= 0 && blk < A.num_blocks;
+            if (in && !good) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
+            float ks = 0.f, vs = 0.f;
+            if (good) {
+                ks = __ldg(A.k_scales + static_cast<int64_t>(blk) * A.Hkv + kvh);
+                vs = __ldg(A.v_scales + static_cast<int64_t>(blk) * A.Hkv + kvh);
+            }
+            const uint32_t pages = __ballot_sync(0xffffffffu, good);
+            const int y = good ? static_cast<int>((static_cast<int64_t>(blk) * A.Hkv + kvh) * P) : 0;
+            if (i >= T::KS && !wait_bar(T::bKFree + i % T::KS, (i / T::KS - 1) & 1)) break;
+            const int slot = i % T::kRing;
+            if (lane < ppt) {
+                const float lv = log2_scale(vs);
+                float4 *info = reinterpret_cast<float4 *>(smem + T::kInfoOff) + slot * GR;
+                const float4 f = make_float4(ks, lv, fast_exp2(kLShift - lv), 0.f);
+                for (int g = 0; g < P / 16; ++g) info[lane * (P / 16) + g] = f;
+            }
+            if (lane == 0) {
+                uint32_t m = pages;
+                if (P == 32) {  // a bit per 16-token group
+                    m = 0;
+                    for (int g = 0; g < GR; ++g) m |= (pages >> (g / 2) & 1u) << g;
+                }
+                reinterpret_cast<uint32_t *>(smem + T::kOkOff)[slot] = m;
+            }
+            __syncwarp();
+            const uint32_t bytes = good ? static_cast<uint32_t>(P * D) : 0u;
+            auto copy = [&](const CUtensorMap &tm, uint32_t dst, int bar) {  // lanes below ppt
+                const uint32_t mb = saddr(&mbar[bar]);
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+                if (!good) return;
+#pragma unroll
+                for (int x = 0; x < XB; ++x)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                 ::"r"(dst + x * (KT * 128) + lane * P * 128), "l"(reinterpret_cast<uint64_t>(&tm)), "r"(x * 128),
+                                 "r"(y), "r"(mb)
+                                 : "memory");
+            };
+            if (lane < ppt) copy(tmK, sbase + T::kKOff + (i % T::KS) * T::kKBytes, T::bKFull + i % T::KS);
+            k_issued = i + 1;
+            if (i >= T::RS && !wait_bar(T::bRFree + i % T::RS, (i / T::RS - 1) & 1)) break;
+            if (lane < ppt) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the widening's reads are done
+                copy(tmV, sbase + T::kROff + (i % T::RS) * T::kKBytes, T::bRFull + i % T::RS);
+            }
+            r_issued = i + 1;
+        }
+        // copies in flight must land before the CTA exits, also when another warp gives up later: the last
+        // issue of each stage (long done in a run that consumed them)
+        auto drain = [&](int bar, int n, int stages) {
+            for (int t = max(0, n - stages); t < n; ++t) {
+                const long long t0 = clock64();
+                while (!umma::mbar_try_wait(&mbar[bar + t % stages], (t / stages) & 1) && clock64() - t0 < kDrainLimit) {
+                }
+            }
+        };
+        drain(T::bKFull, k_issued, T::KS);
+        drain(T::bRFull, r_issued, T::RS);
+    }
+
+    // ---- teardown ----
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    if (*abort_flag && tid < 128 * NQ && tid < ncol) dead_row(tid);  // a wait gave up: nothing of this CTA counts
+    if (warp == T::kMmaWarp) umma::tmem_dealloc(tbase, T::kTmCols);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, cudaStream_t st)
+{
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(prefill_fp8_kernel<D>), Tc<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(a.B) * a.Hkv * a.splits * a.nqt;
+    prefill_fp8_kernel<D><<<grid, Tc<D>::kThreads, Tc<D>::kSmem, st>>>(tk, tv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int prefill_tc_columns(int d) { return d == 128 ? 128 * Tc<128>::NQ : 128 * Tc<256>::NQ; }
+
+cudaError_t launch_prefill_tc(const CUtensorMap &tk, const CUtensorMap &tv, int d, const Args &a, cudaStream_t st)
+{
+    return d == 128 ? launch<128>(tk, tv, a, st) : launch<256>(tk, tv, a, st);
+}
+
+}  // namespace fp8
+}  // namespace tq
