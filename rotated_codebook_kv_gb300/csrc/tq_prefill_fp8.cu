@@ -17,7 +17,7 @@
 // Warps (one CTA per SM):
 //   4 NQ      one thread per column: query operands, online softmax, output
 //   4         value codes of a tile to fp16 (rows of 64 coordinates, 128-byte swizzle, one row per token)
-//   1         tensor-memory allocation; lane 0 issues the MMAs as their operands become ready
+//   NQ        MMA issue, one column tile each (the first also allocates tensor memory)
 //   1         page copies (TMA boxes of a page x 128 bytes, 128-byte swizzle), scales
 // Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT, stops the CTA (its rows
 // then carry no weight), lets copies and MMAs in flight finish, and frees tensor memory.
@@ -31,15 +31,18 @@ namespace {
 template <int D>
 struct Tc {
     static constexpr int NQ = D == 128 ? 2 : 1;         // column tiles
-    static constexpr int KT = D == 128 ? 128 : 64;      // tokens per tile
-    static constexpr int NB = D == 128 ? 1 : 2;         // score buffers per column tile
+    static constexpr int KT = 64;                       // tokens per tile
+    static constexpr int NB = 2;                        // score buffers per column tile
     static constexpr int XB = D / 128;                  // 128-byte column blocks of a row of codes
     static constexpr int kSoftWarps = 4 * NQ;
     static constexpr int kConvWarps = 4;
     static constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-    static constexpr int kLoadWarp = kMmaWarp + 1;
-    static constexpr int kThreads = 32 * (kLoadWarp + 1);
-    static constexpr int KS = 3, RS = 2, VS = 2;        // stages: keys, value codes, fp16 values
+    static constexpr int kLoadWarp = kMmaWarp + NQ;
+    static constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: the last one has one or two idle warps
+    // registers: 512 threads start with 128 each; the column warps take 192 and leave 64 to the others
+    // (2 x 128 x 192 + 2 x 128 x 64 = 512 x 128).  384 threads have 168 each and keep them.
+    static constexpr bool kSplitRegs = NQ == 2;
+    static constexpr int KS = D == 128 ? 4 : 3, RS = D == 128 ? 3 : 2, VS = D == 128 ? 3 : 2;  // stages: keys, value codes, fp16 values
     static constexpr int GR = KT / 16;                  // 16-token groups of a tile (a page holds one or two)
     static constexpr int kRing = 8;                     // tiles whose scales are kept
     static constexpr uint32_t kQBytes = 128u * D;       // one term of one column tile
@@ -62,7 +65,8 @@ struct Tc {
     static constexpr int bSFull = bVFree + VS;   // [NQ][NB] scores in tensor memory
     static constexpr int bPFull = bSFull + NQ * NB;  // [NQ][NB] P in tensor memory, O rescaled
     static constexpr int bPvDone = bPFull + NQ * NB;  // [NQ] O += P V done
-    static constexpr int bEnd = bPvDone + NQ;    // teardown: every MMA issued is done
+    static constexpr int bODone = bPvDone + NQ;  // [NQ] the last O += P V done
+    static constexpr int bEnd = bODone + NQ;     // teardown: every MMA issued is done
     static constexpr int kBars = bEnd + 1;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;  // tensor-memory base, abort flag
     static constexpr size_t kSmem = 1024 + kMiscOff + 16;
@@ -110,6 +114,120 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 lanes side by side: one issue slot for two multiply-adds or sums.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The largest y of a column's KT scores at tensor-memory address ts.  info: (ks, log2 vs, 2^4 / vs, -) per 16
+// tokens; WHOLE: every token is seen, else those below rem of the groups in okm.
+template <int KT, bool WHOLE>
+__device__ __forceinline__ float tile_max(uint32_t ts, const float4 *info, float fac, uint32_t okm, int rem)
+{
+    float top = -INFINITY;
+    uint32_t s[2][32];
+    umma::ld32_issue(ts, s[0]);
+#pragma unroll
+    for (int ch = 0; ch < KT / 32; ++ch) {
+        uint32_t(&v)[32] = s[ch & 1];
+        umma::wait_ld32(v);
+        if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int k = 16 * g; k < 16 * g + 16; k += 4) {
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = WHOLE || 32 * ch + k + j < rem ? __uint_as_float(v[k + j]) : -INFINITY;
+                m0 = max3(m0, x[0], x[1]);
+                m1 = max3(m1, x[2], x[3]);
+            }
+            m0 = fmaxf(m0, m1);
+            const float4 f = info[2 * ch + g];
+            if (WHOLE || ((okm >> (2 * ch + g) & 1u) && m0 != -INFINITY)) top = fmaxf(top, fmaf(m0, fac * f.x, f.y));
+        }
+    }
+    return top;
+}
+
+// P = 2^(y - ref) in fp16 over the scores (two tokens per column); returns the sum of 2^4 P / vs.
+template <int KT, bool WHOLE>
+__device__ __forceinline__ float tile_exp(uint32_t ts, const float4 *info, float fac, float ref, uint32_t okm, int rem)
+{
+    float l = 0.f;
+    uint32_t s[2][32];
+    umma::ld32_issue(ts, s[0]);
+#pragma unroll
+    for (int ch = 0; ch < KT / 32; ++ch) {
+        uint32_t(&v)[32] = s[ch & 1];
+        umma::wait_ld32(v);
+        if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
+        uint32_t p[16];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const float4 f = info[2 * ch + g];
+            const float a = fac * f.x, sh = f.y - ref;
+            const uint64_t a2 = pack2(a, a), sh2 = pack2(sh, sh);
+            const bool gok = WHOLE || (okm >> (2 * ch + g) & 1u);
+            uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+            for (int k = 16 * g; k < 16 * g + 16; k += 4) {
+                float2 x0 = unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), a2, sh2));
+                float2 x1 = unpack2(fma2(pack2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), a2, sh2));
+                x0.x = fast_exp2(x0.x);
+                x0.y = fast_exp2(x0.y);
+                x1.x = fast_exp2(x1.x);
+                x1.y = fast_exp2(x1.y);
+                if (!WHOLE) {
+                    const int t = 32 * ch + k;
+                    if (!gok || t >= rem) x0.x = 0.f;
+                    if (!gok || t + 1 >= rem) x0.y = 0.f;
+                    if (!gok || t + 2 >= rem) x1.x = 0.f;
+                    if (!gok || t + 3 >= rem) x1.y = 0.f;
+                }
+                sum0 = add2(sum0, pack2(x0.x, x0.y));
+                sum1 = add2(sum1, pack2(x1.x, x1.y));
+                p[k / 2] = half2_of(x0.x, x0.y);
+                p[k / 2 + 1] = half2_of(x1.x, x1.y);
+            }
+            const float2 t = unpack2(add2(sum0, sum1));
+            if (gok) l = fmaf(t.x + t.y, f.z, l);
+        }
+        umma::st16(ts + 16 * ch, p);
+    }
+    return l;
 }
 
 template <int D>
@@ -178,7 +296,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         umma::mbar_init(&mbar[T::bQ], T::kSoftWarps);
         for (int i = 0; i < T::KS; ++i) {
             umma::mbar_init(&mbar[T::bKFull + i], ppt);
-            umma::mbar_init(&mbar[T::bKFree + i], 1);
+            umma::mbar_init(&mbar[T::bKFree + i], NQ);
         }
         for (int i = 0; i < T::RS; ++i) {
             umma::mbar_init(&mbar[T::bRFull + i], ppt);
@@ -186,14 +304,17 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         }
         for (int i = 0; i < T::VS; ++i) {
             umma::mbar_init(&mbar[T::bVFull + i], T::kConvWarps);
-            umma::mbar_init(&mbar[T::bVFree + i], 1);
+            umma::mbar_init(&mbar[T::bVFree + i], NQ);
         }
         for (int i = 0; i < NQ * NB; ++i) {
             umma::mbar_init(&mbar[T::bSFull + i], 1);
             umma::mbar_init(&mbar[T::bPFull + i], 4);
         }
-        for (int i = 0; i < NQ; ++i) umma::mbar_init(&mbar[T::bPvDone + i], 1);
-        umma::mbar_init(&mbar[T::bEnd], 1);
+        for (int i = 0; i < NQ; ++i) {
+            umma::mbar_init(&mbar[T::bPvDone + i], 1);
+            umma::mbar_init(&mbar[T::bODone + i], 1);
+        }
+        umma::mbar_init(&mbar[T::bEnd], NQ);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -206,10 +327,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     // status bit); a zero limit tests once
     auto wait_bar = [&](int i, uint32_t par) -> bool {
         uint64_t *mb = &mbar[i];
-        bool ok = false;
-        if (A.wait_limit <= 0) {
-            ok = umma::mbar_test_wait(mb, par);
-        } else {
+        bool ok = umma::mbar_test_wait(mb, par);
+        if (__all_sync(0xffffffffu, ok)) return true;  // the usual way, without a look at the clock
+        if (A.wait_limit > 0) {
             const long long t0 = clock64();
             while (!(ok = umma::mbar_try_wait(mb, par))) {
                 if (*abort_flag || clock64() - t0 > A.wait_limit) break;
@@ -222,6 +342,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         return __all_sync(0xffffffffu, ok);  // the lanes poll separately: decide as a warp
     };
 
+    if constexpr (T::kSplitRegs) {
+        if (warp < T::kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    }
     if (warp < T::kSoftWarps) {
         // ================= columns: query operands, softmax, output =================
         const int q = warp >> 2, r = tid & 127, c = 128 * q + r;
@@ -288,50 +412,26 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
             const int rem = lim - (tok0 + i * KT);  // tokens of the tile that this column sees
             const bool whole = __all_sync(0xffffffffu, rem >= KT) && okm == (1u << GR) - 1u;
-            // ---- the tile's maximum ----
-            float top = -INFINITY;
-            uint32_t s[2][32];
-            umma::ld32_issue(ts, s[0]);
-#pragma unroll
-            for (int ch = 0; ch < KT / 32; ++ch) {
-                umma::wait_ld32(s[ch & 1]);
-                if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 f = info[2 * ch + g];
-                    float m0 = -INFINITY, m1 = -INFINITY;
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            m0 = fmaxf(m0, fmaxf(__uint_as_float(s[ch & 1][16 * g + k]), __uint_as_float(s[ch & 1][16 * g + k + 1])));
-                            m1 = fmaxf(m1, fmaxf(__uint_as_float(s[ch & 1][16 * g + k + 2]), __uint_as_float(s[ch & 1][16 * g + k + 3])));
-                        }
-                    } else if (okm >> (2 * ch + g) & 1u) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (32 * ch + 16 * g + k < rem) m0 = fmaxf(m0, __uint_as_float(s[ch & 1][16 * g + k]));
-                    }
-                    m0 = fmaxf(m0, m1);
-                    if (m0 != -INFINITY) top = fmaxf(top, fmaf(m0, fac * f.x, f.y));
-                }
-            }
+            const float top = whole ? tile_max<KT, true>(ts, info, fac, okm, rem) : tile_max<KT, false>(ts, info, fac, okm, rem);
             // ---- lazy rescale ----
             const float m_new = fmaxf(m_run, top);
             const bool need = m_run != -INFINITY && m_new > m_run + kLazy;
             if (m_run == -INFINITY) m_run = m_new;  // O's row is zero or unwritten so far
             if (__any_sync(0xffffffffu, need)) {
-                // with one score buffer O += P V of the tile before is done when the scores are there
+                // with one score buffer O += P V of the tile before is done when the scores are there; with two
+                // that of the tile before it is, so the parity tells the one from the other
                 if (NB > 1 && !(ok = wait_bar(T::bPvDone + q, (i - 1) & 1))) break;
                 umma::fence_after_sync();
                 const float al = need ? fast_exp2(m_run - m_new) : 1.f;
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     const uint32_t to = lane_base + T::kTmO + q * D + 32 * ch;
-                    umma::ld32_issue(to, s[0]);
-                    umma::wait_ld32(s[0]);
+                    uint32_t o[32];
+                    umma::ld32_issue(to, o);
+                    umma::wait_ld32(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[0][k] = __float_as_uint(__uint_as_float(s[0][k]) * al);
-                    umma::st32(to, s[0]);
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                    umma::st32(to, o);
                 }
                 umma::wait_st();
                 if (need) {
@@ -339,41 +439,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                     m_run = m_new;
                 }
             }
-            // ---- P = 2^(y - m) over the scores ----
             const float ref = m_run == -INFINITY ? 0.f : m_run;
-            umma::ld32_issue(ts, s[0]);
-#pragma unroll
-            for (int ch = 0; ch < KT / 32; ++ch) {
-                umma::wait_ld32(s[ch & 1]);
-                if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
-                uint32_t p[16];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 f = info[2 * ch + g];
-                    const float a = fac * f.x, sh = f.y - ref;
-                    const bool gok = whole || (okm >> (2 * ch + g) & 1u);
-                    float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        float p0 = fast_exp2(fmaf(__uint_as_float(s[ch & 1][16 * g + k]), a, sh));
-                        float p1 = fast_exp2(fmaf(__uint_as_float(s[ch & 1][16 * g + k + 1]), a, sh));
-                        if (!whole) {
-                            if (!gok || 32 * ch + 16 * g + k >= rem) p0 = 0.f;
-                            if (!gok || 32 * ch + 16 * g + k + 1 >= rem) p1 = 0.f;
-                        }
-                        sum0 += p0;
-                        sum1 += p1;
-                        p[8 * g + k / 2] = half2_of(p0, p1);
-                    }
-                    if (gok) l_run = fmaf(sum0 + sum1, f.z, l_run);
-                }
-                umma::st16(ts + 16 * ch, p);
-            }
+            l_run += whole ? tile_exp<KT, true>(ts, info, fac, ref, okm, rem) : tile_exp<KT, false>(ts, info, fac, ref, okm, rem);
             umma::wait_st();
             umma::fence_before_sync();
             warp_arrive(&mbar[T::bPFull + q * NB + i % NB]);
         }
-        if (ok && my_nt > 0) ok = wait_bar(T::bPvDone + q, (my_nt - 1) & 1);
+        // a barrier of its own: bPvDone may be a phase behind or at the end here, which a parity cannot tell
+        if (ok && my_nt > 0) ok = wait_bar(T::bODone + q, 0);
         if (ok && my_nt > 0) {
             umma::fence_after_sync();
             const size_t rr = col_row(cv ? c : 0);
@@ -448,98 +521,82 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             warp_arrive(&mbar[T::bRFree + i % T::RS]);
             warp_arrive(&mbar[T::bVFull + i % T::VS]);
         }
-    } else if (warp == T::kMmaWarp) {
-        // ================= MMA issue (lane 0) =================
-        if (lane == 0) {
-            constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
-            constexpr uint32_t id_o = umma::idesc_f16(128, D) | (1u << 16);                             // B along N
-            int total = 0, ns[NQ], npv[NQ];
+    } else if (warp < T::kLoadWarp) {
+        // ================= MMA issue: a warp per column tile, one elected lane =================
+        // The order is fixed and the warp stays converged, so that the descriptors live in uniform registers: an
+        // issue from one lane's divergent branch took ~110 cycles an MMA against the tensor core's 64.
+        const int q = warp - T::kMmaWarp;
+        const int my_nt = q ? nt[NQ - 1] : nt[0];
+        constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
+        constexpr uint32_t id_o = umma::idesc_f16(128, 128) | (1u << 16);                           // B along N
+        // descriptors are built once: a step only adds to the low word (the address in units of 16 bytes)
+        const uint64_t dq = umma::make_desc_sw128(sbase + T::kQOff + 2 * q * T::kQBytes, 16, 1024);
+        const uint64_t dk = umma::make_desc_sw128(sbase + T::kKOff, 16, 1024);
+        const uint64_t dv = umma::make_desc_sw128(sbase + T::kVOff, KT * 128, 1024);
+        const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), v_lo = static_cast<uint32_t>(dv);
+        const uint32_t kq_hi = static_cast<uint32_t>(dk >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
+        const uint32_t tm_s = tbase + T::kTmS + q * NB * KT, tm_o = tbase + T::kTmO + q * D;
+        auto scores = [&](int i) -> bool {  // S of tile i, once its keys are there
+            if (!wait_bar(T::bKFull + i % T::KS, (i / T::KS) & 1)) return false;
+            umma::fence_after_sync();
+            const uint32_t ka = k_lo + (i % T::KS) * (T::kKBytes / 16), ds = tm_s + (i % NB) * KT;
+            if (umma::elect_one()) {
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                ns[q] = npv[q] = 0;
-                total += 2 * nt[q];
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint32_t kd = ka + (k >> 2) * (KT * 8) + 2 * (k & 3), qd = q_lo + (k >> 2) * (128 * 8) + 2 * (k & 3);
+                    umma::mma_e4m3_lohi(ds, qd, kq_hi, kd, kq_hi, id_s, k > 0 ? 1 : 0);
+                    umma::mma_e4m3_lohi(ds, qd + T::kQBytes / 16, kq_hi, kd, kq_hi, id_s, 1);
+                }
+                umma::commit(&mbar[T::bSFull + q * NB + i % NB]);
+                umma::commit(&mbar[T::bKFree + i % T::KS]);
             }
-            bool have_q = false;
-            long long t_last = clock64();
-            while (total > 0) {
-                bool moved = false;
-                if (!have_q) {
-                    have_q = umma::mbar_test_wait(&mbar[T::bQ], 0);
-                    if (have_q) umma::fence_after_sync();
-                    moved = have_q;
-                }
+            __syncwarp();
+            return true;
+        };
+        auto values = [&](int i) -> bool {  // O += P V of tile i, once P and its values are there
+            if (!wait_bar(T::bVFull + i % T::VS, (i / T::VS) & 1)) return false;
+            if (!wait_bar(T::bPFull + q * NB + i % NB, (i / NB) & 1)) return false;
+            umma::fence_after_sync();
+            const uint32_t va = v_lo + (i % T::VS) * (2 * T::kKBytes / 16), tp = tm_s + (i % NB) * KT;
+            if (umma::elect_one()) {
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    // O += P V of tile i, as soon as P is there
-                    int i = npv[q];
-                    if (i < ns[q] && umma::mbar_test_wait(&mbar[T::bPFull + q * NB + i % NB], (i / NB) & 1) &&
-                        umma::mbar_test_wait(&mbar[T::bVFull + i % T::VS], (i / T::VS) & 1) &&
-                        (NB == 1 || i == 0 || umma::mbar_test_wait(&mbar[T::bPvDone + q], (i - 1) & 1))) {
-                        umma::fence_after_sync();
-                        const uint32_t va = sbase + T::kVOff + (i % T::VS) * 2 * T::kKBytes;
-                        const uint32_t tp = tbase + T::kTmS + (q * NB + i % NB) * KT;
+                for (int k = 0; k < KT / 16; ++k)
 #pragma unroll
-                        for (int k = 0; k < KT / 16; ++k) {
-                            const uint64_t dv = umma::make_desc_sw128(va + 2048 * k, KT * 128, 1024);
-                            umma::mma_f16_tmem_a(tbase + T::kTmO + q * D, tp + 8 * k, static_cast<uint32_t>(dv),
-                                                 static_cast<uint32_t>(dv >> 32), id_o, (i > 0 || k > 0) ? 1 : 0);
-                        }
-                        umma::commit(&mbar[T::bPvDone + q]);
-                        ++npv[q];
-                        bool all = true;
-#pragma unroll
-                        for (int p = 0; p < NQ; ++p) all = all && (nt[p] <= i || npv[p] > i);
-                        if (all) umma::commit(&mbar[T::bVFree + i % T::VS]);
-                        --total;
-                        moved = true;
-                    }
-                    // scores of tile i, as soon as its keys are there and its score buffer is free
-                    i = ns[q];
-                    if (have_q && i < nt[q] && umma::mbar_test_wait(&mbar[T::bKFull + i % T::KS], (i / T::KS) & 1) &&
-                        (i < NB || npv[q] > i - NB) &&
-                        (i < NB || (NB > 1 && npv[q] > i - 1) || umma::mbar_test_wait(&mbar[T::bPvDone + q], (i - NB) & 1))) {
-                        umma::fence_after_sync();
-                        const uint32_t ka = sbase + T::kKOff + (i % T::KS) * T::kKBytes;
-                        const uint32_t qa = sbase + T::kQOff + 2 * q * T::kQBytes;
-                        const uint32_t ds = tbase + T::kTmS + (q * NB + i % NB) * KT;
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            const uint32_t step = 32 * (k & 3);
-                            const uint64_t dk = umma::make_desc_sw128(ka + (k >> 2) * (KT * 128) + step, 16, 1024);
-                            const uint64_t dh = umma::make_desc_sw128(qa + (k >> 2) * (128 * 128) + step, 16, 1024);
-                            const uint64_t dl = umma::make_desc_sw128(qa + T::kQBytes + (k >> 2) * (128 * 128) + step, 16, 1024);
-                            umma::mma_e4m3(ds, dh, dk, id_s, k > 0 ? 1 : 0);
-                            umma::mma_e4m3(ds, dl, dk, id_s, 1);
-                        }
-                        umma::commit(&mbar[T::bSFull + q * NB + i % NB]);
-                        ++ns[q];
-                        bool all = true;
-#pragma unroll
-                        for (int p = 0; p < NQ; ++p) all = all && (nt[p] <= i || ns[p] > i);
-                        if (all) umma::commit(&mbar[T::bKFree + i % T::KS]);
-                        --total;
-                        moved = true;
-                    }
-                }
-                if (moved) {
-                    t_last = clock64();
-                    continue;
-                }
-                if (*abort_flag) break;
-                if (A.wait_limit <= 0 || clock64() - t_last > A.wait_limit) {
-                    *abort_flag = 1;
-                    atomicOr(A.status, TQ_DEVERR_TIMEOUT);
-                    break;
-                }
+                    for (int x = 0; x < XB; ++x)  // 128 coordinates at a time
+                        umma::mma_f16_tmem_a(tm_o + 128 * x, tp + 8 * k, va + x * (2 * KT * 8) + 128 * k, v_hi, id_o,
+                                             (i > 0 || k > 0) ? 1 : 0);
+                umma::commit(&mbar[T::bPvDone + q]);
+                if (i == my_nt - 1) umma::commit(&mbar[T::bODone + q]);
+                umma::commit(&mbar[T::bVFree + i % T::VS]);
             }
-            // every MMA issued must be done before tensor memory is freed
-            umma::commit(&mbar[T::bEnd]);
-            const long long t0 = clock64();
-            while (!umma::mbar_try_wait(&mbar[T::bEnd], 0) && clock64() - t0 < kDrainLimit) {
+            __syncwarp();
+            return true;
+        };
+        auto done = [&](int i) -> bool {  // O += P V of tile i is done: its score buffer is free
+            return i < 0 || wait_bar(T::bPvDone + q, i & 1);
+        };
+        bool ok = wait_bar(T::bQ, 0);
+        if (my_nt > 0) ok = ok && scores(0);
+        for (int i = 0; ok && i < my_nt; ++i) {
+            if (NB > 1) ok = done(i - 1) && (i + 1 >= my_nt || scores(i + 1));
+            ok = ok && values(i);
+            if (NB == 1 && i + 1 < my_nt) ok = ok && done(i) && scores(i + 1);
+        }
+        for (int i = my_nt; ok && i < nt_all; ++i) {  // tiles that only the other column tile sees: hand the stages on
+            ok = wait_bar(T::bKFull + i % T::KS, (i / T::KS) & 1) && wait_bar(T::bVFull + i % T::VS, (i / T::VS) & 1);
+            if (ok && lane == 0) {
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[T::bKFree + i % T::KS])) : "memory");
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[T::bVFree + i % T::VS])) : "memory");
             }
         }
+        // every MMA issued must be done before tensor memory is freed
+        if (umma::elect_one()) umma::commit(&mbar[T::bEnd]);
         __syncwarp();
-    } else {
+        const long long t0 = clock64();
+        while (!umma::mbar_try_wait(&mbar[T::bEnd], 0) && clock64() - t0 < kDrainLimit) {
+        }
+        __syncwarp();
+    } else if (warp == T::kLoadWarp) {
         // ================= page copies and scales =================
         int k_issued = 0, r_issued = 0;
         for (int i = 0; i < nt_all; ++i) {

@@ -83,12 +83,21 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
 }
 
 // kind::f8f6f4 with both operands e4m3 in shared memory, K-major (idesc_f16's fields with the 8-bit
-// types' zero codes); a k-step is 32 elements.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, int accum)
+// types' zero codes); a k-step is 32 elements.  Descriptors as halves, see mma_f16_lohi.
+__device__ __forceinline__ void mma_e4m3_lohi(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                              uint32_t idesc, int accum)
 {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum));
+    asm volatile("{\n.reg .pred p;\n.reg .b64 da, db;\nsetp.ne.b32 p, %5, 0;\nmov.b64 da, {%1, %2};\n"
+                 "mov.b64 db, {%3, %4};\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %6, p;\n}\n"
+                 ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(accum), "r"(idesc));
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e != 0;
 }
 
 // Arrive on `mbar` when every tcgen05 operation this thread issued so far is done.
