@@ -6,18 +6,18 @@
 //   O[c][j] += sum_t P[c][t] vc_t[j]   kind::f16: P in fp16 from tensor memory, the value codes widened to fp16
 //                                      (exact) in shared memory, N = D coordinates j
 // with y = sm_scale log2(e) 2^-e ks[page] S + log2 vs[page], P = 2^(y - m), m a running maximum that is
-// only moved when it grows by more than 2^8 (P <= 2^8: fp16 keeps 11 bits of it down to 2^-14), and the
+// only moved when the maximum has grown far beyond it (below), and the
 // denominator the sum of P / vs in fp32.
 //
 // A CTA takes NQ tiles of 128 columns, (query token, head) pairs of one sequence and kv head, and the
 // KT-token tiles that they see in its split.  Two tiles at head dim 128: while one's scores are turned into
 // P, the tensor core works for the other.  At head dim 256 tensor memory holds one tile's O (256 columns)
-// and two score buffers.  P overwrites the scores that it came from.
+// and four score buffers.  P overwrites the scores that it came from.
 //
 // Warps (one CTA per SM):
 //   4 NQ      one thread per column: query operands, online softmax, output
 //   4         value codes of a tile to fp16 (rows of 64 coordinates, 128-byte swizzle, one row per token)
-//   NQ        MMA issue, one column tile each (the first also allocates tensor memory)
+//   1 + NQ    MMA issue: the scores (and tensor-memory allocation); P.V of a column tile each
 //   1         page copies (TMA boxes of a page x 128 bytes, 128-byte swizzle), scales
 // Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT, stops the CTA (its rows
 // then carry no weight), lets copies and MMAs in flight finish, and frees tensor memory.
@@ -32,13 +32,13 @@ template <int D>
 struct Tc {
     static constexpr int NQ = D == 128 ? 2 : 1;         // column tiles
     static constexpr int KT = 64;                       // tokens per tile
-    static constexpr int NB = 2;                        // score buffers per column tile
+    static constexpr int NB = D == 128 ? 2 : 4;         // score buffers per column tile
     static constexpr int XB = D / 128;                  // 128-byte column blocks of a row of codes
     static constexpr int kSoftWarps = 4 * NQ;
     static constexpr int kConvWarps = 4;
-    static constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-    static constexpr int kLoadWarp = kMmaWarp + NQ;
-    static constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: the last one has one or two idle warps
+    static constexpr int kMmaWarp = kSoftWarps + kConvWarps;  // scores; then a warp per column tile for P.V
+    static constexpr int kLoadWarp = kMmaWarp + 1 + NQ;
+    static constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups (one idle warp at head dim 256)
     // registers: 512 threads start with 128 each; the column warps take 192 and leave 64 to the others
     // (2 x 128 x 192 + 2 x 128 x 64 = 512 x 128).  384 threads have 168 each and keep them.
     static constexpr bool kSplitRegs = NQ == 2;
@@ -51,12 +51,12 @@ struct Tc {
     static constexpr uint32_t kKOff = kQOff + 2 * NQ * kQBytes;
     static constexpr uint32_t kROff = kKOff + KS * kKBytes;
     static constexpr uint32_t kVOff = kROff + RS * kKBytes;
-    static constexpr uint32_t kInfoOff = kVOff + VS * 2 * kKBytes;  // [ring][GR] (ks, log2 vs, 2^4 / vs, -)
+    static constexpr uint32_t kInfoOff = kVOff + VS * 2 * kKBytes;  // [ring][GR] (ks, log2 vs, 2^-6 / vs, -)
     static constexpr uint32_t kOkOff = kInfoOff + kRing * GR * 16;  // [ring] bit g: group g's page is valid
     static constexpr uint32_t kBarOff = kOkOff + kRing * 4;
     // barriers
     static constexpr int bQ = 0;                 // query operands in shared memory
-    static constexpr int bKFull = 1;             // [KS] keys landed (one arrival per page, and bytes)
+    static constexpr int bKFull = 1;             // [KS] keys landed (one arrival, and bytes)
     static constexpr int bKFree = bKFull + KS;   // [KS] the score MMAs of every tile are done
     static constexpr int bRFull = bKFree + KS;   // [RS] value codes landed
     static constexpr int bRFree = bRFull + RS;   // [RS] widened
@@ -64,9 +64,8 @@ struct Tc {
     static constexpr int bVFree = bVFull + VS;   // [VS] the P.V MMAs of every tile are done
     static constexpr int bSFull = bVFree + VS;   // [NQ][NB] scores in tensor memory
     static constexpr int bPFull = bSFull + NQ * NB;  // [NQ][NB] P in tensor memory, O rescaled
-    static constexpr int bPvDone = bPFull + NQ * NB;  // [NQ] O += P V done
-    static constexpr int bODone = bPvDone + NQ;  // [NQ] the last O += P V done
-    static constexpr int bEnd = bODone + NQ;     // teardown: every MMA issued is done
+    static constexpr int bPvDone = bPFull + NQ * NB;  // [NQ][NB] O += P V of a score buffer's P done
+    static constexpr int bEnd = bPvDone + NQ * NB;    // teardown: every MMA issued is done
     static constexpr int kBars = bEnd + 1;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;  // tensor-memory base, abort flag
     static constexpr size_t kSmem = 1024 + kMiscOff + 16;
@@ -74,11 +73,19 @@ struct Tc {
     static constexpr uint32_t kTmS = 0;                              // [NQ][NB] KT columns
     static constexpr uint32_t kTmO = NQ * NB * KT;                   // [NQ] D columns
     static constexpr uint32_t kTmCols = 512;
+    static_assert(KT == 64, "the softmax holds a column's 64 scores");
+    static_assert(KS + NB < kRing, "a tile's scales are written over those of a tile that every column is done with");
     static_assert(kTmO + NQ * D <= kTmCols, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-constexpr float kLazy = 8.f;  // rescale O when the maximum grows by more than this (log2 units)
+// The reference m of a column's probabilities is set kAim above the scores' maximum and O rescaled only when the maximum
+// has since passed m by kLazy (log2 units): P = 2^(y - m) is at most 2^12 in fp16 (65504 its largest), 2^-4 after a
+// rescale, where everything down to 2^-10 of the largest keeps 11 bits and down to 2^-20 something.  A rescale waits
+// for the tensor core and moves all of O, so a few strong tokens in every tile made it the longest step of many tiles.
+constexpr float kAim = 4.f, kLazy = 12.f;
+// Denominators are summed as 2^-6 P / vs: vs in 2^-100 .. 2^119 neither overflows nor flushes.
+constexpr float kSumShift = -6.f;
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -149,83 +156,66 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
-// The largest y of a column's KT scores at tensor-memory address ts.  info: (ks, log2 vs, 2^4 / vs, -) per 16
-// tokens; WHOLE: every token is seen, else those below rem of the groups in okm.
-template <int KT, bool WHOLE>
-__device__ __forceinline__ float tile_max(uint32_t ts, const float4 *info, float fac, uint32_t okm, int rem)
+// A column's 64 scores of a tile, and the tile's scales: a = fac ks, b = log2 vs, inv = 2^-6 / vs per 16 tokens.
+struct Scores {
+    uint32_t v[64];
+    float a[4], b[4], inv[4];
+};
+
+// The largest y of the tile.  WHOLE: every token is seen, else those below rem of the groups in okm.
+template <bool WHOLE>
+__device__ __forceinline__ float tile_max(const Scores &s, uint32_t okm, int rem)
 {
     float top = -INFINITY;
-    uint32_t s[2][32];
-    umma::ld32_issue(ts, s[0]);
 #pragma unroll
-    for (int ch = 0; ch < KT / 32; ++ch) {
-        uint32_t(&v)[32] = s[ch & 1];
-        umma::wait_ld32(v);
-        if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
+    for (int g = 0; g < 4; ++g) {
+        float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            float m0 = -INFINITY, m1 = -INFINITY;
+        for (int k = 16 * g; k < 16 * g + 16; k += 4) {
+            float x[4];
 #pragma unroll
-            for (int k = 16 * g; k < 16 * g + 16; k += 4) {
-                float x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = WHOLE || 32 * ch + k + j < rem ? __uint_as_float(v[k + j]) : -INFINITY;
-                m0 = max3(m0, x[0], x[1]);
-                m1 = max3(m1, x[2], x[3]);
-            }
-            m0 = fmaxf(m0, m1);
-            const float4 f = info[2 * ch + g];
-            if (WHOLE || ((okm >> (2 * ch + g) & 1u) && m0 != -INFINITY)) top = fmaxf(top, fmaf(m0, fac * f.x, f.y));
+            for (int j = 0; j < 4; ++j) x[j] = WHOLE || k + j < rem ? __uint_as_float(s.v[k + j]) : -INFINITY;
+            m0 = max3(m0, x[0], x[1]);
+            m1 = max3(m1, x[2], x[3]);
         }
+        m0 = fmaxf(m0, m1);
+        if (WHOLE || ((okm >> g & 1u) && m0 != -INFINITY)) top = fmaxf(top, fmaf(m0, s.a[g], s.b[g]));
     }
     return top;
 }
 
-// P = 2^(y - ref) in fp16 over the scores (two tokens per column); returns the sum of 2^4 P / vs.
-template <int KT, bool WHOLE>
-__device__ __forceinline__ float tile_exp(uint32_t ts, const float4 *info, float fac, float ref, uint32_t okm, int rem)
+// P = 2^(y - ref) in fp16, two tokens per word; returns the sum of 2^-6 P / vs.
+template <bool WHOLE>
+__device__ __forceinline__ float tile_exp(const Scores &s, uint32_t (&p)[32], float ref, uint32_t okm, int rem)
 {
     float l = 0.f;
-    uint32_t s[2][32];
-    umma::ld32_issue(ts, s[0]);
 #pragma unroll
-    for (int ch = 0; ch < KT / 32; ++ch) {
-        uint32_t(&v)[32] = s[ch & 1];
-        umma::wait_ld32(v);
-        if (ch + 1 < KT / 32) umma::ld32_issue(ts + 32 * (ch + 1), s[(ch + 1) & 1]);
-        uint32_t p[16];
+    for (int g = 0; g < 4; ++g) {
+        const float sh = s.b[g] - ref;
+        const uint64_t a2 = pack2(s.a[g], s.a[g]), sh2 = pack2(sh, sh);
+        const bool gok = WHOLE || (okm >> g & 1u);
+        uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const float4 f = info[2 * ch + g];
-            const float a = fac * f.x, sh = f.y - ref;
-            const uint64_t a2 = pack2(a, a), sh2 = pack2(sh, sh);
-            const bool gok = WHOLE || (okm >> (2 * ch + g) & 1u);
-            uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-            for (int k = 16 * g; k < 16 * g + 16; k += 4) {
-                float2 x0 = unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), a2, sh2));
-                float2 x1 = unpack2(fma2(pack2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), a2, sh2));
-                x0.x = fast_exp2(x0.x);
-                x0.y = fast_exp2(x0.y);
-                x1.x = fast_exp2(x1.x);
-                x1.y = fast_exp2(x1.y);
-                if (!WHOLE) {
-                    const int t = 32 * ch + k;
-                    if (!gok || t >= rem) x0.x = 0.f;
-                    if (!gok || t + 1 >= rem) x0.y = 0.f;
-                    if (!gok || t + 2 >= rem) x1.x = 0.f;
-                    if (!gok || t + 3 >= rem) x1.y = 0.f;
-                }
-                sum0 = add2(sum0, pack2(x0.x, x0.y));
-                sum1 = add2(sum1, pack2(x1.x, x1.y));
-                p[k / 2] = half2_of(x0.x, x0.y);
-                p[k / 2 + 1] = half2_of(x1.x, x1.y);
+        for (int k = 16 * g; k < 16 * g + 16; k += 4) {
+            float2 x0 = unpack2(fma2(pack2(__uint_as_float(s.v[k]), __uint_as_float(s.v[k + 1])), a2, sh2));
+            float2 x1 = unpack2(fma2(pack2(__uint_as_float(s.v[k + 2]), __uint_as_float(s.v[k + 3])), a2, sh2));
+            x0.x = fast_exp2(x0.x);
+            x0.y = fast_exp2(x0.y);
+            x1.x = fast_exp2(x1.x);
+            x1.y = fast_exp2(x1.y);
+            if (!WHOLE) {
+                if (!gok || k >= rem) x0.x = 0.f;
+                if (!gok || k + 1 >= rem) x0.y = 0.f;
+                if (!gok || k + 2 >= rem) x1.x = 0.f;
+                if (!gok || k + 3 >= rem) x1.y = 0.f;
             }
-            const float2 t = unpack2(add2(sum0, sum1));
-            if (gok) l = fmaf(t.x + t.y, f.z, l);
+            sum0 = add2(sum0, pack2(x0.x, x0.y));
+            sum1 = add2(sum1, pack2(x1.x, x1.y));
+            p[k / 2] = half2_of(x0.x, x0.y);
+            p[k / 2 + 1] = half2_of(x1.x, x1.y);
         }
-        umma::st16(ts + 16 * ch, p);
+        const float2 t = unpack2(add2(sum0, sum1));
+        if (gok) l = fmaf(t.x + t.y, s.inv[g], l);
     }
     return l;
 }
@@ -295,11 +285,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     if (tid == 0) {
         umma::mbar_init(&mbar[T::bQ], T::kSoftWarps);
         for (int i = 0; i < T::KS; ++i) {
-            umma::mbar_init(&mbar[T::bKFull + i], ppt);
-            umma::mbar_init(&mbar[T::bKFree + i], NQ);
+            umma::mbar_init(&mbar[T::bKFull + i], 1);
+            umma::mbar_init(&mbar[T::bKFree + i], 1);
         }
         for (int i = 0; i < T::RS; ++i) {
-            umma::mbar_init(&mbar[T::bRFull + i], ppt);
+            umma::mbar_init(&mbar[T::bRFull + i], 1);
             umma::mbar_init(&mbar[T::bRFree + i], T::kConvWarps);
         }
         for (int i = 0; i < T::VS; ++i) {
@@ -309,12 +299,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         for (int i = 0; i < NQ * NB; ++i) {
             umma::mbar_init(&mbar[T::bSFull + i], 1);
             umma::mbar_init(&mbar[T::bPFull + i], 4);
-        }
-        for (int i = 0; i < NQ; ++i) {
             umma::mbar_init(&mbar[T::bPvDone + i], 1);
-            umma::mbar_init(&mbar[T::bODone + i], 1);
         }
-        umma::mbar_init(&mbar[T::bEnd], NQ);
+        umma::mbar_init(&mbar[T::bEnd], 1 + NQ);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -331,7 +318,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         if (__all_sync(0xffffffffu, ok)) return true;  // the usual way, without a look at the clock
         if (A.wait_limit > 0) {
             const long long t0 = clock64();
-            while (!(ok = umma::mbar_try_wait(mb, par))) {
+            while (!(ok = umma::mbar_try_wait_for(mb, par, 10000))) {
                 if (*abort_flag || clock64() - t0 > A.wait_limit) break;
             }
         }
@@ -400,7 +387,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             umma::fence_proxy_async();
             warp_arrive(&mbar[T::bQ]);
         }
-        const int lim = cv ? min(col_lim(c), tok1) : 0;
+        const int lim = cv ? min(col_lim(c), tok1) : tok1;  // an idle column (zero query) goes the way of the full ones
         const int my_nt = q ? nt[NQ - 1] : nt[0];
         float m_run = -INFINITY, l_run = 0.f;
         bool ok = true;
@@ -408,49 +395,58 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             if (!(ok = wait_bar(T::bSFull + q * NB + i % NB, (i / NB) & 1))) break;
             umma::fence_after_sync();
             const uint32_t ts = lane_base + T::kTmS + (q * NB + i % NB) * KT;
+            Scores s;
+            umma::ld64_issue(ts, s.v);
             const float4 *info = reinterpret_cast<const float4 *>(smem + T::kInfoOff) + (i % T::kRing) * GR;
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+                const float4 f = info[g];
+                s.a[g] = fac * f.x;
+                s.b[g] = f.y;
+                s.inv[g] = f.z;
+            }
             const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
             const int rem = lim - (tok0 + i * KT);  // tokens of the tile that this column sees
             const bool whole = __all_sync(0xffffffffu, rem >= KT) && okm == (1u << GR) - 1u;
-            const float top = whole ? tile_max<KT, true>(ts, info, fac, okm, rem) : tile_max<KT, false>(ts, info, fac, okm, rem);
+            umma::wait_ld64(s.v);
+            const float top = whole ? tile_max<true>(s, okm, rem) : tile_max<false>(s, okm, rem);
             // ---- lazy rescale ----
-            const float m_new = fmaxf(m_run, top);
-            const bool need = m_run != -INFINITY && m_new > m_run + kLazy;
-            if (m_run == -INFINITY) m_run = m_new;  // O's row is zero or unwritten so far
+            const bool need = m_run != -INFINITY && top > m_run + kLazy;
+            if (m_run == -INFINITY) m_run = top + kAim;  // O's row is zero or unwritten so far
             if (__any_sync(0xffffffffu, need)) {
-                // with one score buffer O += P V of the tile before is done when the scores are there; with two
-                // that of the tile before it is, so the parity tells the one from the other
-                if (NB > 1 && !(ok = wait_bar(T::bPvDone + q, (i - 1) & 1))) break;
+                if (i > 0 && !(ok = wait_bar(T::bPvDone + q * NB + (i - 1) % NB, ((i - 1) / NB) & 1))) break;  // O is at rest
                 umma::fence_after_sync();
-                const float al = need ? fast_exp2(m_run - m_new) : 1.f;
+                const float al = need ? fast_exp2(m_run - (top + kAim)) : 1.f;
+                const uint32_t to = lane_base + T::kTmO + q * D;
 #pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    const uint32_t to = lane_base + T::kTmO + q * D + 32 * ch;
-                    uint32_t o[32];
-                    umma::ld32_issue(to, o);
-                    umma::wait_ld32(o);
+                for (int ch = 0; ch < D; ch += 64) {
+                    uint32_t o[64];
+                    umma::ld64_issue(to + ch, o);
+                    umma::wait_ld64(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                    umma::st32(to, o);
+                    for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                    umma::st64(to + ch, o);
                 }
                 umma::wait_st();
                 if (need) {
                     l_run *= al;
-                    m_run = m_new;
+                    m_run = top + kAim;
                 }
             }
+            // ---- P = 2^(y - m) over the scores ----
             const float ref = m_run == -INFINITY ? 0.f : m_run;
-            l_run += whole ? tile_exp<KT, true>(ts, info, fac, ref, okm, rem) : tile_exp<KT, false>(ts, info, fac, ref, okm, rem);
+            uint32_t p[32];
+            l_run += whole ? tile_exp<true>(s, p, ref, okm, rem) : tile_exp<false>(s, p, ref, okm, rem);
+            umma::st32(ts, p);
             umma::wait_st();
             umma::fence_before_sync();
             warp_arrive(&mbar[T::bPFull + q * NB + i % NB]);
         }
-        // a barrier of its own: bPvDone may be a phase behind or at the end here, which a parity cannot tell
-        if (ok && my_nt > 0) ok = wait_bar(T::bODone + q, 0);
+        if (ok && my_nt > 0) ok = wait_bar(T::bPvDone + q * NB + (my_nt - 1) % NB, ((my_nt - 1) / NB) & 1);
         if (ok && my_nt > 0) {
             umma::fence_after_sync();
             const size_t rr = col_row(cv ? c : 0);
-            const float l = l_run * (1.f / 16.f);  // 2^-kLShift
+            const float l = l_run * 64.f;  // 2^-kSumShift
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
@@ -491,102 +487,113 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         // item (token t, chunk of 16 codes): eight lanes take four chunks of tokens t and t ^ 5, whose reads
         // and writes fall in eight different 16-byte bank groups
         const int ct = tid - 32 * T::kSoftWarps;
+        const int hi = (ct >> 3) % (2 * XB), tp = ct / (16 * XB), x = hi >> 1, ch = 4 * (hi & 1) + (ct & 3);
+        const int t = 8 * (tp >> 2) + ((ct & 4) ? (tp & 3) ^ 5 : tp & 3);  // further items: 16 / XB tokens on
+        const uint32_t off_raw = x * (KT * 128) + t * 128 + ((ch ^ (t & 7)) << 4);
+        const uint32_t off_dst = (2 * x + (ch >> 2)) * (KT * 128) + t * 128;
+        const uint32_t off0 = off_dst + (((2 * (ch & 3)) ^ (t & 7)) << 4), off1 = off_dst + (((2 * (ch & 3) + 1) ^ (t & 7)) << 4);
         for (int i = 0; i < nt_all; ++i) {
             if (!wait_bar(T::bRFull + i % T::RS, (i / T::RS) & 1)) break;
             if (i >= T::VS && !wait_bar(T::bVFree + i % T::VS, (i / T::VS - 1) & 1)) break;
-            const uint32_t raw = sbase + T::kROff + (i % T::RS) * T::kKBytes;
-            const uint32_t dst = sbase + T::kVOff + (i % T::VS) * 2 * T::kKBytes;
+            const uint32_t raw = sbase + T::kROff + (i % T::RS) * T::kKBytes + off_raw;
+            const uint32_t dst = sbase + T::kVOff + (i % T::VS) * 2 * T::kKBytes, dst0 = dst + off0, dst1 = dst + off1;
             const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
             const int rem = tok1 - (tok0 + i * KT);
-#pragma unroll 2
-            for (int e = ct; e < KT * D / 16; e += 32 * T::kConvWarps) {
-                const int cl = e & 3, pr = (e >> 2) & 1, hi = (e >> 3) % (2 * XB), tp = e / (16 * XB);  // tp: token pair
-                const int t8 = tp >> 2, k = tp & 3;
-                const int t = 8 * t8 + (pr ? k ^ 5 : k);
-                const int x = hi >> 1, ch = 4 * (hi & 1) + cl;  // column block of codes, chunk in it
-                uint4 w = lds128(raw + x * (KT * 128) + t * 128 + ((ch ^ (t & 7)) << 4));
-                if (t >= rem || !(okm >> (t >> 4) & 1u)) w = make_uint4(0u, 0u, 0u, 0u);  // not a token: holds anything
-                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                uint32_t h[8];
+            const bool whole = rem >= KT && okm == (1u << GR) - 1u;
+            // four reads ahead of their writes
 #pragma unroll
-                for (int k2 = 0; k2 < 4; ++k2) {
-                    h[2 * k2] = e4m3_to_half2(v[k2]);
-                    h[2 * k2 + 1] = e4m3_to_half2(v[k2] >> 16);
+            for (int n0 = 0; n0 < KT * D / 16 / (32 * T::kConvWarps); n0 += 4) {
+                uint4 w[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int dt = (n0 + n) * (16 / XB);
+                    w[n] = lds128(raw + dt * 128);
+                    if (!whole && (t + dt >= rem || !(okm >> ((t + dt) >> 4) & 1u))) w[n] = make_uint4(0u, 0u, 0u, 0u);  // no token: holds anything
                 }
-                const uint32_t at = dst + (2 * x + (ch >> 2)) * (KT * 128) + t * 128;
-                sts128(at + (((2 * (ch & 3)) ^ (t & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
-                sts128(at + (((2 * (ch & 3) + 1) ^ (t & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int dt = (n0 + n) * (16 / XB);
+                    const uint32_t v[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int k2 = 0; k2 < 4; ++k2) {
+                        h[2 * k2] = e4m3_to_half2(v[k2]);
+                        h[2 * k2 + 1] = e4m3_to_half2(v[k2] >> 16);
+                    }
+                    sts128(dst0 + dt * 128, make_uint4(h[0], h[1], h[2], h[3]));
+                    sts128(dst1 + dt * 128, make_uint4(h[4], h[5], h[6], h[7]));
+                }
             }
             umma::fence_proxy_async();
             warp_arrive(&mbar[T::bRFree + i % T::RS]);
             warp_arrive(&mbar[T::bVFull + i % T::VS]);
         }
     } else if (warp < T::kLoadWarp) {
-        // ================= MMA issue: a warp per column tile, one elected lane =================
-        // The order is fixed and the warp stays converged, so that the descriptors live in uniform registers: an
-        // issue from one lane's divergent branch took ~110 cycles an MMA against the tensor core's 64.
-        const int q = warp - T::kMmaWarp;
-        const int my_nt = q ? nt[NQ - 1] : nt[0];
-        constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
-        constexpr uint32_t id_o = umma::idesc_f16(128, 128) | (1u << 16);                           // B along N
-        // descriptors are built once: a step only adds to the low word (the address in units of 16 bytes)
-        const uint64_t dq = umma::make_desc_sw128(sbase + T::kQOff + 2 * q * T::kQBytes, 16, 1024);
-        const uint64_t dk = umma::make_desc_sw128(sbase + T::kKOff, 16, 1024);
-        const uint64_t dv = umma::make_desc_sw128(sbase + T::kVOff, KT * 128, 1024);
-        const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), v_lo = static_cast<uint32_t>(dv);
-        const uint32_t kq_hi = static_cast<uint32_t>(dk >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
-        const uint32_t tm_s = tbase + T::kTmS + q * NB * KT, tm_o = tbase + T::kTmO + q * D;
-        auto scores = [&](int i) -> bool {  // S of tile i, once its keys are there
-            if (!wait_bar(T::bKFull + i % T::KS, (i / T::KS) & 1)) return false;
-            umma::fence_after_sync();
-            const uint32_t ka = k_lo + (i % T::KS) * (T::kKBytes / 16), ds = tm_s + (i % NB) * KT;
-            if (umma::elect_one()) {
+        // ================= MMA issue: a warp for the scores, one per column tile for P.V =================
+        // Each has its own waits, so that work is queued at the tensor core while another one's operands are awaited,
+        // in a fixed order with the warp converged, so that the descriptors live in uniform registers (from one
+        // lane's divergent branch an issue took ~110 cycles against the tensor core's 64).  A step only adds to
+        // a descriptor's low word (the address in units of 16 bytes).
+        bool ok = true;
+        if (warp == T::kMmaWarp) {
+            constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
+            const uint64_t dq = umma::make_desc_sw128(sbase + T::kQOff, 16, 1024);
+            const uint64_t dk = umma::make_desc_sw128(sbase + T::kKOff, 16, 1024);
+            const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), hi = static_cast<uint32_t>(dk >> 32);
+            ok = wait_bar(T::bQ, 0);
+            for (int i = 0; ok && i < nt_all; ++i) {
+                const int st = i % T::KS, buf = i % NB;
+                if (!(ok = wait_bar(T::bKFull + st, (i / T::KS) & 1))) break;
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    const uint32_t kd = ka + (k >> 2) * (KT * 8) + 2 * (k & 3), qd = q_lo + (k >> 2) * (128 * 8) + 2 * (k & 3);
-                    umma::mma_e4m3_lohi(ds, qd, kq_hi, kd, kq_hi, id_s, k > 0 ? 1 : 0);
-                    umma::mma_e4m3_lohi(ds, qd + T::kQBytes / 16, kq_hi, kd, kq_hi, id_s, 1);
+                for (int q = 0; q < NQ; ++q) {
+                    if (i >= nt[q]) continue;
+                    if (i >= NB && !(ok = wait_bar(T::bPvDone + q * NB + buf, (i / NB - 1) & 1))) break;
+                    umma::fence_after_sync();
+                    const uint32_t ka = k_lo + st * (T::kKBytes / 16), qa = q_lo + 2 * q * (T::kQBytes / 16);
+                    const uint32_t ds = tbase + T::kTmS + (q * NB + buf) * KT;
+                    if (umma::elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            const uint32_t kd = ka + (k >> 2) * (KT * 8) + 2 * (k & 3), qd = qa + (k >> 2) * (128 * 8) + 2 * (k & 3);
+                            umma::mma_e4m3_lohi(ds, qd, hi, kd, hi, id_s, k > 0 ? 1 : 0);
+                            umma::mma_e4m3_lohi(ds, qd + T::kQBytes / 16, hi, kd, hi, id_s, 1);
+                        }
+                        umma::commit(&mbar[T::bSFull + q * NB + buf]);
+                    }
+                    __syncwarp();
                 }
-                umma::commit(&mbar[T::bSFull + q * NB + i % NB]);
-                umma::commit(&mbar[T::bKFree + i % T::KS]);
+                if (umma::elect_one()) umma::commit(&mbar[T::bKFree + st]);
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](int i) -> bool {  // O += P V of tile i, once P and its values are there
-            if (!wait_bar(T::bVFull + i % T::VS, (i / T::VS) & 1)) return false;
-            if (!wait_bar(T::bPFull + q * NB + i % NB, (i / NB) & 1)) return false;
-            umma::fence_after_sync();
-            const uint32_t va = v_lo + (i % T::VS) * (2 * T::kKBytes / 16), tp = tm_s + (i % NB) * KT;
-            if (umma::elect_one()) {
+        } else {
+            const int q = warp - T::kMmaWarp - 1;
+            const int my_nt = q ? nt[NQ - 1] : nt[0];
+            constexpr uint32_t id_o = umma::idesc_f16(128, 128) | (1u << 16);  // B along N
+            const uint64_t dv = umma::make_desc_sw128(sbase + T::kVOff, KT * 128, 1024);
+            const uint32_t v_lo = static_cast<uint32_t>(dv), hi = static_cast<uint32_t>(dv >> 32);
+            const uint32_t tm_s = tbase + T::kTmS + q * NB * KT, tm_o = tbase + T::kTmO + q * D;
+            for (int i = 0; i < nt_all; ++i) {
+                const int st = i % T::VS, buf = i % NB;
+                if (!(ok = wait_bar(T::bVFull + st, (i / T::VS) & 1))) break;
+                if (i >= my_nt) {  // only the other column tile sees it: hand the stage on
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[T::bVFree + st])) : "memory");
+                    continue;
+                }
+                if (!(ok = wait_bar(T::bPFull + q * NB + buf, (i / NB) & 1))) break;
+                umma::fence_after_sync();
+                const uint32_t va = v_lo + st * (2 * T::kKBytes / 16), tp = tm_s + buf * KT;
+                if (umma::elect_one()) {
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
+                    for (int k = 0; k < KT / 16; ++k)
 #pragma unroll
-                    for (int x = 0; x < XB; ++x)  // 128 coordinates at a time
-                        umma::mma_f16_tmem_a(tm_o + 128 * x, tp + 8 * k, va + x * (2 * KT * 8) + 128 * k, v_hi, id_o,
-                                             (i > 0 || k > 0) ? 1 : 0);
-                umma::commit(&mbar[T::bPvDone + q]);
-                if (i == my_nt - 1) umma::commit(&mbar[T::bODone + q]);
-                umma::commit(&mbar[T::bVFree + i % T::VS]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto done = [&](int i) -> bool {  // O += P V of tile i is done: its score buffer is free
-            return i < 0 || wait_bar(T::bPvDone + q, i & 1);
-        };
-        bool ok = wait_bar(T::bQ, 0);
-        if (my_nt > 0) ok = ok && scores(0);
-        for (int i = 0; ok && i < my_nt; ++i) {
-            if (NB > 1) ok = done(i - 1) && (i + 1 >= my_nt || scores(i + 1));
-            ok = ok && values(i);
-            if (NB == 1 && i + 1 < my_nt) ok = ok && done(i) && scores(i + 1);
-        }
-        for (int i = my_nt; ok && i < nt_all; ++i) {  // tiles that only the other column tile sees: hand the stages on
-            ok = wait_bar(T::bKFull + i % T::KS, (i / T::KS) & 1) && wait_bar(T::bVFull + i % T::VS, (i / T::VS) & 1);
-            if (ok && lane == 0) {
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[T::bKFree + i % T::KS])) : "memory");
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[T::bVFree + i % T::VS])) : "memory");
+                        for (int x = 0; x < XB; ++x)  // 128 coordinates at a time
+                            umma::mma_f16_tmem_a(tm_o + 128 * x, tp + 8 * k, va + x * (2 * KT * 8) + 128 * k, hi, id_o,
+                                                 (i > 0 || k > 0) ? 1 : 0);
+                    umma::commit(&mbar[T::bPvDone + q * NB + buf]);
+                    umma::commit(&mbar[T::bVFree + st]);
+                }
+                __syncwarp();
             }
         }
         // every MMA issued must be done before tensor memory is freed
@@ -598,57 +605,75 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         __syncwarp();
     } else if (warp == T::kLoadWarp) {
         // ================= page copies and scales =================
+        // The copies of all tiles go through this warp one after another, so little stands between two: block ids are
+        // read three tiles ahead and scales two, and a tile's scales are written while the tile before it is copied.
         int k_issued = 0, r_issued = 0;
-        for (int i = 0; i < nt_all; ++i) {
-            const int pos = tok0 + (i * ppt + lane) * P;  // lane p: the tile's page p
-            const bool in = lane < ppt && pos < tok1;
-            int blk = in ? __ldg(A.block_table + static_cast<int64_t>(b) * A.max_blocks + (pos >> A.pshift)) : -1;
-            const bool good = in && blk >= 0 && blk < A.num_blocks;
-            if (in && !good) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
-            float ks = 0.f, vs = 0.f;
-            if (good) {
-                ks = __ldg(A.k_scales + static_cast<int64_t>(blk) * A.Hkv + kvh);
-                vs = __ldg(A.v_scales + static_cast<int64_t>(blk) * A.Hkv + kvh);
-            }
+        const int32_t *table = A.block_table + static_cast<int64_t>(b) * A.max_blocks;
+        const bool mine = lane < ppt;  // lane p: a tile's page p
+        auto fetch_id = [&](int i) -> int {
+            const int pos = tok0 + (i * ppt + lane) * P;
+            return mine && pos < tok1 ? __ldg(table + (pos >> A.pshift)) : -1;
+        };
+        auto valid = [&](int blk) -> bool { return blk >= 0 && blk < A.num_blocks; };
+        auto scale_of = [&](const float *p, int blk) -> float {
+            return valid(blk) ? __ldg(p + static_cast<int64_t>(blk) * A.Hkv + kvh) : 0.f;
+        };
+        auto write_info = [&](int i, int blk, float ks, float vs) -> uint32_t {  // returns the tile's valid pages
+            const bool good = valid(blk);
+            if (mine && !good && tok0 + (i * ppt + lane) * P < tok1) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
             const uint32_t pages = __ballot_sync(0xffffffffu, good);
-            const int y = good ? static_cast<int>((static_cast<int64_t>(blk) * A.Hkv + kvh) * P) : 0;
-            if (i >= T::KS && !wait_bar(T::bKFree + i % T::KS, (i / T::KS - 1) & 1)) break;
             const int slot = i % T::kRing;
-            if (lane < ppt) {
+            if (mine) {
                 const float lv = log2_scale(vs);
+                const float4 f = make_float4(ks, lv, fast_exp2(kSumShift - lv), 0.f);
                 float4 *info = reinterpret_cast<float4 *>(smem + T::kInfoOff) + slot * GR;
-                const float4 f = make_float4(ks, lv, fast_exp2(kLShift - lv), 0.f);
-                for (int g = 0; g < P / 16; ++g) info[lane * (P / 16) + g] = f;
-            }
-            if (lane == 0) {
-                uint32_t m = pages;
-                if (P == 32) {  // a bit per 16-token group
-                    m = 0;
-                    for (int g = 0; g < GR; ++g) m |= (pages >> (g / 2) & 1u) << g;
+                if (P == 16) {
+                    info[lane] = f;
+                } else {
+                    info[2 * lane] = f;
+                    info[2 * lane + 1] = f;
                 }
-                reinterpret_cast<uint32_t *>(smem + T::kOkOff)[slot] = m;
             }
-            __syncwarp();
-            const uint32_t bytes = good ? static_cast<uint32_t>(P * D) : 0u;
-            auto copy = [&](const CUtensorMap &tm, uint32_t dst, int bar) {  // lanes below ppt
+            if (lane == 0)  // a bit per 16-token group
+                reinterpret_cast<uint32_t *>(smem + T::kOkOff)[slot] = P == 16 ? pages : (pages & 1u) * 3u + (pages >> 1 & 1u) * 12u;
+            return pages;
+        };
+        int blk = fetch_id(0), blk1 = fetch_id(1), blk2 = fetch_id(2);
+        float ks1 = scale_of(A.k_scales, blk1), vs1 = scale_of(A.v_scales, blk1);
+        uint32_t pages = write_info(0, blk, scale_of(A.k_scales, blk), scale_of(A.v_scales, blk));
+        const uint32_t k_dst = sbase + T::kKOff + lane * P * 128, r_dst = sbase + T::kROff + lane * P * 128;
+        for (int i = 0; i < nt_all; ++i) {
+            const int blk3 = fetch_id(i + 3);
+            const float ks2 = scale_of(A.k_scales, blk2), vs2 = scale_of(A.v_scales, blk2);
+            const bool good = valid(blk);
+            const int y = static_cast<int>((static_cast<int64_t>(blk) * A.Hkv + kvh) * P);
+            const uint32_t bytes = __popc(pages) * static_cast<uint32_t>(P * D);
+            auto copy = [&](const CUtensorMap &tm, uint32_t dst, int bar) {
                 const uint32_t mb = saddr(&mbar[bar]);
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
-                if (!good) return;
+                if (lane == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+                __syncwarp();
+                if (good) {
 #pragma unroll
-                for (int x = 0; x < XB; ++x)
-                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                                 ::"r"(dst + x * (KT * 128) + lane * P * 128), "l"(reinterpret_cast<uint64_t>(&tm)), "r"(x * 128),
-                                 "r"(y), "r"(mb)
-                                 : "memory");
+                    for (int x = 0; x < XB; ++x)
+                        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                     ::"r"(dst + x * (KT * 128)), "l"(reinterpret_cast<uint64_t>(&tm)), "r"(x * 128), "r"(y), "r"(mb)
+                                     : "memory");
+                }
             };
-            if (lane < ppt) copy(tmK, sbase + T::kKOff + (i % T::KS) * T::kKBytes, T::bKFull + i % T::KS);
+            if (i >= T::KS && !wait_bar(T::bKFree + i % T::KS, (i / T::KS - 1) & 1)) break;
+            copy(tmK, k_dst + (i % T::KS) * T::kKBytes, T::bKFull + i % T::KS);
             k_issued = i + 1;
             if (i >= T::RS && !wait_bar(T::bRFree + i % T::RS, (i / T::RS - 1) & 1)) break;
-            if (lane < ppt) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the widening's reads are done
-                copy(tmV, sbase + T::kROff + (i % T::RS) * T::kKBytes, T::bRFull + i % T::RS);
-            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the widening's reads are done
+            copy(tmV, r_dst + (i % T::RS) * T::kKBytes, T::bRFull + i % T::RS);
             r_issued = i + 1;
+            if (i + 1 < nt_all) pages = write_info(i + 1, blk1, ks1, vs1);  // that tile's keys arrive after this
+            blk = blk1;
+            blk1 = blk2;
+            blk2 = blk3;
+            ks1 = ks2;
+            vs1 = vs2;
         }
         // copies in flight must land before the CTA exits, also when another warp gives up later: the last
         // issue of each stage (long done in a run that consumed them)
