@@ -329,6 +329,20 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         return __all_sync(0xffffffffu, ok);  // the lanes poll separately: decide as a warp
     };
 
+    // the same by one thread alone
+    auto wait_one = [&](int i, uint32_t par) -> bool {
+        uint64_t *mb = &mbar[i];
+        if (A.wait_limit > 0 ? umma::mbar_try_wait(mb, par) : umma::mbar_test_wait(mb, par)) return true;
+        const long long t0 = clock64();
+        while (A.wait_limit > 0 && !*abort_flag && clock64() - t0 <= A.wait_limit)
+            if (umma::mbar_try_wait(mb, par)) return true;
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            atomicOr(A.status, TQ_DEVERR_TIMEOUT);
+        }
+        return false;
+    };
+
     if constexpr (T::kSplitRegs) {
         if (warp < T::kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -340,18 +354,25 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         float fac;  // sm_scale log2(e) 2^-e >= 0: a negative scale goes into q's sign
         {
+            // 128 coordinates at a time in registers, all of their loads in flight together (at head dim 256 the second
+            // half is read again, from cache, once the maximum is known)
             const uint4 *src = reinterpret_cast<const uint4 *>(A.q + col_row(cv ? c : 0) * D);
+            uint4 w[16];
             float mx = 0.f;
             bool nan = false;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 w = cv ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x0 = fabsf(__uint_as_float(v[k] << 16)), x1 = fabsf(__uint_as_float(v[k] & 0xffff0000u));
-                    nan |= !(x0 <= 3.4e38f) || !(x1 <= 3.4e38f);
-                    mx = fmaxf(mx, fmaxf(x0, x1));
+            for (int x = XB - 1; x >= 0; --x) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = cv ? __ldg(src + 16 * x + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x0 = fabsf(__uint_as_float(v[k] << 16)), x1 = fabsf(__uint_as_float(v[k] & 0xffff0000u));
+                        nan |= !(x0 <= 3.4e38f) || !(x1 <= 3.4e38f);
+                        mx = fmaxf(mx, fmaxf(x0, x1));
+                    }
                 }
             }
             int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // 2^(7 - ex) brings the largest into [2^7, 2^8)
@@ -360,29 +381,30 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             fac = fabsf(A.sm_scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
             if (nan) fac = __uint_as_float(0x7fc00000u);
             if (A.sm_scale < 0.f) up = -up;
-            const uint32_t qs = sbase + T::kQOff + 2 * q * T::kQBytes;
-#pragma unroll 2
-            for (int i = 0; i < D / 16; ++i) {  // 16 coordinates: one 16-byte chunk of each term
-                uint32_t hi[4], lo[4];
+            const uint32_t qs = sbase + T::kQOff + 2 * q * T::kQBytes + r * 128;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 w = cv ? __ldg(src + 2 * i + h) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t ph[4], pl[4];
+            for (int x = 0; x < XB; ++x) {
+                if (x > 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = cv ? __ldg(src + 16 * x + i) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // 16 coordinates: one 16-byte chunk of each term
+                    const uint32_t v[8] = {w[2 * i].x, w[2 * i].y, w[2 * i].z, w[2 * i].w,
+                                           w[2 * i + 1].x, w[2 * i + 1].y, w[2 * i + 1].z, w[2 * i + 1].w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float x0 = __uint_as_float(v[k] << 16) * up, x1 = __uint_as_float(v[k] & 0xffff0000u) * up;
-                        ph[k] = e4m3x2_rest(x0, x1);
-                        pl[k] = e4m3x2(x0, x1);
+                        float x0 = __uint_as_float(v[2 * k] << 16) * up, x1 = __uint_as_float(v[2 * k] & 0xffff0000u) * up;
+                        float x2 = __uint_as_float(v[2 * k + 1] << 16) * up, x3 = __uint_as_float(v[2 * k + 1] & 0xffff0000u) * up;
+                        hi[k] = e4m3x2_rest(x0, x1);
+                        hi[k] |= e4m3x2_rest(x2, x3) << 16;
+                        lo[k] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
                     }
-                    hi[2 * h] = ph[0] | (ph[1] << 16);
-                    hi[2 * h + 1] = ph[2] | (ph[3] << 16);
-                    lo[2 * h] = pl[0] | (pl[1] << 16);
-                    lo[2 * h + 1] = pl[2] | (pl[3] << 16);
+                    const uint32_t at = qs + x * (128 * 128) + ((i ^ (r & 7)) << 4);
+                    sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts128(at + T::kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                 }
-                const uint32_t at = qs + (i >> 3) * (128 * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4);
-                sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                sts128(at + T::kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
             umma::fence_proxy_async();
             warp_arrive(&mbar[T::bQ]);
@@ -396,7 +418,6 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             umma::fence_after_sync();
             const uint32_t ts = lane_base + T::kTmS + (q * NB + i % NB) * KT;
             Scores s;
-            umma::ld64_issue(ts, s.v);
             const float4 *info = reinterpret_cast<const float4 *>(smem + T::kInfoOff) + (i % T::kRing) * GR;
 #pragma unroll
             for (int g = 0; g < GR; ++g) {
@@ -408,7 +429,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
             const int rem = lim - (tok0 + i * KT);  // tokens of the tile that this column sees
             const bool whole = __all_sync(0xffffffffu, rem >= KT) && okm == (1u << GR) - 1u;
-            umma::wait_ld64(s.v);
+            umma::ld64(ts, s.v);
             const float top = whole ? tile_max<true>(s, okm, rem) : tile_max<false>(s, okm, rem);
             // ---- lazy rescale ----
             const bool need = m_run != -INFINITY && top > m_run + kLazy;
@@ -421,8 +442,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
 #pragma unroll 1
                 for (int ch = 0; ch < D; ch += 64) {
                     uint32_t o[64];
-                    umma::ld64_issue(to + ch, o);
-                    umma::wait_ld64(o);
+                    umma::ld64(to + ch, o);
 #pragma unroll
                     for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
                     umma::st64(to + ch, o);
@@ -530,28 +550,27 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         }
     } else if (warp < T::kLoadWarp) {
         // ================= MMA issue: a warp for the scores, one per column tile for P.V =================
-        // Each has its own waits, so that work is queued at the tensor core while another one's operands are awaited,
-        // in a fixed order with the warp converged, so that the descriptors live in uniform registers (from one
-        // lane's divergent branch an issue took ~110 cycles against the tensor core's 64).  A step only adds to
-        // a descriptor's low word (the address in units of 16 bytes).
-        bool ok = true;
-        if (warp == T::kMmaWarp) {
-            constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
-            const uint64_t dq = umma::make_desc_sw128(sbase + T::kQOff, 16, 1024);
-            const uint64_t dk = umma::make_desc_sw128(sbase + T::kKOff, 16, 1024);
-            const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), hi = static_cast<uint32_t>(dk >> 32);
-            ok = wait_bar(T::bQ, 0);
-            for (int i = 0; ok && i < nt_all; ++i) {
-                const int st = i % T::KS, buf = i % NB;
-                if (!(ok = wait_bar(T::bKFull + st, (i / T::KS) & 1))) break;
+        // Each has its own waits, so that work is queued at the tensor core while another one's operands are awaited.
+        // One elected thread runs the loop: votes and converged issues around every wait had made a warp's round of
+        // waits longer (~2000 cycles) than the MMAs of a tile (~1300).  Descriptors are built once; a step only adds to
+        // their low words (the address in units of 16 bytes).
+        if (umma::elect_one()) {
+            if (warp == T::kMmaWarp) {
+                constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(KT >> 3) << 17) | (8u << 24);  // e4m3, fp32, M = 128
+                const uint64_t dq = umma::make_desc_sw128(sbase + T::kQOff, 16, 1024);
+                const uint64_t dk = umma::make_desc_sw128(sbase + T::kKOff, 16, 1024);
+                const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), hi = static_cast<uint32_t>(dk >> 32);
+                bool ok = wait_one(T::bQ, 0);
+                for (int i = 0; ok && i < nt_all; ++i) {
+                    const int st = i % T::KS, buf = i % NB;
+                    ok = wait_one(T::bKFull + st, (i / T::KS) & 1);
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    if (i >= nt[q]) continue;
-                    if (i >= NB && !(ok = wait_bar(T::bPvDone + q * NB + buf, (i / NB - 1) & 1))) break;
-                    umma::fence_after_sync();
-                    const uint32_t ka = k_lo + st * (T::kKBytes / 16), qa = q_lo + 2 * q * (T::kQBytes / 16);
-                    const uint32_t ds = tbase + T::kTmS + (q * NB + buf) * KT;
-                    if (umma::elect_one()) {
+                    for (int q = 0; q < NQ; ++q) {
+                        if (!ok || i >= nt[q]) continue;
+                        if (i >= NB && !(ok = wait_one(T::bPvDone + q * NB + buf, (i / NB - 1) & 1))) continue;
+                        umma::fence_after_sync();
+                        const uint32_t ka = k_lo + st * (T::kKBytes / 16), qa = q_lo + 2 * q * (T::kQBytes / 16);
+                        const uint32_t ds = tbase + T::kTmS + (q * NB + buf) * KT;
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k) {
                             const uint32_t kd = ka + (k >> 2) * (KT * 8) + 2 * (k & 3), qd = qa + (k >> 2) * (128 * 8) + 2 * (k & 3);
@@ -560,30 +579,25 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                         }
                         umma::commit(&mbar[T::bSFull + q * NB + buf]);
                     }
-                    __syncwarp();
+                    umma::commit(&mbar[T::bKFree + st]);
                 }
-                if (umma::elect_one()) umma::commit(&mbar[T::bKFree + st]);
-                __syncwarp();
-            }
-        } else {
-            const int q = warp - T::kMmaWarp - 1;
-            const int my_nt = q ? nt[NQ - 1] : nt[0];
-            constexpr uint32_t id_o = umma::idesc_f16(128, 128) | (1u << 16);  // B along N
-            const uint64_t dv = umma::make_desc_sw128(sbase + T::kVOff, KT * 128, 1024);
-            const uint32_t v_lo = static_cast<uint32_t>(dv), hi = static_cast<uint32_t>(dv >> 32);
-            const uint32_t tm_s = tbase + T::kTmS + q * NB * KT, tm_o = tbase + T::kTmO + q * D;
-            for (int i = 0; i < nt_all; ++i) {
-                const int st = i % T::VS, buf = i % NB;
-                if (!(ok = wait_bar(T::bVFull + st, (i / T::VS) & 1))) break;
-                if (i >= my_nt) {  // only the other column tile sees it: hand the stage on
-                    if (lane == 0)
+            } else {
+                const int q = warp - T::kMmaWarp - 1;
+                const int my_nt = q ? nt[NQ - 1] : nt[0];
+                constexpr uint32_t id_o = umma::idesc_f16(128, 128) | (1u << 16);  // B along N
+                const uint64_t dv = umma::make_desc_sw128(sbase + T::kVOff, KT * 128, 1024);
+                const uint32_t v_lo = static_cast<uint32_t>(dv), hi = static_cast<uint32_t>(dv >> 32);
+                const uint32_t tm_s = tbase + T::kTmS + q * NB * KT, tm_o = tbase + T::kTmO + q * D;
+                for (int i = 0; i < nt_all; ++i) {
+                    const int st = i % T::VS, buf = i % NB;
+                    if (!wait_one(T::bVFull + st, (i / T::VS) & 1)) break;
+                    if (i >= my_nt) {  // only the other column tile sees it: hand the stage on
                         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[T::bVFree + st])) : "memory");
-                    continue;
-                }
-                if (!(ok = wait_bar(T::bPFull + q * NB + buf, (i / NB) & 1))) break;
-                umma::fence_after_sync();
-                const uint32_t va = v_lo + st * (2 * T::kKBytes / 16), tp = tm_s + buf * KT;
-                if (umma::elect_one()) {
+                        continue;
+                    }
+                    if (!wait_one(T::bPFull + q * NB + buf, (i / NB) & 1)) break;
+                    umma::fence_after_sync();
+                    const uint32_t va = v_lo + st * (2 * T::kKBytes / 16), tp = tm_s + buf * KT;
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
 #pragma unroll
@@ -593,14 +607,12 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                     umma::commit(&mbar[T::bPvDone + q * NB + buf]);
                     umma::commit(&mbar[T::bVFree + st]);
                 }
-                __syncwarp();
             }
-        }
-        // every MMA issued must be done before tensor memory is freed
-        if (umma::elect_one()) umma::commit(&mbar[T::bEnd]);
-        __syncwarp();
-        const long long t0 = clock64();
-        while (!umma::mbar_try_wait(&mbar[T::bEnd], 0) && clock64() - t0 < kDrainLimit) {
+            // every MMA issued must be done before tensor memory is freed
+            umma::commit(&mbar[T::bEnd]);
+            const long long t0 = clock64();
+            while (!umma::mbar_try_wait(&mbar[T::bEnd], 0) && clock64() - t0 < kDrainLimit) {
+            }
         }
         __syncwarp();
     } else if (warp == T::kLoadWarp) {
