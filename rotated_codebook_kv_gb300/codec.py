@@ -27,6 +27,11 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# The current stream's handle; the plain call builds a Stream object each time (1.1 against 0.1 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 class Codec:
     """One set of codec tables (Pi, S, codebook) on the current device."""
 
@@ -151,28 +156,21 @@ class Codec:
         return out
 
     # ---- plain bf16 pages and 8-bit pages ------------------------------------------
-    def _need(self, ok, what: str):
-        if not ok:
-            raise ValueError(what)
-
-    def _on_device(self, *tensors):
-        """Every tensor on the handle's device (the current one when the Codec was made)."""
-        for t in tensors:
-            if t is not None and (not t.is_cuda or t.device.index != self.device):
-                raise ValueError(f"tensor must be on cuda:{self.device}, the device of this Codec (there is no CPU path)")
-
-    @contextlib.contextmanager
-    def _launch(self, stream):
-        """The handle's device current, and the stream to launch on: the caller's, or that device's current one.
-        What is allocated inside belongs to that stream."""
-        with torch.cuda.device(self.device):
-            if stream is None:
-                yield torch.cuda.current_stream(self.device).cuda_stream
-                return
+    # The calls below are made once per layer and token, so their checks are few and plain: what the library cannot
+    # see (types, contiguity, sizes, devices) is checked here, everything else by the library.
+    def _on(self, stream):
+        """Context for a call whose stream or device is not the current one: both made current, so that what the
+        call allocates belongs to its stream."""
+        stack = contextlib.ExitStack()
+        stack.enter_context(torch.cuda.device(self.device))
+        if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+            stack.enter_context(torch.cuda.stream(stream))
+        return stack
+
+    def _elsewhere(self, stream) -> bool:
+        return stream is not None or torch.cuda.current_device() != self.device
 
     def rope_table(self, rows: int, rot_dim: int, base: float = 10000.0):
         """cos | sin of positions 0 .. rows - 1, fp32 [rows, rot_dim], from angles in 64 bits."""
@@ -194,54 +192,60 @@ class Codec:
         pools = [torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
         return (*pools, *(torch.ones(shape[:2], dtype=torch.float32, device=dev) for _ in range(2)))
 
-    def _rows(self, x, heads, what):
-        """Token stride of x [T, heads, head_dim] with contiguous heads and rows."""
-        T = x.shape[0]
-        self._need(x.dim() == 3 and x.dtype == torch.bfloat16 and x.shape[1] == heads and x.shape[2] == self.head_dim,
-                   f"{what} must be bf16 [T, heads, {self.head_dim}]")
-        self._need(x.stride(2) == 1 and (heads == 1 or x.stride(1) == self.head_dim),
-                   f"{what}: the heads of a token must be contiguous")
-        return x.stride(0) if T > 1 else max(x.stride(0), heads * self.head_dim)
+    def _flat(self, t, dtype, numel: int, what: str) -> int:
+        """The address of a contiguous tensor of this type and size on the handle's device."""
+        if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError(f"{what} must be contiguous {dtype} with {numel} elements on cuda:{self.device}, the device "
+                             f"of this Codec; got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
 
-    def _pools(self, pools, dtype, num_kv_heads, page_size, num_blocks, scales=()):
-        for p in pools:
-            self._need(p.dtype == dtype and p.is_contiguous() and
-                       p.numel() == num_blocks * num_kv_heads * page_size * self.head_dim,
-                       f"pools must be contiguous {dtype} [num_blocks, num_kv_heads, page_size, head_dim]")
-        for s in scales:
-            self._need(s.dtype == torch.float32 and s.is_contiguous() and s.numel() == num_blocks * num_kv_heads,
-                       "scales must be contiguous fp32 [num_blocks, num_kv_heads]")
+    def _rows(self, x, T: int, heads: int, what: str):
+        """Address and token stride of bf16 rows x [T, heads, head_dim], the heads of a token side by side."""
+        d = self.head_dim
+        if x.dtype is not torch.bfloat16 or x.shape != (T, heads, d) or x.get_device() != self.device:
+            raise ValueError(f"{what} must be bf16 [{T}, {heads}, {d}] on cuda:{self.device}; got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
+        st, sh, sd = x.stride()
+        if T > 0 and (sd != 1 or (heads > 1 and sh != d)):
+            raise ValueError(f"{what}: the heads of a token must be contiguous")
+        return x.data_ptr(), st if T > 1 else heads * d
 
-    def _append_args(self, k, v, slot_mapping, q, q_out, positions, rope, interleaved):
-        """Checked arguments of both appends up to the slots."""
-        T, H = k.shape[0], k.shape[1]
-        self._need(v.shape == k.shape, "k and v must have one shape")
-        self._need(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() == T,
-                   "slot_mapping must be contiguous int64 [T]")
-        ks, vs = self._rows(k, H, "k"), self._rows(v, H, "v")
-        qp = qs = Hq = qo = 0
-        if q is not None:
-            Hq = q.shape[1]
-            self._need(q.shape[0] == T, "q must have k's tokens")
-            qs = self._rows(q, Hq, "q")
-            if q_out is None:
-                q_out = torch.zeros(T, Hq, self.head_dim, dtype=torch.bfloat16, device=q.device)
-            self._need(q_out.dtype == torch.bfloat16 and q_out.is_contiguous() and q_out.shape == q.shape,
-                       "q_out must be contiguous bf16 of q's shape")
-            qp, qo = q.data_ptr(), q_out.data_ptr()
-        else:
-            self._need(q_out is None, "q_out without q")
-        rp = rows = rot = pp = 0
+    def _append(self, call, dtype, k, v, slot_mapping, pools, scales, page_size, num_blocks, q, q_out, positions, rope,
+                interleaved, stream):
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self._append(call, dtype, k, v, slot_mapping, pools, scales, page_size, num_blocks, q, q_out,
+                                    positions, rope, interleaved, None)
+        if k.dim() != 3:
+            raise ValueError("k must be [T, num_kv_heads, head_dim]")
+        T, H, _ = k.shape
+        kp, ks = self._rows(k, T, H, "k")
+        vp, vs = self._rows(v, T, H, "v")
+        sp = self._flat(slot_mapping, torch.int64, T, "slot_mapping")
+        qp = qs = Hq = qo = rp = rows = rot = pp = 0
         if rope is not None:
-            self._need(rope.dim() == 2 and rope.dtype == torch.float32 and rope.is_contiguous(),
-                       "rope must be contiguous fp32 [rows, rot_dim]")
-            self._need(positions is not None and positions.dtype == torch.int64 and positions.is_contiguous() and
-                       positions.numel() == T, "positions must be contiguous int64 [T]")
-            rp, rows, rot, pp = rope.data_ptr(), rope.shape[0], rope.shape[1], positions.data_ptr()
-        self._on_device(k, v, slot_mapping, q, q_out, positions if rope is not None else None, rope)
-        style = native.TQ_ROPE_INTERLEAVED if interleaved else native.TQ_ROPE_HALF
-        return q_out, (qp, k.data_ptr(), v.data_ptr(), T, Hq, H, qs, ks, vs, pp, rp, rows, rot, style,
-                       slot_mapping.data_ptr()), qo
+            if rope.dim() != 2 or positions is None:
+                raise ValueError("rope must be fp32 [rows, rot_dim], and goes with positions")
+            rows, rot = rope.shape
+            rp = self._flat(rope, torch.float32, rows * rot, "rope")
+            pp = self._flat(positions, torch.int64, T, "positions")
+        cells = num_blocks * H * page_size * self.head_dim
+        ptrs = [self._flat(p, dtype, cells, "a pool [num_blocks, num_kv_heads, page_size, head_dim]") for p in pools]
+        ptrs += [self._flat(s, torch.float32, num_blocks * H, "scales [num_blocks, num_kv_heads]") for s in scales]
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q must be [T, num_q_heads, head_dim]")
+            Hq = q.shape[1]
+            qp, qs = self._rows(q, T, Hq, "q")
+            if q_out is None:  # zeros: rows of skipped tokens are not written
+                q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+            qo = self._flat(q_out, torch.bfloat16, T * Hq * self.head_dim, "q_out")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        call(self.handle, qp, kp, vp, T, Hq, H, qs, ks, vs, pp, rp, rows, rot,
+             native.TQ_ROPE_INTERLEAVED if interleaved else native.TQ_ROPE_HALF, sp, *ptrs, page_size, num_blocks, qo,
+             _raw_stream(self.device))
+        return q_out
 
     def append_kv_bf16(self, k, v, slot_mapping, k_pool, v_pool, page_size: int, num_blocks: int, q=None, q_out=None,
                        positions=None, rope=None, interleaved: bool = False, stream=None):
@@ -249,24 +253,14 @@ class Codec:
 
         k, v: [T, Hkv, d] bf16, tokens strided; q: [T, Hq, d], rotated into q_out, which is returned (None without q).
         rope: fp32 [rows, rot_dim] as rope_table makes it; positions: int64 [T]."""
-        with self._launch(stream) as st:
-            q_out, args, qo = self._append_args(k, v, slot_mapping, q, q_out, positions, rope, interleaved)
-            self._pools((k_pool, v_pool), torch.bfloat16, k.shape[1], page_size, num_blocks)
-            self._on_device(k_pool, v_pool)
-            native.tq_append_kv_bf16(self.handle, *args, k_pool.data_ptr(), v_pool.data_ptr(), page_size, num_blocks,
-                                     qo, st)
-        return q_out
+        return self._append(native.tq_append_kv_bf16, torch.bfloat16, k, v, slot_mapping, (k_pool, v_pool), (), page_size,
+                            num_blocks, q, q_out, positions, rope, interleaved, stream)
 
     def append_kv_fp8(self, k, v, slot_mapping, k_pool, v_pool, k_scales, v_scales, page_size: int, num_blocks: int,
                       q=None, q_out=None, positions=None, rope=None, interleaved: bool = False, stream=None):
         """append_kv_bf16 into e4m3 pools with one scale per (page, kv head)."""
-        with self._launch(stream) as st:
-            q_out, args, qo = self._append_args(k, v, slot_mapping, q, q_out, positions, rope, interleaved)
-            self._pools((k_pool, v_pool), torch.float8_e4m3fn, k.shape[1], page_size, num_blocks, (k_scales, v_scales))
-            self._on_device(k_pool, v_pool, k_scales, v_scales)
-            native.tq_append_kv_fp8(self.handle, *args, k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
-                                    v_scales.data_ptr(), page_size, num_blocks, qo, st)
-        return q_out
+        return self._append(native.tq_append_kv_fp8, torch.float8_e4m3fn, k, v, slot_mapping, (k_pool, v_pool),
+                            (k_scales, v_scales), page_size, num_blocks, q, q_out, positions, rope, interleaved, stream)
 
     def decode_splits_fp8(self, batch: int, num_kv_heads: int, max_blocks_per_seq: int, page_size: int) -> int:
         return native.tq_decode_splits_fp8(self.handle, batch, num_kv_heads, max_blocks_per_seq, page_size)
@@ -283,41 +277,44 @@ class Codec:
 
     def _attention_fp8(self, q, tq, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, num_kv_heads, page_size,
                        num_blocks, sm_scale, splits, workspace, out, stream):
-        B, Hq = q.shape[0], q.shape[-2]
-        self._need(q.dtype == torch.bfloat16 and q.is_contiguous() and q.shape[-1] == self.head_dim,
-                   f"q must be contiguous bf16 with head dim {self.head_dim}")
-        self._need(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.is_contiguous() and
-                   block_table.shape[0] == B, "block_table must be contiguous int32 [B, max_blocks]")
-        self._need(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.numel() == B,
-                   "seq_lens must be contiguous int32 [B]")
-        self._pools((k_pool, v_pool), torch.float8_e4m3fn, num_kv_heads, page_size, num_blocks, (k_scales, v_scales))
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self._attention_fp8(q, tq, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, num_kv_heads,
+                                           page_size, num_blocks, sm_scale, splits, workspace, out, None)
+        B, Hq, d = q.shape[0], q.shape[-2], self.head_dim
+        if q.shape[-1] != d or block_table.dim() != 2:
+            raise ValueError(f"q must have head dim {d}, block_table be [B, max_blocks]")
         maxb = block_table.shape[1]
-        with self._launch(stream) as st:
-            if splits == 0:
-                splits = self.decode_splits_fp8(B, num_kv_heads, maxb, page_size) if tq == 0 else \
-                    self.prefill_splits_fp8(B, tq, Hq, num_kv_heads, maxb, page_size)
-            if workspace is None:
-                workspace = self.workspace_fp8(B * max(tq, 1), Hq, splits)
-            if out is None:
-                out = torch.empty_like(q)
-            self._need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape,
-                       "out must be contiguous bf16 of q's shape")
-            self._on_device(q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, workspace, out)
-            pools = (k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                     block_table.data_ptr(), seq_lens.data_ptr())
-            rest = (Hq, num_kv_heads, page_size, maxb, num_blocks, float(sm_scale), splits, workspace.data_ptr(),
-                    workspace.numel() * workspace.element_size(), out.data_ptr(), st)
-            if tq == 0:
-                native.tq_decode_attention_fp8(self.handle, q.data_ptr(), *pools, B, *rest)
-            else:
-                native.tq_prefill_attention_fp8(self.handle, q.data_ptr(), *pools, B, tq, *rest)
+        cells = num_blocks * num_kv_heads
+        f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+        qp = self._flat(q, torch.bfloat16, B * max(tq, 1) * Hq * d, "q")
+        args = (self._flat(k_pool, f8, cells * page_size * d, "k_pool"), self._flat(v_pool, f8, cells * page_size * d, "v_pool"),
+                self._flat(k_scales, f32, cells, "k_scales"), self._flat(v_scales, f32, cells, "v_scales"),
+                self._flat(block_table, i32, B * maxb, "block_table"), self._flat(seq_lens, i32, B, "seq_lens"))
+        if splits == 0:
+            splits = self.decode_splits_fp8(B, num_kv_heads, maxb, page_size) if tq == 0 else \
+                self.prefill_splits_fp8(B, tq, Hq, num_kv_heads, maxb, page_size)
+        if workspace is None:
+            workspace = self.workspace_fp8(B * max(tq, 1), Hq, splits)
+        if workspace.get_device() != self.device:
+            raise ValueError(f"workspace must be on cuda:{self.device}, the device of this Codec")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        op = self._flat(out, torch.bfloat16, q.numel(), "out")
+        rest = (Hq, num_kv_heads, page_size, maxb, num_blocks, sm_scale, splits, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), op, _raw_stream(self.device))
+        if tq == 0:
+            native.tq_decode_attention_fp8(self.handle, qp, *args, B, *rest)
+        else:
+            native.tq_prefill_attention_fp8(self.handle, qp, *args, B, tq, *rest)
         return out
 
     def decode_attention_fp8(self, q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, num_kv_heads: int,
                              page_size: int, num_blocks: int, sm_scale: float, splits: int = 0, workspace=None,
                              out=None, stream=None):
         """Attention of one query token per sequence (q [B, Hq, d] bf16) over its 8-bit pages."""
-        self._need(q.dim() == 3, "q must be [B, Hq, head_dim]")
+        if q.dim() != 3:
+            raise ValueError("q must be [B, Hq, head_dim]")
         return self._attention_fp8(q, 0, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, num_kv_heads,
                                    page_size, num_blocks, sm_scale, splits, workspace, out, stream)
 
@@ -326,7 +323,8 @@ class Codec:
                               out=None, stream=None):
         """Causal attention of the last q.shape[1] positions of every sequence (q [B, Tq, Hq, d] bf16) over its
         8-bit pages."""
-        self._need(q.dim() == 4 and q.shape[1] >= 1, "q must be [B, Tq, Hq, head_dim]")
+        if q.dim() != 4 or q.shape[1] < 1:
+            raise ValueError("q must be [B, Tq, Hq, head_dim]")
         return self._attention_fp8(q, q.shape[1], k_pool, v_pool, k_scales, v_scales, block_table, seq_lens,
                                    num_kv_heads, page_size, num_blocks, sm_scale, splits, workspace, out, stream)
 

@@ -50,32 +50,39 @@ def test_null_handle_refused():
     assert native.tq_workspace_bytes_fp8(None, 1, 1, 2) == 0
 
 
-def test_wrapper_refuses_before_any_call():
+def test_wrapper_refuses_before_any_call(monkeypatch):
     """Shapes, types and devices are checked before the library is called (no handle is needed to refuse)."""
+    monkeypatch.setattr(Codec, "_elsewhere", lambda self, stream: False)
     c = Codec.__new__(Codec)
     c.head_dim, c.device, c.handle = 128, 0, None
     x = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
     s = torch.zeros(3, dtype=torch.int64)
     rope = torch.zeros(4, 64)
-    good = dict(k=x, v=x, slot_mapping=s, q=None, q_out=None, positions=None, rope=None, interleaved=False)
-    for bad in (dict(v=x[:2]), dict(k=x.float(), v=x.float()), dict(slot_mapping=s.int()), dict(slot_mapping=s[:2]),
-                dict(q=x[:2]), dict(q_out=x), dict(q=x, q_out=x.float()), dict(rope=rope), dict(rope=rope, positions=s.int()),
-                dict(rope=rope.double(), positions=s), dict(k=x.transpose(1, 2), v=x.transpose(1, 2)),
-                dict()):  # the last one: tensors that are not on the handle's device
-        with pytest.raises(ValueError):
-            c._append_args(**{**good, **bad})
     pool = torch.zeros(2, 2, 16, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
     sc = torch.ones(2, 2)
-    c._pools((pool, pool), torch.float8_e4m3fn, 2, 16, 2, (sc, sc))
-    for args in ((pool.view(torch.uint8), 2, sc), (pool, 3, sc), (pool, 2, sc.double()), (pool, 2, sc[:1])):
+    c.device = -1  # get_device() of a CPU tensor: everything but the device is right in the calls below
+    assert c._flat(sc, torch.float32, 4, "x") == sc.data_ptr() and c._rows(x, 3, 2, "x") == (x.data_ptr(), 256)
+    for bad in (dict(v=x[:2]), dict(k=x.float(), v=x.float()), dict(s=s.int()), dict(s=s[:2]), dict(q=x[:2]),
+                dict(q_out=x), dict(q=x, q_out=x.float()), dict(rope=rope), dict(rope=rope, positions=s.int()),
+                dict(rope=rope.double(), positions=s), dict(rope=rope[0], positions=s),
+                dict(k=x.transpose(0, 1), v=x.transpose(0, 1)), dict(k=x[0], v=x[0]), dict(kp=pool.view(torch.uint8)),
+                dict(nb=3), dict(ks=sc.double()), dict(ks=sc[:1]), dict(k=x.repeat(1, 1, 2)[:, :, ::2])):
+        a = dict(k=x, v=x, s=s, kp=pool, ks=sc, nb=2)
+        a.update({k: v for k, v in bad.items() if k in a})
+        more = {k: v for k, v in bad.items() if k not in a}
         with pytest.raises(ValueError):
-            c._pools((args[0],), torch.float8_e4m3fn, 2, 16, args[1], (args[2],))
+            c.append_kv_fp8(a["k"], a["v"], a["s"], a["kp"], pool, a["ks"], sc, 16, a["nb"], **more)
     q, lens, table = torch.zeros(1, 4, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)
     for bad in (dict(q=q.float()), dict(q=q[..., :64]), dict(block_table=table.long()), dict(seq_lens=lens.long()),
-                dict(seq_lens=torch.zeros(2, dtype=torch.int32)), dict(q=q[0])):
+                dict(seq_lens=torch.zeros(2, dtype=torch.int32)), dict(q=q[0]), dict(block_table=table[0])):
         a = dict(q=q, block_table=table, seq_lens=lens)
         a.update(bad)
         with pytest.raises(ValueError):
             c.decode_attention_fp8(a["q"], pool, pool, sc, sc, a["block_table"], a["seq_lens"], 2, 16, 2, 0.1)
     with pytest.raises(ValueError):
         c.prefill_attention_fp8(q, pool, pool, sc, sc, table, lens, 2, 16, 2, 0.1)
+    c.device = 0  # tensors that are not on the handle's device
+    with pytest.raises(ValueError, match="cuda:0"):
+        c.append_kv_fp8(x, x, s, pool, pool, sc, sc, 16, 2)
+    with pytest.raises(ValueError, match="cuda:0"):
+        c.decode_attention_fp8(q, pool, pool, sc, sc, table, lens, 2, 16, 2, 0.1)
