@@ -1,10 +1,8 @@
 // tq_decode_fp8.cu -- attention over 8-bit pages: e4m3 codes with one scale per
 // (page, kv head) for keys and for values.
 //
-// One CTA = (split, kv head, sequence), W warps (four at head dim 128, three at 256);
-// warp w takes the 32-token rounds w, w + W, ... of its split.  The pages of a round come by the tensor memory
-// accelerator (boxes of one page x 128 bytes, 128-byte swizzle) into the warp's own
-// stages.  Codes enter the products as they are stored (mma.m16n8k32, e4m3 in, fp32
+// The pages of a 32-token round come by the tensor memory accelerator (boxes of one page x 128 bytes, 128-byte
+// swizzle) into a warp's own stages.  Codes enter the products as they are stored (mma.m16n8k32, e4m3 in, fp32
 // sums), nothing is widened first:
 //   S[t][h] = <kc_t, q_h 2^e>, tokens as M, heads as N; q 2^e as two e4m3 terms, which is
 //             exact: a bf16 has 8 significant bits, an e4m3 4 and a sign for the rest;
@@ -15,9 +13,12 @@
 // any scales share one accumulator, and the denominator adds P / vs.  P enters as
 // two e4m3 terms (about 8 bits of the largest), the rest is fp32.
 //
-// Split partials (max, denominator, numerators) are merged by merge_kernel; with one
-// split the CTA writes the output itself.  Up to eight (query token, head) columns of a
-// sequence and kv head go through this kernel, more through tq_prefill_fp8.cu.
+// Work is dealt out on the GPU, where the lengths are: the rounds of all (sequence, kv head) units in a row, an
+// equal share for each of one wave of CTAs (three per SM at head dim 128, two at 256).  A CTA's share is cut at
+// unit ends into segments; the W warps of a CTA take a segment's rounds in turn and merge.  A unit that one CTA has whole
+// is written at once, the others' partials (max, denominator, numerators) are merged by merge_fp8_kernel.  With one
+// split a CTA has one whole unit.  Up to eight (query token, head) columns of a sequence and kv head go through this
+// kernel, more through tq_prefill_fp8.cu.
 #include <cmath>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -91,8 +92,41 @@ __device__ __forceinline__ bool mbar_try(uint32_t mb, uint32_t par)
     return done != 0;
 }
 
-// The eight columns of a CTA are (query token, head of the group) pairs: with one query
-// token per sequence its G heads, else qpc = 8 / G tokens, each with its causal limit.
+// The first `n` sequences' rounds, summed, and the longest one's, by the whole block.
+template <int THREADS>
+__device__ __forceinline__ void count_rounds(const Args &A, long long *s_sum, int *s_max, long long &total, int &longest)
+{
+    long long sum = 0;
+    int mx = 0;
+    for (int b = threadIdx.x; b < A.B; b += THREADS) {
+        const int L = A.seq_lens[b];
+        if (L > A.max_blocks * A.P && blockIdx.x == 0) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
+        const int r = (min(max(L, 0), A.max_blocks * A.P) + kTok - 1) / kTok;
+        sum += r;
+        mx = max(mx, r);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if ((threadIdx.x & 31) == 0) {
+        s_sum[threadIdx.x >> 5] = sum;
+        s_max[threadIdx.x >> 5] = mx;
+    }
+    __syncthreads();
+    total = 0;
+    longest = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        total += s_sum[w];
+        longest = max(longest, s_max[w]);
+    }
+    __syncthreads();
+}
+
+// The columns of a CTA are the (query token, head) pairs of a sequence and kv head, eight at most, each with its causal
+// limit (one query token: the G heads, which see all).
 template <int D>
 __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     attention_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args A)
@@ -106,38 +140,10 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *mbar = reinterpret_cast<uint64_t *>(smem + SM::kData);  // [warp][stage]
     volatile int *cta_abort = reinterpret_cast<volatile int *>(mbar + kStages * kWarps);
-
-    const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / A.nqt, qt = blockIdx.z % A.nqt;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = lane & 3, row = lane >> 2;
-    const int P = A.P, G = A.G;
-    int L = A.seq_lens[b];
-    if (L < 0) L = 0;
-    if (L > A.max_blocks * P) {
-        if (split == 0 && kvh == 0 && qt == 0 && tid == 0) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
-        L = A.max_blocks * P;
-    }
-    const int q0 = qt * A.qpc;
-    const int ncol = min(A.qpc, A.Tq - q0) * G;
-    auto col_row = [&](int c) -> size_t {  // output row of column c
-        return (static_cast<size_t>(b) * A.Tq + q0 + c / G) * A.Hq + static_cast<size_t>(kvh) * G + c % G;
-    };
-    auto col_lim = [&](int c) -> int { return max(0, L - A.Tq + q0 + c / G + 1); };  // positions that it sees
+    const int P = A.P, G = A.G, ncol = A.Tq * G;
     const size_t rows_total = static_cast<size_t>(A.B) * A.Tq * A.Hq;
-    const int tok0 = split * A.pages_per_split * P;
-    const int tok1 = min(col_lim(ncol - 1), tok0 + A.pages_per_split * P);
-    if (tok0 >= tok1) {
-        if (A.splits == 1) {
-            for (int e = tid; e < ncol * (D / 2); e += kThreads)
-                reinterpret_cast<uint32_t *>(A.out + col_row(e / (D / 2)) * D)[e % (D / 2)] = 0u;
-        } else if (tid < ncol) {
-            float *ml = A.ml + (static_cast<size_t>(split) * rows_total + col_row(tid)) * 2;
-            ml[0] = -INFINITY;
-            ml[1] = 0.f;
-        }
-        return;
-    }
-    const int nrounds = (tok1 - tok0 + kTok - 1) / kTok;
 
     if (tid < kStages * kWarps)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&mbar[tid]))));
@@ -145,340 +151,459 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
 
+    // ---- this CTA's share: rounds [pos, end) of all units in a row, and the unit that it begins in ----
+    long long pos, end, share, unit0;  // unit0: where the unit at hand begins
+    int b, kvh;
+    auto length = [&](int i) -> int { return min(max(A.seq_lens[i], 0), A.max_blocks * P); };
+    if (A.splits == 1) {
+        b = blockIdx.x / A.Hkv;
+        kvh = blockIdx.x % A.Hkv;
+        if (kvh == 0 && tid == 0 && A.seq_lens[b] > A.max_blocks * P) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
+        pos = unit0 = 0;
+        end = share = max(1, (length(b) + kTok - 1) / kTok);
+    } else {
+        long long *s_sum = reinterpret_cast<long long *>(smem);
+        int *s_max = reinterpret_cast<int *>(smem + 64);
+        long long total;
+        int longest;
+        count_rounds<kThreads>(A, s_sum, s_max, total, longest);
+        total *= A.Hkv;
+        // at least two rounds a warp, and no unit in more pieces than there are splits
+        share = (total + gridDim.x - 1) / gridDim.x;
+        share = max(share, static_cast<long long>(2 * kWarps));
+        share = max(share, static_cast<long long>((longest + A.splits - 2) / (A.splits - 1)));
+        pos = share * blockIdx.x;
+        end = min(total, pos + share);
+        if (pos >= end) return;
+        // the sequence that holds round pos: running sums over blockDim sequences at a time
+        long long before = 0;  // rounds of the sequences before this stretch, all kv heads
+        int *s_b = reinterpret_cast<int *>(smem + 128);
+        long long *s_u = reinterpret_cast<long long *>(smem + 136);
+        b = 0;
+        for (int b0 = 0;; b0 += kThreads) {
+            const long long r = b0 + tid < A.B ? static_cast<long long>((length(b0 + tid) + kTok - 1) / kTok) * A.Hkv : 0;
+            long long inc = r;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) s_sum[warp] = inc;
+            __syncthreads();
+            long long base = before, all = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) base += s_sum[w];
+                all += s_sum[w];
+            }
+            const bool here = pos >= base + inc - r && pos < base + inc;
+            if (here) {
+                *s_b = b0 + tid;
+                *s_u = base + inc - r;
+            }
+            before += all;
+            if (__syncthreads_or(here) || b0 + kThreads >= A.B) break;
+        }
+        b = *s_b;
+        unit0 = *s_u;
+        const int per = (length(b) + kTok - 1) / kTok;
+        kvh = static_cast<int>((pos - unit0) / per);
+        unit0 += static_cast<long long>(kvh) * per;
+        __syncthreads();  // the stages may be written
+    }
+
     const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    auto stage_off = [&](int st) -> uint32_t { return static_cast<uint32_t>((warp * kStages + st) * SM::kStage); };
+    auto stage_addr = [&](int st) -> uint32_t { return sbase + static_cast<uint32_t>((warp * kStages + st) * SM::kStage); };
     auto mbar_addr = [&](int st) -> uint32_t {
         return static_cast<uint32_t>(__cvta_generic_to_shared(&mbar[warp * kStages + st]));
-    };
-    const int32_t *table = A.block_table + static_cast<int64_t>(b) * A.max_blocks;
-    auto round_tok = [&](int rr) -> int { return tok0 + (kWarps * rr + warp) * kTok; };
-    auto fetch_id = [&](int rr, int half) -> int {  // block of a round's 16-token half, -1 past the split
-        const int t = round_tok(rr) + 16 * half;
-        return t < tok1 ? __ldg(table + (t >> A.pshift)) : -1;
-    };
-    auto good = [&](int blk) -> bool { return blk >= 0 && blk < A.num_blocks; };
-    auto issue = [&](int rr, int st, const int (&blk)[2]) {  // lane 0: the round's pages into a stage
-        const int t = round_tok(rr);
-        const int boxes = P == 16 ? 2 : 1;
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-            if (p < boxes && good(blk[p])) bytes += static_cast<uint32_t>(2 * P * D);
-            else if (p < boxes && t + 16 * p < tok1) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
-        const uint32_t mb = mbar_addr(st);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // this warp's accesses of the stage are done
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            if (p >= boxes || !good(blk[p])) continue;
-            const int y = static_cast<int>((static_cast<int64_t>(blk[p]) * A.Hkv + kvh) * P) + (P == 32 ? (t & 31) : 0);
-            const uint32_t dk = sbase + stage_off(st) + p * 16 * 128;
-#pragma unroll
-            for (int x = 0; x < XB; ++x) {
-                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                             ::"r"(dk + x * kBoxBytes), "l"(reinterpret_cast<uint64_t>(&tmK)), "r"(x * 128), "r"(y), "r"(mb)
-                             : "memory");
-                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                             ::"r"(dk + SM::kTileBytes + x * kBoxBytes), "l"(reinterpret_cast<uint64_t>(&tmV)), "r"(x * 128),
-                             "r"(y), "r"(mb)
-                             : "memory");
-            }
-        }
     };
     auto drain = [&](int st, uint32_t par) {
         const long long t0 = clock64();
         while (!mbar_try(mbar_addr(st), par) && clock64() - t0 < kDrainLimit) {
         }
     };
-
-    const int my_rounds = (nrounds - warp + kWarps - 1) / kWarps;  // rounds warp, warp + kWarps, ...
-    int ids[2] = {-1, -1}, ids1[2] = {-1, -1};  // blocks of the round to compute and of the next one
-    if (my_rounds > 0) {
-        ids[0] = fetch_id(0, 0);
-        ids[1] = fetch_id(0, 1);
-        if (lane == 0) issue(0, 0, ids);
-    }
-    // a zero limit tests the first copy at once, while it cannot be done: the way to the timeout path
-    const bool first_ok = A.wait_limit > 0 || my_rounds == 0 || mbar_test(mbar_addr(0), 0);
-    if (my_rounds > 1) {
-        ids1[0] = fetch_id(1, 0);
-        ids1[1] = fetch_id(1, 1);
-    }
-
-    // query fragments (B operand of the score product): column `row`, coordinates 32 s + 4 quad (+ 16)
-    uint32_t qh[KS][2], ql[KS][2];
-    float qfac;  // 2^-e of column `row`
-    {
-        const bool cv = row < ncol;
-        const uint2 *qr = reinterpret_cast<const uint2 *>(A.q + col_row(cv ? row : 0) * D);
-        uint2 w[KS][2];
-        float mx = 0.f;
-        bool nan = false;
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                w[s][i] = cv ? __ldg(qr + 8 * s + 4 * i + quad) : make_uint2(0u, 0u);
-                const uint32_t u[2] = {w[s][i].x, w[s][i].y};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float x0 = fabsf(__uint_as_float(u[k] << 16)), x1 = fabsf(__uint_as_float(u[k] & 0xffff0000u));
-                    nan |= !(x0 <= 3.4e38f) || !(x1 <= 3.4e38f);
-                    mx = fmaxf(mx, fmaxf(x0, x1));
-                }
-            }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        nan = (__ballot_sync(0xffffffffu, nan) >> (lane & ~3)) & 15u;
-        // 2^e brings the largest element into [2^7, 2^8)
-        int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-        if (ex < -100) ex = -100;
-        if (ex > 120) ex = 120;
-        const float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
-        qfac = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float x0 = __uint_as_float(w[s][i].x << 16) * up, x1 = __uint_as_float(w[s][i].x & 0xffff0000u) * up;
-                float x2 = __uint_as_float(w[s][i].y << 16) * up, x3 = __uint_as_float(w[s][i].y & 0xffff0000u) * up;
-                const uint32_t lo = e4m3x2_rest(x0, x1), hi = e4m3x2_rest(x2, x3);
-                qh[s][i] = lo | (hi << 16);
-                ql[s][i] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
-            }
-    }
-    float fac[2];  // columns 2 quad + e: sm_scale log2(e) 2^-e
-    int lim[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int c = 2 * quad + e;
-        fac[e] = __shfl_sync(0xffffffffu, qfac, 4 * c) * A.sm_scale * kLog2e;
-        lim[e] = c < ncol ? col_lim(c) : 0;
-    }
-
-    float o[MT][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY};  // columns 2 quad + e
-    float l_run[2] = {0.f, 0.f};              // this lane's tokens' share of the denominators
+    // this lane's ldmatrix offsets; a k-step or coordinate chunk flips address bits 4-6
     const int mi = lane >> 3, ri = lane & 7;
-    const int krow = ri + 8 * (mi & 1), kch = mi >> 1;  // keys: matrices (rows 0-7 | 8-15) x (chunk c | c + 1)
+    const int krow = ri + 8 * (mi & 1);  // keys: matrices (rows 0-7 | 8-15) x (chunk c | c + 1)
+    const uint32_t koff = krow * 128 + (((mi >> 1) ^ ri) << 4), voff = SM::kTileBytes + lane * 128 + (ri << 4);
+    const int half = lane & 1;  // a round's scales and ids: even lanes hold its first 16 tokens', odd ones its last
 
-    auto scale_of = [&](const float *p, int blk) -> float {
-        return good(blk) ? __ldg(p + static_cast<int64_t>(blk) * A.Hkv + kvh) : 0.f;
-    };
-    float ks[2], vs[2];  // scales of the round to compute
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        ks[h] = scale_of(A.k_scales, ids[h]);
-        vs[h] = scale_of(A.v_scales, ids[h]);
-    }
-    for (int c = 0; c < my_rounds; ++c) {
-        const int st = c & 1;
-        __syncwarp();  // every lane is done with the stage the next copy overwrites
-        float ks1[2] = {0.f, 0.f}, vs1[2] = {0.f, 0.f};
-        int ids2[2] = {-1, -1};
-        if (c + 1 < my_rounds) {
-            if (lane == 0) issue(c + 1, st ^ 1, ids1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ks1[h] = scale_of(A.k_scales, ids1[h]);
-                vs1[h] = scale_of(A.v_scales, ids1[h]);
-                if (c + 2 < my_rounds) ids2[h] = fetch_id(c + 2, h);
-            }
-        }
-        {
-            const uint32_t par = (c >> 1) & 1;
-            bool ok = true;
-            if (A.wait_limit <= 0) {
-                ok = c == 0 ? first_ok : mbar_test(mbar_addr(st), par);
-            } else {
-                const long long t0 = clock64();
-                while (!mbar_try(mbar_addr(st), par))
-                    if (clock64() - t0 > A.wait_limit) {
-                        ok = false;
-                        break;
-                    }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                if (lane == 0) {
-                    atomicOr(A.status, TQ_DEVERR_TIMEOUT);
-                    *cta_abort = 1;
-                }
-                drain(st, par);
-                if (c + 1 < my_rounds) drain(st ^ 1, ((c + 1) >> 1) & 1);
-                break;
-            }
-        }
-        const int t = round_tok(c);
-        int nv[2];  // visible tokens of each half (of the column that sees most)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) nv[h] = good(ids[h]) ? max(0, min(16, tok1 - t - 16 * h)) : 0;
-        const uint32_t kbase = sbase + stage_off(st), vbase = kbase + SM::kTileBytes;
-        if (nv[0] + nv[1] < kTok) {  // rows behind the end or of a bad page hold anything: zero the values
-            unsigned char *vz = smem + stage_off(st) + SM::kTileBytes;
-            for (int e = lane; e < kTok * (D / 16); e += 32) {
-                const int rr = e / (D / 16), cc = e % (D / 16);
-                if ((rr & 15) >= nv[rr >> 4])
-                    *reinterpret_cast<uint4 *>(vz + (cc / 8) * kBoxBytes + rr * 128 + (cc % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
+    int done = 0;  // rounds that this warp has copied since the start: stage done % 2
+    for (;;) {
+        const int L = length(b);
+        const int unit_rounds = max(1, (L + kTok - 1) / kTok);
+        const int r0 = static_cast<int>(pos - unit0), r1 = static_cast<int>(min(end, unit0 + unit_rounds) - unit0);
+        auto col_row = [&](int c) -> size_t {  // output row of column c
+            return (static_cast<size_t>(b) * A.Tq + c / G) * A.Hq + static_cast<size_t>(kvh) * G + c % G;
+        };
+        auto col_lim = [&](int c) -> int { return max(0, L - A.Tq + c / G + 1); };  // positions that it sees
+        const int tok1 = min(L, r1 * kTok);
+        const int32_t *table = A.block_table + static_cast<int64_t>(b) * A.max_blocks;
+        auto round_tok = [&](int c) -> int { return (r0 + warp + kWarps * c) * kTok; };
+        auto fetch_id = [&](int c) -> int {  // block of this lane's half of a round, -1 past the end
+            const int t = round_tok(c) + 16 * half;
+            return t < tok1 ? __ldg(table + (t >> A.pshift)) : -1;
+        };
+        auto good = [&](int blk) -> bool { return blk >= 0 && blk < A.num_blocks; };
+        auto record = [&](int blk) -> int { return blk * A.Hkv + kvh; };  // below 2^31 / P
+        auto issue = [&](int c, int st, int blk) {  // the round's pages into a stage
+            const bool page = lane < 2 && (P == 16 || lane == 0);
+            const unsigned ok = __ballot_sync(0xffffffffu, page && good(blk));
+            const uint32_t mb = mbar_addr(st);
+            if (page && !good(blk) && round_tok(c) + 16 * half < tok1) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // this warp's accesses of the stage are done
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb),
+                             "r"(__popc(ok) * static_cast<uint32_t>(2 * P * D))
+                             : "memory");
             __syncwarp();
-        }
-        // ---- scores ----
-        float sc[2][4] = {};
+            if (ok >> lane & 1u) {
+                const int y = record(blk) * P;
+                const uint32_t dk = stage_addr(st) + lane * 16 * 128;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const uint32_t at = kbase + (s >> 2) * kBoxBytes + krow * 128 + (((2 * (s & 3) + kch) ^ (krow & 7)) << 4);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4(at + h * 16 * 128, a0, a1, a2, a3);
-                mma_e4m3(sc[h], a0, a1, a2, a3, qh[s][0], qh[s][1]);
-                mma_e4m3(sc[h], a0, a1, a2, a3, ql[s][0], ql[s][1]);
+                for (int x = 0; x < XB; ++x) {
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                 ::"r"(dk + x * kBoxBytes), "l"(reinterpret_cast<uint64_t>(&tmK)), "r"(x * 128), "r"(y), "r"(mb)
+                                 : "memory");
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                 ::"r"(dk + SM::kTileBytes + x * kBoxBytes), "l"(reinterpret_cast<uint64_t>(&tmV)), "r"(x * 128),
+                                 "r"(y), "r"(mb)
+                                 : "memory");
+                }
             }
+        };
+
+        const int my_rounds = L > 0 ? (r1 - r0 - warp + kWarps - 1) / kWarps : 0;  // rounds r0 + warp, + kWarps, ...
+        int id = -1, id1 = -1;  // block of the round to compute and of the next one
+        if (my_rounds > 0) {
+            id = fetch_id(0);
+            issue(0, done & 1, id);
         }
-        // ---- mask, online softmax (base 2): this lane holds tokens row, row + 8 of each half, columns 2 quad + e ----
-        float y[2][2][2], lv[2];
+        // a zero limit tests the first copy at once, while it cannot be done: the way to the timeout path
+        const bool first_ok = A.wait_limit > 0 || my_rounds == 0 || mbar_test(mbar_addr(done & 1), (done >> 1) & 1);
+        if (my_rounds > 1) id1 = fetch_id(1);
+
+        // query fragments (B operand of the score product): column `row`, coordinates 32 s + 4 quad (+ 16)
+        uint32_t qh[KS][2], ql[KS][2];
+        float qfac;  // 2^-e of column `row`
+        {
+            const bool cv = row < ncol;
+            const uint2 *qr = reinterpret_cast<const uint2 *>(A.q + col_row(cv ? row : 0) * D);
+            uint2 w[KS][2];
+            float mx = 0.f;
+            bool nan = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            lv[h] = log2_scale(vs[h]);
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                for (int i = 0; i < 2; ++i) w[s][i] = cv ? __ldg(qr + 8 * s + 4 * i + quad) : make_uint2(0u, 0u);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = row + 8 * r;
-                    const bool seen = i < nv[h] && t + 16 * h + i < lim[e];
-                    y[h][r][e] = seen ? fmaf(sc[h][2 * r + e], fac[e] * ks[h], lv[h]) : -INFINITY;
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t u[2] = {w[s][i].x, w[s][i].y};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float x0 = fabsf(__uint_as_float(u[k] << 16)), x1 = fabsf(__uint_as_float(u[k] & 0xffff0000u));
+                        nan |= !(x0 <= 3.4e38f) || !(x1 <= 3.4e38f);
+                        mx = fmaxf(mx, fmaxf(x0, x1));
+                    }
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            nan = (__ballot_sync(0xffffffffu, nan) >> (lane & ~3)) & 15u;
+            // 2^e brings the largest element into [2^7, 2^8)
+            int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+            ex = min(max(ex, -100), 120);
+            const float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
+            qfac = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x0 = __uint_as_float(w[s][i].x << 16) * up, x1 = __uint_as_float(w[s][i].x & 0xffff0000u) * up;
+                    float x2 = __uint_as_float(w[s][i].y << 16) * up, x3 = __uint_as_float(w[s][i].y & 0xffff0000u) * up;
+                    const uint32_t lo = e4m3x2_rest(x0, x1), hi = e4m3x2_rest(x2, x3);
+                    qh[s][i] = lo | (hi << 16);
+                    ql[s][i] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
                 }
         }
-        float alpha[2], shift[2];
+        float fac[2];  // columns 2 quad + e: sm_scale log2(e) 2^-e
+        int lim[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float mt = fmaxf(fmaxf(y[0][0][e], y[0][1][e]), fmaxf(y[1][0][e], y[1][1][e]));
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-            const float m_new = fmaxf(m_run[e], mt);
-            const bool none = m_new == -INFINITY;  // nothing seen so far (or only NaN)
-            alpha[e] = none ? 1.f : fast_exp2(m_run[e] - m_new);
-            shift[e] = none ? kPShift : kPShift - m_new;
-            m_run[e] = m_new;
-            l_run[e] *= alpha[e];
+            const int c = 2 * quad + e;
+            fac[e] = __shfl_sync(0xffffffffu, qfac, 4 * c) * A.sm_scale * kLog2e;
+            lim[e] = min(tok1, c < ncol ? col_lim(c) : tok1);
         }
-        if (alpha[0] != 1.f || alpha[1] != 1.f) {
+        const int low = min(tok1, col_lim(0));  // every column sees the positions below
+
+        float o[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+        float m_run[2] = {-INFINITY, -INFINITY};  // columns 2 quad + e
+        float l_run[2] = {0.f, 0.f};              // this lane's tokens' share of the denominators
+
+        auto scale_of = [&](const float *p, int blk) -> float { return good(blk) ? __ldg(p + record(blk)) : 0.f; };
+        float ks = scale_of(A.k_scales, id), vs = scale_of(A.v_scales, id);  // of this lane's half of the round
+        for (int c = 0; c < my_rounds; ++c, ++done) {
+            const int st = done & 1;
+            __syncwarp();  // every lane is done with the stage the next copy overwrites
+            float ks1 = 0.f, vs1 = 0.f;
+            int id2 = -1;
+            if (c + 1 < my_rounds) {
+                issue(c + 1, st ^ 1, id1);
+                ks1 = scale_of(A.k_scales, id1);
+                vs1 = scale_of(A.v_scales, id1);
+                if (c + 2 < my_rounds) id2 = fetch_id(c + 2);
+            }
+            const float lvl = log2_scale(vs);
+            const float downl = fast_exp2(kLShift - kPShift - lvl);
+            const int t = round_tok(c);
+            const unsigned okm = __ballot_sync(0xffffffffu, good(id));
+            {
+                const uint32_t par = (done >> 1) & 1;
+                bool ok = true;
+                if (A.wait_limit <= 0) {
+                    ok = c == 0 ? first_ok : mbar_test(mbar_addr(st), par);
+                } else if (!mbar_try(mbar_addr(st), par)) {
+                    const long long t0 = clock64();
+                    while (!(ok = mbar_try(mbar_addr(st), par)))
+                        if (clock64() - t0 > A.wait_limit) break;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0) {
+                        atomicOr(A.status, TQ_DEVERR_TIMEOUT);
+                        *cta_abort = 1;
+                    }
+                    drain(st, par);
+                    if (c + 1 < my_rounds) drain(st ^ 1, ((done + 1) >> 1) & 1);
+                    break;
+                }
+            }
+            const uint32_t stage = stage_addr(st);
+            const bool whole = (okm & 3u) == 3u && t + kTok <= low;  // every token is seen by every column
+            int nv[2];                                               // tokens of each half
+#pragma unroll
+            for (int h = 0; h < 2; ++h) nv[h] = (okm >> h & 1u) ? max(0, min(16, tok1 - t - 16 * h)) : 0;
+            if (!whole && nv[0] + nv[1] < kTok) {  // rows behind the end or of a bad page hold anything: zero the values
+                unsigned char *vz = smem + (stage - sbase) + SM::kTileBytes;
+                for (int e = lane; e < kTok * (D / 16); e += 32) {
+                    const int rr = e / (D / 16), cc = e % (D / 16);
+                    if ((rr & 15) >= nv[rr >> 4])
+                        *reinterpret_cast<uint4 *>(vz + (cc / 8) * kBoxBytes + rr * 128 + (cc % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+            // ---- scores ----
+            float sc[2][4] = {};
+            const uint32_t kat = stage + koff;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a0, a1, a2, a3;
+                    ldsm_x4((kat ^ (32 * (s & 3))) + (s >> 2) * kBoxBytes + h * 16 * 128, a0, a1, a2, a3);
+                    mma_e4m3(sc[h], a0, a1, a2, a3, qh[s][0], qh[s][1]);
+                    mma_e4m3(sc[h], a0, a1, a2, a3, ql[s][0], ql[s][1]);
+                }
+            }
+            // ---- mask, online softmax (base 2): this lane holds tokens row, row + 8 of each half, columns 2 quad + e ----
+            float y[2][2][2], down[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float k1 = __shfl_sync(0xffffffffu, ks, h), lv = __shfl_sync(0xffffffffu, lvl, h);
+                down[h] = __shfl_sync(0xffffffffu, downl, h);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float a = fac[e] * k1;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) y[h][r][e] = fmaf(sc[h][2 * r + e], a, lv);
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = row + 8 * r;
+                            if (i >= nv[h] || t + 16 * h + i >= lim[e]) y[h][r][e] = -INFINITY;
+                        }
+            }
+            float alpha[2], shift[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mt = max3(y[0][0][e], y[0][1][e], fmaxf(y[1][0][e], y[1][1][e]));
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                mt = max3(mt, __shfl_xor_sync(0xffffffffu, mt, 16), m_run[e]);
+                const bool none = mt == -INFINITY;  // nothing seen so far (or only NaN)
+                alpha[e] = none ? 1.f : fast_exp2(m_run[e] - mt);
+                shift[e] = none ? kPShift : kPShift - mt;
+                m_run[e] = mt;
+                l_run[e] *= alpha[e];
+            }
+            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[mt][0] *= alpha[0]; o[mt][1] *= alpha[1]; o[mt][2] *= alpha[0]; o[mt][3] *= alpha[1];
+                }
+            }
+            // ---- P as the B operand: byte pairs (high, low) of a token and column, transposed
+            // to (column `row`; tokens 2 quad, 2 quad + 1 | + 8, + 9), then high and low bytes apart ----
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t tr[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = fast_exp2(y[h][r][0] + shift[0]), p1 = fast_exp2(y[h][r][1] + shift[1]);
+                    l_run[0] = fmaf(p0, down[h], l_run[0]);
+                    l_run[1] = fmaf(p1, down[h], l_run[1]);
+                    __half2 p = __floats2half2_rn(p0, p1);  // 11 bits, of which the two terms keep about 8
+                    const uint32_t hi = e4m3x2_rest(p);
+                    tr[r] = movmatrix_trans(__byte_perm(hi, e4m3x2(p), 0x5140));
+                }
+                bh[h] = __byte_perm(tr[0], tr[1], 0x6420);
+                bl[h] = __byte_perm(tr[0], tr[1], 0x7531);
+            }
+            // ---- O[coordinate][column] += V^T P: the m-tile's rows are its even coordinates, then its odd ones ----
+            const uint32_t vat = stage + voff;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                o[mt][0] *= alpha[0]; o[mt][1] *= alpha[1]; o[mt][2] *= alpha[0]; o[mt][3] *= alpha[1];
+                uint32_t v0, v1, v2, v3;
+                ldsm_x4_trans((vat ^ ((mt & 7) << 4)) + (mt >> 3) * kBoxBytes, v0, v1, v2, v3);
+                const uint32_t a0 = __byte_perm(v0, v1, 0x6420), a1 = __byte_perm(v0, v1, 0x7531);
+                const uint32_t a2 = __byte_perm(v2, v3, 0x6420), a3 = __byte_perm(v2, v3, 0x7531);
+                mma_e4m3(o[mt], a0, a1, a2, a3, bh[0], bh[1]);
+                mma_e4m3(o[mt], a0, a1, a2, a3, bl[0], bl[1]);
             }
+            ks = ks1;
+            vs = vs1;
+            id = id1;
+            id1 = id2;
         }
-        // ---- P as the B operand: byte pairs (high, low) of a token and column, transposed
-        // to (column `row`; tokens 2 quad, 2 quad + 1 | + 8, + 9), then high and low bytes apart ----
-        uint32_t bh[2], bl[2];
+        __syncthreads();  // every warp is done with the stages before they hold merge data
+        const bool dead = *cta_abort != 0;
+        float *red = reinterpret_cast<float *>(smem);
+        float *r_m = red;                   // [warps][8]
+        float *r_l = r_m + kWarps * 8;      // [warps][8]
+        float *r_o = r_l + kWarps * 8;      // [warps][D][8]
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float down = fast_exp2(kLShift - kPShift - lv[h]);
-            uint32_t tr[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float p0 = fast_exp2(y[h][r][0] + shift[0]), p1 = fast_exp2(y[h][r][1] + shift[1]);
-                l_run[0] = fmaf(p0, down, l_run[0]);
-                l_run[1] = fmaf(p1, down, l_run[1]);
-                const uint32_t hi = e4m3x2_rest(p0, p1), lo = e4m3x2(p0, p1);
-                tr[r] = movmatrix_trans(__byte_perm(hi, lo, 0x5140));
-            }
-            bh[h] = __byte_perm(tr[0], tr[1], 0x6420);
-            bl[h] = __byte_perm(tr[0], tr[1], 0x7531);
+        for (int e = 0; e < 2; ++e) {
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 4);
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 8);
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 16);
         }
-        // ---- O[coordinate][column] += V^T P: the m-tile's rows are its even coordinates, then its odd ones ----
+        if (row == 0) {
+            r_m[warp * 8 + 2 * quad] = m_run[0];
+            r_m[warp * 8 + 2 * quad + 1] = m_run[1];
+            r_l[warp * 8 + 2 * quad] = l_run[0];
+            r_l[warp * 8 + 2 * quad + 1] = l_run[1];
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            uint32_t r0, r1, r2, r3;
-            ldsm_x4_trans(vbase + (mt >> 3) * kBoxBytes + lane * 128 + (((mt & 7) ^ ri) << 4), r0, r1, r2, r3);
-            const uint32_t a0 = __byte_perm(r0, r1, 0x6420), a1 = __byte_perm(r0, r1, 0x7531);
-            const uint32_t a2 = __byte_perm(r2, r3, 0x6420), a3 = __byte_perm(r2, r3, 0x7531);
-            mma_e4m3(o[mt], a0, a1, a2, a3, bh[0], bh[1]);
-            mma_e4m3(o[mt], a0, a1, a2, a3, bl[0], bl[1]);
+            float *p = r_o + (warp * D + 16 * mt + 2 * row) * 8 + 2 * quad;
+            *reinterpret_cast<float2 *>(p) = make_float2(o[mt][0], o[mt][1]);
+            *reinterpret_cast<float2 *>(p + 8) = make_float2(o[mt][2], o[mt][3]);
         }
+        __syncthreads();
+        // a unit's pieces are numbered from the CTA that holds its first round; a unit in one piece is done here
+        const long long first = unit0 / share;
+        const int pieces = A.splits == 1 ? 1 : static_cast<int>((unit0 + unit_rounds - 1) / share - first) + 1;
+        const int piece = A.splits == 1 ? 0 : static_cast<int>(blockIdx.x - first);
+        if (piece == 0 && tid == 0 && A.splits > 1) A.pieces[static_cast<int64_t>(b) * A.Hkv + kvh] = pieces;
+        const float downp = fast_exp2(-kPShift), ldown = fast_exp2(-kLShift);
+        for (int e = tid; e < ncol * D; e += kThreads) {
+            const int c = e / D, j = e - c * D;
+            float M = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            ks[h] = ks1[h];
-            vs[h] = vs1[h];
-            ids[h] = ids1[h];
-            ids1[h] = ids2[h];
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, r_m[w * 8 + c]);
+            const float ref = M == -INFINITY ? 0.f : M;
+            float acc = 0.f, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (r_l[w * 8 + c] == 0.f) continue;  // a warp that saw nothing
+                const float f = r_m[w * 8 + c] == -INFINITY ? 1.f : fast_exp2(r_m[w * 8 + c] - ref);
+                acc = fmaf(f, r_o[(w * D + j) * 8 + c], acc);
+                l = fmaf(f, r_l[w * 8 + c], l);
+            }
+            acc *= downp;
+            l *= ldown;
+            if (dead) {
+                M = -INFINITY;
+                acc = l = 0.f;
+            }
+            const size_t orow = col_row(c);
+            if (pieces == 1) {
+                A.out[orow * D + j] = float_to_bf16_bits(l == 0.f ? 0.f : acc / l);
+            } else {
+                const size_t pr = static_cast<size_t>(piece) * rows_total + orow;
+                A.acc[pr * D + j] = acc;
+                if (j == 0) {
+                    A.ml[2 * pr] = M;
+                    A.ml[2 * pr + 1] = l;
+                }
+            }
         }
-    }
-    __syncthreads();  // every warp is done with the stages before they hold merge data
-    const bool dead = *cta_abort != 0;
-    float *red = reinterpret_cast<float *>(smem);
-    float *r_m = red;                   // [warps][8]
-    float *r_l = r_m + kWarps * 8;      // [warps][8]
-    float *r_o = r_l + kWarps * 8;      // [warps][D][8]
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 4);
-        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 8);
-        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 16);
-    }
-    if (row == 0) {
-        r_m[warp * 8 + 2 * quad] = m_run[0];
-        r_m[warp * 8 + 2 * quad + 1] = m_run[1];
-        r_l[warp * 8 + 2 * quad] = l_run[0];
-        r_l[warp * 8 + 2 * quad + 1] = l_run[1];
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        float *p = r_o + (warp * D + 16 * mt + 2 * row) * 8 + 2 * quad;
-        *reinterpret_cast<float2 *>(p) = make_float2(o[mt][0], o[mt][1]);
-        *reinterpret_cast<float2 *>(p + 8) = make_float2(o[mt][2], o[mt][3]);
-    }
-    __syncthreads();
-    const float down = fast_exp2(-kPShift), ldown = fast_exp2(-kLShift);
-    for (int e = tid; e < ncol * D; e += kThreads) {
-        const int c = e / D, j = e - c * D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, r_m[w * 8 + c]);
-        const float ref = M == -INFINITY ? 0.f : M;
-        float acc = 0.f, l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (r_l[w * 8 + c] == 0.f) continue;  // a warp that saw nothing
-            const float f = r_m[w * 8 + c] == -INFINITY ? 1.f : fast_exp2(r_m[w * 8 + c] - ref);
-            acc = fmaf(f, r_o[(w * D + j) * 8 + c], acc);
-            l = fmaf(f, r_l[w * 8 + c], l);
+        // ---- the next unit of the share ----
+        pos = unit0 + unit_rounds;
+        unit0 = pos;
+        if (pos >= end) return;
+        if (++kvh == A.Hkv) {
+            kvh = 0;
+            do ++b;
+            while (length(b) == 0);  // pos < end: there is a later unit with rounds
         }
-        acc *= down;
-        l *= ldown;
+        __syncthreads();  // the merge data is read
+        // the waits of a CTA that gave up are not in step with its stages any more: its other units count as unseen
         if (dead) {
-            M = -INFINITY;
-            acc = l = 0.f;
-        }
-        const size_t orow = col_row(c);
-        if (A.splits == 1) {
-            A.out[orow * D + j] = float_to_bf16_bits(l == 0.f ? 0.f : acc / l);
-        } else {
-            const size_t pr = static_cast<size_t>(split) * rows_total + orow;
-            A.acc[pr * D + j] = acc;
-            if (j == 0) {
-                A.ml[2 * pr] = M;
-                A.ml[2 * pr + 1] = l;
+            for (;;) {
+                const int n = (length(b) + kTok - 1) / kTok;
+                const long long f0 = unit0 / share;
+                const int np = static_cast<int>((unit0 + n - 1) / share - f0) + 1;
+                if (blockIdx.x == f0 && tid == 0) A.pieces[static_cast<int64_t>(b) * A.Hkv + kvh] = np;
+                for (int e = tid; e < ncol * D; e += kThreads) {
+                    const size_t orow = (static_cast<size_t>(b) * A.Tq + e / D / G) * A.Hq + static_cast<size_t>(kvh) * G + e / D % G;
+                    if (np == 1) A.out[orow * D + e % D] = 0;
+                    else if (e % D == 0) {
+                        const size_t pr = static_cast<size_t>(blockIdx.x - f0) * rows_total + orow;
+                        A.ml[2 * pr] = -INFINITY;
+                        A.ml[2 * pr + 1] = 0.f;
+                    }
+                }
+                unit0 += n;
+                if (unit0 >= end) return;
+                if (++kvh == A.Hkv) {
+                    kvh = 0;
+                    do ++b;
+                    while (length(b) == 0);
+                }
             }
         }
     }
 }
 
-// Merges the splits of an output row: o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.
-// One warp per row, D / 32 coordinates per lane; a split that saw nothing (l = 0) has
-// no partial to read.  A NaN of any split stays one.
+// Merges the pieces of an output row: o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.
+// One warp per row, D / 32 coordinates per lane; a piece that saw nothing (l = 0) has
+// no partial to read.  A NaN of any piece stays one.  `pieces`: how many each (sequence, kv head) has, where its CTAs
+// chose; a unit in one piece is done, an empty sequence gives zeros.  NULL: A.splits.
 template <int D>
-__global__ void __launch_bounds__(128) merge_fp8_kernel(const float *__restrict__ ml, const float *__restrict__ acc,
-                                                        uint16_t *__restrict__ out, int64_t rows, int splits)
+__global__ void __launch_bounds__(128) merge_fp8_kernel(const Args A, const int64_t rows, const int *__restrict__ pieces)
 {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
+    const float *ml = A.ml, *acc = A.acc;
+    int splits = A.splits;
+    if (pieces) {
+        const int64_t b = row / A.Hq / A.Tq;
+        splits = A.seq_lens[b] > 0 ? pieces[b * A.Hkv + row % A.Hq / A.G] : 0;
+        if (splits == 1) return;
+    }
     float M = -INFINITY;
     for (int s = lane; s < splits; s += 32) M = fmaxf(M, __ldg(ml + (s * rows + row) * 2));
     M = warp_max(M);
@@ -510,7 +635,7 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const float *__restrict_
         }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(out + row * D + lane * E);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(A.out + row * D + lane * E);
 #pragma unroll
     for (int i = 0; i < E; i += 2)
         dst[i / 2] = float_to_bf16_bits(n[i] * inv) | (static_cast<uint32_t>(float_to_bf16_bits(n[i + 1] * inv)) << 16);
@@ -518,15 +643,16 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const float *__restrict_
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// The pieces of a unit: [splits][rows] (max, denominator), [splits][rows][d] numerators, and how many there are.
 size_t workspace_bytes(int d, int64_t rows, int splits)
 {
     if (splits <= 1) return 0;
     return align256(static_cast<size_t>(splits) * rows * 2 * sizeof(float)) +
-           align256(static_cast<size_t>(splits) * rows * d * sizeof(float));
+           align256(static_cast<size_t>(splits) * rows * d * sizeof(float)) + align256(static_cast<size_t>(rows) * sizeof(int));
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, bool tc, cudaStream_t st)
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, bool tc, int num_sms, cudaStream_t st)
 {
     cudaError_t e;
     if (tc) {
@@ -535,19 +661,20 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, 
         const size_t smem = Fp8Smem<D>::kBytes;
         e = ensure_smem_attr(reinterpret_cast<const void *>(attention_fp8_kernel<D>), smem);
         if (e != cudaSuccess) return e;
-        attention_fp8_kernel<D><<<dim3(a.splits, a.Hkv, a.B * a.nqt), Fp8Smem<D>::kThreads, smem, st>>>(tk, tv, a);
+        const unsigned grid = a.splits == 1 ? static_cast<unsigned>(a.B) * a.Hkv : static_cast<unsigned>(num_sms) * Fp8Smem<D>::kCtas;
+        attention_fp8_kernel<D><<<grid, Fp8Smem<D>::kThreads, smem, st>>>(tk, tv, a);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || a.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.Tq * a.Hq;
-    merge_fp8_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a.ml, a.acc, a.out, rows, a.splits);
+    merge_fp8_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a, rows, tc ? nullptr : a.pieces);
     return cudaGetLastError();
 }
 
 int clamp_splits(long long splits, long long most)
 {
     if (splits > most) splits = most;
-    if (splits > 256) splits = 256;
+    if (splits > 64) splits = 64;
     return splits < 1 ? 1 : static_cast<int>(splits);
 }
 
@@ -616,17 +743,17 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint8_t 
     a.num_blocks = num_blocks;
     a.sm_scale = sm_scale;
     a.splits = splits;
-    // whole 32-token rounds per split, so that a split never begins inside a round's page pair
-    const int ppr = kTok / P;
-    a.pages_per_split = ((max_blocks + splits - 1) / splits + ppr - 1) / ppr * ppr;
+    a.pages_per_split = (max_blocks + splits - 1) / splits;
     a.ml = static_cast<float *>(workspace);
     a.acc = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                       align256(static_cast<size_t>(splits) * rows * 2 * sizeof(float)));
+    a.pieces = reinterpret_cast<int *>(reinterpret_cast<char *>(a.acc) +
+                                       align256(static_cast<size_t>(splits) * rows * c.d * sizeof(float)));
     a.out = out;
     a.status = c.status;
     a.wait_limit = c.wait_limit;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = c.d == 128 ? launch<128>(tk, tv, a, tc, st) : launch<256>(tk, tv, a, tc, st);
+    e = c.d == 128 ? launch<128>(tk, tv, a, tc, c.num_sms, st) : launch<256>(tk, tv, a, tc, c.num_sms, st);
     if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return TQ_OK;
 }
@@ -637,10 +764,15 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint8_t 
 extern "C" int tq_decode_splits_fp8(tq_handle h, int batch, int num_kv_heads, int max_blocks_per_seq, int page_size)
 {
     if (!h || batch < 1 || num_kv_heads < 1 || max_blocks_per_seq < 1 || page_size < 1) return 1;
+    // Up to 1024 positions a CTA per (sequence, kv head) and no merge.  Else one wave of CTAs shares the rounds, and a
+    // unit of four times the mean length may still be cut at every CTA's share.
+    if (static_cast<long long>(max_blocks_per_seq) * page_size <= 1024) return 1;
     const long long units = static_cast<long long>(batch) * num_kv_heads;
-    const long long ctas = 8LL * tq::handle_codec(h).num_sms;
+    const tq::Codec &c = tq::handle_codec(h);
+    const long long ctas = static_cast<long long>(c.num_sms) * (c.d == 128 ? tq::Fp8Smem<128>::kCtas : tq::Fp8Smem<256>::kCtas);
     const long long tiles = (static_cast<long long>(max_blocks_per_seq) * page_size + 127) / 128;
-    return tq::clamp_splits((ctas + units - 1) / units, tiles);
+    const int splits = tq::clamp_splits((4 * ctas + units - 1) / units + 1, tiles);
+    return splits < 2 ? 2 : splits;
 }
 
 extern "C" size_t tq_workspace_bytes_fp8(tq_handle h, int batch, int num_q_heads, int splits)

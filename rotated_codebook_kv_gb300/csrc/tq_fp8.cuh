@@ -43,6 +43,31 @@ __device__ __forceinline__ uint32_t e4m3x2_rest(float &x, float &y)
     return c;
 }
 
+// Two halves to e4m3 and what is left of them (exact).
+__device__ __forceinline__ uint32_t e4m3x2_rest(__half2 &x)
+{
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    uint32_t b;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(c));
+    x = __hsub2(x, *reinterpret_cast<const __half2 *>(&b));
+    return c;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(__half2 x)
+{
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    return c;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t e4m3x2(float x, float y)
 {
     uint16_t c;
@@ -60,6 +85,7 @@ struct Args {
     int splits, pages_per_split;
     int Tq, qpc, nqt;  // query tokens per sequence, per CTA, and CTAs over them
     float *ml, *acc;   // [splits][B][Tq][Hq][2], [splits][B][Tq][Hq][D]; unused with one split
+    int *pieces;       // [B][Hkv] pieces of a unit (decode)
     uint16_t *out;
     unsigned *status;
     long long wait_limit;

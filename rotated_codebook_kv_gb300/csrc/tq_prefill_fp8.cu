@@ -123,13 +123,6 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // Two fp32 lanes side by side: one issue slot for two multiply-adds or sums.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {

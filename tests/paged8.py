@@ -107,9 +107,9 @@ def attention(q, codes_k, codes_v, ks, vs, table, lens, page, sm):
 
     The bound, per output element (T tokens seen, p the probabilities, v the values):
       * bf16 output: half a step, 2^-8 |out|;
-      * p as two e4m3 terms of 2^8 p: the rest of the first is at most 2^-4 of p, the rest of the second 2^-4 of
-        that: 2^-8 p, at least half a subnormal step of the second, 2^-10 / 2^8 of the largest p vs: together
-        2^-8 A + 2^-18 sum_t max_t(p vs) |code_t| / sum p, A = sum p |v|;
+      * p as two e4m3 terms of fp16(2^8 p): fp16 2^-11 p, the rest of the first term at most 2^-4 of p, the rest of
+        the second 2^-4 of that: (2^-8 + 2^-11) p, at least half a subnormal step of the second, 2^-10 / 2^8 of the
+        largest p vs: together (2^-8 + 2^-11) A + 2^-18 sum_t max_t(p vs) |code_t| / sum p, A = sum p |v|;
       * ex2.approx (2^-22), fp32 sums and the log2-domain score in fp32: its argument is within 2^-22 |x| + 2^-21
         of the exact one, |x| <= X = max |x|, so e^x is within (X + 4) 2^-21 (twice: p and the sum);
       * q as two e4m3 terms of 2^e q <= 2^8: exact down to 2^-2, then off by at most 2^-10, 2^-17 of the largest
@@ -148,6 +148,6 @@ def attention(q, codes_k, codes_v, ks, vs, table, lens, page, sm):
                     dA = (p * dx) @ np.abs(v[:n]) + (p @ dx) * A
                     sub = 2.0 ** -18 * (p * s[:n]).max() * np.abs(cv[:n]).sum(0)
                     out[b, i, h * G + g] = o
-                    bound[b, i, h * G + g] = 2.0 ** -8 * (np.abs(o) + A) + sub + dA + (n / 8 + 4) * 2.0 ** -23 * A + 1e-30
+                    bound[b, i, h * G + g] = 2.0 ** -8 * (np.abs(o) + A) + 2.0 ** -11 * A + sub + dA + (n / 8 + 4) * 2.0 ** -23 * A + 1e-30
     return out, bound
 
