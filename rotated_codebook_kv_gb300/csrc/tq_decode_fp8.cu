@@ -32,15 +32,15 @@ namespace {
 using namespace fp8;
 
 constexpr int kTok = 32;                  // tokens of a warp's round
-constexpr int kStages = 2;
 constexpr int kBoxBytes = kTok * 128;     // one 128-byte-wide column block of a round
 constexpr float kPShift = 8.f;            // probabilities enter the product as 2^8 p <= 256
 
 template <int D>
 struct Fp8Smem {
-    static constexpr int kWarps = D == 128 ? 4 : 3;   // with two stages each: 64 KB and 96 KB a CTA, three and two CTAs per SM
+    static constexpr int kWarps = D == 128 ? 4 : 7;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kCtas = D == 128 ? 3 : 2;
+    static constexpr int kCtas = D == 128 ? 3 : 1;
+    static constexpr int kStages = 2;
     static constexpr int kTileBytes = kTok * D;       // keys or values of one round
     static constexpr int kStage = 2 * kTileBytes;     // keys, then values
     static constexpr size_t kData = static_cast<size_t>(kWarps) * kStages * kStage;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     attention_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args A)
 {
     using SM = Fp8Smem<D>;
-    constexpr int kWarps = SM::kWarps, kThreads = SM::kThreads;
+    constexpr int kWarps = SM::kWarps, kThreads = SM::kThreads, kStages = SM::kStages;
     constexpr int KS = D / 32;   // k-steps of the score product
     constexpr int MT = D / 16;   // m-tiles of the value product
     constexpr int XB = D / 128;  // 128-byte column blocks of a row
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         end = share = max(1, (length(b) + kTok - 1) / kTok);
     } else {
         long long *s_sum = reinterpret_cast<long long *>(smem);
-        int *s_max = reinterpret_cast<int *>(smem + 64);
+        int *s_max = reinterpret_cast<int *>(smem + 128);
         long long total;
         int longest;
         count_rounds<kThreads>(A, s_sum, s_max, total, longest);
@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         if (pos >= end) return;
         // the sequence that holds round pos: running sums over blockDim sequences at a time
         long long before = 0;  // rounds of the sequences before this stretch, all kv heads
-        int *s_b = reinterpret_cast<int *>(smem + 128);
-        long long *s_u = reinterpret_cast<long long *>(smem + 136);
+        int *s_b = reinterpret_cast<int *>(smem + 192);
+        long long *s_u = reinterpret_cast<long long *>(smem + 200);
         b = 0;
         for (int b0 = 0;; b0 += kThreads) {
             const long long r = b0 + tid < A.B ? static_cast<long long>((length(b0 + tid) + kTok - 1) / kTok) * A.Hkv : 0;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     const uint32_t koff = krow * 128 + (((mi >> 1) ^ ri) << 4), voff = SM::kTileBytes + lane * 128 + (ri << 4);
     const int half = lane & 1;  // a round's scales and ids: even lanes hold its first 16 tokens', odd ones its last
 
-    int done = 0;  // rounds that this warp has copied since the start: stage done % 2
+    int done = 0;  // rounds that this warp has computed since the start: stage done % kStages
     for (;;) {
         const int L = length(b);
         const int unit_rounds = max(1, (L + kTok - 1) / kTok);
@@ -274,14 +274,15 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         };
 
         const int my_rounds = L > 0 ? (r1 - r0 - warp + kWarps - 1) / kWarps : 0;  // rounds r0 + warp, + kWarps, ...
-        int id = -1, id1 = -1;  // block of the round to compute and of the next one
-        if (my_rounds > 0) {
-            id = fetch_id(0);
-            issue(0, done & 1, id);
-        }
+        // blocks of this and the next kStages rounds; kStages - 1 rounds are on their way while one is computed
+        int id[kStages + 1];
+#pragma unroll
+        for (int n = 0; n <= kStages; ++n) id[n] = n < my_rounds ? fetch_id(n) : -1;
+#pragma unroll
+        for (int n = 0; n < kStages - 1; ++n)
+            if (n < my_rounds) issue(n, (done + n) % kStages, id[n]);
         // a zero limit tests the first copy at once, while it cannot be done: the way to the timeout path
-        const bool first_ok = A.wait_limit > 0 || my_rounds == 0 || mbar_test(mbar_addr(done & 1), (done >> 1) & 1);
-        if (my_rounds > 1) id1 = fetch_id(1);
+        const bool first_ok = A.wait_limit > 0 || my_rounds == 0 || mbar_test(mbar_addr(done % kStages), (done / kStages) & 1);
 
         // query fragments (B operand of the score product): column `row`, coordinates 32 s + 4 quad (+ 16)
         uint32_t qh[KS][2], ql[KS][2];
@@ -344,24 +345,19 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         float l_run[2] = {0.f, 0.f};              // this lane's tokens' share of the denominators
 
         auto scale_of = [&](const float *p, int blk) -> float { return good(blk) ? __ldg(p + record(blk)) : 0.f; };
-        float ks = scale_of(A.k_scales, id), vs = scale_of(A.v_scales, id);  // of this lane's half of the round
+        float ks = scale_of(A.k_scales, id[0]), vs = scale_of(A.v_scales, id[0]);  // of this lane's half of the round
         for (int c = 0; c < my_rounds; ++c, ++done) {
-            const int st = done & 1;
+            const int st = done % kStages;
             __syncwarp();  // every lane is done with the stage the next copy overwrites
-            float ks1 = 0.f, vs1 = 0.f;
-            int id2 = -1;
-            if (c + 1 < my_rounds) {
-                issue(c + 1, st ^ 1, id1);
-                ks1 = scale_of(A.k_scales, id1);
-                vs1 = scale_of(A.v_scales, id1);
-                if (c + 2 < my_rounds) id2 = fetch_id(c + 2);
-            }
+            if (c + kStages - 1 < my_rounds) issue(c + kStages - 1, (done + kStages - 1) % kStages, id[kStages - 1]);
+            const float ks1 = scale_of(A.k_scales, id[1]), vs1 = scale_of(A.v_scales, id[1]);
+            const int id_new = c + kStages + 1 < my_rounds ? fetch_id(c + kStages + 1) : -1;
             const float lvl = log2_scale(vs);
             const float downl = fast_exp2(kLShift - kPShift - lvl);
             const int t = round_tok(c);
-            const unsigned okm = __ballot_sync(0xffffffffu, good(id));
+            const unsigned okm = __ballot_sync(0xffffffffu, good(id[0]));
             {
-                const uint32_t par = (done >> 1) & 1;
+                const uint32_t par = (done / kStages) & 1;
                 bool ok = true;
                 if (A.wait_limit <= 0) {
                     ok = c == 0 ? first_ok : mbar_test(mbar_addr(st), par);
@@ -376,8 +372,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
                         atomicOr(A.status, TQ_DEVERR_TIMEOUT);
                         *cta_abort = 1;
                     }
-                    drain(st, par);
-                    if (c + 1 < my_rounds) drain(st ^ 1, ((done + 1) >> 1) & 1);
+                    for (int n = 0; n < kStages && c + n < my_rounds; ++n) drain((done + n) % kStages, ((done + n) / kStages) & 1);
                     break;
                 }
             }
@@ -482,8 +477,9 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             }
             ks = ks1;
             vs = vs1;
-            id = id1;
-            id1 = id2;
+#pragma unroll
+            for (int n = 0; n < kStages; ++n) id[n] = id[n + 1];
+            id[kStages] = id_new;
         }
         __syncthreads();  // every warp is done with the stages before they hold merge data
         const bool dead = *cta_abort != 0;
