@@ -40,6 +40,7 @@ struct AppendArgs {
     void *k_pool, *v_pool;
     float *k_scales, *v_scales;
     unsigned *status;
+    bool small;                    // query rows are counted in 32 bits
 };
 
 // First coordinates of a unit's two 8-wide chunks.
@@ -110,41 +111,52 @@ __device__ __forceinline__ void turn_unit(float (&a)[8], float (&b)[8], const Tu
     }
 }
 
-// Whether token t is written: its slot lies in the pool and its position in the table.
+// Whether a token is written: its slot lies in the pool and its position in the table.
 // One caller per token reports what is wrong.
-__device__ __forceinline__ bool token_ok(const AppendArgs &A, int64_t t, int64_t slot, int64_t &pos, bool report)
+__device__ __forceinline__ bool token_ok(const AppendArgs &A, int64_t slot, int64_t pos, bool report)
 {
-    pos = 0;
     if (slot < 0) return false;
     if (slot >= A.num_slots) {
         if (report) atomicOr(A.status, TQ_DEVERR_SLOT_RANGE);
         return false;
     }
-    if (A.r) {
-        pos = __ldg(A.positions + t);
-        if (pos < 0 || pos >= A.rope_rows) {
-            if (report) atomicOr(A.status, TQ_DEVERR_POSITION);
-            return false;
-        }
+    if (A.r && (pos < 0 || pos >= A.rope_rows)) {
+        if (report) atomicOr(A.status, TQ_DEVERR_POSITION);
+        return false;
     }
     return true;
 }
 
-// Rows row0, row0 + step, ... of one token: the Hq query rows and, with KV, the key and
-// value rows, into q_out and the bf16 pools.  A thread keeps one unit of every row it takes, so
-// the token's cosines and sines are loaded once.
-template <int D, bool KV>
+// One unit of a row, rotated by tn where `turn`, to bf16.
+__device__ __forceinline__ void put_unit(uint16_t *dst, int j0, int j1, uint4 wa, uint4 wb, bool turn, const Turn &tn,
+                                         int interleaved)
+{
+    if (turn) {
+        float a[8], b[8];
+        unpack8(wa, a);
+        unpack8(wb, b);
+        turn_unit(a, b, tn, interleaved);
+        wa = pack8(a);
+        wb = pack8(b);
+    }
+    *reinterpret_cast<uint4 *>(dst + j0) = wa;
+    *reinterpret_cast<uint4 *>(dst + j1) = wb;
+}
+
+// Rows row0, row0 + step, ... of one token, its query, key and value rows, into q_out and the bf16 pools.  A thread keeps
+// one unit of every row it takes, so the token's cosines and sines are loaded once.
+template <int D>
 __device__ __forceinline__ void token_rows(const AppendArgs &A, int64_t t, int row0, int step, int u)
 {
-    const int64_t slot = __ldg(A.slots + t);
-    int64_t pos;
-    if (!token_ok(A, t, slot, pos, row0 == 0 && u == 0)) return;
-    const bool pair = u < A.r / kUnit;
+    const int64_t slot = ld_pinned_s64(A.slots + t);
+    const int64_t pos = A.r ? ld_pinned_s64(A.positions + t) : 0;
+    const int rows = A.Hq + 2 * A.Hkv;
     int j0, j1;
     unit_chunks(u, A.r, A.interleaved, j0, j1);
+    if (!token_ok(A, slot, pos, row0 == 0 && u == 0)) return;
+    const bool pair = u < A.r / kUnit;
     Turn tn{};
     if (pair) tn = load_turn(A.rope + pos * A.r, u, A.r);
-    const int rows = A.Hq + (KV ? 2 * A.Hkv : 0);
     const int64_t blk = slot >> A.pshift;
     const int o = static_cast<int>(slot & (A.P - 1));
     auto source = [&](int row) -> const uint16_t * {
@@ -164,18 +176,9 @@ __device__ __forceinline__ void token_rows(const AppendArgs &A, int64_t t, int r
             dst = pool + ((blk * A.Hkv + (val ? hk - A.Hkv : hk)) * A.P + o) * D;
             turn = pair && !val;
         }
-        if (turn) {
-            float a[8], b[8];
-            unpack8(wa, a);
-            unpack8(wb, b);
-            turn_unit(a, b, tn, A.interleaved);
-            wa = pack8(a);
-            wb = pack8(b);
-        }
-        *reinterpret_cast<uint4 *>(dst + j0) = wa;
-        *reinterpret_cast<uint4 *>(dst + j1) = wb;
+        put_unit(dst, j0, j1, wa, wb, turn, tn, A.interleaved);
     };
-    for (int row = row0; row < rows; row += 2 * step) {
+    for (int row = row0; row < rows; row += 2 * step) {  // two rows on their way at a time
         const bool two = row + step < rows;
         const uint16_t *s0 = source(row), *s1 = source(two ? row + step : row);
         const uint4 a0 = ld_pinned(s0 + j0), b0 = ld_pinned(s0 + j1);
@@ -189,13 +192,45 @@ __device__ __forceinline__ void token_rows(const AppendArgs &A, int64_t t, int r
     }
 }
 
+// The query rows alone: thread i's unit of rows r, r + n, r + 2 n and r + 3 n of token i / n, r = i % n, n = ceil(Hq / 4).
+// All of them are on their way with the token's slot and position, and share its cosines and sines.
+constexpr int kQueryRows = 4;
+template <int D>
+__device__ __forceinline__ void query_rows(const AppendArgs &A, int64_t i, int u)
+{
+    const int n = (A.Hq + kQueryRows - 1) / kQueryRows;
+    const int64_t t = A.small ? static_cast<uint32_t>(i) / static_cast<uint32_t>(n) : i / n;
+    if (t >= A.T) return;
+    const int r = static_cast<int>(i - t * n);
+    int j0, j1;
+    unit_chunks(u, A.r, A.interleaved, j0, j1);
+    const uint16_t *src = A.q + t * A.qs + static_cast<int64_t>(r) * D;
+    uint4 w[kQueryRows][2];
+#pragma unroll
+    for (int k = 0; k < kQueryRows; ++k)
+        if (r + k * n < A.Hq) {
+            w[k][0] = ld_pinned(src + k * n * D + j0);
+            w[k][1] = ld_pinned(src + k * n * D + j1);
+        }
+    const int64_t slot = ld_pinned_s64(A.slots + t);
+    const int64_t pos = A.r ? ld_pinned_s64(A.positions + t) : 0;
+    if (!token_ok(A, slot, pos, false)) return;  // what is wrong is reported with the pages
+    Turn tn{};
+    const bool pair = u < A.r / kUnit;
+    if (pair) tn = load_turn(A.rope + pos * A.r, u, A.r);
+    uint16_t *dst = A.q_out + (t * A.Hq + r) * D;
+#pragma unroll
+    for (int k = 0; k < kQueryRows; ++k)
+        if (r + k * n < A.Hq) put_unit(dst + k * n * D, j0, j1, w[k][0], w[k][1], pair, tn, A.interleaved);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const AppendArgs A)
 {
     constexpr int U = D / kUnit;           // units of a row
     constexpr int RL = kThreads / U;       // rows in flight
     const int u = threadIdx.x % U, rl = threadIdx.x / U;
-    token_rows<D, true>(A, blockIdx.x, blockIdx.y * RL + rl, RL * gridDim.y, u);
+    token_rows<D>(A, blockIdx.x, blockIdx.y * RL + rl, RL * gridDim.y, u);
 }
 
 __device__ __forceinline__ float pow2_scale(float amax)
@@ -242,28 +277,34 @@ __device__ __forceinline__ float finite_abs(float x)
     return a <= 3.402823466e38f ? a : 0.f;
 }
 
-// Query rows of a token (blocks below q_blocks), then the pages: a block takes the
-// runs (consecutive tokens on consecutive slots of one page) that begin among its
-// `chunk` tokens, threads 0-127 their keys, 128-255 their values.
-template <int D, int UP>
-__global__ void __launch_bounds__(kThreads) append_fp8_kernel(const AppendArgs A, const int q_blocks, const int chunk)
+// kv_blocks blocks (gridDim.y of each over the heads) for the pages, then blocks for the query rows.
+//
+// A block finds the runs (consecutive tokens on consecutive slots of one page) that begin among its `chunk` tokens; groups
+// of its warps take items (run, kv head, keys or values) in turn.  A page's scale needs its rows twice, for the maximum
+// and for the codes: a group has one, two or four warps, so that each lane holds four units, rotated, in registers
+// between, and only a group of several meets at a barrier of its own.
+template <int D, int P>
+__global__ void __launch_bounds__(kThreads, 2)
+    append_fp8_kernel(const AppendArgs A, const int kv_blocks, const int chunk)
 {
     constexpr int U = D / kUnit;
-    if (blockIdx.x < q_blocks) {
+    constexpr int NK = 4;                       // units of an item per lane: the lane's unit of rows row0, row0 + kRowStep, ...
+    constexpr int W = P * U / (32 * NK);        // warps of a group
+    constexpr int kGroups = kThreads / 32 / W;
+    constexpr int kRowStep = 32 * W / U;
+    if (blockIdx.x >= kv_blocks) {
         constexpr int RL = kThreads / U;
-        const int per = gridDim.y;
-        token_rows<D, false>(A, blockIdx.x, blockIdx.y * RL + threadIdx.x / U, RL * per, threadIdx.x % U);
+        const int64_t i = (static_cast<int64_t>(blockIdx.x - kv_blocks) * gridDim.y + blockIdx.y) * RL;
+        query_rows<D>(A, i + threadIdx.x / U, threadIdx.x % U);
         return;
     }
-    constexpr int kHalf = kThreads / 2;
-    constexpr int kMaxChunk = 16;
+    constexpr int kMaxChunk = 32;
     __shared__ int64_t win[kWindow + kMaxChunk + kWindow];
-    __shared__ float red[kThreads / 32];
-    __shared__ int s_len[kMaxChunk];
-    const int tid = threadIdx.x;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x - q_blocks) * chunk;
-    const int P = A.P;
-    for (int i = tid; i < 2 * kWindow + chunk; i += kThreads) {
+    __shared__ int s_at[kMaxChunk], s_len[kMaxChunk], s_runs;
+    __shared__ float s_max[kGroups][2][W];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
+    for (int i = tid; i < 2 * kWindow + kMaxChunk; i += kThreads) {
         const int64_t t = t0 - kWindow + i;
         int64_t s = (t >= 0 && t < A.T) ? __ldg(A.slots + t) : -1;
         if (s >= A.num_slots) {
@@ -273,106 +314,109 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(const AppendArgs A
         win[i] = s;
     }
     __syncthreads();
-    if (tid < chunk) {  // length of the run that begins at this token, 0 where none does
-        const int64_t *w = win + kWindow + tid;
-        const int64_t s = w[0];
-        int len = 0;
-        if (s >= 0 && !((s & (P - 1)) != 0 && w[-1] == s - 1)) {
-            const int64_t page = s >> A.pshift;
-            bool clash = false;
-            for (int i = 1; i <= kWindow; ++i) clash |= w[-i] >= 0 && (w[-i] >> A.pshift) == page;
-            if (clash) {
-                if (blockIdx.y == 0) atomicOr(A.status, TQ_DEVERR_SLOT_ORDER);
-            } else {
-                const int most = P - static_cast<int>(s & (P - 1));
-                len = 1;
-                while (len < most && w[len] == s + len) ++len;
+    if (warp == 0) {
+        // lane i: token i of the chunk and the one 32 on; a token continues a run where its slot follows the one before
+        const int64_t *w = win + kWindow + lane;
+        const int64_t v = w[0], ahead = w[32];
+        const bool more = v >= 0 && v == w[-1] + 1 && (v & (P - 1));
+        const uint64_t cont = __ballot_sync(0xffffffffu, more) |
+                              static_cast<uint64_t>(__ballot_sync(0xffffffffu, ahead >= 0 && ahead == w[31] + 1 && (ahead & (P - 1)))) << 32;
+        unsigned starts = __ballot_sync(0xffffffffu, lane < chunk && v >= 0 && !more);
+        const int len = __ffsll(~(cont >> lane >> 1));  // the run that begins here: this token and those that continue it
+        for (unsigned left = starts; left; left &= left - 1) {
+            const int i = __ffs(left) - 1;
+            const int64_t page = __shfl_sync(0xffffffffu, v, i) / P, other = win[kWindow + i - 1 - lane];
+            if (__any_sync(0xffffffffu, other >= 0 && other / P == page)) {  // the page stands earlier in the call, too
+                starts &= ~(1u << i);
+                if (lane == 0 && blockIdx.y == 0) atomicOr(A.status, TQ_DEVERR_SLOT_ORDER);
             }
         }
-        s_len[tid] = len;
+        if (starts >> lane & 1u) {
+            const int n = __popc(starts & ((1u << lane) - 1u));
+            s_at[n] = lane;
+            s_len[n] = len;
+        }
+        if (lane == 0) s_runs = __popc(starts);
     }
     __syncthreads();
-    const bool val = tid >= kHalf;
-    const int ht = tid & (kHalf - 1);
-    const uint16_t *src = val ? A.v : A.k;
-    const int64_t stride = val ? A.vs : A.ks;
-    unsigned char *pool = static_cast<unsigned char *>(val ? A.v_pool : A.k_pool);
-    float *scales = val ? A.v_scales : A.k_scales;
-    for (int c = 0; c < chunk; ++c) {
-        const int len = s_len[c];
-        if (len == 0) continue;
-        const int64_t t = t0 + c, slot = win[kWindow + c], page = slot >> A.pshift;
+    const int group = warp / W, gl = tid % (32 * W);
+    const int u = gl % U, row0 = gl / U;
+    int j0, j1;
+    unit_chunks(u, A.r, A.interleaved, j0, j1);
+    const int gy = static_cast<int>(gridDim.y);
+    const int heads = (A.Hkv - static_cast<int>(blockIdx.y) + gy - 1) / gy;
+    int flip = 0;
+    for (int it = group; it < 2 * heads * s_runs; it += kGroups, flip ^= 1) {
+        const int run = it / (2 * heads), x = it - run * (2 * heads);
+        const bool val = x >= heads;
+        const int h = static_cast<int>(blockIdx.y) + (val ? x - heads : x) * gy;
+        const int len = s_len[run];
+        const int64_t t = t0 + s_at[run], slot = win[kWindow + s_at[run]];
         const int o = static_cast<int>(slot & (P - 1));
-        for (int h = blockIdx.y; h < A.Hkv; h += gridDim.y) {
-            const int64_t rec = page * A.Hkv + h;
-            const float old = o > 0 ? scales[rec] : 0.f;
-            uint4 wa[UP], wb[UP];
-            bool live[UP];
-            int64_t pos[UP];
+        const int64_t rec = slot / P * A.Hkv + h;
+        const int64_t stride = val ? A.vs : A.ks;
+        const uint16_t *src = (val ? A.v : A.k) + t * stride + static_cast<int64_t>(h) * D;
+        float *scale_at = (val ? A.v_scales : A.k_scales) + rec;
+        unsigned char *base = static_cast<unsigned char *>(val ? A.v_pool : A.k_pool) + rec * P * D;
+        const bool pair = !val && u < A.r / kUnit;
+        uint4 wa[NK], wb[NK];
+        int64_t pos[NK];
 #pragma unroll
-            for (int i = 0; i < UP; ++i) {
-                const int e = ht + i * kHalf, row = e / U, u = e % U;
-                pos[i] = 0;
-                live[i] = row < len;
-                if (live[i] && A.r) {
-                    pos[i] = __ldg(A.positions + t + row);
-                    if (pos[i] < 0 || pos[i] >= A.rope_rows) {
-                        if (u == 0 && h == 0 && !val) atomicOr(A.status, TQ_DEVERR_POSITION);
-                        live[i] = false;
-                    }
-                }
-                if (live[i]) {
-                    int j0, j1;
-                    unit_chunks(u, A.r, A.interleaved, j0, j1);
-                    const uint16_t *p = src + (t + row) * stride + static_cast<int64_t>(h) * D;
-                    wa[i] = ld_pinned(p + j0);
-                    wb[i] = ld_pinned(p + j1);
-                }
+        for (int n = 0; n < NK; ++n) {
+            const int row = row0 + n * kRowStep;
+            pos[n] = -1;
+            if (row < len) {
+                wa[n] = ld_pinned(src + row * stride + j0);
+                wb[n] = ld_pinned(src + row * stride + j1);
+                pos[n] = A.r ? ld_pinned_s64(A.positions + t + row) : 0;
             }
-            float a[UP][8], b[UP][8];
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < UP; ++i) {
-                if (!live[i]) continue;
-                const int u = (ht + i * kHalf) % U;
-                unpack8(wa[i], a[i]);
-                unpack8(wb[i], b[i]);
-                if (!val && u < A.r / kUnit)
-                    turn_unit(a[i], b[i], load_turn(A.rope + pos[i] * A.r, u, A.r), A.interleaved);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(finite_abs(a[i][j]), finite_abs(b[i][j])));
-            }
-            amax = warp_max(amax);
-            __syncthreads();  // the last pass's readers of `red` are done
-            if ((tid & 31) == 0) red[tid >> 5] = amax;
-            __syncthreads();
-            const float *rw = red + (val ? kHalf / 32 : 0);
-            amax = fmaxf(fmaxf(rw[0], rw[1]), fmaxf(rw[2], rw[3]));
-            const float need = pow2_scale(amax);
-            const bool keep = o > 0 && old > 0.f && old <= 3.402823466e38f;  // the page's rows and scale so far
-            const float scale = keep ? fmaxf(old, need) : need;
-            const float inv = 1.f / scale;
-            unsigned char *base = pool + rec * P * D;
-            if (keep && scale > old) {  // code the earlier rows anew
-                const float ratio = old * inv;
-                for (int e = ht; e < o * (D / 16); e += kHalf) {
-                    uint4 *p = reinterpret_cast<uint4 *>(base) + e;
-                    const uint4 w = *p;
-                    *p = make_uint4(recode4(w.x, ratio), recode4(w.y, ratio), recode4(w.z, ratio), recode4(w.w, ratio));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < UP; ++i) {
-                if (!live[i]) continue;
-                const int e = ht + i * kHalf, row = e / U, u = e % U;
-                int j0, j1;
-                unit_chunks(u, A.r, A.interleaved, j0, j1);
-                unsigned char *p = base + static_cast<int64_t>(o + row) * D;
-                *reinterpret_cast<uint2 *>(p + j0) = codes8(a[i], inv);
-                *reinterpret_cast<uint2 *>(p + j1) = codes8(b[i], inv);
-            }
-            if (ht == 0 && !(keep && scale == old)) scales[rec] = scale;
         }
+        const float old = o > 0 ? *scale_at : 0.f;
+        float a[NK][8], b[NK][8];
+        float amax = 0.f;
+        unsigned live = 0;  // units that are written
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+            if (row0 + n * kRowStep >= len) continue;
+            if (A.r && (pos[n] < 0 || pos[n] >= A.rope_rows)) {
+                if (h == 0 && !val && u == 0) atomicOr(A.status, TQ_DEVERR_POSITION);
+                continue;
+            }
+            live |= 1u << n;
+            unpack8(wa[n], a[n]);
+            unpack8(wb[n], b[n]);
+            if (pair) turn_unit(a[n], b[n], load_turn(A.rope + pos[n] * A.r, u, A.r), A.interleaved);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = max3(amax, finite_abs(a[n][j]), finite_abs(b[n][j]));
+        }
+        amax = warp_max(amax);
+        if constexpr (W > 1) {
+            if (lane == 0) s_max[group][flip][warp % W] = amax;
+            // two sets, so that the next item's do not wait for this one's readers
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
+#pragma unroll
+            for (int k = 0; k < W; ++k) amax = fmaxf(amax, s_max[group][flip][k]);
+        }
+        const float need = pow2_scale(amax);
+        const bool keep = o > 0 && old > 0.f && old <= 3.402823466e38f;  // the page's rows and scale so far
+        const float scale = keep ? fmaxf(old, need) : need;
+        const float inv = 1.f / scale;
+        if (keep && scale > old) {  // code the earlier rows anew
+            const float ratio = old * inv;
+            for (int e = gl; e < o * (D / 16); e += 32 * W) {
+                uint4 *p = reinterpret_cast<uint4 *>(base) + e;
+                const uint4 w = *p;
+                *p = make_uint4(recode4(w.x, ratio), recode4(w.y, ratio), recode4(w.z, ratio), recode4(w.w, ratio));
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+            if (live >> n & 1u) {
+                unsigned char *p = base + (o + row0 + n * kRowStep) * D;
+                *reinterpret_cast<uint2 *>(p + j0) = codes8(a[n], inv);
+                *reinterpret_cast<uint2 *>(p + j1) = codes8(b[n], inv);
+            }
+        if (gl == 0 && !(keep && scale == old)) *scale_at = scale;
     }
 }
 
@@ -387,18 +431,26 @@ cudaError_t launch_bf16(const AppendArgs &a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_fp8(const AppendArgs &a, cudaStream_t st)
+template <int D, int P>
+cudaError_t launch_fp8(const AppendArgs &a, int num_sms, cudaStream_t st)
 {
-    // few tokens: every token may begin a page's run, so a block each; many: 16 tokens,
-    // among which about one run begins
-    const int chunk = a.T < 1024 ? 1 : 16;
-    const int q_blocks = a.Hq ? static_cast<int>(a.T) : 0;
-    const unsigned gy = static_cast<unsigned>(a.Hkv < 65535 ? a.Hkv : 65535);
-    const dim3 grid(static_cast<unsigned>(q_blocks + (a.T + chunk - 1) / chunk), gy);
-    if (a.P == 16) append_fp8_kernel<D, 16 * (D / kUnit) / (kThreads / 2)><<<grid, kThreads, 0, st>>>(a, q_blocks, chunk);
-    else append_fp8_kernel<D, 32 * (D / kUnit) / (kThreads / 2)><<<grid, kThreads, 0, st>>>(a, q_blocks, chunk);
+    // Few tokens: every one may begin a page's run, so a block for each.  Many: a page's rows of tokens per block (about
+    // one run begins among them).  A block takes two to eight items at a time, so further blocks over the heads only
+    // where there would be fewer than eight blocks an SM.
+    const int chunk = a.T < 1024 ? 1 : P;
+    const int64_t kv = (a.T + chunk - 1) / chunk;
+    const int64_t want = (8LL * num_sms + kv - 1) / kv, most = (2LL * a.Hkv + 7) / 8;
+    const int gy = static_cast<int>(want < most ? want : most < 65535 ? most : 65535);
+    const int64_t per = static_cast<int64_t>(kThreads / (D / kUnit)) * gy;
+    const int64_t q = (a.T * ((a.Hq + kQueryRows - 1) / kQueryRows) + per - 1) / per;
+    append_fp8_kernel<D, P><<<dim3(static_cast<unsigned>(kv + q), gy), kThreads, 0, st>>>(a, static_cast<int>(kv), chunk);
     return cudaGetLastError();
+}
+
+cudaError_t launch_fp8(const AppendArgs &a, int d, int num_sms, cudaStream_t st)
+{
+    if (d == 128) return a.P == 16 ? launch_fp8<128, 16>(a, num_sms, st) : launch_fp8<128, 32>(a, num_sms, st);
+    return a.P == 16 ? launch_fp8<256, 16>(a, num_sms, st) : launch_fp8<256, 32>(a, num_sms, st);
 }
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -445,6 +497,7 @@ tq_status check(const char *who, tq_handle h, AppendArgs *a, int64_t num_blocks,
     a->pshift = a->P == 16 ? 4 : 5;
     a->num_slots = num_blocks * a->P;
     a->status = c.status;
+    a->small = a->T * a->Hq < (int64_t(1) << 31);
     *run = true;
     return TQ_OK;
 }
@@ -461,7 +514,7 @@ extern "C" tq_status tq_append_kv_bf16(tq_handle h, const uint16_t *q, const uin
 {
     tq::AppendArgs a{q, k, v, T, num_q_heads, num_kv_heads, q_stride_tok, k_stride_tok, v_stride_tok, positions, rope,
                      rope_rows, rot_dim, 0, slot_mapping, page_size, 0, 0, q_out, k_pool, v_pool, nullptr, nullptr,
-                     nullptr};
+                     nullptr, false};
     bool run;
     const tq_status s = tq::check("tq_append_kv_bf16", h, &a, num_blocks, style, 2, &run);
     if (s != TQ_OK || !run) return s;
@@ -480,7 +533,7 @@ extern "C" tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint
 {
     tq::AppendArgs a{q, k, v, T, num_q_heads, num_kv_heads, q_stride_tok, k_stride_tok, v_stride_tok, positions, rope,
                      rope_rows, rot_dim, 0, slot_mapping, page_size, 0, 0, q_out, k_pool, v_pool, k_scales, v_scales,
-                     nullptr};
+                     nullptr, false};
     bool run;
     const tq_status s = tq::check("tq_append_kv_fp8", h, &a, num_blocks, style, 1, &run);
     if (s != TQ_OK || !run) return s;
@@ -488,7 +541,8 @@ extern "C" tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint
     if (!tq::aligned(k_scales, 4) || !tq::aligned(v_scales, 4))
         return tq::api_error(TQ_ERR_INVALID_ARG, "tq_append_kv_fp8: misaligned pointer");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = tq::handle_codec(h).d == 128 ? tq::launch_fp8<128>(a, st) : tq::launch_fp8<256>(a, st);
+    const tq::Codec &c = tq::handle_codec(h);
+    const cudaError_t e = tq::launch_fp8(a, c.d, c.num_sms, st);
     if (e != cudaSuccess) return tq::api_error(TQ_ERR_CUDA, "tq_append_kv_fp8: launch: %s", cudaGetErrorString(e));
     return TQ_OK;
 }

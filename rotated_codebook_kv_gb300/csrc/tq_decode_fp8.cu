@@ -33,6 +33,7 @@ using namespace fp8;
 
 constexpr int kTok = 32;                  // tokens of a warp's round
 constexpr int kBoxBytes = kTok * 128;     // one 128-byte-wide column block of a round
+constexpr int kUnitCost = 8;               // what a unit costs beside its rounds, in rounds (queries, first copies, merge)
 constexpr float kPShift = 8.f;            // probabilities enter the product as 2^8 p <= 256
 
 template <int D>
@@ -92,7 +93,10 @@ __device__ __forceinline__ bool mbar_try(uint32_t mb, uint32_t par)
     return done != 0;
 }
 
-// The first `n` sequences' rounds, summed, and the longest one's, by the whole block.
+// Size of a unit of L tokens when work is dealt out: its rounds and what it costs beside them.
+__device__ __forceinline__ int unit_size(int L) { return L > 0 ? (L + kTok - 1) / kTok + kUnitCost : 0; }
+
+// The sequences' sizes, summed, and the longest one's, by the whole block.
 template <int THREADS>
 __device__ __forceinline__ void count_rounds(const Args &A, long long *s_sum, int *s_max, long long &total, int &longest)
 {
@@ -101,7 +105,7 @@ __device__ __forceinline__ void count_rounds(const Args &A, long long *s_sum, in
     for (int b = threadIdx.x; b < A.B; b += THREADS) {
         const int L = A.seq_lens[b];
         if (L > A.max_blocks * A.P && blockIdx.x == 0) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
-        const int r = (min(max(L, 0), A.max_blocks * A.P) + kTok - 1) / kTok;
+        const int r = unit_size(min(max(L, 0), A.max_blocks * A.P));
         sum += r;
         mx = max(mx, r);
     }
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
 
-    // ---- this CTA's share: rounds [pos, end) of all units in a row, and the unit that it begins in ----
+    // ---- this CTA's share: [pos, end) of all units' sizes in a row, and the unit that it begins in ----
     long long pos, end, share, unit0;  // unit0: where the unit at hand begins
     int b, kvh;
     auto length = [&](int i) -> int { return min(max(A.seq_lens[i], 0), A.max_blocks * P); };
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         kvh = blockIdx.x % A.Hkv;
         if (kvh == 0 && tid == 0 && A.seq_lens[b] > A.max_blocks * P) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
         pos = unit0 = 0;
-        end = share = max(1, (length(b) + kTok - 1) / kTok);
+        end = share = max(1, unit_size(length(b)));
     } else {
         long long *s_sum = reinterpret_cast<long long *>(smem);
         int *s_max = reinterpret_cast<int *>(smem + 128);
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         total *= A.Hkv;
         // at least two rounds a warp, and no unit in more pieces than there are splits
         share = (total + gridDim.x - 1) / gridDim.x;
-        share = max(share, static_cast<long long>(2 * kWarps));
+        share = max(share, static_cast<long long>(2 * kWarps + kUnitCost));
         share = max(share, static_cast<long long>((longest + A.splits - 2) / (A.splits - 1)));
         pos = share * blockIdx.x;
         end = min(total, pos + share);
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         long long *s_u = reinterpret_cast<long long *>(smem + 200);
         b = 0;
         for (int b0 = 0;; b0 += kThreads) {
-            const long long r = b0 + tid < A.B ? static_cast<long long>((length(b0 + tid) + kTok - 1) / kTok) * A.Hkv : 0;
+            const long long r = b0 + tid < A.B ? static_cast<long long>(unit_size(length(b0 + tid))) * A.Hkv : 0;
             long long inc = r;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         }
         b = *s_b;
         unit0 = *s_u;
-        const int per = (length(b) + kTok - 1) / kTok;
+        const int per = unit_size(length(b));
         kvh = static_cast<int>((pos - unit0) / per);
         unit0 += static_cast<long long>(kvh) * per;
         __syncthreads();  // the stages may be written
@@ -231,8 +235,10 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     int done = 0;  // rounds that this warp has computed since the start: stage done % kStages
     for (;;) {
         const int L = length(b);
-        const int unit_rounds = max(1, (L + kTok - 1) / kTok);
-        const int r0 = static_cast<int>(pos - unit0), r1 = static_cast<int>(min(end, unit0 + unit_rounds) - unit0);
+        const int size = max(1, unit_size(L));
+        // a unit's rounds stand behind its cost: a share may end within that and hold none of them
+        const int r0 = max(0, static_cast<int>(pos - unit0) - kUnitCost);
+        const int r1 = max(0, static_cast<int>(min(end, unit0 + size) - unit0) - kUnitCost);
         auto col_row = [&](int c) -> size_t {  // output row of column c
             return (static_cast<size_t>(b) * A.Tq + c / G) * A.Hq + static_cast<size_t>(kvh) * G + c % G;
         };
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             }
         };
 
-        const int my_rounds = L > 0 ? (r1 - r0 - warp + kWarps - 1) / kWarps : 0;  // rounds r0 + warp, + kWarps, ...
+        const int my_rounds = r1 - r0 > warp ? (r1 - r0 - warp + kWarps - 1) / kWarps : 0;  // rounds r0 + warp, + kWarps, ...
         // blocks of this and the next kStages rounds; kStages - 1 rounds are on their way while one is computed
         int id[kStages + 1];
 #pragma unroll
@@ -508,7 +514,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         __syncthreads();
         // a unit's pieces are numbered from the CTA that holds its first round; a unit in one piece is done here
         const long long first = unit0 / share;
-        const int pieces = A.splits == 1 ? 1 : static_cast<int>((unit0 + unit_rounds - 1) / share - first) + 1;
+        const int pieces = A.splits == 1 ? 1 : static_cast<int>((unit0 + size - 1) / share - first) + 1;
         const int piece = A.splits == 1 ? 0 : static_cast<int>(blockIdx.x - first);
         if (piece == 0 && tid == 0 && A.splits > 1) A.pieces[static_cast<int64_t>(b) * A.Hkv + kvh] = pieces;
         const float downp = fast_exp2(-kPShift), ldown = fast_exp2(-kLShift);
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             }
         }
         // ---- the next unit of the share ----
-        pos = unit0 + unit_rounds;
+        pos = unit0 + size;
         unit0 = pos;
         if (pos >= end) return;
         if (++kvh == A.Hkv) {
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
         // the waits of a CTA that gave up are not in step with its stages any more: its other units count as unseen
         if (dead) {
             for (;;) {
-                const int n = (length(b) + kTok - 1) / kTok;
+                const int n = unit_size(length(b));
                 const long long f0 = unit0 / share;
                 const int np = static_cast<int>((unit0 + n - 1) / share - f0) + 1;
                 if (blockIdx.x == f0 && tid == 0) A.pieces[static_cast<int64_t>(b) * A.Hkv + kvh] = np;
@@ -583,43 +589,97 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
 }
 
 // Merges the pieces of an output row: o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.
-// One warp per row, D / 32 coordinates per lane; a piece that saw nothing (l = 0) has
-// no partial to read.  A NaN of any piece stays one.  `pieces`: how many each (sequence, kv head) has, where its CTAs
-// chose; a unit in one piece is done, an empty sequence gives zeros.  NULL: A.splits.
+// A block per row: D / 4 threads side by side over the coordinates, 512 / D groups of them over the pieces, so that a
+// row's partials are all on their way at once.  A piece that saw nothing (l = 0) has no partial to read.  A NaN of any
+// piece stays one.  A unit in one piece is done, an empty sequence gives zeros.
 template <int D>
-__global__ void __launch_bounds__(128) merge_fp8_kernel(const Args A, const int64_t rows, const int *__restrict__ pieces)
+__global__ void __launch_bounds__(128) merge_fp8_kernel(const Args A, const int64_t rows)
+{
+    constexpr int TC = D / 4, GROUPS = 128 / TC;
+    __shared__ float s_w[1024];
+    __shared__ float s_part[GROUPS][D];
+    __shared__ float s_red[4], s_den;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x;
+    const int64_t b = row / A.Hq / A.Tq;
+    const int splits = A.seq_lens[b] > 0 ? A.pieces[b * A.Hkv + row % A.Hq / A.G] : 0;
+    if (splits == 1) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(A.ml);
+    float M = -INFINITY;
+    for (int s = tid; s < splits; s += 128) M = fmaxf(M, __ldg(ml + s * rows + row).x);
+    M = warp_max(M);
+    if (lane == 0) s_red[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+    const float ref = M == -INFINITY ? 0.f : M;
+    __syncthreads();
+    float den = 0.f;
+    for (int s = tid; s < splits; s += 128) {
+        const float2 v = __ldg(ml + s * rows + row);
+        const float w = v.y == 0.f ? 0.f : (v.x == -INFINITY ? 1.f : fast_exp2(v.x - ref));
+        s_w[s] = v.y == 0.f ? -1.f : w;  // -1: nothing to read
+        den += v.y == 0.f ? 0.f : w * v.y;
+    }
+    den = warp_sum(den);
+    if (lane == 0) s_red[warp] = den;
+    __syncthreads();
+    if (tid == 0) s_den = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+    const int col = 4 * (tid % TC);
+    float4 n = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = tid / TC; s < splits; s += GROUPS) {
+        const float w = s_w[s];
+        if (w == -1.f) continue;
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(A.acc + (s * rows + row) * D + col));
+        n.x = fmaf(w, v.x, n.x);
+        n.y = fmaf(w, v.y, n.y);
+        n.z = fmaf(w, v.z, n.z);
+        n.w = fmaf(w, v.w, n.w);
+    }
+    *reinterpret_cast<float4 *>(&s_part[tid / TC][col]) = n;
+    __syncthreads();
+    const float inv = s_den == 0.f ? 0.f : 1.f / s_den;
+    for (int j = 2 * tid; j < D; j += 256) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            x += s_part[g][j];
+            y += s_part[g][j + 1];
+        }
+        reinterpret_cast<uint32_t *>(A.out + row * D)[j / 2] =
+            float_to_bf16_bits(x * inv) | (static_cast<uint32_t>(float_to_bf16_bits(y * inv)) << 16);
+    }
+}
+
+// The same for many rows in few pieces (prefill): a warp per row, D / 32 coordinates a lane, every row in A.splits pieces.
+template <int D>
+__global__ void __launch_bounds__(128) merge_rows_fp8_kernel(const Args A, const int64_t rows)
 {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
-    const float *ml = A.ml, *acc = A.acc;
-    int splits = A.splits;
-    if (pieces) {
-        const int64_t b = row / A.Hq / A.Tq;
-        splits = A.seq_lens[b] > 0 ? pieces[b * A.Hkv + row % A.Hq / A.G] : 0;
-        if (splits == 1) return;
-    }
+    const float2 *ml = reinterpret_cast<const float2 *>(A.ml);
     float M = -INFINITY;
-    for (int s = lane; s < splits; s += 32) M = fmaxf(M, __ldg(ml + (s * rows + row) * 2));
+    for (int s = lane; s < A.splits; s += 32) M = fmaxf(M, __ldg(ml + s * rows + row).x);
     M = warp_max(M);
     const float ref = M == -INFINITY ? 0.f : M;
     float n[E] = {}, den = 0.f;
-    for (int s0 = 0; s0 < splits; s0 += 32) {
+    for (int s0 = 0; s0 < A.splits; s0 += 32) {
         float w = 0.f, l = 0.f;
-        if (s0 + lane < splits) {
-            const float2 v = __ldg(reinterpret_cast<const float2 *>(ml) + (s0 + lane) * rows + row);
+        if (s0 + lane < A.splits) {
+            const float2 v = __ldg(ml + (s0 + lane) * rows + row);
             l = v.y;
             w = v.y == 0.f ? 0.f : (v.x == -INFINITY ? 1.f : fast_exp2(v.x - ref));
         }
         den += warp_sum(l == 0.f ? 0.f : w * l);
         const unsigned some = __ballot_sync(0xffffffffu, l != 0.f);
-        const int k1 = min(32, splits - s0);
+        const int k1 = min(32, A.splits - s0);
 #pragma unroll 4
         for (int k = 0; k < k1; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
             if (!(some >> k & 1u)) continue;
-            const float *p = acc + ((s0 + k) * rows + row) * D + lane * E;
+            const float *p = A.acc + ((s0 + k) * rows + row) * D + lane * E;
 #pragma unroll
             for (int i = 0; i < E; i += 4) {
                 const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
@@ -663,7 +723,8 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, 
     }
     if (e != cudaSuccess || a.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.Tq * a.Hq;
-    merge_fp8_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a, rows, tc ? nullptr : a.pieces);
+    if (tc) merge_rows_fp8_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a, rows);
+    else merge_fp8_kernel<D><<<static_cast<unsigned>(rows), 128, 0, st>>>(a, rows);
     return cudaGetLastError();
 }
 

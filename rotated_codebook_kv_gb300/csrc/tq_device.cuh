@@ -69,6 +69,13 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Asynchronous prefetch of [p, p + bytes) into L2 by the bulk-copy engine; no
 // registers or shared memory are held.  p and bytes must be multiples of 16
 // and the range must lie inside one allocation.

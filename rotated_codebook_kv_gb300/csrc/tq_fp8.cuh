@@ -61,13 +61,6 @@ __device__ __forceinline__ uint32_t e4m3x2(__half2 x)
     return c;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 __device__ __forceinline__ uint32_t e4m3x2(float x, float y)
 {
     uint16_t c;
