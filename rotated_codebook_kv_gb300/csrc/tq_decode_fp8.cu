@@ -651,7 +651,8 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args A, const int6
     }
 }
 
-// The same for many rows in few pieces (prefill): a warp per row, D / 32 coordinates a lane, every row in A.splits pieces.
+// The same for the prefill's rows, many in few pieces: a warp per row, D / 32 coordinates a lane; the rows of the first
+// A.whole units are done.
 template <int D>
 __global__ void __launch_bounds__(128) merge_rows_fp8_kernel(const Args A, const int64_t rows)
 {
@@ -659,6 +660,9 @@ __global__ void __launch_bounds__(128) merge_rows_fp8_kernel(const Args A, const
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
+    const int64_t t = row / A.Hq, b = t / A.Tq;
+    const int qt = static_cast<int>(t - b * A.Tq) / A.qpc, kvh = static_cast<int>(row - t * A.Hq) / A.G;
+    if ((b * A.Hkv + kvh) * A.nqt + A.nqt - 1 - qt < A.whole) return;
     const float2 *ml = reinterpret_cast<const float2 *>(A.ml);
     float M = -INFINITY;
     for (int s = lane; s < A.splits; s += 32) M = fmaxf(M, __ldg(ml + s * rows + row).x);
@@ -801,6 +805,8 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint8_t 
     a.sm_scale = sm_scale;
     a.splits = splits;
     a.pages_per_split = (max_blocks + splits - 1) / splits;
+    const int64_t units = static_cast<int64_t>(batch) * Hkv * a.nqt;
+    a.whole = tc && splits > 1 ? static_cast<int>(units / c.num_sms * c.num_sms) : 0;
     a.ml = static_cast<float *>(workspace);
     a.acc = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                       align256(static_cast<size_t>(splits) * rows * 2 * sizeof(float)));
@@ -861,9 +867,22 @@ extern "C" int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int n
         return tq_decode_splits_fp8(h, batch, num_kv_heads, max_blocks_per_seq, page_size);
     const int qpc = tq::fp8::prefill_tc_columns(tq::handle_codec(h).d) / G;
     const long long units = static_cast<long long>(batch) * num_kv_heads * ((q_tokens + qpc - 1) / qpc);
-    // one CTA per SM: about two waves, each split at least 512 tokens
+    // One CTA per SM.  Whole waves of units stay whole; of the rest the pieces (at least 512 tokens each) are what makes the
+    // last waves shortest: ceil(rest * n / SMs) / n of a unit's time, and a few percent for each further piece.
+    const long long sms = tq::handle_codec(h).num_sms, rest = units % sms;
     const long long most = (static_cast<long long>(max_blocks_per_seq) * page_size + 511) / 512;
-    return tq::clamp_splits((2LL * tq::handle_codec(h).num_sms + units - 1) / units, most);
+    if (rest == 0) return 1;
+    if (units < sms) return tq::clamp_splits((2 * sms + units - 1) / units, most);
+    int best = 1;
+    double least = 1.0;
+    for (int n = 2; n <= 4 && n <= most; ++n) {
+        const double t = static_cast<double>((rest * n + sms - 1) / sms) / n + 0.03 * n;
+        if (t < least) {
+            least = t;
+            best = n;
+        }
+    }
+    return best;
 }
 
 extern "C" tq_status tq_prefill_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t *k_pool,

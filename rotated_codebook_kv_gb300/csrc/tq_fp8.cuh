@@ -76,6 +76,7 @@ struct Args {
     int64_t num_blocks;
     float sm_scale;
     int splits, pages_per_split;
+    int whole;         // prefill: units (sequence, kv head, query block) that are not cut
     int Tq, qpc, nqt;  // query tokens per sequence, per CTA, and CTAs over them
     float *ml, *acc;   // [splits][B][Tq][Hq][2], [splits][B][Tq][Hq][D]; unused with one split
     int *pieces;       // [B][Hkv] pieces of a unit (decode)

@@ -10,7 +10,7 @@
 // denominator the sum of P / vs in fp32.
 //
 // A CTA takes NQ tiles of 128 columns, (query token, head) pairs of one sequence and kv head, and the
-// KT-token tiles that they see in its split.  Two tiles at head dim 128: while one's scores are turned into
+// KT-token tiles that they see (of units behind the last whole wave: a piece of those).  Two tiles at head dim 128: while one's scores are turned into
 // P, the tensor core works for the other.  At head dim 256 tensor memory holds one tile's O (256 columns)
 // and four score buffers.  P overwrites the scores that it came from.
 //
@@ -222,13 +222,12 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // the CTAs over one sequence's query tokens are neighbours (they share its pages in L2), the longest first
-    int u = blockIdx.x;
-    const int qt = A.nqt - 1 - u % A.nqt;
-    u /= A.nqt;
-    const int split = u % A.splits;
-    u /= A.splits;
-    const int kvh = u % A.Hkv, b = u / A.Hkv;
+    // The units that fill whole waves of CTAs stay whole; the ones behind them are cut into A.splits pieces.
+    // The query blocks of one sequence and kv head are neighbours (they share its pages in L2), the longest first.
+    const int at = static_cast<int>(blockIdx.x) - A.whole;
+    const int unit = at < 0 ? static_cast<int>(blockIdx.x) : A.whole + at / A.splits, split = at < 0 ? 0 : at % A.splits;
+    const bool uncut = at < 0 || A.splits == 1;
+    const int qt = A.nqt - 1 - unit % A.nqt, kvh = unit / A.nqt % A.Hkv, b = unit / A.nqt / A.Hkv;
     const int G = A.G, P = A.P;
     int L = A.seq_lens[b];
     if (L < 0) L = 0;
@@ -244,10 +243,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     auto col_lim = [&](int c) -> int { return max(0, L - A.Tq + q0 + c / G + 1); };
     const size_t rows_total = static_cast<size_t>(A.B) * A.Tq * A.Hq;
     const int tok0 = split * A.pages_per_split * P;
-    const int tok1 = min(col_lim(ncol - 1), tok0 + A.pages_per_split * P);
+    const int tok1 = min(col_lim(ncol - 1), uncut ? A.max_blocks * P : tok0 + A.pages_per_split * P);
     auto dead_row = [&](int c) {  // a row that this CTA has nothing for
         const size_t rr = col_row(c);
-        if (A.splits == 1) {
+        if (uncut) {
             uint4 *dst = reinterpret_cast<uint4 *>(A.out + rr * D);
             for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
         } else {
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 umma::ld32_issue(lane_base + T::kTmO + q * D + 32 * ch, o);
                 umma::wait_ld32(o);
                 if (!cv) continue;
-                if (A.splits == 1) {
+                if (uncut) {
                     uint4 *dst = reinterpret_cast<uint4 *>(A.out + rr * D + 32 * ch);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                     for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
             }
-            if (cv && A.splits > 1) {
+            if (cv && !uncut) {
                 float *ml = A.ml + (static_cast<size_t>(split) * rows_total + rr) * 2;
                 ml[0] = m_run;
                 ml[1] = l;
@@ -706,7 +705,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, 
 {
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(prefill_fp8_kernel<D>), Tc<D>::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(a.B) * a.Hkv * a.splits * a.nqt;
+    const unsigned units = static_cast<unsigned>(a.B) * a.Hkv * a.nqt, grid = a.whole + (units - a.whole) * a.splits;
     prefill_fp8_kernel<D><<<grid, Tc<D>::kThreads, Tc<D>::kSmem, st>>>(tk, tv, a);
     return cudaGetLastError();
 }
