@@ -342,9 +342,9 @@ tq_status tq_append_kv_bf16(tq_handle h, const uint16_t *q, const uint16_t *k, c
  * slot_mapping: as above, and the tokens of one page stand next to each other in the
  *       call with ascending slots (as packed sequences have them): where another
  *       token of the page, or the same slot again, stands up to 32 tokens before a
- *       run of consecutive slots, that run is skipped and TQ_DEVERR_SLOT_ORDER set;
- *       farther apart they race.  A token with a bad position inside a run keeps its
- *       place but is not written.
+ *       run of consecutive slots, that run is skipped (its q_out rows are written) and
+ *       TQ_DEVERR_SLOT_ORDER set; farther apart they race.  A token with a bad position
+ *       inside a run keeps its place but is not written.
  * Everything else as in tq_append_kv_bf16.
  */
 tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, const uint16_t *v, int64_t T,
@@ -359,7 +359,9 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
  * tq_append_kv_fp8 writes: tq_decode_attention_bf16 with pools and scales as above
  * (any non-negative finite scales; powers of two are what append writes).
  *
- * splits: split-K count, 0 = tq_decode_splits_fp8(...).  workspace: ws_bytes >=
+ * splits: most pieces that the work of one (sequence, kv head) is cut into (the cuts
+ *   are chosen on the GPU, from the lengths), 0 = tq_decode_splits_fp8(...); results
+ *   depend on the cuts, so on the batch, within rounding.  workspace: ws_bytes >=
  *   tq_workspace_bytes_fp8(h, batch, num_q_heads, splits), 256-byte aligned; not
  *   needed (may be NULL) where that is 0.  Its contents after the call are not
  *   specified, and calls that may overlap need one each.
@@ -380,7 +382,9 @@ tq_status tq_decode_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t 
  * tq_prefill_attention_fp8 -- the last q_tokens positions of every sequence attend
  * causally to its 8-bit pages, their own rows included (tq_prefill_attention's
  * contract over the pools above).  q, out: device bf16 [B][q_tokens][Hq][d].
- * splits = 0 picks tq_prefill_splits_fp8(...); workspace: ws_bytes >=
+ * A NaN in a key or value row reaches the query tokens that see it and no others.
+ * splits: pieces of the (sequence, kv head, query block) units that fill no whole
+ * wave of CTAs, 0 = tq_prefill_splits_fp8(...); workspace: ws_bytes >=
  * tq_workspace_bytes_fp8(h, batch * q_tokens, num_q_heads, splits).
  */
 int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int num_q_heads, int num_kv_heads,

@@ -301,7 +301,7 @@ class Codec:
         if out is None:
             out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         op = self._flat(out, torch.bfloat16, q.numel(), "out")
-        rest = (Hq, num_kv_heads, page_size, maxb, num_blocks, sm_scale, splits, workspace.data_ptr(),
+        rest = (Hq, num_kv_heads, page_size, maxb, num_blocks, float(sm_scale), splits, workspace.data_ptr(),
                 workspace.numel() * workspace.element_size(), op, _raw_stream(self.device))
         if tq == 0:
             native.tq_decode_attention_fp8(self.handle, qp, *args, B, *rest)

@@ -37,7 +37,10 @@ tq_status fail(tq_status s, const char *fmt, ...)
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
+    try {
+        g_last_error = buf;
+    } catch (...) {  // no memory for the message: the status still says what happened
+    }
     return s;
 }
 
@@ -87,12 +90,16 @@ cudaError_t tq::ensure_smem_attr(const void *func, size_t bytes)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> guard(lock);
-    size_t &g = granted[std::make_pair(func, dev)];
-    if (g >= bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess) g = bytes;
-    return e;
+    try {
+        std::lock_guard<std::mutex> guard(lock);
+        size_t &g = granted[std::make_pair(func, dev)];
+        if (g >= bytes) return cudaSuccess;
+        e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (e == cudaSuccess) g = bytes;
+        return e;
+    } catch (...) {  // no exception leaves a C entry
+        return cudaErrorMemoryAllocation;
+    }
 }
 
 tq_status tq::api_error(tq_status s, const char *fmt, ...)
@@ -102,7 +109,10 @@ tq_status tq::api_error(tq_status s, const char *fmt, ...)
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
+    try {
+        g_last_error = buf;
+    } catch (...) {  // no memory for the message: the status still says what happened
+    }
     return s;
 }
 

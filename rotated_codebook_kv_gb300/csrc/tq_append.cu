@@ -473,10 +473,11 @@ tq_status check(const char *who, tq_handle h, AppendArgs *a, int64_t num_blocks,
         return api_error(TQ_ERR_UNSUPPORTED, "%s: unknown rotation style %d", who, style);
     if ((a->q == nullptr) != (a->q_out == nullptr))
         return api_error(TQ_ERR_INVALID_ARG, "%s: q and q_out go together", who);
-    if (a->Hq > (1 << 20) || a->Hkv > (1 << 20))
-        return api_error(TQ_ERR_UNSUPPORTED, "%s: more than 2^20 heads", who);
-    // grid size, and byte offsets within a pool
-    if (a->T >= (int64_t(1) << 30)) return api_error(TQ_ERR_UNSUPPORTED, "%s: too many tokens in one call", who);
+    if (a->Hq > (1 << 18) || a->Hkv > (1 << 18))
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: more than 2^18 heads", who);
+    // grid sizes, and byte offsets within a pool
+    if (a->T >= (int64_t(1) << 30) || a->T * (a->Hq + 2 * a->Hkv) >= (int64_t(1) << 34))
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: too many tokens in one call", who);
     if (num_blocks > (int64_t(1) << 50) / (static_cast<int64_t>(a->Hkv) * a->P * d * static_cast<int64_t>(cell)))
         return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who,
                          static_cast<long long>(num_blocks));

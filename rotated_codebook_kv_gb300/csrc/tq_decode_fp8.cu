@@ -19,6 +19,7 @@
 // is written at once, the others' partials (max, denominator, numerators) are merged by merge_fp8_kernel.  With one
 // split a CTA has one whole unit.  Up to eight (query token, head) columns of a sequence and kv head go through this
 // kernel, more through tq_prefill_fp8.cu.
+#include <climits>
 #include <cmath>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -45,7 +46,8 @@ struct Fp8Smem {
     static constexpr int kTileBytes = kTok * D;       // keys or values of one round
     static constexpr int kStage = 2 * kTileBytes;     // keys, then values
     static constexpr size_t kData = static_cast<size_t>(kWarps) * kStages * kStage;
-    static constexpr size_t kBytes = 1024 + kData + 128;  // alignment slack, stages, barriers and flag
+    static constexpr size_t kBytes = 1024 + kData + 128 + 4 * D;  // alignment slack, stages, barriers and flag, NaN tokens
+    static_assert(kBytes <= 232448, "shared memory");
     static_assert(kData >= sizeof(float) * kWarps * (D * 8 + 16), "merge area");
 };
 
@@ -144,6 +146,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *mbar = reinterpret_cast<uint64_t *>(smem + SM::kData);  // [warp][stage]
     volatile int *cta_abort = reinterpret_cast<volatile int *>(mbar + kStages * kWarps);
+    int *nan_at = reinterpret_cast<int *>(smem + SM::kData + 128);  // [D] first token behind the causal limits with a NaN value
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = lane & 3, row = lane >> 2;
     const int P = A.P, G = A.G, ncol = A.Tq * G;
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     if (tid < kStages * kWarps)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&mbar[tid]))));
     if (tid == 0) *cta_abort = 0;
+    for (int j = tid; j < D; j += kThreads) nan_at[j] = INT_MAX;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
 
@@ -387,12 +391,19 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             int nv[2];                                               // tokens of each half
 #pragma unroll
             for (int h = 0; h < 2; ++h) nv[h] = (okm >> h & 1u) ? max(0, min(16, tok1 - t - 16 * h)) : 0;
-            if (!whole && nv[0] + nv[1] < kTok) {  // rows behind the end or of a bad page hold anything: zero the values
+            if (!whole && (nv[0] + nv[1] < kTok || A.Tq > 1)) {
+                // rows behind the end or of a bad page hold anything: zero the values; among query tokens, NaN that some do not see
                 unsigned char *vz = smem + (stage - sbase) + SM::kTileBytes;
                 for (int e = lane; e < kTok * (D / 16); e += 32) {
                     const int rr = e / (D / 16), cc = e % (D / 16);
-                    if ((rr & 15) >= nv[rr >> 4])
-                        *reinterpret_cast<uint4 *>(vz + (cc / 8) * kBoxBytes + rr * 128 + (cc % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    uint4 *at = reinterpret_cast<uint4 *>(vz + (cc / 8) * kBoxBytes + rr * 128 + (cc % 8) * 16);
+                    if ((rr & 15) >= nv[rr >> 4]) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (t + rr >= low) {
+                        uint4 w = *at;
+                        hide_nan(w, nan_at + (cc / 8) * 128 + ((cc ^ rr) & 7) * 16, t + rr);
+                        *at = w;
+                    }
                 }
                 __syncwarp();
             }
@@ -534,6 +545,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             }
             acc *= downp;
             l *= ldown;
+            if (A.Tq > 1 && nan_at[j] < col_lim(c)) acc = __int_as_float(0x7fffffff);
             if (dead) {
                 M = -INFINITY;
                 acc = l = 0.f;
@@ -560,6 +572,10 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             while (length(b) == 0);  // pos < end: there is a later unit with rounds
         }
         __syncthreads();  // the merge data is read
+        if (A.Tq > 1) {
+            for (int j = tid; j < D; j += kThreads) nan_at[j] = INT_MAX;
+            __syncthreads();
+        }
         // the waits of a CTA that gave up are not in step with its stages any more: its other units count as unseen
         if (dead) {
             for (;;) {

@@ -68,6 +68,24 @@ __device__ __forceinline__ uint32_t e4m3x2(float x, float y)
     return c;
 }
 
+// NaN among 16 value codes of a token that not every query token sees: 0 times NaN would carry it to those that do not.
+// Taken out of the products and noted as the coordinate's first such token; the rows that see it get their NaN at the end.
+__device__ __forceinline__ void hide_nan(uint4 &w, int *nan_at, int token)
+{
+    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t nan = ((v[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // the codes 0x7f and 0xff
+        while (nan) {
+            const int byte = __ffs(nan) / 8 - 1;
+            atomicMin(nan_at + 4 * i + byte, token);
+            v[i] &= ~(0xffu << (8 * byte));
+            nan &= nan - 1;
+        }
+    }
+    w = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 struct Args {
     const uint16_t *q;
     const float *k_scales, *v_scales;

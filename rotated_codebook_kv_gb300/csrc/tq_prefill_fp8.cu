@@ -10,8 +10,8 @@
 // denominator the sum of P / vs in fp32.
 //
 // A CTA takes NQ tiles of 128 columns, (query token, head) pairs of one sequence and kv head, and the
-// KT-token tiles that they see (of units behind the last whole wave: a piece of those).  Two tiles at head dim 128: while one's scores are turned into
-// P, the tensor core works for the other.  At head dim 256 tensor memory holds one tile's O (256 columns)
+// KT-token tiles that they see (of units behind the last whole wave: a piece of those).  Two tiles at head
+// dim 128: while one's scores are turned into P, the tensor core works for the other.  At head dim 256 tensor memory holds one tile's O (256 columns)
 // and four score buffers.  P overwrites the scores that it came from.
 //
 // Warps (one CTA per SM):
@@ -21,6 +21,8 @@
 //   1         page copies (TMA boxes of a page x 128 bytes, 128-byte swizzle), scales
 // Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT, stops the CTA (its rows
 // then carry no weight), lets copies and MMAs in flight finish, and frees tensor memory.
+#include <climits>
+
 #include "tq_fp8.cuh"
 #include "tq_umma.cuh"
 
@@ -68,7 +70,8 @@ struct Tc {
     static constexpr int bEnd = bPvDone + NQ * NB;    // teardown: every MMA issued is done
     static constexpr int kBars = bEnd + 1;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;  // tensor-memory base, abort flag
-    static constexpr size_t kSmem = 1024 + kMiscOff + 16;
+    static constexpr uint32_t kNanOff = (kMiscOff + 8 + 15) / 16 * 16;  // [D] first token behind a causal limit with a NaN value
+    static constexpr size_t kSmem = 1024 + kNanOff + 4 * D;
     // tensor-memory columns
     static constexpr uint32_t kTmS = 0;                              // [NQ][NB] KT columns
     static constexpr uint32_t kTmO = NQ * NB * KT;                   // [NQ] D columns
@@ -271,9 +274,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + T::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + T::kMiscOff + 4);
     const uint32_t sbase = saddr(smem);
+    int *nan_at = reinterpret_cast<int *>(smem + T::kNanOff);
     const int ppt = KT / P;  // pages per tile
 
     if (warp == T::kMmaWarp) umma::tmem_alloc(tmem_slot, T::kTmCols);
+    if (tid < D) nan_at[tid] = INT_MAX;
     if (tid == 0) {
         umma::mbar_init(&mbar[T::bQ], T::kSoftWarps);
         for (int i = 0; i < T::KS; ++i) {
@@ -466,6 +471,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 umma::ld32_issue(lane_base + T::kTmO + q * D + 32 * ch, o);
                 umma::wait_ld32(o);
                 if (!cv) continue;
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const int4 at = *reinterpret_cast<const int4 *>(nan_at + 32 * ch + k);
+                    if (at.x < lim) o[k] = 0x7fffffffu;
+                    if (at.y < lim) o[k + 1] = 0x7fffffffu;
+                    if (at.z < lim) o[k + 2] = 0x7fffffffu;
+                    if (at.w < lim) o[k + 3] = 0x7fffffffu;
+                }
                 if (uncut) {
                     uint4 *dst = reinterpret_cast<uint4 *>(A.out + rr * D + 32 * ch);
 #pragma unroll
@@ -512,6 +525,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const uint32_t okm = reinterpret_cast<const uint32_t *>(smem + T::kOkOff)[i % T::kRing];
             const int rem = tok1 - (tok0 + i * KT);
             const bool whole = rem >= KT && okm == (1u << GR) - 1u;
+            const int seen = col_lim(0) - (tok0 + i * KT);  // tokens of the tile that every column sees
             // four reads ahead of their writes
 #pragma unroll
             for (int n0 = 0; n0 < KT * D / 16 / (32 * T::kConvWarps); n0 += 4) {
@@ -521,6 +535,13 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                     const int dt = (n0 + n) * (16 / XB);
                     w[n] = lds128(raw + dt * 128);
                     if (!whole && (t + dt >= rem || !(okm >> ((t + dt) >> 4) & 1u))) w[n] = make_uint4(0u, 0u, 0u, 0u);  // no token: holds anything
+                }
+                if (seen < KT) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int dt = (n0 + n) * (16 / XB);
+                        if (t + dt >= seen) hide_nan(w[n], nan_at + 128 * x + 16 * ch, tok0 + i * KT + t + dt);
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {

@@ -244,6 +244,35 @@ def test_append_bad_slots_positions_and_order():
     assert s8 == native.TQ_DEVERR_SLOT_ORDER
 
 
+@pytest.mark.parametrize("d,P,H,T", [(128, 16, 2, 1300), (256, 32, 1, 1100), (128, 32, 5, 1024), (256, 16, 3, 999)])
+def test_append_many_single_tokens(d, P, H, T):
+    """A page per token, in any order; some pages come again within the next 32 tokens, which leaves those out."""
+    codec = _codec(d)
+    g = torch.Generator().manual_seed(T)
+    k, v = [torch.randn(T, H, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    rope = codec.rope_table(50, d)
+    pos = torch.randint(0, 50, (T,), generator=g)
+    slots = torch.randperm(T, generator=g) * P + torch.randint(0, P - 1, (T,), generator=g)
+    for again in (False, True):
+        ok = np.ones(T, bool)
+        if again:
+            # neighbours (the slot itself once more, and an earlier one), one page 15 and one 31 tokens on, around where
+            # stretches of 16 and 32 tokens meet
+            for a, b, o in ((15, 16, 0), (100, 101, None), (31, 46, 3), (500, 531, 1), (959, 990, 0)):
+                slots[b] = slots[a] if o is None else slots[a] // P * P + (slots[a] % P + P - 1 - o) % P
+                ok[b] = False
+        pools = fp8_pools(codec, T, H, P, seed=T)
+        want = [codes_of(pools[0]).copy(), codes_of(pools[1]).copy(), pools[2].cpu().double().numpy(), pools[3].cpu().double().numpy()]
+        c = dict(rope=rope, pos=pos, T=T, interleaved=True)
+        R.append_fp8(want[0], want[2], rotated(k, c), np.where(ok, slots.numpy(), -1), ok, P)
+        R.append_fp8(want[1], want[3], R.bf16(v), np.where(ok, slots.numpy(), -1), ok, P)
+        codec.append_kv_fp8(k, v, slots.to(DEV), *pools, P, T, positions=pos.to(DEV), rope=rope, interleaved=True)
+        torch.cuda.synchronize()
+        assert codec.get_status() == (native.TQ_DEVERR_SLOT_ORDER if again else 0)
+        assert np.array_equal(pools[2].cpu().numpy(), want[2]) and np.array_equal(pools[3].cpu().numpy(), want[3])
+        assert np.array_equal(codes_of(pools[0]), want[0]) and np.array_equal(codes_of(pools[1]), want[1])
+
+
 def test_append_captured_in_a_graph_and_on_another_stream():
     d, P = 128, 16
     codec = _codec(d)

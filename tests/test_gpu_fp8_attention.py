@@ -125,6 +125,69 @@ def test_prefill(d, P, Hkv, G, lens, Tq):
 
 
 @pytest.mark.parametrize("d", [128, 256])
+def test_decode_of_many_sequences(d):
+    """More sequences than a block has threads, lengths from 0 on: work dealt out over several stretches of them."""
+    g = torch.Generator().manual_seed(d)
+    lens = torch.randint(0, 120, (500,), generator=g).tolist()
+    lens[0], lens[250], lens[499] = 700, 0, 333
+    c = case(d, 16, 1, 2, lens, seed=d)
+    ref, bound = reference(c)
+    for splits in (0, 1, 2, 9):
+        check(run(c, splits), ref, bound)
+    assert _codec(d).get_status() == 0
+
+
+def test_decode_of_empty_sequences():
+    c = case(128, 16, 2, 2, [0, 0, 0], seed=1)
+    for splits in (1, 2, 5):
+        assert torch.all(run(c, splits) == 0)
+
+
+@pytest.mark.parametrize("d,Hkv,G,B,Tq", [(128, 8, 1, 20, 33), (256, 8, 2, 25, 9)])
+def test_prefill_with_units_behind_a_whole_wave(d, Hkv, G, B, Tq):
+    """More units than SMs: those that fill waves stay whole, the others are cut."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(1, 160, (B,), generator=g).tolist()
+    c = case(d, 16, Hkv, G, lens, Tq=Tq, seed=B)
+    ref, bound = reference(c)
+    for splits in (0, 1, 3):
+        check(run(c, splits), ref, bound)
+
+
+def test_pool_offsets_past_32_bits():
+    """Rows of a pool beyond 4 GiB: appended and attended to."""
+    d, P, Hkv = 128, 16, 8
+    codec = _codec(d)
+    nb = (1 << 32) // (Hkv * P * d) + 40
+    kp, vp = [torch.zeros(nb, Hkv, P, d, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+    ks, vs = [torch.ones(nb, Hkv, device=DEV) for _ in range(2)]
+    g = torch.Generator().manual_seed(3)
+    n = 45
+    blocks = torch.tensor([nb - 1, nb - 30, nb - 7], dtype=torch.int32)
+    pos = torch.arange(n)
+    slots = blocks[pos // P].long() * P + pos % P
+    k, v = [torch.randn(n, Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2)]
+    codec.append_kv_fp8(k.to(DEV), v.to(DEV), slots.to(DEV), kp, vp, ks, vs, P, nb)
+    small = [torch.zeros(3, Hkv, P, d, dtype=torch.uint8).numpy() for _ in range(2)]
+    sc = [np.ones((3, Hkv)) for _ in range(2)]
+    for x, code, s in ((k, small[0], sc[0]), (v, small[1], sc[1])):
+        R.append_fp8(code, s, R.bf16(x), pos.numpy(), np.ones(n, bool), P)
+    at = blocks.long().to(DEV)
+    assert np.array_equal(kp.view(torch.uint8)[at].cpu().numpy(), small[0])
+    assert np.array_equal(vp.view(torch.uint8)[at].cpu().numpy(), small[1])
+    lens = torch.tensor([n], dtype=torch.int32)
+    for tq in (None, 12):
+        q = torch.randn((1, Hkv, d) if tq is None else (1, tq, Hkv, d), generator=g).to(torch.bfloat16)
+        call = codec.decode_attention_fp8 if tq is None else codec.prefill_attention_fp8
+        out = call(q.to(DEV), kp, vp, ks, vs, blocks[None].to(DEV), lens.to(DEV), Hkv, P, nb, d ** -0.5)
+        c = dict(q=q, codes=[torch.from_numpy(x) for x in small], scales=[torch.from_numpy(x) for x in sc],
+                 table=torch.arange(3, dtype=torch.int32)[None], lens=lens, nb=3, P=P, Hkv=Hkv, d=d)
+        ref, bound = reference(c)
+        check(out, ref, bound)
+    assert codec.get_status() == 0
+
+
+@pytest.mark.parametrize("d", [128, 256])
 def test_scales_far_apart(d):
     """Pages whose key and value scales differ by many powers of two, one with a zero scale."""
     c = case(d, 16, 2, 4, [200, 90], seed=1)
@@ -202,6 +265,33 @@ def test_nan_in_the_cache_and_in_the_query_stays_one():
     c["q"][0, 1, 5] = float("nan")
     out = R.bf16(run(c, 2))
     assert np.all(np.isnan(out[0, 1])) and np.all(np.isfinite(out[0, 0])) and np.all(np.isfinite(out[1]))
+
+
+@pytest.mark.parametrize("d,G,Tq,splits", [(128, 2, 4, 1), (128, 2, 4, 3), (256, 1, 7, 2), (128, 4, 100, 1), (128, 8, 33, 2),
+                                           (256, 2, 90, 1), (256, 3, 40, 2)])
+def test_nan_of_a_later_token_stays_hidden(d, G, Tq, splits):
+    """NaN among the last tokens' values and keys: in the rows that see them, and in no others."""
+    lens = [200, 131]
+    clean = case(d, 16, 2, G, lens, Tq=Tq, seed=11)
+    ref, bound = reference(clean)
+    c = dict(clean, codes=[x.clone() for x in clean["codes"]])
+    want = np.zeros(ref.shape, bool)
+    for b, head, back, j in ((0, 0, 1, 5), (0, 1, Tq // 2, d - 1), (0, 1, 2, d - 1), (1, 0, 2, 77), (1, 1, Tq - 1, 64)):
+        pos = lens[b] - back
+        c["codes"][1][c["table"][b, pos // 16], head, pos % 16, j] = 0xFF if j % 2 else 0x7F
+        want[b, Tq - back:, head * G: head * G + G, j] = True
+    out = R.bf16(run(c, splits))
+    assert np.array_equal(np.isnan(out), want)
+    # without the NaN codes the other coordinates are what they were
+    assert np.all(np.abs(out - ref)[~want] <= bound[~want])
+    c = dict(clean, codes=[x.clone() for x in clean["codes"]])
+    pos = lens[1] - 3
+    c["codes"][0][c["table"][1, pos // 16], 1, pos % 16, 9] = 0x7F
+    out = R.bf16(run(c, splits))
+    want = np.zeros(ref.shape, bool)
+    want[1, Tq - 3:, G:] = True
+    assert np.array_equal(np.isnan(out), want)
+    assert np.all(np.abs(out - ref)[~want] <= bound[~want])
 
 
 @pytest.mark.parametrize("d,Tq", [(128, None), (256, None), (128, 40), (256, 40)])
