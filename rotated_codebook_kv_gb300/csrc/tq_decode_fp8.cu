@@ -132,8 +132,9 @@ __device__ __forceinline__ void count_rounds(const Args &A, long long *s_sum, in
 }
 
 // The columns of a CTA are the (query token, head) pairs of a sequence and kv head, eight at most, each with its causal
-// limit (one query token: the G heads, which see all).
-template <int D>
+// limit (one query token: the G heads, which see all; MANY: several, which is a kernel of its own because what it does for
+// values that only some see cost the decode 2-4 % at head dim 128).
+template <int D, bool MANY>
 __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     attention_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args A)
 {
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
     if (tid < kStages * kWarps)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&mbar[tid]))));
     if (tid == 0) *cta_abort = 0;
-    for (int j = tid; j < D; j += kThreads) nan_at[j] = INT_MAX;
+    if (MANY)
+        for (int j = tid; j < D; j += kThreads) nan_at[j] = INT_MAX;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
 
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             int nv[2];                                               // tokens of each half
 #pragma unroll
             for (int h = 0; h < 2; ++h) nv[h] = (okm >> h & 1u) ? max(0, min(16, tok1 - t - 16 * h)) : 0;
-            if (!whole && (nv[0] + nv[1] < kTok || A.Tq > 1)) {
+            if (!whole && (nv[0] + nv[1] < kTok || MANY)) {
                 // rows behind the end or of a bad page hold anything: zero the values; among query tokens, NaN that some do not see
                 unsigned char *vz = smem + (stage - sbase) + SM::kTileBytes;
                 for (int e = lane; e < kTok * (D / 16); e += 32) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
                     uint4 *at = reinterpret_cast<uint4 *>(vz + (cc / 8) * kBoxBytes + rr * 128 + (cc % 8) * 16);
                     if ((rr & 15) >= nv[rr >> 4]) {
                         *at = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (t + rr >= low) {
+                    } else if (MANY && t + rr >= low) {
                         uint4 w = *at;
                         hide_nan(w, nan_at + (cc / 8) * 128 + ((cc ^ rr) & 7) * 16, t + rr);
                         *at = w;
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             }
             acc *= downp;
             l *= ldown;
-            if (A.Tq > 1 && nan_at[j] < col_lim(c)) acc = __int_as_float(0x7fffffff);
+            if (MANY && nan_at[j] < col_lim(c)) acc = __int_as_float(0x7fffffff);
             if (dead) {
                 M = -INFINITY;
                 acc = l = 0.f;
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             while (length(b) == 0);  // pos < end: there is a later unit with rounds
         }
         __syncthreads();  // the merge data is read
-        if (A.Tq > 1) {
+        if (MANY) {
             for (int j = tid; j < D; j += kThreads) nan_at[j] = INT_MAX;
             __syncthreads();
         }
@@ -735,10 +737,11 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, 
         e = launch_prefill_tc(tk, tv, D, a, st);
     } else {
         const size_t smem = Fp8Smem<D>::kBytes;
-        e = ensure_smem_attr(reinterpret_cast<const void *>(attention_fp8_kernel<D>), smem);
+        auto *kernel = a.Tq == 1 ? attention_fp8_kernel<D, false> : attention_fp8_kernel<D, true>;
+        e = ensure_smem_attr(reinterpret_cast<const void *>(kernel), smem);
         if (e != cudaSuccess) return e;
         const unsigned grid = a.splits == 1 ? static_cast<unsigned>(a.B) * a.Hkv : static_cast<unsigned>(num_sms) * Fp8Smem<D>::kCtas;
-        attention_fp8_kernel<D><<<grid, Fp8Smem<D>::kThreads, smem, st>>>(tk, tv, a);
+        kernel<<<grid, Fp8Smem<D>::kThreads, smem, st>>>(tk, tv, a);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || a.splits == 1) return e;
