@@ -34,7 +34,8 @@ template <int D>
 struct Tc {
     static constexpr int NQ = D == 128 ? 2 : 1;         // column tiles
     static constexpr int KT = 64;                       // tokens per tile
-    static constexpr int NB = D == 128 ? 2 : 4;         // score buffers per column tile
+    static constexpr int NB = 2;                        // score buffers per column tile
+    static constexpr bool kQTm = NQ == 1;               // query operands in tensor memory (two column tiles leave no room)
     static constexpr int XB = D / 128;                  // 128-byte column blocks of a row of codes
     static constexpr int kSoftWarps = 4 * NQ;
     static constexpr int kConvWarps = 4;
@@ -44,13 +45,13 @@ struct Tc {
     // registers: 512 threads start with 128 each; the column warps take 192 and leave 64 to the others
     // (2 x 128 x 192 + 2 x 128 x 64 = 512 x 128).  384 threads have 168 each and keep them.
     static constexpr bool kSplitRegs = NQ == 2;
-    static constexpr int KS = D == 128 ? 4 : 3, RS = D == 128 ? 3 : 2, VS = D == 128 ? 3 : 2;  // stages: keys, value codes, fp16 values
+    static constexpr int KS = 4, RS = 3, VS = 3;  // stages: keys, value codes, fp16 values
     static constexpr int GR = KT / 16;                  // 16-token groups of a tile (a page holds one or two)
     static constexpr int kRing = 8;                     // tiles whose scales are kept
     static constexpr uint32_t kQBytes = 128u * D;       // one term of one column tile
     static constexpr uint32_t kKBytes = static_cast<uint32_t>(KT) * D;
     static constexpr uint32_t kQOff = 0;
-    static constexpr uint32_t kKOff = kQOff + 2 * NQ * kQBytes;
+    static constexpr uint32_t kKOff = kQOff + (kQTm ? 0 : 2 * NQ * kQBytes);
     static constexpr uint32_t kROff = kKOff + KS * kKBytes;
     static constexpr uint32_t kVOff = kROff + RS * kKBytes;
     static constexpr uint32_t kInfoOff = kVOff + VS * 2 * kKBytes;  // [ring][GR] (ks, log2 vs, 2^-6 / vs, -)
@@ -74,7 +75,8 @@ struct Tc {
     static constexpr size_t kSmem = 1024 + kNanOff + 4 * D;
     // tensor-memory columns
     static constexpr uint32_t kTmS = 0;                              // [NQ][NB] KT columns
-    static constexpr uint32_t kTmO = NQ * NB * KT;                   // [NQ] D columns
+    static constexpr uint32_t kTmQ = NQ * NB * KT;                   // D / 4 columns of either term
+    static constexpr uint32_t kTmO = kTmQ + (kQTm ? D / 2 : 0);      // [NQ] D columns
     static constexpr uint32_t kTmCols = 512;
     static_assert(KT == 64, "the softmax holds a column's 64 scores");
     static_assert(KS + NB < kRing, "a tile's scales are written over those of a tile that every column is done with");
@@ -381,6 +383,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const uint32_t qs = sbase + T::kQOff + 2 * q * T::kQBytes + r * 128;
 #pragma unroll
             for (int x = 0; x < XB; ++x) {
+                uint32_t th[32], tl[32];  // the terms' words, where they go to tensor memory
                 if (x > 0) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = cv ? __ldg(src + 16 * x + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -398,12 +401,29 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                         hi[k] |= e4m3x2_rest(x2, x3) << 16;
                         lo[k] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
                     }
-                    const uint32_t at = qs + x * (128 * 128) + ((i ^ (r & 7)) << 4);
-                    sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    sts128(at + T::kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    if constexpr (T::kQTm) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            th[4 * i + k] = hi[k];
+                            tl[4 * i + k] = lo[k];
+                        }
+                    } else {
+                        const uint32_t at = qs + x * (128 * 128) + ((i ^ (r & 7)) << 4);
+                        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        sts128(at + T::kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    }
+                }
+                if constexpr (T::kQTm) {
+                    umma::st32(lane_base + T::kTmQ + 32 * x, th);
+                    umma::st32(lane_base + T::kTmQ + D / 4 + 32 * x, tl);
                 }
             }
-            umma::fence_proxy_async();
+            if constexpr (T::kQTm) {
+                umma::wait_st();
+                umma::fence_before_sync();
+            } else {
+                umma::fence_proxy_async();
+            }
             warp_arrive(&mbar[T::bQ]);
         }
         const int lim = cv ? min(col_lim(c), tok1) : tok1;  // an idle column (zero query) goes the way of the full ones
@@ -587,8 +607,13 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k) {
                             const uint32_t kd = ka + (k >> 2) * (KT * 8) + 2 * (k & 3), qd = qa + (k >> 2) * (128 * 8) + 2 * (k & 3);
-                            umma::mma_e4m3_lohi(ds, qd, hi, kd, hi, id_s, k > 0 ? 1 : 0);
-                            umma::mma_e4m3_lohi(ds, qd + T::kQBytes / 16, hi, kd, hi, id_s, 1);
+                            if constexpr (T::kQTm) {
+                                umma::mma_e4m3_tmem_a(ds, tbase + T::kTmQ + 8 * k, kd, hi, id_s, k > 0 ? 1 : 0);
+                                umma::mma_e4m3_tmem_a(ds, tbase + T::kTmQ + D / 4 + 8 * k, kd, hi, id_s, 1);
+                            } else {
+                                umma::mma_e4m3_lohi(ds, qd, hi, kd, hi, id_s, k > 0 ? 1 : 0);
+                                umma::mma_e4m3_lohi(ds, qd + T::kQBytes / 16, hi, kd, hi, id_s, 1);
+                            }
                         }
                         umma::commit(&mbar[T::bSFull + q * NB + buf]);
                     }
@@ -690,7 +715,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             copy(tmK, k_dst + (i % T::KS) * T::kKBytes, T::bKFull + i % T::KS);
             k_issued = i + 1;
             if (i >= T::RS && !wait_bar(T::bRFree + i % T::RS, (i / T::RS - 1) & 1)) break;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the widening's reads are done
+            // (the widening warps order their reads before these writes: a proxy fence ahead of their arrival; one here
+            // waited for the loads of ids and scales in flight, ~700 cycles of every tile)
             copy(tmV, r_dst + (i % T::RS) * T::kKBytes, T::bRFull + i % T::RS);
             r_issued = i + 1;
             if (i + 1 < nt_all) pages = write_info(i + 1, blk1, ks1, vs1);  // that tile's keys arrive after this

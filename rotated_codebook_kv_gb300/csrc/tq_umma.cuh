@@ -92,6 +92,16 @@ __device__ __forceinline__ void mma_e4m3_lohi(uint32_t d_tmem, uint32_t a_lo, ui
                  ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(accum), "r"(idesc));
 }
 
+// The same MMA with A read from tensor memory: row m of A in lane m, elements 4c .. 4c + 3 of a row in column c (the first
+// in the low byte); a k-step of 32 elements advances a_tmem by 8 columns.
+__device__ __forceinline__ void mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                                int accum)
+{
+    asm volatile("{\n.reg .pred p;\n.reg .b64 db;\nsetp.ne.b32 p, %4, 0;\nmov.b64 db, {%2, %3};\n"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], db, %5, p;\n}\n"
+                 ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(accum), "r"(idesc));
+}
+
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one()
 {
