@@ -15,7 +15,7 @@
 // and four score buffers.  P overwrites the scores that it came from.
 //
 // Warps (one CTA per SM):
-//   4 NQ      one thread per column: query operands, online softmax, output
+//   4 NQ      one thread per column: online softmax, output (and, with the next ones, the query operands at first)
 //   4         value codes of a tile to fp16 (rows of 64 coordinates, 128-byte swizzle, one row per token)
 //   1 + NQ    MMA issue: the scores (and tensor-memory allocation); P.V of a column tile each
 //   1         page copies (TMA boxes of a page x 128 bytes, 128-byte swizzle), scales
@@ -58,8 +58,9 @@ struct Tc {
     static constexpr uint32_t kOkOff = kInfoOff + kRing * GR * 16;  // [ring] bit g: group g's page is valid
     static constexpr uint32_t kBarOff = kOkOff + kRing * 4;
     // barriers
-    static constexpr int bQ = 0;                 // query operands in shared memory
-    static constexpr int bKFull = 1;             // [KS] keys landed (one arrival, and bytes)
+    static constexpr int bQ = 0;                 // query terms in shared memory, and every column's factor
+    static constexpr int bQTm = 1;               // query terms in tensor memory
+    static constexpr int bKFull = 2;             // [KS] keys landed (one arrival, and bytes)
     static constexpr int bKFree = bKFull + KS;   // [KS] the score MMAs of every tile are done
     static constexpr int bRFull = bKFree + KS;   // [RS] value codes landed
     static constexpr int bRFree = bRFull + RS;   // [RS] widened
@@ -72,7 +73,9 @@ struct Tc {
     static constexpr int kBars = bEnd + 1;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;  // tensor-memory base, abort flag
     static constexpr uint32_t kNanOff = (kMiscOff + 8 + 15) / 16 * 16;  // [D] first token behind a causal limit with a NaN value
-    static constexpr size_t kSmem = 1024 + kNanOff + 4 * D;
+    static constexpr uint32_t kFacOff = kNanOff + 4 * D;  // [128 NQ] sm_scale log2(e) 2^-e of a column
+    static constexpr uint32_t kStageOff = kQTm ? kVOff : kQOff;  // query terms on their way to tensor memory; output rows
+    static constexpr size_t kSmem = 1024 + kFacOff + 4 * 128 * NQ;
     // tensor-memory columns
     static constexpr uint32_t kTmS = 0;                              // [NQ][NB] KT columns
     static constexpr uint32_t kTmQ = NQ * NB * KT;                   // D / 4 columns of either term
@@ -282,7 +285,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     if (warp == T::kMmaWarp) umma::tmem_alloc(tmem_slot, T::kTmCols);
     if (tid < D) nan_at[tid] = INT_MAX;
     if (tid == 0) {
-        umma::mbar_init(&mbar[T::bQ], T::kSoftWarps);
+        umma::mbar_init(&mbar[T::bQ], T::kMmaWarp);
+        umma::mbar_init(&mbar[T::bQTm], T::kSoftWarps);
         for (int i = 0; i < T::KS; ++i) {
             umma::mbar_init(&mbar[T::bKFull + i], 1);
             umma::mbar_init(&mbar[T::bKFree + i], 1);
@@ -342,6 +346,55 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         return false;
     };
 
+    float *s_fac = reinterpret_cast<float *>(smem + T::kFacOff);
+    if (warp < T::kMmaWarp) {
+        // ================= query operands =================
+        // Coordinates 8 j .. 8 j + 7 of a row by lane j of its D / 8 lanes, four loads of a warp in flight.  A thread per
+        // row, all unrolled, took 10-14 thousand cycles of a unit's 240: most of its ~2000 instructions ran once, from
+        // memory, and a load touched 32 rows.
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
+        const int j = lane % kLanes;
+#pragma unroll 1
+        for (int i0 = warp * kBatch; i0 < 128 * NQ / kRows; i0 += T::kMmaWarp * kBatch) {
+            uint4 w[kBatch];
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                const int c = (i0 + n) * kRows + lane / kLanes;
+                w[n] = c < ncol ? __ldg(reinterpret_cast<const uint4 *>(A.q + col_row(c) * D) + j) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                const int c = (i0 + n) * kRows + lane / kLanes;
+                const uint32_t v[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+                uint32_t m = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu), __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+                m = max(m & 0xffffu, m >> 16);  // the largest magnitude's bits
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int ex = min(max(static_cast<int>(m >> 7) - 127, -100), 120);  // 2^(7 - ex) brings the largest into [2^7, 2^8)
+                float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
+                if (j == 0)  // >= 0: a negative scale goes into q's sign; an infinity or NaN makes the row NaN
+                    s_fac[c] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                            : fabsf(A.sm_scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
+                if (A.sm_scale < 0.f) up = -up;
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float x0 = __uint_as_float(v[2 * k] << 16) * up, x1 = __uint_as_float(v[2 * k] & 0xffff0000u) * up;
+                    float x2 = __uint_as_float(v[2 * k + 1] << 16) * up, x3 = __uint_as_float(v[2 * k + 1] & 0xffff0000u) * up;
+                    hi[k] = e4m3x2_rest(x0, x1);
+                    hi[k] |= e4m3x2_rest(x2, x3) << 16;
+                    lo[k] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
+                }
+                // chunks of 16 coordinates, the 128-byte swizzle of the operand; on the way to tensor memory rows of both terms
+                const uint32_t at = (((j >> 1) ^ (c & 7)) << 4) + 8 * (j & 1) +
+                                    (T::kQTm ? T::kStageOff + c * 512 : T::kQOff + 2 * (c >> 7) * T::kQBytes + (c & 127) * 128);
+                *reinterpret_cast<uint2 *>(smem + at) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(smem + at + (T::kQTm ? 256 : T::kQBytes)) = make_uint2(lo[0], lo[1]);
+            }
+        }
+        if constexpr (!T::kQTm) umma::fence_proxy_async();
+        warp_arrive(&mbar[T::bQ]);
+    }
     if constexpr (T::kSplitRegs) {
         if (warp < T::kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -351,86 +404,33 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         const int q = warp >> 2, r = tid & 127, c = 128 * q + r;
         const bool cv = c < ncol;
         const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-        float fac;  // sm_scale log2(e) 2^-e >= 0: a negative scale goes into q's sign
-        {
-            // 128 coordinates at a time in registers, all of their loads in flight together (at head dim 256 the second
-            // half is read again, from cache, once the maximum is known)
-            const uint4 *src = reinterpret_cast<const uint4 *>(A.q + col_row(cv ? c : 0) * D);
-            uint4 w[16];
-            float mx = 0.f;
-            bool nan = false;
+        bool ok = wait_bar(T::bQ, 0);
+        const float fac = s_fac[c];
+        if constexpr (T::kQTm) {
+            if (ok) {
+                const uint32_t row = sbase + T::kStageOff + r * 512;
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {  // 128 coordinates of a term
+                    uint32_t w[32];
 #pragma unroll
-            for (int x = XB - 1; x >= 0; --x) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = cv ? __ldg(src + 16 * x + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float x0 = fabsf(__uint_as_float(v[k] << 16)), x1 = fabsf(__uint_as_float(v[k] & 0xffff0000u));
-                        nan |= !(x0 <= 3.4e38f) || !(x1 <= 3.4e38f);
-                        mx = fmaxf(mx, fmaxf(x0, x1));
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 v = lds128(row + (((8 * x + i) ^ (r & 7)) << 4));
+                        w[4 * i] = v.x;
+                        w[4 * i + 1] = v.y;
+                        w[4 * i + 2] = v.z;
+                        w[4 * i + 3] = v.w;
                     }
+                    umma::st32(lane_base + T::kTmQ + 32 * x, w);
                 }
-            }
-            int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // 2^(7 - ex) brings the largest into [2^7, 2^8)
-            ex = min(max(ex, -100), 120);
-            float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
-            fac = fabsf(A.sm_scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
-            if (nan) fac = __uint_as_float(0x7fc00000u);
-            if (A.sm_scale < 0.f) up = -up;
-            const uint32_t qs = sbase + T::kQOff + 2 * q * T::kQBytes + r * 128;
-#pragma unroll
-            for (int x = 0; x < XB; ++x) {
-                uint32_t th[32], tl[32];  // the terms' words, where they go to tensor memory
-                if (x > 0) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = cv ? __ldg(src + 16 * x + i) : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {  // 16 coordinates: one 16-byte chunk of each term
-                    const uint32_t v[8] = {w[2 * i].x, w[2 * i].y, w[2 * i].z, w[2 * i].w,
-                                           w[2 * i + 1].x, w[2 * i + 1].y, w[2 * i + 1].z, w[2 * i + 1].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float x0 = __uint_as_float(v[2 * k] << 16) * up, x1 = __uint_as_float(v[2 * k] & 0xffff0000u) * up;
-                        float x2 = __uint_as_float(v[2 * k + 1] << 16) * up, x3 = __uint_as_float(v[2 * k + 1] & 0xffff0000u) * up;
-                        hi[k] = e4m3x2_rest(x0, x1);
-                        hi[k] |= e4m3x2_rest(x2, x3) << 16;
-                        lo[k] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
-                    }
-                    if constexpr (T::kQTm) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            th[4 * i + k] = hi[k];
-                            tl[4 * i + k] = lo[k];
-                        }
-                    } else {
-                        const uint32_t at = qs + x * (128 * 128) + ((i ^ (r & 7)) << 4);
-                        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        sts128(at + T::kQBytes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                    }
-                }
-                if constexpr (T::kQTm) {
-                    umma::st32(lane_base + T::kTmQ + 32 * x, th);
-                    umma::st32(lane_base + T::kTmQ + D / 4 + 32 * x, tl);
-                }
-            }
-            if constexpr (T::kQTm) {
                 umma::wait_st();
                 umma::fence_before_sync();
-            } else {
-                umma::fence_proxy_async();
+                warp_arrive(&mbar[T::bQTm]);
             }
-            warp_arrive(&mbar[T::bQ]);
         }
         const int lim = cv ? min(col_lim(c), tok1) : tok1;  // an idle column (zero query) goes the way of the full ones
         const int my_nt = q ? nt[NQ - 1] : nt[0];
         float m_run = -INFINITY, l_run = 0.f;
-        bool ok = true;
-        for (int i = 0; i < my_nt; ++i) {
+        for (int i = 0; ok && i < my_nt; ++i) {
             if (!(ok = wait_bar(T::bSFull + q * NB + i % NB, (i / NB) & 1))) break;
             umma::fence_after_sync();
             const uint32_t ts = lane_base + T::kTmS + (q * NB + i % NB) * KT;
@@ -485,22 +485,39 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const size_t rr = col_row(cv ? c : 0);
             const float l = l_run * 64.f;  // 2^-kSumShift
             const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t o[32];
-                umma::ld32_issue(lane_base + T::kTmO + q * D + 32 * ch, o);
+            // through shared memory, so that the lanes of a warp write whole rows (a row per thread: 6 thousand cycles)
+            const uint32_t stage = sbase + T::kStageOff + (128 * q + 32 * (warp & 3)) * (2 * D);  // 32 rows of 2 D bytes
+            auto fetch = [&](int col, uint32_t (&o)[32]) {  // 32 coordinates of O, NaN where the column sees one
+                umma::ld32_issue(lane_base + T::kTmO + q * D + col, o);
                 umma::wait_ld32(o);
-                if (!cv) continue;
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const int4 at = *reinterpret_cast<const int4 *>(nan_at + 32 * ch + k);
+                    const int4 at = *reinterpret_cast<const int4 *>(nan_at + col + k);
                     if (at.x < lim) o[k] = 0x7fffffffu;
                     if (at.y < lim) o[k + 1] = 0x7fffffffu;
                     if (at.z < lim) o[k + 2] = 0x7fffffffu;
                     if (at.w < lim) o[k + 3] = 0x7fffffffu;
                 }
-                if (uncut) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + rr * D + 32 * ch);
+            };
+            auto put = [&](int chunk, uint4 v) { sts128(stage + lane * (2 * D) + ((chunk ^ (lane & 7)) << 4), v); };
+            auto write_rows = [&](char *base, size_t pitch) {  // row rr of 2 D bytes at base + rr pitch
+                __syncwarp();
+                constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+                const int piece = lane % kLanes;
+#pragma unroll 4
+                for (int n0 = 0; n0 < 32; n0 += kRows) {
+                    const int n = n0 + lane / kLanes;
+                    const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(rr), n);
+                    if (128 * q + 32 * (warp & 3) + n < ncol)
+                        *reinterpret_cast<uint4 *>(base + at * pitch + 16 * piece) = lds128(stage + n * (2 * D) + ((piece ^ (n & 7)) << 4));
+                }
+                __syncwarp();
+            };
+            if (uncut) {
+#pragma unroll 1
+                for (int col = 0; col < D; col += 32) {
+                    uint32_t o[32];
+                    fetch(col, o);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t w[4];
@@ -510,12 +527,21 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                             w[m] = float_to_bf16_bits(l == 0.f ? 0.f : x0) |
                                    (static_cast<uint32_t>(float_to_bf16_bits(l == 0.f ? 0.f : x1)) << 16);
                         }
-                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                        put(col / 8 + k, make_uint4(w[0], w[1], w[2], w[3]));
                     }
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(A.acc + (static_cast<size_t>(split) * rows_total + rr) * D + 32 * ch);
+                }
+                write_rows(reinterpret_cast<char *>(A.out), 2 * D);
+            } else {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += D / 2) {  // half a row of sums fits
+#pragma unroll 1
+                    for (int col = 0; col < D / 2; col += 32) {
+                        uint32_t o[32];
+                        fetch(c0 + col, o);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        for (int k = 0; k < 8; ++k) put(col / 4 + k, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+                    }
+                    write_rows(reinterpret_cast<char *>(A.acc + static_cast<size_t>(split) * rows_total * D + c0), 4 * D);
                 }
             }
             if (cv && !uncut) {
@@ -537,7 +563,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         const uint32_t off_raw = x * (KT * 128) + t * 128 + ((ch ^ (t & 7)) << 4);
         const uint32_t off_dst = (2 * x + (ch >> 2)) * (KT * 128) + t * 128;
         const uint32_t off0 = off_dst + (((2 * (ch & 3)) ^ (t & 7)) << 4), off1 = off_dst + (((2 * (ch & 3) + 1) ^ (t & 7)) << 4);
-        for (int i = 0; i < nt_all; ++i) {
+        const bool go = !T::kQTm || wait_bar(T::bQTm, 0);  // the query terms went through these stages
+        for (int i = 0; go && i < nt_all; ++i) {
             if (!wait_bar(T::bRFull + i % T::RS, (i / T::RS) & 1)) break;
             if (i >= T::VS && !wait_bar(T::bVFree + i % T::VS, (i / T::VS - 1) & 1)) break;
             const uint32_t raw = sbase + T::kROff + (i % T::RS) * T::kKBytes + off_raw;
@@ -593,7 +620,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 const uint64_t dq = umma::make_desc_sw128(sbase + T::kQOff, 16, 1024);
                 const uint64_t dk = umma::make_desc_sw128(sbase + T::kKOff, 16, 1024);
                 const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk), hi = static_cast<uint32_t>(dk >> 32);
-                bool ok = wait_one(T::bQ, 0);
+                bool ok = wait_one(T::kQTm ? T::bQTm : T::bQ, 0);
                 for (int i = 0; ok && i < nt_all; ++i) {
                     const int st = i % T::KS, buf = i % NB;
                     ok = wait_one(T::bKFull + st, (i / T::KS) & 1);
