@@ -131,6 +131,13 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Two fp32 lanes side by side: one issue slot for two multiply-adds or sums.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi)
 {
@@ -245,10 +252,12 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     }
     const int q0 = qt * A.qpc;
     const int ncol = min(A.qpc, A.Tq - q0) * G;
+    const int ginv = (65536 + G - 1) / G;  // c / G = c ginv >> 16 for c < 256
     auto col_row = [&](int c) -> size_t {
-        return (static_cast<size_t>(b) * A.Tq + q0 + c / G) * A.Hq + static_cast<size_t>(kvh) * G + c % G;
+        const int t = c * ginv >> 16;
+        return (static_cast<size_t>(b) * A.Tq + q0 + t) * A.Hq + static_cast<size_t>(kvh) * G + (c - t * G);
     };
-    auto col_lim = [&](int c) -> int { return max(0, L - A.Tq + q0 + c / G + 1); };
+    auto col_lim = [&](int c) -> int { return max(0, L - A.Tq + q0 + (c * ginv >> 16) + 1); };
     const size_t rows_total = static_cast<size_t>(A.B) * A.Tq * A.Hq;
     const int tok0 = split * A.pages_per_split * P;
     const int tok1 = min(col_lim(ncol - 1), uncut ? A.max_blocks * P : tok0 + A.pages_per_split * P);
@@ -349,48 +358,51 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     float *s_fac = reinterpret_cast<float *>(smem + T::kFacOff);
     if (warp < T::kMmaWarp) {
         // ================= query operands =================
-        // Coordinates 8 j .. 8 j + 7 of a row by lane j of its D / 8 lanes, four loads of a warp in flight.  A thread per
-        // row, all unrolled, took 10-14 thousand cycles of a unit's 240: most of its ~2000 instructions ran once, from
-        // memory, and a load touched 32 rows.
-        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
-        const int j = lane % kLanes;
-#pragma unroll 1
-        for (int i0 = warp * kBatch; i0 < 128 * NQ / kRows; i0 += T::kMmaWarp * kBatch) {
-            uint4 w[kBatch];
+        // Coordinates 8 j .. 8 j + 7 of a row by lane j of its D / 8 lanes.  All rows of a warp are copied first, each to where
+        // its two terms go (which take the same bytes), so that one latency is paid; then a short loop splits them.  A
+        // thread per row, all unrolled, took 10-14 thousand cycles of a unit's 240: ~2000 instructions that run once, and
+        // loads that touch 32 rows each.
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+        const int j = lane % kLanes, sub = lane / kLanes;
+        auto row_at = [&](int c) -> uint32_t { return T::kQTm ? T::kStageOff + c * 512 : T::kQOff + 2 * (c >> 7) * T::kQBytes + (c & 127) * 128; };
+        constexpr uint32_t kLo = T::kQTm ? 256 : T::kQBytes;  // from the first term to the second
+        const uint32_t raw = (j & 7) * 16 + (T::kQTm ? (j >> 3) * 128 : (j >> 3) * kLo);
+#pragma unroll 2
+        for (int n = warp; n < 128 * NQ / kRows; n += T::kMmaWarp) {
+            const int c = n * kRows + sub;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(sbase + row_at(c) + raw), "l"(A.q + col_row(c < ncol ? c : 0) * D + 8 * j), "r"(c < ncol ? 16 : 0) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+        for (int n = warp; n < 128 * NQ / kRows; n += T::kMmaWarp) {
+            const int c = n * kRows + sub;
+            const uint4 w = lds128(sbase + row_at(c) + raw);  // what this lane copied
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            uint32_t m = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu), __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+            m = max(m & 0xffffu, m >> 16);  // the largest magnitude's bits
 #pragma unroll
-            for (int n = 0; n < kBatch; ++n) {
-                const int c = (i0 + n) * kRows + lane / kLanes;
-                w[n] = c < ncol ? __ldg(reinterpret_cast<const uint4 *>(A.q + col_row(c) * D) + j) : make_uint4(0u, 0u, 0u, 0u);
+            for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int ex = min(max(static_cast<int>(m >> 7) - 127, -100), 120);  // 2^(7 - ex) brings the largest into [2^7, 2^8)
+            float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
+            if (j == 0)  // >= 0: a negative scale goes into q's sign; an infinity or NaN makes the row NaN
+                s_fac[c] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                        : fabsf(A.sm_scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
+            if (A.sm_scale < 0.f) up = -up;
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x0 = __uint_as_float(v[2 * k] << 16) * up, x1 = __uint_as_float(v[2 * k] & 0xffff0000u) * up;
+                float x2 = __uint_as_float(v[2 * k + 1] << 16) * up, x3 = __uint_as_float(v[2 * k + 1] & 0xffff0000u) * up;
+                hi[k] = e4m3x2_rest(x0, x1);
+                hi[k] |= e4m3x2_rest(x2, x3) << 16;
+                lo[k] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
             }
-#pragma unroll
-            for (int n = 0; n < kBatch; ++n) {
-                const int c = (i0 + n) * kRows + lane / kLanes;
-                const uint32_t v[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
-                uint32_t m = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu), __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
-                m = max(m & 0xffffu, m >> 16);  // the largest magnitude's bits
-#pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const int ex = min(max(static_cast<int>(m >> 7) - 127, -100), 120);  // 2^(7 - ex) brings the largest into [2^7, 2^8)
-                float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
-                if (j == 0)  // >= 0: a negative scale goes into q's sign; an infinity or NaN makes the row NaN
-                    s_fac[c] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
-                                            : fabsf(A.sm_scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
-                if (A.sm_scale < 0.f) up = -up;
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float x0 = __uint_as_float(v[2 * k] << 16) * up, x1 = __uint_as_float(v[2 * k] & 0xffff0000u) * up;
-                    float x2 = __uint_as_float(v[2 * k + 1] << 16) * up, x3 = __uint_as_float(v[2 * k + 1] & 0xffff0000u) * up;
-                    hi[k] = e4m3x2_rest(x0, x1);
-                    hi[k] |= e4m3x2_rest(x2, x3) << 16;
-                    lo[k] = e4m3x2(x0, x1) | (e4m3x2(x2, x3) << 16);
-                }
-                // chunks of 16 coordinates, the 128-byte swizzle of the operand; on the way to tensor memory rows of both terms
-                const uint32_t at = (((j >> 1) ^ (c & 7)) << 4) + 8 * (j & 1) +
-                                    (T::kQTm ? T::kStageOff + c * 512 : T::kQOff + 2 * (c >> 7) * T::kQBytes + (c & 127) * 128);
-                *reinterpret_cast<uint2 *>(smem + at) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(smem + at + (T::kQTm ? 256 : T::kQBytes)) = make_uint2(lo[0], lo[1]);
-            }
+            // chunks of 16 coordinates, the 128-byte swizzle of the operand
+            const uint32_t at = row_at(c) + (((j >> 1) ^ (c & 7)) << 4) + 8 * (j & 1);
+            __syncwarp();  // every lane of the row has read
+            *reinterpret_cast<uint2 *>(smem + at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(smem + at + kLo) = make_uint2(lo[0], lo[1]);
         }
         if constexpr (!T::kQTm) umma::fence_proxy_async();
         warp_arrive(&mbar[T::bQ]);
@@ -485,11 +497,16 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const size_t rr = col_row(cv ? c : 0);
             const float l = l_run * 64.f;  // 2^-kSumShift
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            bool nan = false;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) nan |= nan_at[32 * k + lane] != INT_MAX;
+            nan = __any_sync(0xffffffffu, nan);
             // through shared memory, so that the lanes of a warp write whole rows (a row per thread: 6 thousand cycles)
             const uint32_t stage = sbase + T::kStageOff + (128 * q + 32 * (warp & 3)) * (2 * D);  // 32 rows of 2 D bytes
             auto fetch = [&](int col, uint32_t (&o)[32]) {  // 32 coordinates of O, NaN where the column sees one
                 umma::ld32_issue(lane_base + T::kTmO + q * D + col, o);
                 umma::wait_ld32(o);
+                if (!nan) return;
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const int4 at = *reinterpret_cast<const int4 *>(nan_at + col + k);
@@ -522,11 +539,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                     for (int k = 0; k < 4; ++k) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float x0 = __uint_as_float(o[8 * k + 2 * m]) * inv, x1 = __uint_as_float(o[8 * k + 2 * m + 1]) * inv;
-                            w[m] = float_to_bf16_bits(l == 0.f ? 0.f : x0) |
-                                   (static_cast<uint32_t>(float_to_bf16_bits(l == 0.f ? 0.f : x1)) << 16);
-                        }
+                        for (int m = 0; m < 4; ++m)  // with nothing seen O is zero
+                            w[m] = bf16x2_of(__uint_as_float(o[8 * k + 2 * m]) * inv, __uint_as_float(o[8 * k + 2 * m + 1]) * inv);
                         put(col / 8 + k, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
