@@ -368,7 +368,9 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
  * The query enters the products exactly (two e4m3 terms of a power-of-two multiple;
  * elements below 2^-9 of the head's largest lose bits below 2^-17 of it), the
  * probabilities as two e4m3 terms (about 8 bits), sums are fp32.
- * A page with a bad block id (TQ_DEVERR_BLOCK_RANGE) counts as hidden.
+ * A page with a bad block id (TQ_DEVERR_BLOCK_RANGE) counts as hidden.  Rows behind a
+ * sequence's end may hold anything.  A sequence of length 0 gives zeros.
+ * One launch with splits 1, else two (the pieces, and what joins them).
  */
 int tq_decode_splits_fp8(tq_handle h, int batch, int num_kv_heads, int max_blocks_per_seq, int page_size);
 size_t tq_workspace_bytes_fp8(tq_handle h, int batch, int num_q_heads, int splits);
@@ -386,6 +388,9 @@ tq_status tq_decode_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t 
  * splits: pieces of the (sequence, kv head, query block) units that fill no whole
  * wave of CTAs, 0 = tq_prefill_splits_fp8(...); workspace: ws_bytes >=
  * tq_workspace_bytes_fp8(h, batch * q_tokens, num_q_heads, splits).
+ * Up to eight (query token, head) columns per kv head run as in the decode; with more
+ * the probabilities enter in fp16 (11 bits; those below 2^-20 of a row's largest
+ * coarser) and the values as stored.  A query token that sees nothing gives zeros.
  */
 int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int num_q_heads, int num_kv_heads,
                           int max_blocks_per_seq, int page_size);

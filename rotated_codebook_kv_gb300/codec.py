@@ -296,8 +296,8 @@ class Codec:
                 self.prefill_splits_fp8(B, tq, Hq, num_kv_heads, maxb, page_size)
         if workspace is None:
             workspace = self.workspace_fp8(B * max(tq, 1), Hq, splits)
-        if workspace.get_device() != self.device:
-            raise ValueError(f"workspace must be on cuda:{self.device}, the device of this Codec")
+        if workspace.get_device() != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{self.device}, the device of this Codec")
         if out is None:
             out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         op = self._flat(out, torch.bfloat16, q.numel(), "out")

@@ -9,6 +9,14 @@
 // Work is cut into units of 16 coordinates of one row (32 bytes of bf16): a rotated
 // unit i is the eight pairs 8 i .. 8 i + 7 (two 16-byte chunks, rot_dim / 2 apart or
 // adjacent by the style), the others are 16 coordinates that pass through.
+//
+// Bound: HBM, in one pass (every row is read and written once, a page's earlier rows only where its scale grows).
+// Measured on a GB300 (copy 6783 GB/s): to bf16 pages 15,500 tokens of 16 query and 8 kv heads of 256 87 us = 5.8 TB/s, two
+// rows of a thread in flight; to 8-bit pages 32k tokens of 32 query and 8 kv heads of 128 163 us = 4.6 TB/s, of which the
+// query rows take ~90 (6.0 TB/s) and the pages ~74, bound by the latency of a chain (slots, rows, maximum, codes) and
+// the instructions of the rotation and the codes.  A step's few tokens: 11 us, the host's checks and launch.
+// Tried for the pages and slower: rows through shared memory by asynchronous copies (166-172 us; ragged chunks 53 against
+// 45), page and query blocks in turn instead of one after the other (184; every fourth block 152, but ragged chunks 48).
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -425,7 +433,8 @@ cudaError_t launch_bf16(const AppendArgs &a, cudaStream_t st)
 {
     constexpr int RL = kThreads / (D / kUnit);
     const int rows = a.Hq + 2 * a.Hkv;
-    // few tokens: a block per RL rows, for latency; many: the rows of a token in one block
+    // Few tokens: a block per RL rows, for latency.  Many: the rows of a token in one block, which reads slot and position
+    // once.  The limit is where either fills the GPU's SMs several times over.
     const unsigned gy = a.T < 1024 ? static_cast<unsigned>((rows + RL - 1) / RL) : 1u;
     append_bf16_kernel<D><<<dim3(static_cast<unsigned>(a.T), gy), kThreads, 0, st>>>(a);
     return cudaGetLastError();
