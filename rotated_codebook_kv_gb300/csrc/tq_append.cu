@@ -12,11 +12,12 @@
 //
 // Bound: HBM, in one pass (every row is read and written once, a page's earlier rows only where its scale grows).
 // Measured on a GB300 (copy 6783 GB/s): to bf16 pages 15,500 tokens of 16 query and 8 kv heads of 256 87 us = 5.8 TB/s, two
-// rows of a thread in flight; to 8-bit pages 32k tokens of 32 query and 8 kv heads of 128 163 us = 4.6 TB/s, of which the
-// query rows take ~90 (6.0 TB/s) and the pages ~74, bound by the latency of a chain (slots, rows, maximum, codes) and
+// rows of a thread in flight; to 8-bit pages 32k tokens of 32 query and 8 kv heads of 128 147 us = 5.1 TB/s, of which the
+// query rows take ~90 (6.0 TB/s) and the pages ~60, bound by the latency of a chain (slots, rows, maximum, codes) and
 // the instructions of the rotation and the codes.  A step's few tokens: 11 us, the host's checks and launch.
-// Tried for the pages and slower: rows through shared memory by asynchronous copies (166-172 us; ragged chunks 53 against
-// 45), page and query blocks in turn instead of one after the other (184; every fourth block 152, but ragged chunks 48).
+// Tried for the pages and slower when they stood at 163: rows through shared memory by asynchronous copies (166-172 us;
+// ragged chunks 53 against 45), page and query blocks in turn instead of one after the other (184; every fourth block 152,
+// but ragged chunks 48).
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -289,15 +290,20 @@ __device__ __forceinline__ float finite_abs(float x)
 //
 // A block finds the runs (consecutive tokens on consecutive slots of one page) that begin among its `chunk` tokens; groups
 // of its warps take items (run, kv head, keys or values) in turn.  A page's scale needs its rows twice, for the maximum
-// and for the codes: a group has one, two or four warps, so that each lane holds four units, rotated, in registers
-// between, and only a group of several meets at a barrier of its own.
+// and for the codes: a group has two or four warps, so that each lane holds few units, rotated, in registers
+// between; a group meets at a barrier of its own.
+//
+// At head dim 128 a lane holds two units, with three blocks on an SM, at 256 four with two (32k tokens 150 us against 163 at
+// 128, and 208 against 216 at 256; chunks of 200 to 1500 tokens 83 against 91, and 132 against 111).
+constexpr int units_held(int d) { return d == 128 ? 2 : 4; }
+constexpr int group_warps(int d, int p) { return p * (d / kUnit) / (32 * units_held(d)); }
 template <int D, int P>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 2)
     append_fp8_kernel(const AppendArgs A, const int kv_blocks, const int chunk)
 {
     constexpr int U = D / kUnit;
-    constexpr int NK = 4;                       // units of an item per lane: the lane's unit of rows row0, row0 + kRowStep, ...
-    constexpr int W = P * U / (32 * NK);        // warps of a group
+    constexpr int NK = units_held(D);           // units of an item per lane: the lane's unit of rows row0, row0 + kRowStep, ...
+    constexpr int W = group_warps(D, P);        // warps of a group
     constexpr int kGroups = kThreads / 32 / W;
     constexpr int kRowStep = 32 * W / U;
     if (blockIdx.x >= kv_blocks) {
@@ -398,13 +404,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int j = 0; j < 8; ++j) amax = max3(amax, finite_abs(a[n][j]), finite_abs(b[n][j]));
         }
         amax = warp_max(amax);
-        if constexpr (W > 1) {
-            if (lane == 0) s_max[group][flip][warp % W] = amax;
-            // two sets, so that the next item's do not wait for this one's readers
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
+        if (lane == 0) s_max[group][flip][warp % W] = amax;
+        // two sets, so that the next item's do not wait for this one's readers
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
 #pragma unroll
-            for (int k = 0; k < W; ++k) amax = fmaxf(amax, s_max[group][flip][k]);
-        }
+        for (int k = 0; k < W; ++k) amax = fmaxf(amax, s_max[group][flip][k]);
         const float need = pow2_scale(amax);
         const bool keep = o > 0 && old > 0.f && old <= 3.402823466e38f;  // the page's rows and scale so far
         const float scale = keep ? fmaxf(old, need) : need;
@@ -444,11 +448,12 @@ template <int D, int P>
 cudaError_t launch_fp8(const AppendArgs &a, int num_sms, cudaStream_t st)
 {
     // Few tokens: every one may begin a page's run, so a block for each.  Many: a page's rows of tokens per block (about
-    // one run begins among them).  A block takes two to eight items at a time, so further blocks over the heads only
-    // where there would be fewer than eight blocks an SM.
+    // one run begins among them).  A block takes an item for each of its groups at a time, so further blocks over the
+    // heads only where there would be fewer than four blocks an SM (eight: 32k tokens on pages of 32 152 us against 144).
     const int chunk = a.T < 1024 ? 1 : P;
     const int64_t kv = (a.T + chunk - 1) / chunk;
-    const int64_t want = (8LL * num_sms + kv - 1) / kv, most = (2LL * a.Hkv + 7) / 8;
+    constexpr int kGroups = kThreads / 32 / group_warps(D, P);
+    const int64_t want = (4LL * num_sms + kv - 1) / kv, most = (2LL * a.Hkv + kGroups - 1) / kGroups;
     const int gy = static_cast<int>(want < most ? want : most < 65535 ? most : 65535);
     const int64_t per = static_cast<int64_t>(kThreads / (D / kUnit)) * gy;
     const int64_t q = (a.T * ((a.Hq + kQueryRows - 1) / kQueryRows) + per - 1) / per;
