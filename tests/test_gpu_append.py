@@ -323,3 +323,21 @@ def test_append_refusals():
         native.tq_append_kv_fp8(codec.handle, 0, x.data_ptr(), x.data_ptr(), 3, 0, H, 0, 128, 256, 0, 0, 0, 0, 0,
                                 s.data_ptr(), kp.data_ptr(), vp.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, nb, 0, 0)
     assert e.value.status == native.TQ_ERR_INVALID_ARG and "strides" in str(e.value)
+
+
+def test_append_refuses_what_no_grid_holds():
+    codec = _codec(128)
+    x = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    s = torch.zeros(1, dtype=torch.int64, device=DEV)
+    pools = codec.alloc_pools_fp8(1, 2, 16)
+
+    def refused(word, T=1, Hq=2, Hkv=2):
+        with pytest.raises(native.TQError) as e:
+            native.tq_append_kv_fp8(codec.handle, x.data_ptr(), x.data_ptr(), x.data_ptr(), T, Hq, Hkv, Hq * 128, Hkv * 128,
+                                    Hkv * 128, 0, 0, 0, 0, 0, s.data_ptr(), *[p.data_ptr() for p in pools], 16, 1, x.data_ptr(), 0)
+        assert e.value.status == native.TQ_ERR_UNSUPPORTED and word in str(e.value), str(e.value)
+
+    refused("too many tokens", T=1 << 30)
+    refused("too many tokens", T=1 << 28, Hq=64)
+    refused("heads", Hq=(1 << 18) + 1)
+    refused("heads", Hkv=(1 << 18) + 1)

@@ -387,6 +387,38 @@ def test_refusals():
         codec.decode_attention_fp8(q.cpu(), *pools, table, lens, 2, 16, c["nb"], 0.1)
 
 
+def test_refusals_of_sizes_and_of_strided_scratch():
+    p = case(128, 16, 2, 2, [40], Tq=20, seed=9)
+    codec = _codec(128)
+    pools, table, lens, q = gpu_pools(p), p["table"].to(DEV), p["lens"].to(DEV), p["q"].to(DEV)
+    head = (codec.handle, q.data_ptr(), *[x.data_ptr() for x in pools], table.data_ptr(), lens.data_ptr())
+
+    def refused(status, word, B=1, tq=20, Hq=4, Hkv=2, splits=1):
+        with pytest.raises(native.TQError) as e:
+            native.tq_prefill_attention_fp8(*head, B, tq, Hq, Hkv, 16, table.shape[1], p["nb"], 0.1, splits, 0, 0, q.data_ptr(), 0)
+        assert e.value.status == status and word in str(e.value), str(e.value)
+
+    refused(native.TQ_ERR_INVALID_ARG, "bad sizes", tq=0)
+    refused(native.TQ_ERR_UNSUPPORTED, "too many", B=1 << 20, tq=1 << 12)
+    refused(native.TQ_ERR_UNSUPPORTED, "too many", B=1 << 24, tq=20, splits=512)
+    refused(native.TQ_ERR_INVALID_ARG, "workspace", splits=2)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)[::2]
+    with pytest.raises(ValueError):
+        codec.prefill_attention_fp8(q, *pools, table, lens, 2, 16, p["nb"], 0.1, splits=2, workspace=ws)
+    with pytest.raises(ValueError):
+        codec.prefill_attention_fp8(q[0], *pools, table, lens, 2, 16, p["nb"], 0.1)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("sm", [-0.07, 0.0])
+def test_score_scales_of_either_sign_and_zero(d, sm):
+    for Tq in (None, 2, 24):
+        c = case(d, 16, 2, 2, [90, 33], Tq=Tq, seed=12)
+        ref, bound = reference(c, sm)
+        for splits in (1, 2):
+            check(run(c, splits, sm), ref, bound)
+
+
 @pytest.mark.parametrize("d,P", [(128, 16), (256, 32)])
 def test_a_prompt_and_some_tokens_end_to_end(d, P):
     """The set as it is used: append a prompt's chunks and attend to them, then token by token, on both kinds of
