@@ -892,16 +892,20 @@ extern "C" int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int n
         return tq_decode_splits_fp8(h, batch, num_kv_heads, max_blocks_per_seq, page_size);
     const int qpc = tq::fp8::prefill_tc_columns(tq::handle_codec(h).d) / G;
     const long long units = static_cast<long long>(batch) * num_kv_heads * ((q_tokens + qpc - 1) / qpc);
-    // One CTA per SM.  Whole waves of units stay whole; of the rest the pieces (at least 512 tokens each) are what makes the
-    // last waves shortest: ceil(rest * n / SMs) / n of a unit's time, and a few percent for each further piece.
-    const long long sms = tq::handle_codec(h).num_sms, rest = units % sms;
-    const long long most = (static_cast<long long>(max_blocks_per_seq) * page_size + 511) / 512;
+    // One CTA per SM.  Whole waves of units stay whole; the rest is cut into the pieces (of 512 tokens at least) that take
+    // the least time, in steps of 64 tokens (about a microsecond) of the longest sequence: waves of pieces, each with a
+    // start and an end, the merge's launch, and 45 pieces' sums written and read a step.  Measured, in one | two | three |
+    // four | five pieces, us: 128 units of 128 steps at head dim 256 136 | 159 | 170 | 178 | 189, 256 units 212 | 232 | 230
+    // | 227 | 219, 64 units 134 | 86 | 102 | 96 | 86; at 128, 512 units of 256 steps 869 | 840 | 834 | 819 | 816, 128 units
+    // 259 | 281 | 294 | 297 | 310, 256 units of up to 128 steps 204 | 204 | 196 | 192 | 194.
+    const tq::Codec &c = tq::handle_codec(h);
+    const long long sms = c.num_sms, rest = units % sms, tokens = static_cast<long long>(max_blocks_per_seq) * page_size;
+    const double steps = static_cast<double>((tokens + 63) / 64), start = c.d == 128 ? 5 : 9, cut_start = c.d == 128 ? 6 : 11;
     if (rest == 0) return 1;
-    if (units < sms) return tq::clamp_splits((2 * sms + units - 1) / units, most);
     int best = 1;
-    double least = 1.0;
-    for (int n = 2; n <= 4 && n <= most; ++n) {
-        const double t = static_cast<double>((rest * n + sms - 1) / sms) / n + 0.03 * n;
+    double least = steps + start;
+    for (int n = 2; n <= 64 && 512LL * (n - 1) < tokens; ++n) {
+        const double t = static_cast<double>((rest * n + sms - 1) / sms) * (steps / n + cut_start) + 3 + rest * n / 45.;
         if (t < least) {
             least = t;
             best = n;
