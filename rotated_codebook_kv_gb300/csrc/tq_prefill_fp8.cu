@@ -25,9 +25,9 @@
 //
 // Bound: the softmax warps.  A tile pair's step takes ~2000 cycles at head dim 128; its MMAs take 1280 (scores 16 of 48
 // cycles, held there by reading both operands from shared memory; P.V 8 of 64).  Measured on a GB300: the last 4096 of
-// 16,384 tokens, 32 query and 8 kv heads of 128, 836 us = 1.15 PFLOP/s of useful products (cuBLAS bf16: 1.91), tensor pipe
-// 53 % active; 64 tokens of 32 sequences of 1024 to 8192 187 us; the last 1000 of 2 sequences of 5000 to 8192, 16 and 8
-// heads of 256, 221 us.
+// 16,384 tokens, 32 query and 8 kv heads of 128, 810 us = 1.19 PFLOP/s of useful products (cuBLAS bf16: 1.91), tensor pipe
+// 53 % active; 64 tokens of 32 sequences of 1024 to 8192 188 us; the last 1000 of 2 sequences of 5000 to 8192, 16 and 8
+// heads of 256, 209 us.
 #include <climits>
 
 #include "tq_fp8.cuh"
