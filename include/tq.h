@@ -367,7 +367,10 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
  *   specified, and calls that may overlap need one each.
  * The query enters the products exactly (two e4m3 terms of a power-of-two multiple;
  * elements below 2^-9 of the head's largest lose bits below 2^-17 of it), the
- * probabilities as two e4m3 terms (about 8 bits), sums are fp32.
+ * probabilities as two e4m3 terms: off by 2^-8 of themselves, or 2^-18 of the largest
+ * p * v_scale among their 32 positions where that is more, so that a long weak tail behind
+ * a strong token keeps its share; a p * v_scale below 2^-126 of the largest counts as
+ * nothing.  Sums are fp32.
  * A page with a bad block id (TQ_DEVERR_BLOCK_RANGE) counts as hidden.  Rows behind a
  * sequence's end may hold anything.  A sequence of length 0 gives zeros.
  * One launch with splits 1, else two (the pieces, and what joins them).
