@@ -392,8 +392,9 @@ tq_status tq_decode_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t 
  * wave of CTAs, 0 = tq_prefill_splits_fp8(...); workspace: ws_bytes >=
  * tq_workspace_bytes_fp8(h, batch * q_tokens, num_q_heads, splits).
  * Up to eight (query token, head) columns per kv head run as in the decode; with more
- * the probabilities enter in fp16 (11 bits; those below 2^-20 of a row's largest
- * coarser) and the values as stored.  A query token that sees nothing gives zeros.
+ * the probabilities enter in fp16 (off by 2^-12 of themselves, or 2^-29 of the row's largest
+ * p * v_scale where that is more) and the values as stored.  A query token that sees
+ * nothing gives zeros.
  */
 int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int num_q_heads, int num_kv_heads,
                           int max_blocks_per_seq, int page_size);

@@ -690,8 +690,8 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args A, const int6
     }
 }
 
-// The same for the prefill's rows, many in few pieces: a warp per row, D / 32 coordinates a lane; the rows of the first
-// A.whole units are done.
+// The same for the prefill's rows, many in few pieces, with denominators in kSumUnit: a warp per row, D / 32 coordinates a
+// lane; the rows of the first A.whole units are done.
 template <int D>
 __global__ void __launch_bounds__(128) merge_rows_fp8_kernel(const Args A, const int64_t rows)
 {
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(128) merge_rows_fp8_kernel(const Args A, const
             }
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float inv = den == 0.f ? 0.f : kSumUnit / den;
     uint32_t *dst = reinterpret_cast<uint32_t *>(A.out + row * D + lane * E);
 #pragma unroll
     for (int i = 0; i < E; i += 2)

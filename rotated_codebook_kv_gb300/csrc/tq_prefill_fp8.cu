@@ -7,7 +7,7 @@
 //                                      (exact) in shared memory, N = D coordinates j
 // with y = sm_scale log2(e) 2^-e ks[page] S + log2 vs[page], P = 2^(y - m), m a running maximum that is
 // only moved when the maximum has grown far beyond it (below), and the
-// denominator the sum of P / vs in fp32.
+// denominator the sum of kSumUnit P / vs in fp32.
 //
 // A CTA takes NQ tiles of 128 columns, (query token, head) pairs of one sequence and kv head, and the
 // KT-token tiles that they see (of units behind the last whole wave: a piece of those).  Two tiles at head
@@ -61,7 +61,7 @@ struct Tc {
     static constexpr uint32_t kKOff = kQOff + (kQTm ? 0 : 2 * NQ * kQBytes);
     static constexpr uint32_t kROff = kKOff + KS * kKBytes;
     static constexpr uint32_t kVOff = kROff + RS * kKBytes;
-    static constexpr uint32_t kInfoOff = kVOff + VS * 2 * kKBytes;  // [ring][GR] (ks, log2 vs, 2^-6 / vs, -)
+    static constexpr uint32_t kInfoOff = kVOff + VS * 2 * kKBytes;  // [ring][GR] (ks, log2 vs, kSumUnit / vs, -)
     static constexpr uint32_t kOkOff = kInfoOff + kRing * GR * 16;  // [ring] bit g: group g's page is valid
     static constexpr uint32_t kBarOff = kOkOff + kRing * 4;
     // barriers
@@ -94,13 +94,13 @@ struct Tc {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// The reference m of a column's probabilities is set kAim above the scores' maximum and O rescaled only when the maximum
-// has since passed m by kLazy (log2 units): P = 2^(y - m) is at most 2^12 in fp16 (65504 its largest), 2^-4 after a
-// rescale, where everything down to 2^-10 of the largest keeps 11 bits and down to 2^-20 something.  A rescale waits
-// for the tensor core and moves all of O, so a few strong tokens in every tile made it the longest step of many tiles.
-constexpr float kAim = 4.f, kLazy = 12.f;
-// Denominators are summed as 2^-6 P / vs: vs in 2^-100 .. 2^119 neither overflows nor flushes.
-constexpr float kSumShift = -6.f;
+// The reference m of a column's probabilities is set 2^4 below the scores' maximum and O rescaled only when the maximum
+// has since passed m by kLazy (log2 units): the largest P = 2^(y - m) so far lies in 2^4 .. 2^15 (fp16 ends at 65504), so
+// that everything down to 2^-18 of it keeps 11 bits and a P is never off by more than 2^-29 of it (2^17 tokens behind a
+// strong one: 2^-12 of that in all; with m above the maximum their sum lost a tenth).  A rescale waits for the tensor core
+// and moves all of O, so a few strong tokens in every tile made it the longest step of many tiles.  Long prefill below, the
+// same with 2^-1 | 2^2 | 2^4 | 2^6 | 2^8: 814 | 822 | 825 | 828 | 832 us; 64 tokens of 32 sequences 187 | 190 | 195 | 196 | 198.
+constexpr float kAim = -4.f, kLazy = 15.f;
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -171,7 +171,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
-// A column's 64 scores of a tile, and the tile's scales: a = fac ks, b = log2 vs, inv = 2^-6 / vs per 16 tokens.
+// A column's 64 scores of a tile, and the tile's scales: a = fac ks, b = log2 vs, inv = kSumUnit / vs per 16 tokens.
 struct Scores {
     uint32_t v[64];
     float a[4], b[4], inv[4];
@@ -199,7 +199,7 @@ __device__ __forceinline__ float tile_max(const Scores &s, uint32_t okm, int rem
     return top;
 }
 
-// P = 2^(y - ref) in fp16, two tokens per word; returns the sum of 2^-6 P / vs.
+// P = 2^(y - ref) in fp16, two tokens per word; returns the sum of kSumUnit P / vs.
 template <bool WHOLE>
 __device__ __forceinline__ float tile_exp(const Scores &s, uint32_t (&p)[32], float ref, uint32_t okm, int rem)
 {
@@ -502,8 +502,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         if (ok && my_nt > 0) {
             umma::fence_after_sync();
             const size_t rr = col_row(cv ? c : 0);
-            const float l = l_run * 64.f;  // 2^-kSumShift
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = l_run == 0.f ? 0.f : kSumUnit / l_run;
             bool nan = false;
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) nan |= nan_at[32 * k + lane] != INT_MAX;
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             if (cv && !uncut) {
                 float *ml = A.ml + (static_cast<size_t>(split) * rows_total + rr) * 2;
                 ml[0] = m_run;
-                ml[1] = l;
+                ml[1] = l_run;
             }
         } else if (cv && my_nt == 0) {
             dead_row(c);
@@ -723,7 +722,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const int slot = i % T::kRing;
             if (mine) {
                 const float lv = log2_scale(vs);
-                const float4 f = make_float4(ks, lv, fast_exp2(kSumShift - lv), 0.f);
+                const float4 f = make_float4(ks, lv, fast_exp2(-lv) * kSumUnit, 0.f);
                 float4 *info = reinterpret_cast<float4 *>(smem + T::kInfoOff) + slot * GR;
                 if (P == 16) {
                     info[lane] = f;

@@ -63,8 +63,8 @@ def reference(c, sm=None):
       * up to eight columns, P as two e4m3 terms of fp16(2^8 p), the largest p vs of a round of 32 tokens at 1: the first
         leaves at most 2^-4 of p, the second 2^-4 of that or half its least step, 2^-10: (2^-8 + 2^-11) p +
         2^-18 max_round(p vs) |code| (1 + 2^-14 for fp16's own least steps);
-      * more columns, P in fp16: 2^-11 p, or half the least step, 2^-25, where the largest p vs so far stands at 2^8 or
-        above: 2^-33 max(p vs) |code|;
+      * more columns, P in fp16: 2^-11 p, or half the least step, 2^-25, where the largest p vs so far stands at 2^4 or
+        above: 2^-29 max(p vs) |code|;
       * scores, exponentials and fp32 sums as in paged8.attention.
     """
     d, P, G, L = c["d"], c["P"], c["G"], c["L"]
@@ -95,7 +95,7 @@ def reference(c, sm=None):
                 top = np.repeat(top.reshape(-1, 32).max(1), 32)[:n]
                 eps, low = 2.0 ** -8 + 2.0 ** -11, 2.0 ** -18 * (1 + 2.0 ** -14) * top
             else:
-                eps, low = 2.0 ** -11, np.full(n, 2.0 ** -33 * pv.max())
+                eps, low = 2.0 ** -11, np.full(n, 2.0 ** -29 * pv.max())
             dA = (p * dx) @ av[:n] + (p @ dx) * A
             out[i, h] = o
             bound[i, h] = 2.0 ** -8 * np.abs(o) + eps * A + low @ ac[:n] + dA + (n / 8 + 4) * 2.0 ** -23 * A + 1e-30
@@ -125,8 +125,23 @@ def test_decode_keeps_the_tail(d, P, G, L, Tq, gap):
         check(run(c, splits), ref, bound)
 
 
+@pytest.mark.parametrize("gap", [11.0, 13.0, 15.0])
+@pytest.mark.parametrize("d,P,G,L,Tq", [
+    (128, 16, 1, 131072, 9),
+    (128, 32, 4, 4096, 3),
+    (256, 16, 1, 4096, 9),
+    (256, 32, 3, 65536, 4),
+])
+def test_prefill_keeps_the_tail(d, P, G, L, Tq, gap):
+    c = case(d, P, G, L, Tq, gap, seed=int(gap), strong_value=0.02 if gap == 13.0 else 0.0)
+    ref, bound = reference(c)
+    assert float((bound / np.abs(ref)).max()) < 0.06
+    for splits in (1, 0):
+        check(run(c, splits), ref, bound)
+
+
 @pytest.mark.parametrize("d", [128, 256])
-@pytest.mark.parametrize("Tq", [None, 3])
+@pytest.mark.parametrize("Tq", [None, 3, 12])
 @pytest.mark.parametrize("at", [5000, 8191 - 40])
 def test_strong_token_behind_and_within_the_tail(d, Tq, at):
     """The strong token after the tail (all before it is scaled down) and between two halves of it."""
