@@ -344,7 +344,8 @@ tq_status tq_append_kv_bf16(tq_handle h, const uint16_t *q, const uint16_t *k, c
  *       token of the page, or the same slot again, stands up to 32 tokens before a
  *       run of consecutive slots, that run is skipped (its q_out rows are written) and
  *       TQ_DEVERR_SLOT_ORDER set; farther apart they race.  A token with a bad position
- *       inside a run keeps its place but is not written.
+ *       inside a run keeps its place but is not written; a run of none but such tokens
+ *       leaves the page, its scale too, as it was.
  * Everything else as in tq_append_kv_bf16.
  */
 tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, const uint16_t *v, int64_t T,

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 2)
         }
         const float old = o > 0 ? *scale_at : 0.f;
         float a[NK][8], b[NK][8];
-        float amax = 0.f;
+        float amax = -1.f;  // stays below zero where no token of the run is written
         unsigned live = 0;  // units that are written
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 2)
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
 #pragma unroll
         for (int k = 0; k < W; ++k) amax = fmaxf(amax, s_max[group][flip][k]);
+        if (amax < 0.f) continue;  // the page stays as it was
         const float need = pow2_scale(amax);
         const bool keep = o > 0 && old > 0.f && old <= 3.402823466e38f;  // the page's rows and scale so far
         const float scale = keep ? fmaxf(old, need) : need;

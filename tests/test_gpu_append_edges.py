@@ -1,0 +1,81 @@
+"""Appends at the edges of their contract."""
+import numpy as np
+import pytest
+import torch
+
+import paged8 as R
+from rotated_codebook_kv_gb300 import Codec, native
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+_codecs = {}
+
+
+def _codec(d):
+    if d not in _codecs:
+        _codecs[d] = Codec(d, 4, 4, 64)
+    return _codecs[d]
+
+
+def pools_with_something(codec, nb, H, P, seed):
+    g = torch.Generator().manual_seed(seed)
+    pools = codec.alloc_pools_fp8(nb, H, P)
+    for p, s in zip(pools[:2], pools[2:]):
+        c = torch.randint(1, 127, p.shape, generator=g) | (torch.randint(0, 2, p.shape, generator=g) << 7)
+        p.view(torch.uint8).copy_(c.to(torch.uint8))
+        s.copy_(2.0 ** torch.randint(-11, -6, s.shape, generator=g).float())
+    return pools
+
+
+def state(pools):
+    return [p.view(torch.uint8).cpu().numpy().copy() for p in pools[:2]] + [s.cpu().numpy().copy() for s in pools[2:]]
+
+
+@pytest.mark.parametrize("d,P,H", [(128, 16, 2), (128, 32, 5), (256, 16, 1), (256, 32, 3)])
+@pytest.mark.parametrize("T", [1, 5, 1100])   # few tokens, and many (another cut into blocks)
+@pytest.mark.parametrize("row", [0, 3])
+def test_a_run_without_a_written_token_changes_nothing(d, P, H, T, row):
+    """Every position of some runs lies outside the table, of others only some, of the rest none."""
+    codec = _codec(d)
+    g = torch.Generator().manual_seed(T + row)
+    rope = codec.rope_table(40, d)
+    lens, total = [], 0
+    while total < T:
+        lens.append(min(1 + (7 * len(lens)) % (P - row), T - total))
+        total += lens[-1]
+    nb = len(lens) + 1
+    perm = torch.randperm(nb, generator=g)
+    slots = torch.cat([perm[i] * P + row + torch.arange(n) for i, n in enumerate(lens)])
+    pos = torch.randint(0, 40, (T,), generator=g)
+    ok = np.ones(T, bool)
+    at = 0
+    for i, n in enumerate(lens):
+        if i % 3 != 1:  # of every three runs: none written, all written, all but the last of the run written
+            bad = torch.arange(at, at + n) if i % 3 == 0 else torch.tensor([at + n - 1])
+            pos[bad] = torch.where(bad % 2 == 0, torch.tensor(40), torch.tensor(-1))
+            ok[bad.numpy()] = False
+        at += n
+    x = (torch.randn(T, H, d, generator=g) * 3).to(torch.bfloat16)
+    k, v = x.to(DEV), (0.5 * x).to(torch.bfloat16).to(DEV)
+    pools = pools_with_something(codec, nb, H, P, seed=T)
+    # an old scale below the least that a page may ask for is no reason to change it either
+    pools[2][perm[0]] = 2.0 ** -110
+    want = state(pools)
+    table = rope.cpu().numpy()
+    rk = np.stack([R.rotate(R.bf16(k[t:t + 1])[0], int(pos[t]) if ok[t] else 0, table, False) for t in range(T)])
+    live = np.zeros(T, bool)  # tokens of runs that have a written one
+    at = 0
+    for n in lens:
+        live[at: at + n] = ok[at: at + n].any()
+        at += n
+    masked = np.where(live, slots.numpy(), -1)
+    kc, vc, ks, vs = want
+    ks64, vs64 = ks.astype(np.float64), vs.astype(np.float64)
+    R.append_fp8(kc, ks64, rk, masked, ok, P)
+    R.append_fp8(vc, vs64, R.bf16(v), masked, ok, P)
+    codec.append_kv_fp8(k, v, slots.to(DEV), *pools, P, nb, positions=pos.to(DEV), rope=rope)
+    torch.cuda.synchronize()
+    assert codec.get_status() == native.TQ_DEVERR_POSITION
+    got = state(pools)
+    assert np.array_equal(got[2], ks64) and np.array_equal(got[3], vs64)
+    assert np.array_equal(got[0], kc) and np.array_equal(got[1], vc)
