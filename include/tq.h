@@ -336,9 +336,10 @@ tq_status tq_append_kv_bf16(tq_handle h, const uint16_t *q, const uint16_t *k, c
  * fp32).  Tokens that begin a page (row 0) give it their scale and nothing of what
  * it held counts; tokens that continue a page keep the larger of its scale and
  * theirs, and where that grows, the page's earlier rows are coded anew by the ratio
- * -- exact but for elements that become subnormal.  Codes round to nearest even;
- * an infinity saturates to 448, a NaN stays one.  Rows behind the last one written
- * keep their bytes.
+ * -- exact but for elements that become subnormal; a scale of zero always grows.  (A
+ * negative or non-finite scale counts as none: the earlier rows keep their bytes.)
+ * Codes round to nearest even; an infinity saturates to 448, a NaN stays one.  Rows
+ * behind the last one written keep their bytes.
  * slot_mapping: as above, and the tokens of one page stand next to each other in the
  *       call with ascending slots (as packed sequences have them): where another
  *       token of the page, or the same slot again, stands up to 32 tokens before a

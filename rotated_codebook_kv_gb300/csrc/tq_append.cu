@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 2)
         for (int k = 0; k < W; ++k) amax = fmaxf(amax, s_max[group][flip][k]);
         if (amax < 0.f) continue;  // the page stays as it was
         const float need = pow2_scale(amax);
-        const bool keep = o > 0 && old > 0.f && old <= 3.402823466e38f;  // the page's rows and scale so far
+        const bool keep = o > 0 && old >= 0.f && old <= 3.402823466e38f;  // the page's rows and scale so far
         const float scale = keep ? fmaxf(old, need) : need;
         const float inv = 1.f / scale;
         if (keep && scale > old) {  // code the earlier rows anew

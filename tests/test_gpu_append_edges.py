@@ -79,3 +79,28 @@ def test_a_run_without_a_written_token_changes_nothing(d, P, H, T, row):
     got = state(pools)
     assert np.array_equal(got[2], ks64) and np.array_equal(got[3], vs64)
     assert np.array_equal(got[0], kc) and np.array_equal(got[1], vc)
+
+
+@pytest.mark.parametrize("d,P,H", [(128, 16, 2), (128, 32, 1), (256, 16, 3), (256, 32, 1)])
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+def test_a_zero_scale_on_a_continued_page(d, P, H, zero):
+    """Rows under a zero scale stand for zeros, and still do when new rows give the page its scale."""
+    codec = _codec(d)
+    g = torch.Generator().manual_seed(d + P)
+    pools = pools_with_something(codec, 3, H, P, seed=1)
+    for s in pools[2:]:
+        s[1] = zero
+    want = state(pools)
+    x = torch.randn(3, H, d, generator=g).to(torch.bfloat16)
+    slots = torch.tensor([P + 5, P + 6, 2 * P + 1])
+    for c, s in ((want[0], 2), (want[1], 3)):
+        sc = want[s].astype(np.float64)
+        R.append_fp8(c, sc, R.bf16(x), slots.numpy(), np.ones(3, bool), P)
+        want[s] = sc
+    assert np.all((want[0][1, :, :5] & 127) == 0)
+    codec.append_kv_fp8(x.to(DEV), x.to(DEV), slots.to(DEV), *pools, P, 3)
+    torch.cuda.synchronize()
+    assert codec.get_status() == 0
+    got = state(pools)
+    for a, b in zip(got, want):
+        assert np.array_equal(a, b)
