@@ -136,6 +136,15 @@ __device__ __forceinline__ bool token_ok(const AppendArgs &A, int64_t slot, int6
     return true;
 }
 
+// 16 bytes of a row that this launch may rewrite in place (a query): a plain load, pinned like ld_pinned (whose
+// non-coherent path asks for memory that nobody writes meanwhile).  A thread loads what it writes before it writes it.
+__device__ __forceinline__ uint4 ld_query(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // One unit of a row, rotated by tn where `turn`, to bf16.
 __device__ __forceinline__ void put_unit(uint16_t *dst, int j0, int j1, uint4 wa, uint4 wb, bool turn, const Turn &tn,
                                          int interleaved)
@@ -190,11 +199,11 @@ __device__ __forceinline__ void token_rows(const AppendArgs &A, int64_t t, int r
     for (int row = row0; row < rows; row += 2 * step) {  // two rows on their way at a time
         const bool two = row + step < rows;
         const uint16_t *s0 = source(row), *s1 = source(two ? row + step : row);
-        const uint4 a0 = ld_pinned(s0 + j0), b0 = ld_pinned(s0 + j1);
+        const uint4 a0 = ld_query(s0 + j0), b0 = ld_query(s0 + j1);
         uint4 a1{}, b1{};
         if (two) {
-            a1 = ld_pinned(s1 + j0);
-            b1 = ld_pinned(s1 + j1);
+            a1 = ld_query(s1 + j0);
+            b1 = ld_query(s1 + j1);
         }
         finish(row, a0, b0);
         if (two) finish(row + step, a1, b1);
@@ -218,8 +227,8 @@ __device__ __forceinline__ void query_rows(const AppendArgs &A, int64_t i, int u
 #pragma unroll
     for (int k = 0; k < kQueryRows; ++k)
         if (r + k * n < A.Hq) {
-            w[k][0] = ld_pinned(src + k * n * D + j0);
-            w[k][1] = ld_pinned(src + k * n * D + j1);
+            w[k][0] = ld_query(src + k * n * D + j0);
+            w[k][1] = ld_query(src + k * n * D + j1);
         }
     const int64_t slot = ld_pinned_s64(A.slots + t);
     const int64_t pos = A.r ? ld_pinned_s64(A.positions + t) : 0;

@@ -104,3 +104,32 @@ def test_a_zero_scale_on_a_continued_page(d, P, H, zero):
     got = state(pools)
     for a, b in zip(got, want):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("d,Hq,r,interleaved,T", [(128, 8, 128, False, 700), (128, 5, 64, True, 2000), (256, 3, 80, False, 33),
+                                                  (256, 7, 256, True, 1500), (128, 2, 0, False, 40), (128, 6, 32, True, 1)])
+def test_queries_in_place(kind, d, Hq, r, interleaved, T):
+    """q_out = q gives what another q_out gets; rows of skipped tokens stay."""
+    P, H = 16, 2
+    codec = _codec(d)
+    g = torch.Generator().manual_seed(T)
+    nb = -(-T // P) + 1
+    q = torch.randn(T, Hq, d, generator=g).to(torch.bfloat16).to(DEV)
+    k, v = [torch.randn(T, H, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    slots = torch.arange(T).to(DEV)
+    if T > 20:
+        slots[T - 1] = -1
+    more = dict(positions=torch.randint(0, 30, (T,), generator=g).to(DEV), rope=codec.rope_table(30, r), interleaved=interleaved) \
+        if r else {}
+    call, pools = (codec.append_kv_bf16, codec.alloc_pools_bf16(nb, H, P)) if kind == "bf16" else \
+        (codec.append_kv_fp8, codec.alloc_pools_fp8(nb, H, P))
+    apart = q.clone()
+    call(k, v, slots, *pools, P, nb, q=q, q_out=apart, **more)
+    same = q.clone()
+    assert call(k, v, slots, *pools, P, nb, q=same, q_out=same, **more) is same
+    torch.cuda.synchronize()
+    assert torch.equal(apart, same) and codec.get_status() == 0
+    assert T <= 20 or torch.equal(same[T - 1], q[T - 1])
+    if r == d:
+        assert not torch.equal(same, q)
