@@ -368,7 +368,7 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
  *   needed (may be NULL) where that is 0.  Its contents after the call are not
  *   specified, and calls that may overlap need one each.
  * The query enters the products exactly (two e4m3 terms of a power-of-two multiple;
- * elements below 2^-9 of the head's largest lose bits below 2^-17 of it), the
+ * elements below 2^-9 of the head's largest, or of 2^-100, lose bits below 2^-17 of it), the
  * probabilities as two e4m3 terms: off by 2^-8 of themselves, or 2^-18 of the largest
  * p * v_scale among their 32 positions where that is more, so that a long weak tail behind
  * a strong token keeps its share; a p * v_scale below 2^-126 of the largest counts as

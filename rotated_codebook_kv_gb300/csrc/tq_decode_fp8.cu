@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             nan = (__ballot_sync(0xffffffffu, nan) >> (lane & ~3)) & 15u;
             // 2^e brings the largest element into [2^7, 2^8)
             int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            ex = min(max(ex, -100), 120);
+            ex = min(max(ex, -100), 127);
             const float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
             qfac = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
 #pragma unroll

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             m = max(m & 0xffffu, m >> 16);  // the largest magnitude's bits
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int ex = min(max(static_cast<int>(m >> 7) - 127, -100), 120);  // 2^(7 - ex) brings the largest into [2^7, 2^8)
+            const int ex = min(max(static_cast<int>(m >> 7) - 127, -100), 127);  // 2^(7 - ex) brings the largest into [2^7, 2^8)
             float up = __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
             if (j == 0)  // >= 0: a negative scale goes into q's sign; an infinity or NaN makes the row NaN
                 s_fac[c] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)

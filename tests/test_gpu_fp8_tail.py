@@ -194,3 +194,16 @@ def test_long_sequence_of_zero_values(d, Tq):
     ref, bound = reference(c)
     for splits in (1, 0):
         check(run(c, splits), ref, bound)
+
+
+@pytest.mark.parametrize("d,Tq", [(128, None), (256, None), (128, 3), (128, 20), (256, 20)])
+@pytest.mark.parametrize("big", [120, 122, 125, 127])
+def test_largest_queries(d, Tq, big):
+    """Queries up to the largest bf16, keys small in the same measure."""
+    c = case(d, 16, 1, 300, Tq, 1.0, seed=big, strong_value=1.0)
+    q = c["q"].float()
+    c["q"] = (q / q.abs().amax() * 1.9921875 * 2.0 ** big).to(torch.bfloat16)
+    c["scales"][0] = c["scales"][0] * 2.0 ** (2 - big)
+    ref, bound = reference(c)
+    for splits in (1, 0):
+        check(run(c, splits), ref, bound)
