@@ -161,6 +161,8 @@ class Codec:
     def _on(self, stream):
         """Context for a call whose stream or device is not the current one: both made current, so that what the
         call allocates belongs to its stream."""
+        if getattr(stream, "device", None) is not None and torch.device(stream.device).index != self.device:
+            raise ValueError(f"stream must be one of cuda:{self.device}, the device of this Codec; got one of {stream.device}")
         stack = contextlib.ExitStack()
         stack.enter_context(torch.cuda.device(self.device))
         if stream is not None:
