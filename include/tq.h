@@ -359,7 +359,9 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
 /*
  * tq_decode_attention_fp8 -- one query token per sequence over the 8-bit pages that
  * tq_append_kv_fp8 writes: tq_decode_attention_bf16 with pools and scales as above
- * (any non-negative finite scales; powers of two are what append writes).
+ * (non-negative, not only powers of two).  Value scales lie between 2^-100 and 2^120, as
+ * append writes them; smaller ones, zero among them, count as 2^-100 (in the decode, beside a
+ * page more than 2^90 larger, as 2^-90 of that page's); larger ones are not supported.
  *
  * splits: most pieces that the work of one (sequence, kv head) is cut into (the cuts
  *   are chosen on the GPU, from the lengths), 0 = tq_decode_splits_fp8(...); results
@@ -371,8 +373,7 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
  * elements below 2^-9 of the head's largest, or of 2^-100, lose bits below 2^-17 of it), the
  * probabilities as two e4m3 terms: off by 2^-8 of themselves, or 2^-18 of the largest
  * p * v_scale among their 32 positions where that is more, so that a long weak tail behind
- * a strong token keeps its share; a p * v_scale below 2^-126 of the largest counts as
- * nothing.  Sums are fp32.
+ * a strong token keeps its share.  Sums are fp32.
  * A page with a bad block id (TQ_DEVERR_BLOCK_RANGE) counts as hidden.  Rows behind a
  * sequence's end may hold anything.  A sequence of length 0 gives zeros.
  * One launch with splits 1, else two (the pieces, and what joins them).

@@ -375,7 +375,9 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             if (c + kStages - 1 < my_rounds) issue(c + kStages - 1, (done + kStages - 1) % kStages, id[kStages - 1]);
             const float ks1 = scale_of(A.k_scales, id[1]), vs1 = scale_of(A.v_scales, id[1]);
             const int id_new = c + kStages + 1 < my_rounds ? fetch_id(c + kStages + 1) : -1;
-            const float lvl = log2_scale(vs);
+            // one page's values 2^90 below the other's count as 2^90 below, so that P / vs of either half stays in fp32's range
+            float lvl = log2_scale(vs);
+            lvl = fmaxf(lvl, __shfl_xor_sync(0xffffffffu, lvl, 1) - 90.f);
             const float downl = fast_exp2(kLShift - kPShift - lvl);
             const int t = round_tok(c);
             const unsigned okm = __ballot_sync(0xffffffffu, good(id[0]));
@@ -457,7 +459,9 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
                             if (i >= nv[h] || t + 16 * h + i >= lim[e]) y[h][r][e] = -INFINITY;
                         }
             }
-            float alpha[2], shift[2], fall[2];
+            // A page of small values may lie 2^220 below another by its scale (an empty one's is 2^-100): the factors between rounds
+            // are squares of these roots, which the denominator is multiplied by twice.
+            float alpha[2], shift[2], fall[2], alpha_root[2], fall_root[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float top = max3(y[0][0][e], y[0][1][e], fmaxf(y[1][0][e], y[1][1][e]));
@@ -465,10 +469,12 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 const float m = fmaxf(top, m_run[e]);
-                alpha[e] = m == m_run[e] ? 1.f : fast_exp2(m_run[e] - m);
+                alpha_root[e] = m == m_run[e] ? 1.f : fast_exp2(0.5f * (m_run[e] - m));
                 const bool none = top == -INFINITY;  // nothing of the round is seen (or only NaN)
-                fall[e] = none ? 1.f : fast_exp2(top - m);
+                fall_root[e] = none ? 1.f : fast_exp2(0.5f * (top - m));
                 shift[e] = none ? kPShift : kPShift - top;
+                alpha[e] = alpha_root[e] * alpha_root[e];
+                fall[e] = fall_root[e] * fall_root[e];
                 m_run[e] = m;
             }
             if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -514,7 +520,8 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
                 for (int i = 0; i < 4; ++i) o[mt][i] = fmaf(fall[i & 1], c4[i], o[mt][i]);
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) l_run[e] = fmaf(l_run[e], alpha[e], fall[e] * l_round[e]);
+            for (int e = 0; e < 2; ++e)
+                l_run[e] = fmaf(fall_root[e], fall_root[e] * l_round[e], alpha_root[e] * (alpha_root[e] * l_run[e]));
             ks = ks1;
             vs = vs1;
 #pragma unroll
@@ -562,9 +569,9 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 if (r_l[w * 8 + c] == 0.f) continue;  // a warp that saw nothing
-                const float f = r_m[w * 8 + c] == -INFINITY ? 1.f : fast_exp2(r_m[w * 8 + c] - ref);
-                acc = fmaf(f, r_o[(w * D + j) * 8 + c], acc);
-                l = fmaf(f, r_l[w * 8 + c], l);
+                const float f = r_m[w * 8 + c] == -INFINITY ? 1.f : fast_exp2(0.5f * (r_m[w * 8 + c] - ref));
+                acc = fmaf(f * f, r_o[(w * D + j) * 8 + c], acc);
+                l = fmaf(f, f * r_l[w * 8 + c], l);
             }
             acc *= downp;
             l *= ldown;
@@ -655,9 +662,9 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args A, const int6
     float den = 0.f;
     for (int s = tid; s < splits; s += 128) {
         const float2 v = __ldg(ml + s * rows + row);
-        const float w = v.y == 0.f ? 0.f : (v.x == -INFINITY ? 1.f : fast_exp2(v.x - ref));
-        s_w[s] = v.y == 0.f ? -1.f : w;  // -1: nothing to read
-        den += v.y == 0.f ? 0.f : w * v.y;
+        const float root = v.x == -INFINITY ? 1.f : fast_exp2(0.5f * (v.x - ref));
+        s_w[s] = v.y == 0.f ? -1.f : root * root;  // -1: nothing to read
+        den += v.y == 0.f ? 0.f : root * (root * v.y);
     }
     den = warp_sum(den);
     if (lane == 0) s_red[warp] = den;
@@ -709,13 +716,14 @@ __global__ void __launch_bounds__(128) merge_rows_fp8_kernel(const Args A, const
     const float ref = M == -INFINITY ? 0.f : M;
     float n[E] = {}, den = 0.f;
     for (int s0 = 0; s0 < A.splits; s0 += 32) {
-        float w = 0.f, l = 0.f;
+        float root = 0.f, l = 0.f;
         if (s0 + lane < A.splits) {
             const float2 v = __ldg(ml + (s0 + lane) * rows + row);
             l = v.y;
-            w = v.y == 0.f ? 0.f : (v.x == -INFINITY ? 1.f : fast_exp2(v.x - ref));
+            root = v.y == 0.f ? 0.f : (v.x == -INFINITY ? 1.f : fast_exp2(0.5f * (v.x - ref)));
         }
-        den += warp_sum(l == 0.f ? 0.f : w * l);
+        const float w = root * root;
+        den += warp_sum(l == 0.f ? 0.f : root * (root * l));
         const unsigned some = __ballot_sync(0xffffffffu, l != 0.f);
         const int k1 = min(32, A.splits - s0);
 #pragma unroll 4

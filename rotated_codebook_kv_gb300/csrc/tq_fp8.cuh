@@ -12,7 +12,7 @@ namespace tq {
 namespace fp8 {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLShift = 4.f;  // denominators are summed as 2^4 p / vs: vs in 2^-100 .. 2^119 neither overflows nor flushes
+constexpr float kLShift = 4.f;  // denominators are summed as 2^4 p / vs: vs in 2^-100 .. 2^120 neither overflows nor flushes
 // The prefill's denominators are sums of 2^-10 P / vs, P up to 2^15: vs in 2^-100 .. 2^120 neither overflows (4 million tokens)
 // nor flushes.
 constexpr float kSumUnit = 0x1p-10f;

@@ -101,6 +101,10 @@ struct Tc {
 // and moves all of O, so a few strong tokens in every tile made it the longest step of many tiles.  Long prefill below, the
 // same with 2^-1 | 2^2 | 2^4 | 2^6 | 2^8: 814 | 822 | 825 | 828 | 832 us; 64 tokens of 32 sequences 187 | 190 | 195 | 196 | 198.
 constexpr float kAim = -4.f, kLazy = 15.f;
+// Value scales may lie 2^220 apart (an empty page's is 2^-100), and then the P = 2^(y - m) of a page of small values, which its
+// part of the denominator is made from, below what fp32 holds: a tile with a group of 16 tokens whose P are all below
+// 2^kFar is looked through for those, and the factors of a rescale and of the merge are taken as squares of their roots.
+constexpr float kFar = -60.f;
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -177,11 +181,13 @@ struct Scores {
     float a[4], b[4], inv[4];
 };
 
-// The largest y of the tile.  WHOLE: every token is seen, else those below rem of the groups in okm.
+// The largest y of the tile, and the least of its groups' largest.  WHOLE: every token is seen, else those below rem of the
+// groups in okm.
 template <bool WHOLE>
-__device__ __forceinline__ float tile_max(const Scores &s, uint32_t okm, int rem)
+__device__ __forceinline__ float tile_max(const Scores &s, uint32_t okm, int rem, float &low)
 {
     float top = -INFINITY;
+    low = INFINITY;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         float m0 = -INFINITY, m1 = -INFINITY;
@@ -194,7 +200,11 @@ __device__ __forceinline__ float tile_max(const Scores &s, uint32_t okm, int rem
             m1 = max3(m1, x[2], x[3]);
         }
         m0 = fmaxf(m0, m1);
-        if (WHOLE || ((okm >> g & 1u) && m0 != -INFINITY)) top = fmaxf(top, fmaf(m0, s.a[g], s.b[g]));
+        if (WHOLE || ((okm >> g & 1u) && m0 != -INFINITY)) {
+            const float y = fmaf(m0, s.a[g], s.b[g]);
+            top = fmaxf(top, y);
+            low = fminf(low, y);
+        }
     }
     return top;
 }
@@ -231,6 +241,28 @@ __device__ __forceinline__ float tile_exp(const Scores &s, uint32_t (&p)[32], fl
         }
         const float2 t = unpack2(add2(sum0, sum1));
         if (gok) l = fmaf(t.x + t.y, s.inv[g], l);
+    }
+    return l;
+}
+
+// What tile_exp leaves out of a column's denominator: the P below 2^-126 (2^180 times them are summed).  The scores come from
+// tensor memory once more, a group at a time: a second way through tile_exp made every tile 3 % slower, this after tile_exp as
+// well.
+__device__ __forceinline__ float flushed_part(uint32_t ts, const float4 *info, float fac, uint32_t okm, int rem, float ref)
+{
+    float l = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+        float v[16];
+        umma::ld16(ts + 16 * g, v);
+        const float4 f = info[g];
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float y = fmaf(v[k], fac * f.x, f.y - ref);
+            if (y < -126.f && 16 * g + k < rem) sum += fast_exp2(y + 180.f);
+        }
+        if (okm >> g & 1u) l = fmaf(sum, f.z * 0x1p-90f * 0x1p-90f, l);
     }
     return l;
 }
@@ -466,14 +498,15 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             const int rem = lim - (tok0 + i * KT);  // tokens of the tile that this column sees
             const bool whole = __all_sync(0xffffffffu, rem >= KT) && okm == (1u << GR) - 1u;
             umma::ld64(ts, s.v);
-            const float top = whole ? tile_max<true>(s, okm, rem) : tile_max<false>(s, okm, rem);
+            float low;
+            const float top = whole ? tile_max<true>(s, okm, rem, low) : tile_max<false>(s, okm, rem, low);
             // ---- lazy rescale ----
             const bool need = m_run != -INFINITY && top > m_run + kLazy;
             if (m_run == -INFINITY) m_run = top + kAim;  // O's row is zero or unwritten so far
             if (__any_sync(0xffffffffu, need)) {
                 if (i > 0 && !(ok = wait_bar(T::bPvDone + q * NB + (i - 1) % NB, ((i - 1) / NB) & 1))) break;  // O is at rest
                 umma::fence_after_sync();
-                const float al = need ? fast_exp2(m_run - (top + kAim)) : 1.f;
+                const float root = need ? fast_exp2(0.5f * (m_run - (top + kAim))) : 1.f, al = root * root;
                 const uint32_t to = lane_base + T::kTmO + q * D;
 #pragma unroll 1
                 for (int ch = 0; ch < D; ch += 64) {
@@ -484,11 +517,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                     umma::st64(to + ch, o);
                 }
                 umma::wait_st();
-                if (need) {
-                    l_run *= al;
-                    m_run = top + kAim;
-                }
+                l_run = l_run * root * root;  // see kFar
+                if (need) m_run = top + kAim;
             }
+            if (__any_sync(0xffffffffu, low < m_run + kFar)) l_run += flushed_part(ts, info, fac, okm, rem, m_run);
             // ---- P = 2^(y - m) over the scores ----
             const float ref = m_run == -INFINITY ? 0.f : m_run;
             uint32_t p[32];

@@ -98,7 +98,7 @@ def reference(c, sm=None):
                 eps, low = 2.0 ** -11, np.full(n, 2.0 ** -29 * pv.max())
             dA = (p * dx) @ av[:n] + (p @ dx) * A
             out[i, h] = o
-            bound[i, h] = 2.0 ** -8 * np.abs(o) + eps * A + low @ ac[:n] + dA + (n / 8 + 4) * 2.0 ** -23 * A + 1e-30
+            bound[i, h] = 2.0 ** -8 * np.abs(o) + eps * A + low @ ac[:n] + dA + (n / 8 + 4) * 2.0 ** -23 * A + 1e-38
     return out.reshape(q.shape), bound.reshape(q.shape)
 
 
@@ -207,3 +207,21 @@ def test_largest_queries(d, Tq, big):
     ref, bound = reference(c)
     for splits in (1, 0):
         check(run(c, splits), ref, bound)
+
+
+@pytest.mark.parametrize("d,Tq", [(128, None), (256, None), (128, 3), (128, 20), (256, 20)])
+@pytest.mark.parametrize("e", [-100, -60, 60, 120])
+def test_value_scales_at_the_ends_of_their_range(d, Tq, e):
+    c = case(d, 16, 1, 700, Tq, 3.0, seed=5, strong_value=1.0)
+    # codes up to 8, so that the largest scale keeps the values finite
+    x = c["codes"][1].view(torch.float8_e4m3fn).float() / 64
+    c["codes"][1] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    c["scales"][1] = torch.full_like(c["scales"][1], 2.0 ** e)
+    ref, bound = reference(c)
+    for splits in (1, 2):
+        check(run(c, splits), ref, bound)
+    c["scales"][1][3:7] = 0.0  # counts as the least
+    if e > -100:
+        ref, bound = reference(c)
+        for splits in (1, 2):
+            check(run(c, splits), ref, bound)
