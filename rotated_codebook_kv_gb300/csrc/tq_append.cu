@@ -12,9 +12,10 @@
 //
 // Bound: HBM, in one pass (every row is read and written once, a page's earlier rows only where its scale grows).
 // Measured on a GB300 (copy 6783 GB/s): to bf16 pages 15,500 tokens of 16 query and 8 kv heads of 256 87 us = 5.8 TB/s, two
-// rows of a thread in flight; to 8-bit pages 32k tokens of 32 query and 8 kv heads of 128 147 us = 5.1 TB/s, of which the
+// rows of a thread in flight; to 8-bit pages 32k tokens of 32 query and 8 kv heads of 128 148 us = 5.1 TB/s, of which the
 // query rows take ~90 (6.0 TB/s) and the pages ~60, bound by the latency of a chain (slots, rows, maximum, codes) and
-// the instructions of the rotation and the codes.  A step's few tokens: 11 us, the host's checks and launch.
+// the instructions of the rotation and the codes.  A step's few tokens: 11 us, the host's checks and launch
+// (1.7 to bf16 pages and 3.4 to 8-bit ones by graph replay).
 // Tried for the pages and slower when they stood at 163: rows through shared memory by asynchronous copies (166-172 us;
 // ragged chunks 53 against 45), page and query blocks in turn instead of one after the other (184; every fourth block 152,
 // but ragged chunks 48).
@@ -302,7 +303,7 @@ __device__ __forceinline__ float finite_abs(float x)
 // and for the codes: a group has two or four warps, so that each lane holds few units, rotated, in registers
 // between; a group meets at a barrier of its own.
 //
-// At head dim 128 a lane holds two units, with three blocks on an SM, at 256 four with two (32k tokens 150 us against 163 at
+// At head dim 128 a lane holds two units, with three blocks on an SM, at 256 four with two (when chosen, 32k tokens 150 us against 163 at
 // 128, and 208 against 216 at 256; chunks of 200 to 1500 tokens 83 against 91, and 132 against 111).
 constexpr int units_held(int d) { return d == 128 ? 2 : 4; }
 constexpr int group_warps(int d, int p) { return p * (d / kUnit) / (32 * units_held(d)); }

@@ -16,8 +16,9 @@
 // P is taken against the maximum of its own round of 32 tokens, and the round's product added to O with the factor
 // between that and the running maximum: both terms end at 2^-18 of what they are taken against, and against the running
 // maximum the weak tail behind one strong token would lie below that (8 % of the output gone at 13 nats and 32k tokens).
-// 32 multiply-adds a round at head dim 128; the times stayed (175 us long, 179 at head dim 256).  Only for rounds far below
-// the running maximum, by a second copy of the product's code: 177 and 186.
+// 32 multiply-adds a round at head dim 128; the times stayed (174.5 us long, 179 at head dim 256).  Only for rounds far
+// below the running maximum, by a second copy of the product's code: 177 and 186.  Value scales 2^220 apart (squares of
+// roots, see below) took them to 176 and 181; squares for every P 178.6 and 181, a branch for rounds that need it 177 and 183.
 //
 // Work is dealt out on the GPU, where the lengths are: the rounds of all (sequence, kv head) units in a row, an
 // equal share for each of one wave of CTAs (three of four warps per SM at head dim 128, one of seven at 256).  A CTA's
@@ -27,8 +28,9 @@
 // this kernel, more through tq_prefill_fp8.cu.
 //
 // Bound: HBM.  Measured on a GB300 (copy 6783 GB/s): 4 sequences of 131,072 tokens, 8 kv heads, head dim 128: 1.08 GB
-// in 175 us = 6.1 TB/s; head dim 256: 6.0 TB/s.  A short call (11 us) is the host's: checks, tensor maps, launch.
-// Warps of a CTA x CTAs per SM x stages, measured at head dim 128: 4 x 3 x 2 175 us, 3 x 3 x 3 231, 4 x 2 x 3 193,
+// in 176 us = 6.1 TB/s; head dim 256: 181 us, 5.9 TB/s.  A short call takes 10-11 us: checks, tensor maps, launch (9.1 by
+// graph replay, two CTAs for 512 tokens of two kv heads).
+// Warps of a CTA x CTAs per SM x stages, when chosen, at head dim 128: 4 x 3 x 2 175 us, 3 x 3 x 3 231, 4 x 2 x 3 193,
 // 7 x 1 x 4 213, 7 x 2 x 2 255; at 256: 7 x 1 x 2 179, 4 x 1 x 3 223.
 #include <climits>
 #include <cmath>
@@ -916,8 +918,9 @@ extern "C" int tq_prefill_splits_fp8(tq_handle h, int batch, int q_tokens, int n
     const int qpc = tq::fp8::prefill_tc_columns(tq::handle_codec(h).d) / G;
     const long long units = static_cast<long long>(batch) * num_kv_heads * ((q_tokens + qpc - 1) / qpc);
     // One CTA per SM.  Whole waves of units stay whole; the rest is cut into the pieces (of 512 tokens at least) that take
-    // the least time, in steps of 64 tokens (about a microsecond) of the longest sequence: waves of pieces, each with a
-    // start and an end, the merge's launch, and 45 pieces' sums written and read a step.  Measured, in one | two | three |
+    // the least time, in steps of 64 tokens (about a microsecond) of a sequence that fills its table, as all are taken to:
+    // waves of pieces, each with a start and an end, the merge's launch, and 45 pieces' sums written and read a step.  When
+    // chosen (batches of equal length but the last, tables no wider than the longest sequence), in one | two | three |
     // four | five pieces, us: 128 units of 128 steps at head dim 256 136 | 159 | 170 | 178 | 189, 256 units 212 | 232 | 230
     // | 227 | 219, 64 units 134 | 86 | 102 | 96 | 86; at 128, 512 units of 256 steps 869 | 840 | 834 | 819 | 816, 128 units
     // 259 | 281 | 294 | 297 | 310, 256 units of up to 128 steps 204 | 204 | 196 | 192 | 194.

@@ -23,11 +23,10 @@
 // Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT, stops the CTA (its rows
 // then carry no weight), lets copies and MMAs in flight finish, and frees tensor memory.
 //
-// Bound: the softmax warps.  A tile pair's step takes ~2000 cycles at head dim 128; its MMAs take 1280 (scores 16 of 48
-// cycles, held there by reading both operands from shared memory; P.V 8 of 64).  Measured on a GB300: the last 4096 of
-// 16,384 tokens, 32 query and 8 kv heads of 128, 810 us = 1.19 PFLOP/s of useful products (cuBLAS bf16: 1.91), tensor pipe
-// 53 % active; 64 tokens of 32 sequences of 1024 to 8192 188 us; the last 1000 of 2 sequences of 5000 to 8192, 16 and 8
-// heads of 256, 209 us.
+// Bound: the softmax warps.  Measured on a GB300: the last 4096 of 16,384 tokens, 32 query and 8 kv heads of 128, 828 us =
+// 1.16 PFLOP/s of useful products (cuBLAS bf16: 1.91), 756 steps of a tile pair an SM, 1.1 us each, half of which the tensor
+// pipe is active; 64 tokens of 32 sequences of 1024 to 8192 195 us; the last 1000 of 2 sequences of 5000 to 8192, 16 and 8
+// heads of 256, 214 us.
 #include <climits>
 
 #include "tq_fp8.cuh"
