@@ -360,8 +360,8 @@ tq_status tq_append_kv_fp8(tq_handle h, const uint16_t *q, const uint16_t *k, co
  * tq_decode_attention_fp8 -- one query token per sequence over the 8-bit pages that
  * tq_append_kv_fp8 writes: tq_decode_attention_bf16 with pools and scales as above
  * (non-negative, not only powers of two).  Value scales lie between 2^-100 and 2^120, as
- * append writes them; smaller ones, zero among them, count as 2^-100 (in the decode, beside a
- * page more than 2^90 larger, as 2^-90 of that page's); larger ones are not supported.
+ * append writes them; smaller ones, zero among them, count as 2^-100 (with one query token, beside
+ * a page more than 2^90 larger, as 2^-90 of that page's); larger ones are not supported.
  *
  * splits: most pieces that the work of one (sequence, kv head) is cut into (the cuts
  *   are chosen on the GPU, from the lengths), 0 = tq_decode_splits_fp8(...); results

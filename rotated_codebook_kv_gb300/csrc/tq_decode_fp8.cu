@@ -18,7 +18,7 @@
 // maximum the weak tail behind one strong token would lie below that (8 % of the output gone at 13 nats and 32k tokens).
 // 32 multiply-adds a round at head dim 128; the times stayed (174.5 us long, 179 at head dim 256).  Only for rounds far
 // below the running maximum, by a second copy of the product's code: 177 and 186.  Value scales 2^220 apart (squares of
-// roots, see below) took them to 176 and 181; squares for every P 178.6 and 181, a branch for rounds that need it 177 and 183.
+// roots, see below) took them to 176 and 181, a branch for the rounds that need it 177 and 183.
 //
 // Work is dealt out on the GPU, where the lengths are: the rounds of all (sequence, kv head) units in a row, an
 // equal share for each of one wave of CTAs (three of four warps per SM at head dim 128, one of seven at 256).  A CTA's
@@ -377,9 +377,11 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
             if (c + kStages - 1 < my_rounds) issue(c + kStages - 1, (done + kStages - 1) % kStages, id[kStages - 1]);
             const float ks1 = scale_of(A.k_scales, id[1]), vs1 = scale_of(A.v_scales, id[1]);
             const int id_new = c + kStages + 1 < my_rounds ? fetch_id(c + kStages + 1) : -1;
-            // one page's values 2^90 below the other's count as 2^90 below, so that P / vs of either half stays in fp32's range
+            // One page's values more than 2^90 below the other's count as 2^90 below, so that P / vs of either half stays in fp32's
+            // range (squares for every P: 178.6 us against 176).  Among several query tokens, some of which may not see the other
+            // page, squares it is.
             float lvl = log2_scale(vs);
-            lvl = fmaxf(lvl, __shfl_xor_sync(0xffffffffu, lvl, 1) - 90.f);
+            if (!MANY) lvl = fmaxf(lvl, __shfl_xor_sync(0xffffffffu, lvl, 1) - 90.f);
             const float downl = fast_exp2(kLShift - kPShift - lvl);
             const int t = round_tok(c);
             const unsigned okm = __ballot_sync(0xffffffffu, good(id[0]));
@@ -494,9 +496,19 @@ __global__ void __launch_bounds__(Fp8Smem<D>::kThreads, Fp8Smem<D>::kCtas)
                 uint32_t tr[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float p0 = fast_exp2(y[h][r][0] + shift[0]), p1 = fast_exp2(y[h][r][1] + shift[1]);
-                    l_round[0] = fmaf(p0, down[h], l_round[0]);
-                    l_round[1] = fmaf(p1, down[h], l_round[1]);
+                    float p0 = y[h][r][0] + shift[0], p1 = y[h][r][1] + shift[1];
+                    if (MANY) {
+                        const float r0 = fast_exp2(0.5f * p0), r1 = fast_exp2(0.5f * p1);
+                        l_round[0] = fmaf(r0, r0 * down[h], l_round[0]);
+                        l_round[1] = fmaf(r1, r1 * down[h], l_round[1]);
+                        p0 = r0 * r0;
+                        p1 = r1 * r1;
+                    } else {
+                        p0 = fast_exp2(p0);
+                        p1 = fast_exp2(p1);
+                        l_round[0] = fmaf(p0, down[h], l_round[0]);
+                        l_round[1] = fmaf(p1, down[h], l_round[1]);
+                    }
                     __half2 p = __floats2half2_rn(p0, p1);  // 11 bits, of which the two terms keep about 8
                     const uint32_t hi = e4m3x2_rest(p);
                     tr[r] = movmatrix_trans(__byte_perm(hi, e4m3x2(p), 0x5140));

@@ -225,3 +225,15 @@ def test_value_scales_at_the_ends_of_their_range(d, Tq, e):
         ref, bound = reference(c)
         for splits in (1, 2):
             check(run(c, splits), ref, bound)
+
+
+@pytest.mark.parametrize("d,G,Tq", [(128, 1, 5), (128, 2, 4), (256, 1, 8), (128, 4, 9), (256, 3, 12)])
+@pytest.mark.parametrize("L", [20, 33, 52])
+def test_a_later_page_of_far_larger_values_is_not_felt_before_it_is_seen(d, G, Tq, L):
+    """Query tokens that see only the pages before one whose value scale is 2^130 larger."""
+    c = case(d, 16, G, L, Tq, 1.0, seed=L, strong_value=1.0)
+    c["scales"][1][-1] *= 2.0 ** 70
+    c["scales"][1][:-1] *= 2.0 ** -60
+    ref, bound = reference(c)
+    for splits in (1, 2):
+        check(run(c, splits), ref, bound)
