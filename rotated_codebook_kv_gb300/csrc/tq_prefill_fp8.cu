@@ -261,7 +261,7 @@ __device__ __forceinline__ float flushed_part(uint32_t ts, const float4 *info, f
             const float y = fmaf(v[k], fac * f.x, f.y - ref);
             if (y < -126.f && 16 * g + k < rem) sum += fast_exp2(y + 180.f);
         }
-        if (okm >> g & 1u) l = fmaf(sum, f.z * 0x1p-90f * 0x1p-90f, l);
+        if (okm >> g & 1u) l = fmaf(sum * 0x1p-58f * f.z, 0x1p-122f, l);  // in an order that keeps to fp32's range
     }
     return l;
 }

@@ -237,3 +237,18 @@ def test_a_later_page_of_far_larger_values_is_not_felt_before_it_is_seen(d, G, T
     ref, bound = reference(c)
     for splits in (1, 2):
         check(run(c, splits), ref, bound)
+
+
+@pytest.mark.parametrize("d,P,Tq", [(128, 16, None), (256, 16, None), (128, 32, None), (128, 16, 3), (256, 32, 5), (128, 16, 20),
+                                    (128, 32, 12), (256, 16, 20)])
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_value_scales_of_every_size_side_by_side(d, P, Tq, seed):
+    """Every page's value scale somewhere in 2^-85 .. 2^105: all pages have their part of the denominator."""
+    c = case(d, P, 1, 700 - 13 * seed, Tq, 2.0, seed=seed, strong_value=1.0)
+    g = torch.Generator().manual_seed(seed)
+    x = c["codes"][1].view(torch.float8_e4m3fn).float() / 64
+    c["codes"][1] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    c["scales"][1] = 2.0 ** torch.randint(-85, 106, c["scales"][1].shape, generator=g).float()
+    ref, bound = reference(c)
+    for splits in (1, 0, 5):
+        check(run(c, splits), ref, bound)
