@@ -1,4 +1,5 @@
-"""Attention over 8-bit pages where one strong token with small values stands before a long weak tail.
+"""Attention over 8-bit pages where one strong token with small values stands before a long weak tail; queries and value
+scales at the ends of their ranges.
 
 The tail carries most of the output, each of its tokens a probability far below the largest one.  The bound
 (`reference`) has no term in which the largest probability of the whole sequence is multiplied by the number of tokens
