@@ -409,6 +409,72 @@ tq_status tq_prefill_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t
                                    void *stream);
 
 /*
+ * Latent pages: a cache for attention whose keys and values of all heads come from one
+ * shared vector a token.  Row t % page_size of block block_table[b][t / page_size] holds a
+ * token's latent vector c (latent_dim, 256 or 512) and its rotated key part r
+ * (TQ_LATENT_ROPE_DIM), bf16; with queries in the latents' space (the absorbed form) a head's
+ * key is all of the row and its value the latent.  The pool is bf16
+ * [num_blocks][page_size][latent_dim + 64], page_size 16, 32 or 64.  The codec's tables play
+ * no part; any handle serves.
+ *
+ * tq_append_latent -- put T tokens into the pool, normalised and rotated on the way.
+ *
+ * latent, k_rope: device bf16, row t at ptr + t * stride (elements; the slices of one
+ *       projection can be passed).  q, q_out: device bf16, token t / head h at ptr +
+ *       t * stride_tok + h * stride_head, the heads' TQ_LATENT_ROPE_DIM coordinates that take part
+ *       in the rotation: q_out may be the last columns of the attention's queries.  q may
+ *       be NULL (then so is q_out, and their sizes are ignored); q_out may be q itself, else
+ *       it does not overlap the inputs.  Strides are multiples of 8 and no less than a row,
+ *       pointers 16-byte aligned.
+ * norm_weight: device bf16 [latent_dim], or NULL: c w / sqrt(mean(c^2) + norm_eps) in fp32,
+ *       rounded once to bf16; without it c passes through.
+ * rope, rope_rows, positions, style: as in tq_append_kv_bf16 with rot_dim
+ *       TQ_LATENT_ROPE_DIM, for k_rope and q; rope NULL: no rotation (positions ignored).
+ * slot_mapping: as in tq_append_kv_bf16; a skipped token leaves its row and its q_out
+ *       rows as they were.
+ * One launch on `stream`; T == 0 launches nothing.
+ */
+#define TQ_LATENT_ROPE_DIM 64
+tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const uint16_t *k_rope, const uint16_t *q, int64_t T,
+                           int latent_dim, int num_q_heads, int64_t latent_stride, int64_t k_stride,
+                           int64_t q_stride_tok, int64_t q_stride_head, const uint16_t *norm_weight, float norm_eps,
+                           const int64_t *positions, const float *rope, int64_t rope_rows, int style,
+                           const int64_t *slot_mapping, uint16_t *pool, int page_size, int64_t num_blocks,
+                           uint16_t *q_out, int64_t qo_stride_tok, int64_t qo_stride_head, void *stream);
+
+/*
+ * tq_decode_attention_latent -- one query token per sequence over its latent pages:
+ * s_t = sm_scale <q, [c_t | r_t]>, p = softmax(s), out = sum_t p_t c_t, for every head.
+ *
+ * q: device bf16 [B][Hq][latent_dim + 64]; out: device bf16 [B][Hq][latent_dim]; any number
+ *   of heads.  block_table, seq_lens, status bits: as in tq_decode_attention_bf16; a page
+ *   with a bad block id counts as hidden, rows behind a sequence's end may hold anything,
+ *   a sequence of length 0 gives zeros.
+ * Scores are exact bf16 products summed in fp32; the probabilities enter the value product
+ * rounded to bf16 (off by 2^-8 of themselves at most) and the denominator sums what
+ * enters; sums are fp32.
+ * workspace: ws_bytes >= tq_workspace_bytes_latent(...), 256-byte aligned; its contents after
+ *   the call are not specified, and calls that may overlap need one each.  Work is cut on
+ *   the GPU, from the lengths of all sequences, so results depend on the batch, within rounding.
+ * Two launches (attention, and what joins the pieces).
+ *
+ * tq_prefill_attention_latent -- the last q_tokens positions of every sequence attend
+ * causally to its latent pages, their own rows included (tq_prefill_attention's contract).
+ * q: [B][q_tokens][Hq][latent_dim + 64], out: [B][q_tokens][Hq][latent_dim].  A NaN or
+ * infinity in a row reaches the query tokens that see it and no others.  A query token that
+ * sees nothing gives zeros.
+ */
+size_t tq_workspace_bytes_latent(tq_handle h, int batch, int q_tokens, int num_q_heads, int latent_dim);
+tq_status tq_decode_attention_latent(tq_handle h, const uint16_t *q, const uint16_t *pool, const int32_t *block_table,
+                                     const int32_t *seq_lens, int batch, int num_q_heads, int latent_dim,
+                                     int page_size, int max_blocks_per_seq, int64_t num_blocks, float sm_scale,
+                                     void *workspace, size_t ws_bytes, uint16_t *out, void *stream);
+tq_status tq_prefill_attention_latent(tq_handle h, const uint16_t *q, const uint16_t *pool, const int32_t *block_table,
+                                      const int32_t *seq_lens, int batch, int q_tokens, int num_q_heads,
+                                      int latent_dim, int page_size, int max_blocks_per_seq, int64_t num_blocks,
+                                      float sm_scale, void *workspace, size_t ws_bytes, uint16_t *out, void *stream);
+
+/*
  * tq_set_wait_limit -- the number of SM clock cycles a kernel of this handle
  * polls one barrier (a tensor-core completion, a page copy, a hand-off between
  * warps) before it gives up, sets TQ_DEVERR_TIMEOUT and winds its CTA down.

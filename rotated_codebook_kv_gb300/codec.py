@@ -330,6 +330,121 @@ class Codec:
         return self._attention_fp8(q, q.shape[1], k_pool, v_pool, k_scales, v_scales, block_table, seq_lens,
                                    num_kv_heads, page_size, num_blocks, sm_scale, splits, workspace, out, stream)
 
+    # ---- latent pages --------------------------------------------------------------
+    def alloc_pool_latent(self, num_blocks: int, page_size: int, latent_dim: int):
+        """A zeroed pool of latent pages [num_blocks][page_size][latent_dim + 64]."""
+        return torch.zeros(num_blocks, page_size, latent_dim + native.TQ_LATENT_ROPE_DIM, dtype=torch.bfloat16,
+                           device=torch.device("cuda", self.device))
+
+    def _strided(self, x, shape, what: str):
+        """Address and strides of bf16 rows of this shape, the last dimension contiguous; a dimension of one counts as
+        packed."""
+        if x.dtype is not torch.bfloat16 or x.shape != shape or x.get_device() != self.device:
+            raise ValueError(f"{what} must be bf16 {list(shape)} on cuda:{self.device}; got {x.dtype} {tuple(x.shape)} on "
+                             f"{x.device}")
+        if x.numel() and x.stride(-1) != 1:
+            raise ValueError(f"{what}: the coordinates of a row must be contiguous")
+        st, packed = [], shape[-1]
+        for n, s in zip(reversed(shape[:-1]), reversed(x.stride()[:-1])):
+            st.append(s if n > 1 else packed)
+            packed *= n
+        return (x.data_ptr(), *reversed(st))
+
+    def append_latent(self, latent, k_rope, slot_mapping, pool, page_size: int, num_blocks: int, q=None, q_out=None,
+                      positions=None, rope=None, interleaved: bool = False, norm_weight=None, norm_eps: float = 1e-6,
+                      stream=None):
+        """Put tokens into latent pages: latent [T, latent_dim] (normalised where norm_weight [latent_dim] is given) and
+        k_rope [T, 64] (rotated by position where a rope table is given), rows strided.
+
+        q: [T, Hq, 64], any token and head strides, rotated into q_out (the same shape, strided: the last columns of the
+        attention's queries, say), which is returned (None without q).  rope: fp32 [rows, 64] as rope_table makes it;
+        positions: int64 [T]."""
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.append_latent(latent, k_rope, slot_mapping, pool, page_size, num_blocks, q, q_out, positions,
+                                          rope, interleaved, norm_weight, norm_eps)
+        if latent.dim() != 2:
+            raise ValueError("latent must be [T, latent_dim]")
+        r = native.TQ_LATENT_ROPE_DIM
+        T, dl = latent.shape
+        lp, ls = self._strided(latent, (T, dl), "latent")
+        kp, ks = self._strided(k_rope, (T, r), "k_rope")
+        sp = self._flat(slot_mapping, torch.int64, T, "slot_mapping")
+        pp = self._flat(pool, torch.bfloat16, num_blocks * page_size * (dl + r), "pool [num_blocks, page_size, latent_dim + 64]")
+        wp = 0 if norm_weight is None else self._flat(norm_weight, torch.bfloat16, dl, "norm_weight")
+        qp = qs = qh = Hq = op = os = oh = rp = rows = at = 0
+        if rope is not None:
+            if rope.dim() != 2 or positions is None:
+                raise ValueError("rope must be fp32 [rows, 64], and goes with positions")
+            rows = rope.shape[0]
+            rp = self._flat(rope, torch.float32, rows * r, "rope")
+            at = self._flat(positions, torch.int64, T, "positions")
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q must be [T, num_q_heads, 64]")
+            Hq = q.shape[1]
+            qp, qs, qh = self._strided(q, (T, Hq, r), "q")
+            if q_out is None:  # zeros: rows of skipped tokens are not written
+                q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+            op, os, oh = self._strided(q_out, (T, Hq, r), "q_out")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        native.tq_append_latent(self.handle, lp, kp, qp, T, dl, Hq, ls, ks, qs, qh, wp, float(norm_eps), at, rp, rows,
+                                native.TQ_ROPE_INTERLEAVED if interleaved else native.TQ_ROPE_HALF, sp, pp, page_size,
+                                num_blocks, op, os, oh, _raw_stream(self.device))
+        return q_out
+
+    def workspace_latent(self, batch: int, q_tokens: int, num_q_heads: int, latent_dim: int):
+        """Scratch of the attention over latent pages (q_tokens 1 for decode)."""
+        n = native.tq_workspace_bytes_latent(self.handle, batch, q_tokens, num_q_heads, latent_dim)
+        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", self.device))
+
+    def _attention_latent(self, q, tq, pool, block_table, seq_lens, page_size, num_blocks, sm_scale, workspace, out, stream):
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self._attention_latent(q, tq, pool, block_table, seq_lens, page_size, num_blocks, sm_scale, workspace,
+                                              out, None)
+        B, Hq, d = q.shape[0], q.shape[-2], q.shape[-1]
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_blocks]")
+        maxb, dl = block_table.shape[1], d - native.TQ_LATENT_ROPE_DIM
+        rows = B * max(tq, 1) * Hq
+        qp = self._flat(q, torch.bfloat16, rows * d, "q")
+        args = (self._flat(pool, torch.bfloat16, num_blocks * page_size * d, "pool [num_blocks, page_size, latent_dim + 64]"),
+                self._flat(block_table, torch.int32, B * maxb, "block_table"), self._flat(seq_lens, torch.int32, B, "seq_lens"))
+        if workspace is None:
+            workspace = self.workspace_latent(B, max(tq, 1), Hq, dl)
+        if workspace.get_device() != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{self.device}, the device of this Codec")
+        if out is None:
+            out = torch.empty(*q.shape[:-1], max(dl, 0), dtype=torch.bfloat16, device=q.device)
+        op = self._flat(out, torch.bfloat16, rows * dl, "out")
+        rest = (Hq, dl, page_size, maxb, num_blocks, float(sm_scale), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), op, _raw_stream(self.device))
+        if tq == 0:
+            native.tq_decode_attention_latent(self.handle, qp, *args, B, *rest)
+        else:
+            native.tq_prefill_attention_latent(self.handle, qp, *args, B, tq, *rest)
+        return out
+
+    def decode_attention_latent(self, q, pool, block_table, seq_lens, page_size: int, num_blocks: int, sm_scale: float,
+                                workspace=None, out=None, stream=None):
+        """Attention of one query token per sequence (q [B, Hq, latent_dim + 64] bf16) over its latent pages; returns
+        [B, Hq, latent_dim]."""
+        if q.dim() != 3:
+            raise ValueError("q must be [B, Hq, latent_dim + 64]")
+        return self._attention_latent(q, 0, pool, block_table, seq_lens, page_size, num_blocks, sm_scale, workspace, out,
+                                      stream)
+
+    def prefill_attention_latent(self, q, pool, block_table, seq_lens, page_size: int, num_blocks: int, sm_scale: float,
+                                 workspace=None, out=None, stream=None):
+        """Causal attention of the last q.shape[1] positions of every sequence (q [B, Tq, Hq, latent_dim + 64] bf16) over
+        its latent pages; returns [B, Tq, Hq, latent_dim]."""
+        if q.dim() != 4 or q.shape[1] < 1:
+            raise ValueError("q must be [B, Tq, Hq, latent_dim + 64]")
+        return self._attention_latent(q, q.shape[1], pool, block_table, seq_lens, page_size, num_blocks, sm_scale,
+                                      workspace, out, stream)
+
     def get_status(self, stream=None) -> int:
         return native.tq_get_status(self.handle, _stream(stream))
 

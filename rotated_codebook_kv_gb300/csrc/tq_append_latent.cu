@@ -1,0 +1,252 @@
+// tq_append_latent.cu -- appending tokens to latent pages: a token's latent vector, normalised where a weight is given,
+// and its rotated key part side by side in one row; the query heads' parts rotated on the way.
+//
+//   c' = c w / sqrt(mean(c^2) + eps), sums and products in fp32, rounded once
+//   (x, y) -> (x cos - y sin, y cos + x sin), every product and sum rounded once in fp32
+//
+// A block per token (several over the heads where tokens are few).  Its first warp takes the pool row: DL / 32 coordinates of
+// the latent a lane, one pass with the row in registers between the sum and the scaling.  A thread of the rest keeps one
+// unit (eight pairs) of the heads it takes, so the token's cosines and sines are loaded once.
+#include <cmath>
+#include <cuda_runtime.h>
+
+#include "tq.h"
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr int kRope = TQ_LATENT_ROPE_DIM;
+constexpr int kUnits = kRope / 16;      // units of eight pairs in a row
+constexpr int kThreads = 256;
+constexpr int kLanes = kThreads / kUnits;  // heads side by side
+
+struct LatentArgs {
+    const uint16_t *latent, *k, *q;
+    int64_t T;
+    int Hq;
+    int64_t ls, ks, qs, qh, os, oh;  // strides in elements: tokens, and heads of q and q_out
+    const uint16_t *weight;
+    float eps;
+    const int64_t *positions;
+    const float *rope;
+    int64_t rope_rows;
+    int interleaved;
+    const int64_t *slots;
+    int64_t num_slots;
+    uint16_t *pool, *q_out;
+    unsigned *status;
+};
+
+__device__ __forceinline__ uint4 ld_row(const void *p)  // plain: q may be rewritten in place
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8])
+{
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(v[i] << 16);
+        x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+{
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// A unit's cosines and sines, and the turn of its two chunks of eight coordinates.
+struct Turn {
+    float c[8], s[8];
+    __device__ __forceinline__ void load(const float *row, int u)
+    {
+        const float4 *pc = reinterpret_cast<const float4 *>(row + 8 * u), *ps = reinterpret_cast<const float4 *>(row + kRope / 2 + 8 * u);
+        *reinterpret_cast<float4 *>(c) = __ldg(pc);
+        *reinterpret_cast<float4 *>(c + 4) = __ldg(pc + 1);
+        *reinterpret_cast<float4 *>(s) = __ldg(ps);
+        *reinterpret_cast<float4 *>(s + 4) = __ldg(ps + 1);
+    }
+    static __device__ __forceinline__ void pair(float &x, float &y, float c, float s)
+    {
+        const float a = x, b = y;
+        x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+        y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    }
+    __device__ __forceinline__ void turn(uint4 &wa, uint4 &wb, int interleaved) const
+    {
+        float a[8], b[8];
+        unpack8(wa, a);
+        unpack8(wb, b);
+        if (interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pair(a[2 * i], a[2 * i + 1], c[i], s[i]);
+                pair(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pair(a[i], b[i], c[i], s[i]);
+        }
+        wa = pack8(a);
+        wb = pack8(b);
+    }
+};
+
+template <int DL>
+__global__ void __launch_bounds__(kThreads) append_latent_kernel(const LatentArgs A)
+{
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t slot = ld_pinned_s64(A.slots + t);
+    const int64_t pos = A.rope ? ld_pinned_s64(A.positions + t) : 0;
+    const bool report = tid == 0 && blockIdx.y == 0;
+    if (slot < 0) return;
+    if (slot >= A.num_slots) {
+        if (report) atomicOr(A.status, TQ_DEVERR_SLOT_RANGE);
+        return;
+    }
+    if (A.rope && (pos < 0 || pos >= A.rope_rows)) {
+        if (report) atomicOr(A.status, TQ_DEVERR_POSITION);
+        return;
+    }
+    const int u = tid % kUnits;
+    const int j0 = A.interleaved ? 16 * u : 8 * u, j1 = A.interleaved ? 16 * u + 8 : kRope / 2 + 8 * u;
+    Turn tn{};
+    if (A.rope) tn.load(A.rope + pos * kRope, u);
+    if (blockIdx.y == 0 && tid < 32) {
+        constexpr int N = DL / 256;  // chunks of eight coordinates a lane
+        uint16_t *dst = A.pool + slot * (DL + kRope);
+        const uint16_t *src = A.latent + t * A.ls;
+        uint4 w[N], ka, kb;
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = ld_row(src + 8 * (lane + 32 * i));
+        if (lane < kUnits) {
+            ka = ld_row(A.k + t * A.ks + j0);
+            kb = ld_row(A.k + t * A.ks + j1);
+        }
+        if (A.weight) {
+            uint4 g[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = ld_pinned(A.weight + 8 * (lane + 32 * i));
+            float x[N][8], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                unpack8(w[i], x[i]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum = fmaf(x[i][k], x[i][k], sum);
+            }
+            const float inv = 1.f / sqrtf(warp_sum(sum) * (1.f / DL) + A.eps);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float y[8];
+                unpack8(g[i], y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] *= x[i][k] * inv;
+                w[i] = pack8(y);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(dst + 8 * (lane + 32 * i)) = w[i];
+        if (lane < kUnits) {
+            if (A.rope) tn.turn(ka, kb, A.interleaved);
+            *reinterpret_cast<uint4 *>(dst + DL + j0) = ka;
+            *reinterpret_cast<uint4 *>(dst + DL + j1) = kb;
+        }
+    }
+    if (!A.q) return;
+    const uint16_t *q = A.q + t * A.qs;
+    uint16_t *o = A.q_out + t * A.os;
+    const int step = kLanes * gridDim.y;
+    for (int h = blockIdx.y * kLanes + tid / kUnits; h < A.Hq; h += 2 * step) {  // two heads on their way at a time
+        const bool two = h + step < A.Hq;
+        const uint16_t *s0 = q + h * A.qh, *s1 = q + (two ? h + step : h) * A.qh;
+        uint4 a0 = ld_row(s0 + j0), b0 = ld_row(s0 + j1), a1{}, b1{};
+        if (two) {
+            a1 = ld_row(s1 + j0);
+            b1 = ld_row(s1 + j1);
+        }
+        if (A.rope) {
+            tn.turn(a0, b0, A.interleaved);
+            tn.turn(a1, b1, A.interleaved);
+        }
+        *reinterpret_cast<uint4 *>(o + h * A.oh + j0) = a0;
+        *reinterpret_cast<uint4 *>(o + h * A.oh + j1) = b0;
+        if (two) {
+            *reinterpret_cast<uint4 *>(o + (h + step) * A.oh + j0) = a1;
+            *reinterpret_cast<uint4 *>(o + (h + step) * A.oh + j1) = b1;
+        }
+    }
+}
+
+template <int DL>
+cudaError_t launch(const LatentArgs &a, cudaStream_t st)
+{
+    // Few tokens: a block per 64 heads, for latency.  Many: all heads of a token in one block.
+    const unsigned gy = a.T < 1024 && a.q ? static_cast<unsigned>((a.Hq + kLanes - 1) / kLanes) : 1u;
+    append_latent_kernel<DL><<<dim3(static_cast<unsigned>(a.T), gy), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+}  // namespace
+}  // namespace tq
+
+extern "C" tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const uint16_t *k_rope, const uint16_t *q, int64_t T,
+                                      int latent_dim, int num_q_heads, int64_t latent_stride, int64_t k_stride,
+                                      int64_t q_stride_tok, int64_t q_stride_head, const uint16_t *norm_weight, float norm_eps,
+                                      const int64_t *positions, const float *rope, int64_t rope_rows, int style,
+                                      const int64_t *slot_mapping, uint16_t *pool, int page_size, int64_t num_blocks,
+                                      uint16_t *q_out, int64_t qo_stride_tok, int64_t qo_stride_head, void *stream)
+{
+    using tq::aligned;
+    using tq::api_error;
+    const char *who = "tq_append_latent";
+    if (!h) return api_error(TQ_ERR_INVALID_ARG, "%s: NULL handle", who);
+    if (latent_dim != 256 && latent_dim != 512)
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: latent_dim %d not in {256, 512}", who, latent_dim);
+    if (page_size != 16 && page_size != 32 && page_size != 64)
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: page_size %d not in {16, 32, 64}", who, page_size);
+    if (!q) num_q_heads = 0;
+    if (T < 0 || num_blocks < 1 || (q && num_q_heads < 1))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: T=%lld num_q_heads=%d num_blocks=%lld", who, static_cast<long long>(T), num_q_heads,
+                         static_cast<long long>(num_blocks));
+    if (style != TQ_ROPE_HALF && style != TQ_ROPE_INTERLEAVED)
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: unknown rotation style %d", who, style);
+    if ((q == nullptr) != (q_out == nullptr)) return api_error(TQ_ERR_INVALID_ARG, "%s: q and q_out go together", who);
+    if (norm_weight && !(norm_eps >= 0.f && std::isfinite(norm_eps)))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: norm_eps must be finite and >= 0", who);
+    if (T >= (int64_t(1) << 31) || num_q_heads > (1 << 20)) return api_error(TQ_ERR_UNSUPPORTED, "%s: too many tokens or heads in one call", who);
+    if (num_blocks > ((int64_t(1) << 31) - 1) / page_size)
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who, static_cast<long long>(num_blocks));
+    if (T == 0) return TQ_OK;
+    if (!latent || !k_rope || !slot_mapping || !pool || (rope && !positions))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (rope && rope_rows < 1) return api_error(TQ_ERR_INVALID_ARG, "%s: empty rope table", who);
+    if (!aligned(latent, 16) || !aligned(k_rope, 16) || !aligned(q, 16) || !aligned(norm_weight, 16) || !aligned(pool, 16) ||
+        !aligned(q_out, 16) || !aligned(rope, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 8))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+    const int r = TQ_LATENT_ROPE_DIM;
+    const int64_t most = int64_t(1) << 40;  // no offset passes 64 bits
+    auto bad = [&](int64_t s, int64_t least) { return s < least || s > most || s % 8; };
+    if (bad(latent_stride, latent_dim) || bad(k_stride, r) ||
+        (q && (bad(q_stride_tok, r) || bad(q_stride_head, r) || bad(qo_stride_tok, r) || bad(qo_stride_head, r))))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, no less than a row", who);
+    const tq::Codec &c = tq::handle_codec(h);
+    const tq::LatentArgs a{latent, k_rope, q, T, num_q_heads, latent_stride, k_stride, q_stride_tok, q_stride_head, qo_stride_tok,
+                           qo_stride_head, norm_weight, norm_eps, positions, rope, rope_rows, style == TQ_ROPE_INTERLEAVED,
+                           slot_mapping, num_blocks * page_size, pool, q_out, c.status};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = latent_dim == 512 ? tq::launch<512>(a, st) : tq::launch<256>(a, st);
+    if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+    return TQ_OK;
+}

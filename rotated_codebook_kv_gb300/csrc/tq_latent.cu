@@ -1,0 +1,897 @@
+// tq_latent.cu -- attention over latent pages: every head's keys and values are one shared row [c | r] a token.
+//
+//   S[r][t] = <q_r, [c_t | r_t]>    r: (query token, head) rows of a sequence, D = DL + 64 coordinates
+//   O[r][j] = sum_t P[r][t] c_t[j]  j < DL
+// with y = sm_scale log2(e) S, P = 2^(y - m) rounded to bf16, the denominator the fp32 sum of the rounded P.
+//
+// All heads read the same rows, so a tile of 128 tokens serves 128 rows: 2 (D + DL) 128 flops against 2 D bytes a token,
+// 242 flop/B at DL = 512.  O is 128 x 512 in fp32, all of an SM's tensor memory; so a pair of CTAs (a cluster of two)
+// shares a tile, M = 128 across the pair (cta_group::2): a CTA holds 64 rows of Q, O and P, and of each tile
+//   for the scores   its own 64 tokens, all D coordinates (half of B's rows), in blocks of 64 tokens x 64 coordinates;
+//   for P.V          all 128 tokens of its own DL/2 coordinates (half of B's columns).
+// Both products take B from the same offsets in the two CTAs.  Block b of a stage holds the CTA's own tokens' coordinates
+// 64 b .. 64 b + 63 for the scores; then the half of the blocks that are the other CTA's coordinates are dead, and the
+// other CTA's tokens of this CTA's coordinates are loaded over them (from L2, where the other CTA has just brought them):
+// blocks 0 .. NO - 1 hold the tile's first 64 tokens in both CTAs, NO .. 2 NO - 1 the last 64.  So a stage is 64 x D and two
+// stages fit beside Q (four at DL = 256).
+//
+// Work is dealt to the pairs in equal shares of 128-token tiles, in the order of the units (sequence, block of 128 rows):
+// every CTA finds its share from the lengths.  A unit that several pairs share leaves their sums in the workspace, and a
+// second kernel joins them.
+//
+// Warps (one CTA per SM): 4 a thread per (row, half of the tile's tokens): softmax, P, output; 1 issue of the scores and 1 of
+// P.V (in the pair's first CTA, for both); 1 loads of Q and tiles; 1 loads over the dead blocks.
+// Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT and stops the CTA, whose rows then
+// carry no weight; copies and MMAs in flight finish before the pair ends.
+#include <climits>
+#include <cmath>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+#include "tq_umma.cuh"
+
+namespace tq {
+namespace latent {
+namespace {
+
+constexpr int kRope = TQ_LATENT_ROPE_DIM;
+constexpr int kTile = 128;       // tokens of a tile, rows of a unit
+constexpr int kHalf = 64;        // a CTA's tokens and rows
+constexpr int kUnitCost = 1;     // what a unit costs beside its tiles, in tiles
+constexpr int kMinShare = 3;     // least cost of a pair's share
+constexpr int kMaxPairs = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+// The reference m stands 2^kMargin above the running maximum when it is set, and O is rescaled only when the maximum passes
+// it: P <= 1 always, and 2^-16 where it was set, so that sums of 2^16 values near the largest number do not overflow before the
+// division; bf16 has the exponents for what is smaller.
+constexpr float kMargin = 16.f;
+
+struct Args {
+    const uint16_t *pool;
+    const int32_t *block_table, *seq_lens;
+    int B, Tq, Hq, R, RT;  // R = Tq Hq rows of a sequence in RT blocks of 128
+    int P, pshift, max_blocks;
+    int64_t num_blocks;
+    int pairs;
+    float sm_scale;
+    int4 *rec;             // [pairs] unit whose first piece is this pair's: b, row block, pieces (0: none)
+    float2 *ml;            // [2 pairs][128] reference, denominator
+    float *acc;            // [2 pairs][128][DL]
+    uint16_t *out;
+    unsigned *status;
+    long long wait_limit;
+};
+
+template <int DL>
+struct Cfg {
+    static constexpr int D = DL + kRope;
+    static constexpr int NBLK = D / 64;      // blocks of a stage; the last one is the rotated part
+    static constexpr int NO = DL / 128;      // blocks of the CTA's own coordinates
+    static constexpr int NX = DL / 256;      // P.V products of 256 coordinates (128 of each CTA)
+    static constexpr int NS = DL == 512 ? 2 : 4;  // stages
+    static constexpr int NP = DL == 512 ? 1 : 2;  // buffers of P's first half (the second goes over the rotated part)
+    static constexpr int NG = (NBLK + 2) / 3;     // groups of three blocks, each with a barrier
+    static constexpr uint32_t kBlk = 64 * 128;
+    static constexpr uint32_t kStage = NBLK * kBlk;
+    static constexpr uint32_t kQOff = 0;
+    static constexpr uint32_t kKOff = NBLK * kBlk;
+    static constexpr uint32_t kPOff = kKOff + NS * kStage;
+    static constexpr uint32_t kBarOff = kPOff + NP * kBlk;
+    // barriers; (L) the pair's first CTA's counts for both
+    static constexpr int bQFull = 0;                // (L) Q landed
+    static constexpr int bKFull = 1;                // (L) [NS][NG] own tokens' blocks landed
+    static constexpr int bVFull = bKFull + NS * NG; // [NS] the other tokens' blocks landed
+    static constexpr int bSFull = bVFull + NS;      // [2] scores in tensor memory
+    static constexpr int bPFull = bSFull + 2;       // (L) [2] P written, its scores read, O rescaled
+    static constexpr int bPvDone = bPFull + 2;      // [NS] O += P V done: the stage is free
+    static constexpr int bEnd = bPvDone + NS;       // (L) [2] teardown: all MMAs issued by a warp are done
+    static constexpr int kBars = bEnd + 2;
+    static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;   // tensor-memory base, abort, issued counts, NaN flags
+    static constexpr uint32_t kXOff = kMiscOff + 64;            // [128] exchange between the two threads of a row
+    static constexpr uint32_t kPlanOff = (kXOff + 4 * 128 + 15) / 16 * 16;  // scan and plan
+    static constexpr uint32_t kSmem = kPlanOff + 128;
+    static constexpr uint32_t kTmS = 0, kTmO = 256;  // [2] 64 columns; DL / 2 columns
+    static_assert(kSmem <= 232448, "shared memory");
+};
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ float fast_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// The softmax warps' barrier; whether any of their threads says so.
+__device__ __forceinline__ bool any_of_softmax(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, 128, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
+    return r != 0;
+}
+
+// A unit's piece: tokens of tiles t0 .. t1 - 1 of `tiles`, rows of block rt of sequence b.
+struct Piece {
+    int b, rt, n, L, t0, t1, tiles;
+    long long end;  // the unit's last cost + 1
+};
+
+// The unit u's sequence, row block, tokens that its last row sees, and tiles.
+__device__ __forceinline__ void unit_of(const Args &A, int u, Piece &p)
+{
+    p.b = u / A.RT;
+    p.rt = u - p.b * A.RT;
+    const int L = min(max(__ldg(A.seq_lens + p.b), 0), A.max_blocks << A.pshift);
+    const int last = A.Tq == 1 ? 0 : (min((p.rt + 1) * kTile, A.R) - 1) / A.Hq;
+    p.L = L;
+    p.n = max(0, L - A.Tq + last + 1);
+    p.tiles = (p.n + kTile - 1) / kTile;
+}
+
+// The pair's share: costs x0 .. x1 - 1 of the units' costs laid end to end, from unit u, whose first cost is a.
+struct Share {
+    long long x0, x1, a;
+    int u, units;
+    // The next piece (t0 < t1), or a unit without a token (tiles 0).
+    __device__ __forceinline__ bool next(const Args &A, Piece &p)
+    {
+        while (u < units && a < x1) {
+            unit_of(A, u, p);
+            const long long first = a + kUnitCost;
+            a = first + p.tiles;
+            p.end = a;
+            ++u;
+            if (p.tiles == 0) {
+                if (first - kUnitCost >= x0) {
+                    p.t0 = p.t1 = 0;
+                    return true;
+                }
+                continue;
+            }
+            p.t0 = static_cast<int>(min(max(x0 - first, 0LL), static_cast<long long>(p.tiles)));
+            p.t1 = static_cast<int>(min(max(x1 - first, 0LL), static_cast<long long>(p.tiles)));
+            if (p.t0 < p.t1) return true;
+        }
+        return false;
+    }
+};
+
+template <int DL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const Args A)
+{
+    using C = Cfg<DL>;
+    constexpr int NS = C::NS, NG = C::NG, NBLK = C::NBLK, NO = C::NO;
+    extern __shared__ __align__(1024) unsigned char smem[];  // dynamic shared memory begins on a 1024-byte boundary
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = umma::cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    const uint32_t sbase = saddr(smem);
+    uint64_t *mbar = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    volatile int *misc = reinterpret_cast<volatile int *>(smem + C::kMiscOff);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
+    volatile int *abort_flag = misc + 1;
+    // misc[2..3] tiles and [4..5] Qs whose copies this and the other CTA issued; [6..7] NaN flags by a piece's parity
+    float *xch = reinterpret_cast<float *>(smem + C::kXOff);
+    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff);  // [8] warps' sums; then x0, x1, a, u, total, shares
+
+    if (warp == 4) umma::tmem_alloc_pair(tmem_slot, 512);
+    if (tid == 0) {
+        umma::mbar_init(&mbar[C::bQFull], 2);
+        for (int i = 0; i < NS * NG; ++i) umma::mbar_init(&mbar[C::bKFull + i], 2);
+        for (int i = 0; i < NS; ++i) {
+            umma::mbar_init(&mbar[C::bVFull + i], 1);
+            umma::mbar_init(&mbar[C::bPvDone + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(&mbar[C::bSFull + i], 1);
+            umma::mbar_init(&mbar[C::bPFull + i], 8);
+            umma::mbar_init(&mbar[C::bEnd + i], 1);
+        }
+        for (int i = 1; i < 8; ++i) misc[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (rank == 0) A.rec[pair] = make_int4(0, 0, 0, 0);
+    }
+
+    // ---- the pair's share: a scan of the units' costs, a stretch of units per thread ----
+    Share share;
+    share.units = A.B * A.RT;
+    const int per = (share.units + kThreads - 1) / kThreads;
+    const int u0 = min(tid * per, share.units), u1 = min(u0 + per, share.units);
+    long long mine = 0;
+    for (int u = u0; u < u1; ++u) {
+        Piece p;
+        unit_of(A, u, p);
+        mine += p.tiles + kUnitCost;
+        if (blockIdx.x == 0 && p.rt == 0 && __ldg(A.seq_lens + p.b) > (A.max_blocks << A.pshift))
+            atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) plan[warp] = upto;
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    long long total = 0, before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const long long v = plan[w];
+        if (w < warp) before += v;
+        total += v;
+    }
+    const long long shares = min(static_cast<long long>(A.pairs), max(total / kMinShare, 1LL));
+    share.x0 = pair < shares ? pair * total / shares : total;
+    share.x1 = pair < shares ? (pair + 1) * total / shares : total;
+    if (before <= share.x0 && share.x0 < before + mine) {  // one thread
+        long long a = before;
+        int u = u0;
+        for (;; ++u) {
+            Piece p;
+            unit_of(A, u, p);
+            if (a + p.tiles + kUnitCost > share.x0) break;
+            a += p.tiles + kUnitCost;
+        }
+        plan[8] = a;
+        plan[9] = u;
+    }
+    umma::cluster_sync();
+    share.a = plan[8];
+    share.u = share.x0 < share.x1 ? static_cast<int>(plan[9]) : share.units;
+    const uint32_t tbase = *tmem_slot;
+
+    // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
+    // the flag and the status bit); a zero limit tests once
+    auto wait_one = [&](int i, uint32_t par) -> bool {
+        uint64_t *mb = &mbar[i];
+        if (A.wait_limit > 0 ? umma::mbar_try_wait_cluster(mb, par) : umma::mbar_test_wait_cluster(mb, par)) return true;
+        const long long t0 = clock64();
+        while (A.wait_limit > 0 && !*abort_flag && clock64() - t0 <= A.wait_limit)
+            if (umma::mbar_try_wait_cluster(mb, par)) return true;
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            atomicOr(A.status, TQ_DEVERR_TIMEOUT);
+        }
+        return false;
+    };
+    auto wait_bar = [&](int i, uint32_t par) -> bool { return __all_sync(0xffffffffu, wait_one(i, par)); };
+    auto leader = [&](int i) -> uint32_t { return umma::peer_addr(saddr(&mbar[i]), 0); };
+    auto drain = [&](int i, uint32_t par) {
+        const long long t0 = clock64();
+        while (!umma::mbar_try_wait_cluster(&mbar[i], par) && clock64() - t0 < kDrainLimit) {
+        }
+    };
+
+    if (warp < 4) {
+        // ================= a row's half of the tokens: softmax, P, output =================
+        const int r = tid & 63, h = tid >> 6;
+        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * warp) << 16);
+        const float c = fabsf(A.sm_scale) * kLog2e;
+        const uint32_t flip = A.sm_scale < 0.f ? 0x80000000u : 0u;
+        const int *table = nullptr;
+        bool bad = false, dead = false;  // this warp's wait failed; all know
+        int it = 0, sg = 0;
+        Piece p;
+        while (share.next(A, p)) {
+            const int row = p.rt * kTile + static_cast<int>(rank) * kHalf + r;
+            const bool valid = row < A.R;
+            const size_t at = static_cast<size_t>(p.b) * A.R + row;
+            const bool whole_unit = p.t0 == 0 && p.t1 == p.tiles;
+            const size_t slot = (2 * pair + (p.t0 == 0 ? 1 : 0)) * static_cast<size_t>(kTile) + rank * kHalf + r;
+            table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
+            if (tid == 0 && rank == 0 && p.t0 == 0 && !whole_unit) {
+                // the last share with a part of this unit: the least s with (s + 1) total / shares >= end
+                const int last = static_cast<int>((p.end * shares + total - 1) / total) - 1;
+                A.rec[pair] = make_int4(p.b, p.rt, last - pair + 1, 0);
+            }
+            const int lim0 = max(0, p.L - A.Tq + (A.Tq == 1 ? 0 : p.rt * kTile / A.Hq) + 1);  // tokens that every row sees
+            const int lim = A.Tq == 1 || !valid ? p.n : max(0, p.L - A.Tq + row / A.Hq + 1);
+            // a bit per 16 tokens of this half of tile i: they lie behind the last token or on a valid page
+            auto valid_groups = [&](int i) -> uint32_t {
+                const int pos = i * kTile + h * kHalf + 16 * (lane & 3);
+                const int blk = pos < p.n ? __ldg(table + (pos >> A.pshift)) : 0;
+                return __ballot_sync(0xffffffffu, blk >= 0 && blk < A.num_blocks) & 15u;
+            };
+            float m_run = -INFINITY, l_run = 0.f;
+            const int it0 = it;
+            uint32_t groups_ok = p.t0 < p.t1 ? valid_groups(p.t0) : 0u;
+            for (int i = p.t0; i < p.t1 && !dead; ++i, ++it) {
+                bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
+                umma::fence_after_sync();
+                uint32_t s[64];
+                umma::ld64(lane_base + C::kTmS + 64 * (it & 1), s);
+                umma::fence_before_sync();
+                const int rem = lim - i * kTile - h * kHalf;  // of this half's tokens, those that the row sees
+                const uint32_t ok16 = groups_ok;
+                if (i + 1 < p.t1) groups_ok = valid_groups(i + 1);
+                const bool whole = __all_sync(0xffffffffu, rem >= kHalf && ok16 == 15u);
+                if (flip) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) s[k] ^= flip;
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (k >= rem || !(ok16 >> (k >> 4) & 1u)) s[k] = 0xff800000u;  // -inf
+                }
+                float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                    m0 = max3(m0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    m1 = max3(m1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                }
+                float top = fmaxf(m0, m1);
+                top = top == -INFINITY ? top : top * c;
+                if (any_of_softmax(bad || top > m_run)) {
+                    if (any_of_softmax(bad)) {
+                        dead = true;
+                        break;
+                    }
+                    xch[tid] = top;
+                    any_of_softmax(false);
+                    top = fmaxf(top, xch[tid ^ 64]);
+                    const bool need = valid && m_run != -INFINITY && top > m_run;
+                    const float al = need ? fast_exp2(m_run - (top + kMargin)) : 1.f;
+                    if (top > m_run) m_run = top + kMargin;
+                    if (__any_sync(0xffffffffu, need)) {  // need: there was a tile before
+                        bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);  // O is at rest
+                        umma::fence_after_sync();
+                        const uint32_t to = lane_base + C::kTmO;
+#pragma unroll 1
+                        for (int ch = 0; ch < DL / 2; ch += 32) {
+                            float o[32];
+                            umma::ld32(to + ch, o);
+                            uint32_t w[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(o[k] * al);
+                            umma::st32(to + ch, w);
+                        }
+                        umma::wait_st();
+                        umma::fence_before_sync();
+                        l_run *= al;
+                    }
+                }
+                const float ref = m_run == -INFINITY ? 0.f : m_run;
+                const uint64_t c2 = pack2(c, c), ref2 = pack2(-ref, -ref);
+                uint64_t sum0 = 0, sum1 = 0;
+                uint32_t w[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                    float2 x0 = unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, ref2));
+                    float2 x1 = unpack2(fma2(pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, ref2));
+                    x0.x = fast_exp2(x0.x);
+                    x0.y = fast_exp2(x0.y);
+                    x1.x = fast_exp2(x1.x);
+                    x1.y = fast_exp2(x1.y);
+                    w[k / 2] = bf16x2_of(x0.x, x0.y);
+                    w[k / 2 + 1] = bf16x2_of(x1.x, x1.y);
+                }
+                if (!whole) {  // hidden: zero also where c is 0 or the reference infinite
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (k >= rem || !(ok16 >> (k >> 4) & 1u)) w[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    sum0 = add2(sum0, pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)));
+                    sum1 = add2(sum1, pack2(__uint_as_float(w[k + 1] << 16), __uint_as_float(w[k + 1] & 0xffff0000u)));
+                }
+                const float2 sum = unpack2(add2(sum0, sum1));
+                l_run += sum.x + sum.y;
+                // P: the first half's buffer is free when an earlier tile's P.V is done, the rotated part with these scores
+                if (h == 0 && it >= C::NP) {
+                    bad |= !wait_bar(C::bPvDone + (it - C::NP) % NS, ((it - C::NP) / NS) & 1);
+                }
+                const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
+                const uint32_t pd = (h == 0 ? sbase + C::kPOff + (it % C::NP) * C::kBlk : st + (NBLK - 1) * C::kBlk) + r * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sts128(pd + ((k ^ (r & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+                bad |= !wait_bar(C::bVFull + it % NS, (it / NS) & 1);
+                const int rem_n = p.n - i * kTile, rem_0 = lim0 - i * kTile;
+                if (rem_n < kTile || rem_0 < min(rem_n, kTile)) {
+                    // Values that some row must not see: 0 times NaN or infinity would reach it.  Tokens behind the last one
+                    // become zeros.  Of those that only some rows see, what is not finite becomes zero, and the rows that
+                    // see it get their NaN at the end.
+                    const int f = max(rem_0, 0);
+                    for (int e = tid; e < (kTile - f) * 8 * NO; e += 128) {
+                        const int t = f + e / (8 * NO), x = e % (8 * NO);
+                        const uint32_t ad = st + ((t >> 6) * NO + (x >> 3)) * C::kBlk + (t & 63) * 128 + (((x & 7) ^ (t & 7)) << 4);
+                        if (t >= rem_n) {
+                            sts128(ad, make_uint4(0u, 0u, 0u, 0u));
+                            continue;
+                        }
+                        uint4 v = lds128(ad);
+                        uint32_t q[4] = {v.x, v.y, v.z, v.w};
+                        bool found = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((q[k] & 0x7f80u) == 0x7f80u) q[k] &= 0xffff0000u, found = true;
+                            if ((q[k] & 0x7f800000u) == 0x7f800000u) q[k] &= 0x0000ffffu, found = true;
+                        }
+                        if (found) {
+                            sts128(ad, make_uint4(q[0], q[1], q[2], q[3]));
+                            const uint32_t flag = sbase + C::kMiscOff + 4 * (6 + (sg & 1));
+                            for (uint32_t to = 0; to < 2; ++to)
+                                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(umma::peer_addr(flag, to)), "r"(1u) : "memory");
+                            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        }
+                    }
+                }
+                umma::fence_proxy_async();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) umma::cluster_arrive(leader(C::bPFull + (it & 1)));
+            }
+            if (p.t0 < p.t1 && !dead) {
+                bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);
+                umma::fence_after_sync();
+                xch[tid] = l_run;
+                dead = any_of_softmax(bad);
+                if (!dead) {
+                    l_run += xch[tid ^ 64];
+                    const bool nan = misc[6 + (sg & 1)] != 0;
+                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+#pragma unroll 1
+                    for (int ch = 0; ch < DL / 2; ch += 32) {
+                        // columns 128 x .. of the first lanes are coordinates 128 x .., of the last ones DL / 2 + 128 x ..
+                        const int j0 = h * (DL / 2) + ch;
+                        float o[32];
+                        umma::ld32(lane_base + C::kTmO + ch, o);
+                        if (nan && valid) {
+                            for (int t = lim0; t < lim; ++t) {
+                                const int blk = __ldg(table + (t >> A.pshift));
+                                if (blk < 0 || blk >= A.num_blocks) continue;
+                                const uint16_t *src = A.pool + (static_cast<int64_t>(blk) * A.P + (t & (A.P - 1))) * C::D + j0;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if ((src[k] & 0x7f80u) == 0x7f80u) o[k] = __uint_as_float(0x7fffffffu);
+                            }
+                        }
+                        if (!valid) continue;
+                        if (whole_unit) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + j0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) w[m] = bf16x2_of(o[8 * k + 2 * m] * inv, o[8 * k + 2 * m + 1] * inv);
+                                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(A.acc + slot * DL + j0);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                    }
+                    umma::fence_before_sync();
+                    if (!whole_unit && h == 0) A.ml[slot] = make_float2(m_run, l_run);
+                    any_of_softmax(false);  // the exchange and the flag have been read
+                    if (tid == 0) misc[6 + (sg & 1)] = 0;
+                }
+            }
+            if (dead || p.tiles == 0) {  // nothing counts: zeros, or a piece without weight
+                it = it0 + p.t1 - p.t0;
+                if (valid && (p.tiles == 0 || whole_unit)) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + h * (DL / 2));
+                    for (int k = 0; k < DL / 16; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+                } else if (valid && h == 0) {
+                    A.ml[slot] = make_float2(-INFINITY, 0.f);
+                }
+            }
+            if (p.tiles) ++sg;
+        }
+    } else if (warp == 4) {
+        // ================= issue of the scores, for both CTAs =================
+        if (rank == 0 && umma::elect_one()) {
+            constexpr uint32_t id = umma::idesc_bf16(128, kTile, false);
+            const uint64_t d0 = umma::make_desc_sw128(sbase + C::kQOff, 16, 1024);
+            const uint32_t q_lo = static_cast<uint32_t>(d0), hi = static_cast<uint32_t>(d0 >> 32);
+            bool ok = true;
+            int it = 0, sg = 0;
+            Piece p;
+            while (ok && share.next(A, p)) {
+                if (p.tiles == 0) continue;
+                ok = wait_one(C::bQFull, sg & 1);
+                ++sg;
+                for (int i = p.t0; ok && i < p.t1; ++i, ++it) {
+                    if (it >= 2 && !(ok = wait_one(C::bPFull + (it & 1), ((it >> 1) - 1) & 1))) break;  // these columns are read
+                    const uint32_t k_lo = q_lo + (C::kKOff + (it % NS) * C::kStage) / 16;
+                    const uint32_t ds = tbase + C::kTmS + 64 * (it & 1);
+#pragma unroll
+                    for (int b = 0; b < NBLK; ++b) {
+                        if (b % 3 == 0) {
+                            if (!(ok = wait_one(C::bKFull + (it % NS) * NG + b / 3, (it / NS) & 1))) break;
+                            umma::fence_after_sync();
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma::mma_f16_pair(ds, q_lo + b * (C::kBlk / 16) + 2 * k, hi, k_lo + b * (C::kBlk / 16) + 2 * k, hi, id,
+                                               b + k > 0);
+                    }
+                    if (ok) umma::commit_pair(&mbar[C::bSFull + (it & 1)]);
+                }
+            }
+            umma::commit_pair(&mbar[C::bEnd]);
+            drain(C::bEnd, 0);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ================= issue of P.V, for both CTAs =================
+        if (rank == 0 && umma::elect_one()) {
+            constexpr uint32_t id = umma::idesc_bf16(128, 256, true);
+            const uint64_t dp = umma::make_desc_sw128(sbase, 16, 1024), dv = umma::make_desc_sw128(sbase, C::kBlk, 1024);
+            const uint32_t lo_p = static_cast<uint32_t>(dp), hi_p = static_cast<uint32_t>(dp >> 32);
+            const uint32_t lo_v = static_cast<uint32_t>(dv), hi_v = static_cast<uint32_t>(dv >> 32);
+            bool ok = true;
+            int it = 0;
+            Piece p;
+            while (ok && share.next(A, p)) {
+                for (int i = p.t0; ok && i < p.t1; ++i, ++it) {
+                    if (!(ok = wait_one(C::bPFull + (it & 1), (it >> 1) & 1))) break;
+                    umma::fence_after_sync();
+                    const uint32_t st = (C::kKOff + (it % NS) * C::kStage) / 16;
+#pragma unroll
+                    for (int x = 0; x < C::NX; ++x)
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {  // 16 tokens
+                            const uint32_t pa = lo_p + 2 * (t & 3) + (t < 4 ? (C::kPOff + (it % C::NP) * C::kBlk) / 16
+                                                                            : st + (NBLK - 1) * (C::kBlk / 16));
+                            const uint32_t va = lo_v + st + ((t >> 2) * NO + 2 * x) * (C::kBlk / 16) + (t & 3) * 128;
+                            umma::mma_f16_pair(tbase + C::kTmO + 128 * x, pa, hi_p, va, hi_v, id, i > p.t0 || t > 0);
+                        }
+                    umma::commit_pair(&mbar[C::bPvDone + it % NS]);
+                }
+            }
+            umma::commit_pair(&mbar[C::bEnd + 1]);
+            drain(C::bEnd + 1, 0);
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ================= loads: Q, and the tiles' own tokens =================
+        const int ppt = kTile >> A.pshift, ppc = ppt >> 1;  // pages of a tile and of its half
+        const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;  // a row behind the pool: reads zeros
+        int it = 0, sg = 0;
+        bool ok = true;
+        Piece p;
+        while (ok && share.next(A, p)) {
+            if (p.tiles == 0) continue;
+            const int32_t *table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
+            auto fetch_id = [&](int i) -> int {  // lane j: the tile's page j
+                const int pos = i * kTile + (lane << A.pshift);
+                return lane < ppt && pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
+            };
+            int blk = fetch_id(p.t0);
+            for (int i = p.t0; i < p.t1; ++i, ++it) {
+                const int ahead = i + 1 < p.t1 ? fetch_id(i + 1) : -1;
+                const bool good = blk >= 0 && blk < A.num_blocks;
+                if (rank == 0 && !good && lane < ppt && i * kTile + (lane << A.pshift) < p.n) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
+                const int y = good ? blk << A.pshift : nowhere;
+                if (it >= NS && !(ok = wait_bar(C::bPvDone + it % NS, (it / NS - 1) & 1))) break;
+                const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t full = leader(C::bKFull + (it % NS) * NG + g);
+                    const int nb = min(3, NBLK - 3 * g);
+                    if (lane == 0) umma::cluster_arrive_expect(full, nb * C::kBlk);
+                    const int b = 3 * g + lane / ppc, pg = lane % ppc;
+                    const int row = __shfl_sync(0xffffffffu, y, static_cast<int>(rank) * ppc + pg);
+                    if (lane < nb * ppc)
+                        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                     ::"r"(st + b * C::kBlk + (pg << A.pshift) * 128), "l"(reinterpret_cast<uint64_t>(&tmK)), "r"(64 * b), "r"(row), "r"(full)
+                                     : "memory");
+                }
+                if (lane == 0) misc[2] = it + 1;
+                if (i == p.t0) {  // Q, once the last scores of the piece before are done
+                    if (sg > 0 && !(ok = wait_bar(C::bSFull + ((it - 1) & 1), ((it - 1) >> 1) & 1))) break;
+                    const uint32_t full = leader(C::bQFull);
+                    if (lane == 0) umma::cluster_arrive_expect(full, NBLK * C::kBlk);
+                    const int row = p.rt * kTile + static_cast<int>(rank) * kHalf;
+                    const int qy = row < A.R ? p.b * A.R + row : A.B * A.R;
+                    if (lane < NBLK)
+                        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                     ::"r"(sbase + C::kQOff + lane * C::kBlk), "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(64 * lane), "r"(qy), "r"(full)
+                                     : "memory");
+                    if (lane == 0) misc[4] = sg + 1;
+                }
+                blk = ahead;
+            }
+            ++sg;
+        }
+    } else {
+        // ================= loads: the other CTA's tokens of the own coordinates =================
+        const int ppt = kTile >> A.pshift, ppc = ppt >> 1;
+        const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;
+        int it = 0, issued = 0;
+        bool ok = true;
+        Piece p;
+        while (ok && share.next(A, p)) {
+            const int32_t *table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
+            const int other = 1 - static_cast<int>(rank);
+            auto fetch_row = [&](int i) -> int {  // lane: page lane % ppc of the other half
+                const int pos = i * kTile + other * kHalf + ((lane % ppc) << A.pshift);
+                const int blk = pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
+                return blk >= 0 && blk < A.num_blocks ? blk << A.pshift : nowhere;
+            };
+            int row = p.t0 < p.t1 ? fetch_row(p.t0) : 0;
+            for (int i = p.t0; i < p.t1; ++i, ++it) {
+                const int ahead = i + 1 < p.t1 ? fetch_row(i + 1) : 0;
+                if (!(ok = wait_bar(C::bSFull + (it & 1), (it >> 1) & 1))) break;
+                const uint32_t full = saddr(&mbar[C::bVFull + it % NS]);
+                const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage + other * NO * C::kBlk;
+                if (lane == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"(NO * C::kBlk) : "memory");
+                __syncwarp();
+                const int b = lane / ppc;
+                if (lane < NO * ppc)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                                 ::"r"(st + b * C::kBlk + ((lane % ppc) << A.pshift) * 128), "l"(reinterpret_cast<uint64_t>(&tmK)),
+                                   "r"(64 * (static_cast<int>(rank) * NO + b)), "r"(row), "r"(full)
+                                 : "memory");
+                issued = it + 1;
+                row = ahead;
+            }
+        }
+        for (int t = max(0, issued - NS); t < issued; ++t) drain(C::bVFull + t % NS, (t / NS) & 1);
+    }
+
+    // ---- teardown: what either CTA has in flight lands before the pair ends, also when a wait gave up ----
+    __syncwarp();
+    if (warp == 6 && lane < 2) {  // tell the other CTA how far this one came
+        const uint32_t to = umma::peer_addr(sbase + C::kMiscOff + 4 * (lane ? 5 : 3), rank ^ 1u);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(misc[lane ? 4 : 2]) : "memory");
+    }
+    umma::fence_before_sync();
+    umma::cluster_sync();
+    umma::fence_after_sync();
+    if (tid == 0) {
+        // a barrier that only the other CTA has announced copies on gets this CTA's arrival, so that its phase ends with them
+        for (int t = misc[2]; t < misc[3]; ++t)
+            for (int g = 0; g < NG; ++g) umma::cluster_arrive(leader(C::bKFull + (t % NS) * NG + g));
+        for (int t = misc[4]; t < misc[5]; ++t) umma::cluster_arrive(leader(C::bQFull));
+        if (rank == 0) {
+            const int tiles = max(misc[2], misc[3]), qs = max(misc[4], misc[5]);
+            for (int t = max(0, tiles - NS); t < tiles; ++t)
+                for (int g = 0; g < NG; ++g) drain(C::bKFull + (t % NS) * NG + g, (t / NS) & 1);
+            if (qs > 0) drain(C::bQFull, (qs - 1) & 1);
+        }
+    }
+    __syncthreads();
+    umma::cluster_sync();
+    if (warp == 4) umma::tmem_dealloc_pair(tbase, 512);
+}
+
+// Joins the pieces of the units that several pairs shared: a block per row at a time, kGroups stretches of its pieces side by
+// side, four coordinates a thread.
+template <int DL>
+__global__ void __launch_bounds__(DL) latent_merge_kernel(const Args A)
+{
+    constexpr int kLanes = DL / 4, kGroups = 4;
+    __shared__ int jobs[kMaxPairs];
+    __shared__ int num_jobs;
+    __shared__ float w[2 * kMaxPairs];
+    __shared__ float4 part[kGroups][kLanes];
+    const int tid = threadIdx.x, lane = tid & 31, j = tid % kLanes, grp = tid / kLanes;
+    if (tid < 32) {
+        int n = 0;
+        for (int p0 = 0; p0 < A.pairs; p0 += 32) {
+            const bool has = p0 + lane < A.pairs && A.rec[p0 + lane].z > 0;
+            const unsigned m = __ballot_sync(0xffffffffu, has);
+            if (has) jobs[n + __popc(m & ((1u << lane) - 1u))] = p0 + lane;
+            n += __popc(m);
+        }
+        if (lane == 0) num_jobs = n;
+    }
+    __syncthreads();
+    for (int e = blockIdx.x; e < num_jobs * kTile; e += gridDim.x) {
+        const int pair = jobs[e / kTile], r = e % kTile;
+        const int4 rec = A.rec[pair];
+        const int row = rec.y * kTile + r, n = rec.z;
+        if (row >= A.R) continue;
+        // piece 0 is the pair's last one, piece k the first one of pair + k
+        auto slot = [&](int k) -> size_t { return (k == 0 ? 2 * pair + 1 : 2 * (pair + k)) * static_cast<size_t>(kTile) + r; };
+        __syncthreads();
+        if (tid < n) {
+            const float2 v = A.ml[slot(tid)];
+            w[tid] = v.x;
+            w[kMaxPairs + tid] = v.y;
+        }
+        __syncthreads();
+        float M = -INFINITY;
+        for (int k = 0; k < n; ++k) M = fmaxf(M, w[k]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float den = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < n; ++k) {
+            const float l = w[kMaxPairs + k];
+            if (l != 0.f) den = fmaf(fast_exp2(w[k] - ref), l, den);
+        }
+#pragma unroll 4
+        for (int k = grp; k < n; k += kGroups) {
+            if (w[kMaxPairs + k] == 0.f) continue;
+            const float a = fast_exp2(w[k] - ref);
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(A.acc + slot(k) * DL) + j);
+            o.x = fmaf(a, v.x, o.x);
+            o.y = fmaf(a, v.y, o.y);
+            o.z = fmaf(a, v.z, o.z);
+            o.w = fmaf(a, v.w, o.w);
+        }
+        part[grp][j] = o;
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+            for (int k = 1; k < kGroups; ++k) {
+                const float4 v = part[k][j];
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
+            }
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(rec.x) * A.R + row) * DL)[j] =
+                make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
+        }
+    }
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+int pairs_of(int num_sms) { return num_sms / 2 < kMaxPairs ? num_sms / 2 : kMaxPairs; }
+
+size_t workspace_bytes(int dl, int pairs)
+{
+    const size_t rows = static_cast<size_t>(2) * pairs * kTile;
+    return align256(kMaxPairs * sizeof(int4)) + align256(rows * sizeof(float2)) + rows * dl * sizeof(float);
+}
+
+template <int DL>
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tq, const Args &a, int num_sms, cudaStream_t st)
+{
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_kernel<DL>), Cfg<DL>::kSmem);
+    if (e != cudaSuccess) return e;
+    latent_kernel<DL><<<2 * a.pairs, kThreads, Cfg<DL>::kSmem, st>>>(tk, tq, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    latent_merge_kernel<DL><<<4 * num_sms, DL, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t *pool, const int32_t *block_table,
+                 const int32_t *seq_lens, int batch, int q_tokens, int Hq, int dl, int P, int max_blocks, int64_t num_blocks,
+                 float sm_scale, void *workspace, size_t ws_bytes, uint16_t *out, void *stream)
+{
+    if (!h) return api_error(TQ_ERR_INVALID_ARG, "%s: NULL handle", who);
+    const Codec &c = handle_codec(h);
+    if (dl != 256 && dl != 512) return api_error(TQ_ERR_UNSUPPORTED, "%s: latent_dim %d not in {256, 512}", who, dl);
+    if (P != 16 && P != 32 && P != 64) return api_error(TQ_ERR_UNSUPPORTED, "%s: page_size %d not in {16, 32, 64}", who, P);
+    if (batch < 0 || q_tokens < 1 || Hq < 1 || max_blocks < 1 || num_blocks < 1)
+        return api_error(TQ_ERR_INVALID_ARG, "%s: bad sizes", who);
+    if (!std::isfinite(sm_scale)) return api_error(TQ_ERR_INVALID_ARG, "%s: sm_scale not finite", who);
+    if (max_blocks > (1 << 30) / P) return api_error(TQ_ERR_UNSUPPORTED, "%s: more than 2^30 positions", who);
+    if (num_blocks > ((int64_t(1) << 31) - 1) / P)
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who, static_cast<long long>(num_blocks));
+    const int64_t rows = static_cast<int64_t>(q_tokens) * Hq;
+    if (rows >= (int64_t(1) << 31) - kTile || rows * batch >= (int64_t(1) << 31) ||
+        (rows + kTile - 1) / kTile * batch >= (int64_t(1) << 30))
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: too many sequences x query tokens in one call", who);
+    if (batch == 0) return TQ_OK;
+    if (!q || !pool || !block_table || !seq_lens || !out) return api_error(TQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256) ||
+        !aligned(out, 16))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+    Args a{};
+    a.pairs = pairs_of(c.num_sms);
+    if (a.pairs < 1) return api_error(TQ_ERR_UNSUPPORTED, "%s: no pair of SMs", who);
+    const size_t need = workspace_bytes(dl, a.pairs);
+    if (ws_bytes < need || !workspace)
+        return api_error(TQ_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace ? ws_bytes : 0, need);
+    CUtensorMap tk, tq;
+    cudaError_t e = cudaSuccess;
+    const int d = dl + kRope;
+    if (!encode_pool_map(&tk, pool, true, d, num_blocks * P, 64, P, &e) || !encode_pool_map(&tq, q, true, d, rows * batch, 64, kHalf, &e))
+        return api_error(TQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled: %s", who, cudaGetErrorString(e));
+    a.pool = pool;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.B = batch;
+    a.Tq = q_tokens;
+    a.Hq = Hq;
+    a.R = static_cast<int>(rows);
+    a.RT = static_cast<int>((rows + kTile - 1) / kTile);
+    a.P = P;
+    a.pshift = P == 16 ? 4 : P == 32 ? 5 : 6;
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.sm_scale = sm_scale;
+    a.rec = static_cast<int4 *>(workspace);
+    a.ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + align256(kMaxPairs * sizeof(int4)));
+    a.acc = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ml) + align256(static_cast<size_t>(2) * a.pairs * kTile * sizeof(float2)));
+    a.out = out;
+    a.status = c.status;
+    a.wait_limit = c.wait_limit;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    e = dl == 512 ? launch<512>(tk, tq, a, c.num_sms, st) : launch<256>(tk, tq, a, c.num_sms, st);
+    if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+    return TQ_OK;
+}
+
+}  // namespace
+}  // namespace latent
+}  // namespace tq
+
+extern "C" size_t tq_workspace_bytes_latent(tq_handle h, int batch, int q_tokens, int num_q_heads, int latent_dim)
+{
+    if (!h || batch < 1 || q_tokens < 1 || num_q_heads < 1 || (latent_dim != 256 && latent_dim != 512)) return 0;
+    return tq::latent::workspace_bytes(latent_dim, tq::latent::pairs_of(tq::handle_codec(h).num_sms));
+}
+
+extern "C" tq_status tq_decode_attention_latent(tq_handle h, const uint16_t *q, const uint16_t *pool, const int32_t *block_table,
+                                                const int32_t *seq_lens, int batch, int num_q_heads, int latent_dim,
+                                                int page_size, int max_blocks_per_seq, int64_t num_blocks, float sm_scale,
+                                                void *workspace, size_t ws_bytes, uint16_t *out, void *stream)
+{
+    return tq::latent::attend("tq_decode_attention_latent", h, q, pool, block_table, seq_lens, batch, 1, num_q_heads, latent_dim,
+                              page_size, max_blocks_per_seq, num_blocks, sm_scale, workspace, ws_bytes, out, stream);
+}
+
+extern "C" tq_status tq_prefill_attention_latent(tq_handle h, const uint16_t *q, const uint16_t *pool, const int32_t *block_table,
+                                                 const int32_t *seq_lens, int batch, int q_tokens, int num_q_heads,
+                                                 int latent_dim, int page_size, int max_blocks_per_seq, int64_t num_blocks,
+                                                 float sm_scale, void *workspace, size_t ws_bytes, uint16_t *out, void *stream)
+{
+    return tq::latent::attend("tq_prefill_attention_latent", h, q, pool, block_table, seq_lens, batch, q_tokens, num_q_heads,
+                              latent_dim, page_size, max_blocks_per_seq, num_blocks, sm_scale, workspace, ws_bytes, out, stream);
+}

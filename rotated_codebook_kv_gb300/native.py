@@ -19,6 +19,7 @@ TQ_DEVERR_SLOT_RANGE, TQ_DEVERR_BLOCK_RANGE, TQ_DEVERR_SEQ_RANGE, TQ_DEVERR_TIME
 TQ_DEVERR_POSITION, TQ_DEVERR_SLOT_ORDER = 0x10, 0x20
 TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
 TQ_DEFAULT_WAIT_LIMIT = 2000000000
+TQ_LATENT_ROPE_DIM = 64
 
 # Every symbol include/tq.h declares, with (restype, argtypes).
 _c = ctypes
@@ -53,6 +54,13 @@ SIGNATURES = {
                                        _f32, _i32, _vp, _sz, _vp, _vp]),
     "tq_prefill_attention_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                         _i64, _f32, _i32, _vp, _sz, _vp, _vp]),
+    "tq_append_latent": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _i64,
+                                _i32, _vp, _vp, _i32, _i64, _vp, _i64, _i64, _vp]),
+    "tq_workspace_bytes_latent": (_sz, [_vp, _i32, _i32, _i32, _i32]),
+    "tq_decode_attention_latent": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i64, _f32, _vp, _sz,
+                                          _vp, _vp]),
+    "tq_prefill_attention_latent": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _f32, _vp,
+                                           _sz, _vp, _vp]),
     "tq_set_wait_limit": (_i32, [_vp, _i64]),
     "tq_get_status": (_i32, [_vp, _c.POINTER(_c.c_uint32), _vp]),
     "tq_export_params": (_i32, [_vp, _vp, _vp, _vp, _vp]),
@@ -224,6 +232,33 @@ def tq_prefill_attention_fp8(h, q, k_pool, v_pool, k_scales, v_scales, block_tab
     _check("tq_prefill_attention_fp8", load().tq_prefill_attention_fp8(
         h, q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, batch, q_tokens, num_q_heads, num_kv_heads,
         page_size, max_blocks_per_seq, num_blocks, sm_scale, splits, workspace, ws_bytes, out, stream))
+
+
+def tq_append_latent(h, latent, k_rope, q, T, latent_dim, num_q_heads, latent_stride, k_stride, q_stride_tok,
+                     q_stride_head, norm_weight, norm_eps, positions, rope, rope_rows, style, slot_mapping, pool,
+                     page_size, num_blocks, q_out, qo_stride_tok, qo_stride_head, stream) -> None:
+    _check("tq_append_latent", load().tq_append_latent(
+        h, latent, k_rope, q, T, latent_dim, num_q_heads, latent_stride, k_stride, q_stride_tok, q_stride_head,
+        norm_weight, norm_eps, positions, rope, rope_rows, style, slot_mapping, pool, page_size, num_blocks, q_out,
+        qo_stride_tok, qo_stride_head, stream))
+
+
+def tq_workspace_bytes_latent(h, batch, q_tokens, num_q_heads, latent_dim) -> int:
+    return load().tq_workspace_bytes_latent(h, batch, q_tokens, num_q_heads, latent_dim)
+
+
+def tq_decode_attention_latent(h, q, pool, block_table, seq_lens, batch, num_q_heads, latent_dim, page_size,
+                               max_blocks_per_seq, num_blocks, sm_scale, workspace, ws_bytes, out, stream) -> None:
+    _check("tq_decode_attention_latent", load().tq_decode_attention_latent(
+        h, q, pool, block_table, seq_lens, batch, num_q_heads, latent_dim, page_size, max_blocks_per_seq, num_blocks,
+        sm_scale, workspace, ws_bytes, out, stream))
+
+
+def tq_prefill_attention_latent(h, q, pool, block_table, seq_lens, batch, q_tokens, num_q_heads, latent_dim, page_size,
+                                max_blocks_per_seq, num_blocks, sm_scale, workspace, ws_bytes, out, stream) -> None:
+    _check("tq_prefill_attention_latent", load().tq_prefill_attention_latent(
+        h, q, pool, block_table, seq_lens, batch, q_tokens, num_q_heads, latent_dim, page_size, max_blocks_per_seq,
+        num_blocks, sm_scale, workspace, ws_bytes, out, stream))
 
 
 def tq_set_wait_limit(h, cycles: int) -> None:
