@@ -144,6 +144,11 @@ const Codec &handle_codec(tq_handle h);
 bool encode_pool_map(CUtensorMap *tm, const void *pool, bool bf16, int cols, int64_t rows, int box_cols, int box_rows,
                      cudaError_t *err);
 
+// A 3-D tensor map of contiguous bf16 rows seen as [cols / 64][num_rows][64]: a box is box_blocks blocks of box_rows rows of
+// 64 columns (128 bytes, 128-byte swizzle); reads past the rows give zeros.
+bool encode_row_blocks_map(CUtensorMap *tm, const void *rows, int cols, int64_t num_rows, int box_rows, int box_blocks,
+                           cudaError_t *err);
+
 // Sets a kernel's dynamic shared-memory limit once per (function, device); thread safe.
 cudaError_t ensure_smem_attr(const void *func, size_t bytes);
 

@@ -73,8 +73,11 @@ struct Cfg {
     static constexpr int NX = DL / 256;      // P.V products of 256 coordinates (128 of each CTA)
     static constexpr int NS = DL == 512 ? 2 : 4;  // stages
     static constexpr int NP = DL == 512 ? 1 : 2;  // buffers of P's first half (the second goes over the rotated part)
-    static constexpr int NG = (NBLK + 2) / 3;     // groups of three blocks, each with a barrier
+    static constexpr int GB = DL == 512 ? 3 : 5;  // blocks of a group, which has a barrier of its own
+    static constexpr int NG = NBLK / GB;
+    static_assert(NG * GB == NBLK, "whole groups");
     static constexpr uint32_t kBlk = 64 * 128;
+    static constexpr uint32_t kOct = NBLK * 1024; // eight tokens of a stage: NBLK blocks of 8 x 128 bytes
     static constexpr uint32_t kStage = NBLK * kBlk;
     static constexpr uint32_t kQOff = 0;
     static constexpr uint32_t kKOff = NBLK * kBlk;
@@ -88,9 +91,11 @@ struct Cfg {
     static constexpr int bPFull = bSFull + 2;       // (L) [2] P written, its scores read, O rescaled
     static constexpr int bPvDone = bPFull + 2;      // [NS] O += P V done: the stage is free
     static constexpr int bEnd = bPvDone + NS;       // (L) [2] teardown: all MMAs issued by a warp are done
-    static constexpr int kBars = bEnd + 2;
+    static constexpr int bQFree = bEnd + 2;         // the piece's scores are done: Q may be overwritten
+    static constexpr int kBars = bQFree + 1;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;   // tensor-memory base, abort, issued counts, NaN flags
-    static constexpr uint32_t kXOff = kMiscOff + 64;            // [128] exchange between the two threads of a row
+    static constexpr uint32_t kOkOff = kMiscOff + 64;           // [8] a bit per 8 tokens of a tile: behind the end, or on a valid page
+    static constexpr uint32_t kXOff = kOkOff + 32;              // [128] exchange between the two threads of a row
     static constexpr uint32_t kPlanOff = (kXOff + 4 * 128 + 15) / 16 * 16;  // scan and plan
     static constexpr uint32_t kSmem = kPlanOff + 128;
     static constexpr uint32_t kTmS = 0, kTmO = 256;  // [2] 64 columns; DL / 2 columns
@@ -208,7 +213,8 @@ struct Share {
 
 template <int DL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const Args A)
+    latent_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ CUtensorMap tmQ, const Args A)
 {
     using C = Cfg<DL>;
     constexpr int NS = C::NS, NG = C::NG, NBLK = C::NBLK, NO = C::NO;
@@ -222,12 +228,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
     volatile int *abort_flag = misc + 1;
     // misc[2..3] tiles and [4..5] Qs whose copies this and the other CTA issued; [6..7] NaN flags by a piece's parity
+    volatile uint32_t *okmask = reinterpret_cast<volatile uint32_t *>(smem + C::kOkOff);
     float *xch = reinterpret_cast<float *>(smem + C::kXOff);
     long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff);  // [8] warps' sums; then x0, x1, a, u, total, shares
 
     if (warp == 4) umma::tmem_alloc_pair(tmem_slot, 512);
     if (tid == 0) {
         umma::mbar_init(&mbar[C::bQFull], 2);
+        umma::mbar_init(&mbar[C::bQFree], 1);
         for (int i = 0; i < NS * NG; ++i) umma::mbar_init(&mbar[C::bKFull + i], 2);
         for (int i = 0; i < NS; ++i) {
             umma::mbar_init(&mbar[C::bVFull + i], 1);
@@ -297,10 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the flag and the status bit); a zero limit tests once
     auto wait_one = [&](int i, uint32_t par) -> bool {
         uint64_t *mb = &mbar[i];
-        if (A.wait_limit > 0 ? umma::mbar_try_wait_cluster(mb, par) : umma::mbar_test_wait_cluster(mb, par)) return true;
+        if (A.wait_limit > 0 ? umma::mbar_try_wait(mb, par) : umma::mbar_test_wait(mb, par)) return true;
         const long long t0 = clock64();
         while (A.wait_limit > 0 && !*abort_flag && clock64() - t0 <= A.wait_limit)
-            if (umma::mbar_try_wait_cluster(mb, par)) return true;
+            if (umma::mbar_try_wait(mb, par)) return true;
         if (!*abort_flag) {
             *abort_flag = 1;
             atomicOr(A.status, TQ_DEVERR_TIMEOUT);
@@ -311,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto leader = [&](int i) -> uint32_t { return umma::peer_addr(saddr(&mbar[i]), 0); };
     auto drain = [&](int i, uint32_t par) {
         const long long t0 = clock64();
-        while (!umma::mbar_try_wait_cluster(&mbar[i], par) && clock64() - t0 < kDrainLimit) {
+        while (!umma::mbar_try_wait(&mbar[i], par) && clock64() - t0 < kDrainLimit) {
         }
     };
 
@@ -339,15 +347,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const int lim0 = max(0, p.L - A.Tq + (A.Tq == 1 ? 0 : p.rt * kTile / A.Hq) + 1);  // tokens that every row sees
             const int lim = A.Tq == 1 || !valid ? p.n : max(0, p.L - A.Tq + row / A.Hq + 1);
-            // a bit per 16 tokens of this half of tile i: they lie behind the last token or on a valid page
-            auto valid_groups = [&](int i) -> uint32_t {
-                const int pos = i * kTile + h * kHalf + 16 * (lane & 3);
-                const int blk = pos < p.n ? __ldg(table + (pos >> A.pshift)) : 0;
-                return __ballot_sync(0xffffffffu, blk >= 0 && blk < A.num_blocks) & 15u;
-            };
             float m_run = -INFINITY, l_run = 0.f;
             const int it0 = it;
-            uint32_t groups_ok = p.t0 < p.t1 ? valid_groups(p.t0) : 0u;
             for (int i = p.t0; i < p.t1 && !dead; ++i, ++it) {
                 bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
                 umma::fence_after_sync();
@@ -355,9 +356,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 umma::ld64(lane_base + C::kTmS + 64 * (it & 1), s);
                 umma::fence_before_sync();
                 const int rem = lim - i * kTile - h * kHalf;  // of this half's tokens, those that the row sees
-                const uint32_t ok16 = groups_ok;
-                if (i + 1 < p.t1) groups_ok = valid_groups(i + 1);
-                const bool whole = __all_sync(0xffffffffu, rem >= kHalf && ok16 == 15u);
+                const uint32_t ok8 = okmask[it & 7] >> (8 * h) & 255u;
+                const bool whole = __all_sync(0xffffffffu, rem >= kHalf && ok8 == 255u);
                 if (flip) {
 #pragma unroll
                     for (int k = 0; k < 64; ++k) s[k] ^= flip;
@@ -365,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!whole) {
 #pragma unroll
                     for (int k = 0; k < 64; ++k)
-                        if (k >= rem || !(ok16 >> (k >> 4) & 1u)) s[k] = 0xff800000u;  // -inf
+                        if (k >= rem || !(ok8 >> (k >> 3) & 1u)) s[k] = 0xff800000u;  // -inf
                 }
                 float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -422,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!whole) {  // hidden: zero also where c is 0 or the reference infinite
 #pragma unroll
                     for (int k = 0; k < 64; ++k)
-                        if (k >= rem || !(ok16 >> (k >> 4) & 1u)) w[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+                        if (k >= rem || !(ok8 >> (k >> 3) & 1u)) w[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
@@ -436,7 +436,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bad |= !wait_bar(C::bPvDone + (it - C::NP) % NS, ((it - C::NP) / NS) & 1);
                 }
                 const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
-                const uint32_t pd = (h == 0 ? sbase + C::kPOff + (it % C::NP) * C::kBlk : st + (NBLK - 1) * C::kBlk) + r * 128;
+                const uint32_t pd = h == 0 ? sbase + C::kPOff + (it % C::NP) * C::kBlk + r * 128
+                                           : st + (r >> 3) * C::kOct + (NBLK - 1) * 1024 + (r & 7) * 128;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     sts128(pd + ((k ^ (r & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
@@ -449,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int f = max(rem_0, 0);
                     for (int e = tid; e < (kTile - f) * 8 * NO; e += 128) {
                         const int t = f + e / (8 * NO), x = e % (8 * NO);
-                        const uint32_t ad = st + ((t >> 6) * NO + (x >> 3)) * C::kBlk + (t & 63) * 128 + (((x & 7) ^ (t & 7)) << 4);
+                        const uint32_t ad = st + ((t & 63) >> 3) * C::kOct + ((t >> 6) * NO + (x >> 3)) * 1024 + (t & 7) * 128 + (((x & 7) ^ (t & 7)) << 4);
                         if (t >= rem_n) {
                             sts128(ad, make_uint4(0u, 0u, 0u, 0u));
                             continue;
@@ -487,6 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll 1
                     for (int ch = 0; ch < DL / 2; ch += 32) {
+                        __syncwarp();
                         // columns 128 x .. of the first lanes are coordinates 128 x .., of the last ones DL / 2 + 128 x ..
                         const int j0 = h * (DL / 2) + ch;
                         float o[32];
@@ -501,8 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     if ((src[k] & 0x7f80u) == 0x7f80u) o[k] = __uint_as_float(0x7fffffffu);
                             }
                         }
-                        if (!valid) continue;
-                        if (whole_unit) {
+                        if (valid && whole_unit) {
                             uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + j0);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -511,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 for (int m = 0; m < 4; ++m) w[m] = bf16x2_of(o[8 * k + 2 * m] * inv, o[8 * k + 2 * m + 1] * inv);
                                 dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                        } else {
+                        } else if (valid) {
                             float4 *dst = reinterpret_cast<float4 *>(A.acc + slot * DL + j0);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -538,8 +539,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ================= issue of the scores, for both CTAs =================
         if (rank == 0 && umma::elect_one()) {
             constexpr uint32_t id = umma::idesc_bf16(128, kTile, false);
-            const uint64_t d0 = umma::make_desc_sw128(sbase + C::kQOff, 16, 1024);
+            const uint64_t d0 = umma::make_desc_sw128(sbase + C::kQOff, 16, 1024), dk = umma::make_desc_sw128(sbase + C::kKOff, 16, C::kOct);
             const uint32_t q_lo = static_cast<uint32_t>(d0), hi = static_cast<uint32_t>(d0 >> 32);
+            const uint32_t kd_lo = static_cast<uint32_t>(dk), hi_k = static_cast<uint32_t>(dk >> 32);
             bool ok = true;
             int it = 0, sg = 0;
             Piece p;
@@ -549,21 +551,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ++sg;
                 for (int i = p.t0; ok && i < p.t1; ++i, ++it) {
                     if (it >= 2 && !(ok = wait_one(C::bPFull + (it & 1), ((it >> 1) - 1) & 1))) break;  // these columns are read
-                    const uint32_t k_lo = q_lo + (C::kKOff + (it % NS) * C::kStage) / 16;
+                    const uint32_t k_lo = kd_lo + (it % NS) * (C::kStage / 16);
                     const uint32_t ds = tbase + C::kTmS + 64 * (it & 1);
 #pragma unroll
                     for (int b = 0; b < NBLK; ++b) {
-                        if (b % 3 == 0) {
-                            if (!(ok = wait_one(C::bKFull + (it % NS) * NG + b / 3, (it / NS) & 1))) break;
+                        if (b % C::GB == 0) {
+                            if (!(ok = wait_one(C::bKFull + (it % NS) * NG + b / C::GB, (it / NS) & 1))) break;
                             umma::fence_after_sync();
                         }
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            umma::mma_f16_pair(ds, q_lo + b * (C::kBlk / 16) + 2 * k, hi, k_lo + b * (C::kBlk / 16) + 2 * k, hi, id,
+                            umma::mma_f16_pair(ds, q_lo + b * (C::kBlk / 16) + 2 * k, hi, k_lo + b * 64 + 2 * k, hi_k, id,
                                                b + k > 0);
                     }
                     if (ok) umma::commit_pair(&mbar[C::bSFull + (it & 1)]);
                 }
+                if (ok) umma::commit_pair(&mbar[C::bQFree]);
             }
             umma::commit_pair(&mbar[C::bEnd]);
             drain(C::bEnd, 0);
@@ -573,8 +576,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ================= issue of P.V, for both CTAs =================
         if (rank == 0 && umma::elect_one()) {
             constexpr uint32_t id = umma::idesc_bf16(128, 256, true);
-            const uint64_t dp = umma::make_desc_sw128(sbase, 16, 1024), dv = umma::make_desc_sw128(sbase, C::kBlk, 1024);
+            const uint64_t dp = umma::make_desc_sw128(sbase, 16, 1024), dr = umma::make_desc_sw128(sbase, 16, C::kOct),
+                           dv = umma::make_desc_sw128(sbase, 1024, C::kOct);
             const uint32_t lo_p = static_cast<uint32_t>(dp), hi_p = static_cast<uint32_t>(dp >> 32);
+            const uint32_t lo_r = static_cast<uint32_t>(dr), hi_r = static_cast<uint32_t>(dr >> 32);
             const uint32_t lo_v = static_cast<uint32_t>(dv), hi_v = static_cast<uint32_t>(dv >> 32);
             bool ok = true;
             int it = 0;
@@ -588,10 +593,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < C::NX; ++x)
 #pragma unroll
                         for (int t = 0; t < 8; ++t) {  // 16 tokens
-                            const uint32_t pa = lo_p + 2 * (t & 3) + (t < 4 ? (C::kPOff + (it % C::NP) * C::kBlk) / 16
-                                                                            : st + (NBLK - 1) * (C::kBlk / 16));
-                            const uint32_t va = lo_v + st + ((t >> 2) * NO + 2 * x) * (C::kBlk / 16) + (t & 3) * 128;
-                            umma::mma_f16_pair(tbase + C::kTmO + 128 * x, pa, hi_p, va, hi_v, id, i > p.t0 || t > 0);
+                            const uint32_t pa = 2 * (t & 3) + (t < 4 ? lo_p + (C::kPOff + (it % C::NP) * C::kBlk) / 16
+                                                                     : lo_r + st + (NBLK - 1) * 64);
+                            const uint32_t va = lo_v + st + (t & 3) * (2 * C::kOct / 16) + ((t >> 2) * NO + 2 * x) * 64;
+                            umma::mma_f16_pair(tbase + C::kTmO + 128 * x, pa, t < 4 ? hi_p : hi_r, va, hi_v, id, i > p.t0 || t > 0);
                         }
                     umma::commit_pair(&mbar[C::bPvDone + it % NS]);
                 }
@@ -602,86 +607,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 6) {
         // ================= loads: Q, and the tiles' own tokens =================
-        const int ppt = kTile >> A.pshift, ppc = ppt >> 1;  // pages of a tile and of its half
+        // Eight tokens are a box (all their coordinates lie side by side in the pool): lane j looks up the tile's tokens
+        // 8 j .. 8 j + 7.  Block ids are read a tile ahead, behind the copies, so that no release waits for them.
         const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;  // a row behind the pool: reads zeros
         int it = 0, sg = 0;
         bool ok = true;
+        const uint32_t q_full = leader(C::bQFull), k_full = leader(C::bKFull);
         Piece p;
         while (ok && share.next(A, p)) {
             if (p.tiles == 0) continue;
             const int32_t *table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
-            auto fetch_id = [&](int i) -> int {  // lane j: the tile's page j
-                const int pos = i * kTile + (lane << A.pshift);
-                return lane < ppt && pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
+            auto fetch_id = [&](int i) -> int {
+                const int pos = i * kTile + 8 * (lane & 15);
+                return pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
             };
             int blk = fetch_id(p.t0);
             for (int i = p.t0; i < p.t1; ++i, ++it) {
-                const int ahead = i + 1 < p.t1 ? fetch_id(i + 1) : -1;
+                const int pos = i * kTile + 8 * (lane & 15);
                 const bool good = blk >= 0 && blk < A.num_blocks;
-                if (rank == 0 && !good && lane < ppt && i * kTile + (lane << A.pshift) < p.n) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
-                const int y = good ? blk << A.pshift : nowhere;
+                if (rank == 0 && !good && pos < p.n) atomicOr(A.status, TQ_DEVERR_BLOCK_RANGE);
+                const uint32_t valid = __ballot_sync(0xffffffffu, good || pos >= p.n) & 0xffffu;
+                const int y = good ? (blk << A.pshift) + (pos & (A.P - 1)) : nowhere;
+                int row[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) row[g] = __shfl_sync(0xffffffffu, y, 8 * static_cast<int>(rank) + g);
                 if (it >= NS && !(ok = wait_bar(C::bPvDone + it % NS, (it / NS - 1) & 1))) break;
-                const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
-                for (int g = 0; g < NG; ++g) {
-                    const uint32_t full = leader(C::bKFull + (it % NS) * NG + g);
-                    const int nb = min(3, NBLK - 3 * g);
-                    if (lane == 0) umma::cluster_arrive_expect(full, nb * C::kBlk);
-                    const int b = 3 * g + lane / ppc, pg = lane % ppc;
-                    const int row = __shfl_sync(0xffffffffu, y, static_cast<int>(rank) * ppc + pg);
-                    if (lane < nb * ppc)
-                        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                                     ::"r"(st + b * C::kBlk + (pg << A.pshift) * 128), "l"(reinterpret_cast<uint64_t>(&tmK)), "r"(64 * b), "r"(row), "r"(full)
-                                     : "memory");
+                if (umma::elect_one()) {
+                    okmask[it & 7] = valid;
+                    const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
+                    const uint32_t full = k_full + 8 * NG * (it % NS);
+#pragma unroll
+                    for (int x = 0; x < NG; ++x) {
+                        umma::cluster_arrive_expect(full + 8 * x, 8 * 1024 * C::GB);
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                                         ::"r"(st + g * C::kOct + x * (C::GB * 1024)), "l"(reinterpret_cast<uint64_t>(&tmK)), "r"(0), "r"(row[g]), "r"(C::GB * x), "r"(full + 8 * x)
+                                         : "memory");
+                    }
+                    misc[2] = it + 1;
                 }
-                if (lane == 0) misc[2] = it + 1;
-                if (i == p.t0) {  // Q, once the last scores of the piece before are done
-                    if (sg > 0 && !(ok = wait_bar(C::bSFull + ((it - 1) & 1), ((it - 1) >> 1) & 1))) break;
-                    const uint32_t full = leader(C::bQFull);
-                    if (lane == 0) umma::cluster_arrive_expect(full, NBLK * C::kBlk);
-                    const int row = p.rt * kTile + static_cast<int>(rank) * kHalf;
-                    const int qy = row < A.R ? p.b * A.R + row : A.B * A.R;
-                    if (lane < NBLK)
-                        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                                     ::"r"(sbase + C::kQOff + lane * C::kBlk), "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(64 * lane), "r"(qy), "r"(full)
+                __syncwarp();
+                if (i == p.t0) {
+                    // Q, once the scores of the piece before are done (a barrier by the piece: this warp may be several tiles
+                    // ahead, and a parity tells only a phase from the next)
+                    if (sg > 0 && !(ok = wait_bar(C::bQFree, (sg - 1) & 1))) break;
+                    const int first = p.rt * kTile + static_cast<int>(rank) * kHalf;
+                    const int qy = first < A.R ? p.b * A.R + first : A.B * A.R;
+                    if (umma::elect_one()) {
+                        umma::cluster_arrive_expect(q_full, NBLK * C::kBlk);
+                        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                                     ::"r"(sbase + C::kQOff), "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(0), "r"(qy), "r"(0), "r"(q_full)
                                      : "memory");
-                    if (lane == 0) misc[4] = sg + 1;
+                        misc[4] = sg + 1;
+                    }
+                    __syncwarp();
                 }
-                blk = ahead;
+                blk = i + 1 < p.t1 ? fetch_id(i + 1) : -1;
             }
             ++sg;
         }
     } else {
         // ================= loads: the other CTA's tokens of the own coordinates =================
-        const int ppt = kTile >> A.pshift, ppc = ppt >> 1;
         const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;
+        const int other = 1 - static_cast<int>(rank);
         int it = 0, issued = 0;
         bool ok = true;
         Piece p;
         while (ok && share.next(A, p)) {
             const int32_t *table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
-            const int other = 1 - static_cast<int>(rank);
-            auto fetch_row = [&](int i) -> int {  // lane: page lane % ppc of the other half
-                const int pos = i * kTile + other * kHalf + ((lane % ppc) << A.pshift);
+            auto fetch_row = [&](int i) -> int {  // lane: tokens 8 (lane % 8) .. of the other half
+                const int pos = i * kTile + other * kHalf + 8 * (lane & 7);
                 const int blk = pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
-                return blk >= 0 && blk < A.num_blocks ? blk << A.pshift : nowhere;
+                return blk >= 0 && blk < A.num_blocks ? (blk << A.pshift) + (pos & (A.P - 1)) : nowhere;
             };
-            int row = p.t0 < p.t1 ? fetch_row(p.t0) : 0;
+            int y = p.t0 < p.t1 ? fetch_row(p.t0) : 0;
             for (int i = p.t0; i < p.t1; ++i, ++it) {
-                const int ahead = i + 1 < p.t1 ? fetch_row(i + 1) : 0;
+                int row[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) row[g] = __shfl_sync(0xffffffffu, y, g);
                 if (!(ok = wait_bar(C::bSFull + (it & 1), (it >> 1) & 1))) break;
-                const uint32_t full = saddr(&mbar[C::bVFull + it % NS]);
-                const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage + other * NO * C::kBlk;
-                if (lane == 0)
+                if (umma::elect_one()) {
+                    const uint32_t full = saddr(&mbar[C::bVFull + it % NS]);
+                    const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage + other * NO * 1024;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"(NO * C::kBlk) : "memory");
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                                     ::"r"(st + g * C::kOct), "l"(reinterpret_cast<uint64_t>(&tmV)), "r"(0), "r"(row[g]),
+                                       "r"(static_cast<int>(rank) * NO), "r"(full)
+                                     : "memory");
+                }
                 __syncwarp();
-                const int b = lane / ppc;
-                if (lane < NO * ppc)
-                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                                 ::"r"(st + b * C::kBlk + ((lane % ppc) << A.pshift) * 128), "l"(reinterpret_cast<uint64_t>(&tmK)),
-                                   "r"(64 * (static_cast<int>(rank) * NO + b)), "r"(row), "r"(full)
-                                 : "memory");
                 issued = it + 1;
-                row = ahead;
+                y = i + 1 < p.t1 ? fetch_row(i + 1) : 0;
             }
         }
         for (int t = max(0, issued - NS); t < issued; ++t) drain(C::bVFull + t % NS, (t / NS) & 1);
@@ -706,6 +725,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = max(0, tiles - NS); t < tiles; ++t)
                 for (int g = 0; g < NG; ++g) drain(C::bKFull + (t % NS) * NG + g, (t / NS) & 1);
             if (qs > 0) drain(C::bQFull, (qs - 1) & 1);
+        } else {
+            // the first CTA's commits arrive here too, and none may find this CTA gone: its last ones, on these
+            drain(C::bEnd, 0);
+            drain(C::bEnd + 1, 0);
         }
     }
     __syncthreads();
@@ -796,11 +819,11 @@ size_t workspace_bytes(int dl, int pairs)
 }
 
 template <int DL>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tq, const Args &a, int num_sms, cudaStream_t st)
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const Args &a, int num_sms, cudaStream_t st)
 {
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_kernel<DL>), Cfg<DL>::kSmem);
     if (e != cudaSuccess) return e;
-    latent_kernel<DL><<<2 * a.pairs, kThreads, Cfg<DL>::kSmem, st>>>(tk, tq, a);
+    latent_kernel<DL><<<2 * a.pairs, kThreads, Cfg<DL>::kSmem, st>>>(tk, tv, tq, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     latent_merge_kernel<DL><<<4 * num_sms, DL, 0, st>>>(a);
@@ -838,10 +861,11 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     const size_t need = workspace_bytes(dl, a.pairs);
     if (ws_bytes < need || !workspace)
         return api_error(TQ_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace ? ws_bytes : 0, need);
-    CUtensorMap tk, tq;
+    CUtensorMap tk, tv, tq;
     cudaError_t e = cudaSuccess;
     const int d = dl + kRope;
-    if (!encode_pool_map(&tk, pool, true, d, num_blocks * P, 64, P, &e) || !encode_pool_map(&tq, q, true, d, rows * batch, 64, kHalf, &e))
+    if (!encode_row_blocks_map(&tk, pool, d, num_blocks * P, 8, dl == 512 ? Cfg<512>::GB : Cfg<256>::GB, &e) || !encode_row_blocks_map(&tv, pool, d, num_blocks * P, 8, dl / 128, &e) ||
+        !encode_row_blocks_map(&tq, q, d, rows * batch, kHalf, d / 64, &e))
         return api_error(TQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled: %s", who, cudaGetErrorString(e));
     a.pool = pool;
     a.block_table = block_table;
@@ -863,7 +887,7 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     a.status = c.status;
     a.wait_limit = c.wait_limit;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = dl == 512 ? launch<512>(tk, tq, a, c.num_sms, st) : launch<256>(tk, tq, a, c.num_sms, st);
+    e = dl == 512 ? launch<512>(tk, tv, tq, a, c.num_sms, st) : launch<256>(tk, tv, tq, a, c.num_sms, st);
     if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return TQ_OK;
 }

@@ -174,34 +174,16 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Arrivals on a barrier of either CTA (a shared::cluster address), the second one announcing bytes to come.
+// Arrivals on a barrier of either CTA (a shared::cluster address), the second one announcing bytes to come.  They order what
+// the tensor core and the copy engine do with each CTA's own shared memory (behind a proxy fence where a thread wrote it); a
+// release at cluster scope waits for all of the SM's copies in flight, ~1200 cycles.
 __device__ __forceinline__ void cluster_arrive(uint32_t mbar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive_expect(uint32_t mbar, uint32_t bytes)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes) : "memory");
-}
-
-// Waits that acquire what the other CTA released.
-__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t *mbar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(ok)
-                 : "r"(smem_u32(mbar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *mbar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(ok)
-                 : "r"(smem_u32(mbar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void mbar_init(uint64_t *mbar, int count)
