@@ -19,8 +19,8 @@
 // every CTA finds its share from the lengths.  A unit that several pairs share leaves their sums in the workspace, and a
 // second kernel joins them.
 //
-// Warps (one CTA per SM): 4 a thread per (row, half of the tile's tokens): softmax, P, output; 1 issue of the scores and 1 of
-// P.V (in the pair's first CTA, for both); 1 loads of Q and tiles; 1 loads over the dead blocks.
+// Warps (one CTA per SM): 8, a thread per row and quarter of the tile's tokens: softmax, P, output; 1 issue of the scores and 1
+// of P.V (in the pair's first CTA, for both); 1 loads of the tiles; 1 loads of Q and over the dead blocks.
 // Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT and stops the CTA, whose rows then
 // carry no weight; copies and MMAs in flight finish before the pair ends.
 #include <climits>
@@ -43,6 +43,8 @@ constexpr int kHalf = 64;        // a CTA's tokens and rows
 constexpr int kUnitCost = 1;     // what a unit costs beside its tiles, in tiles
 constexpr int kMinShare = 3;     // least cost of a pair's share
 constexpr int kMaxPairs = 128;
+constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
+constexpr int kThreads = kSoft + 128;
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference m stands 2^kMargin above the running maximum when it is set, and O is rescaled only when the maximum passes
 // it: P <= 1 always, and 2^-16 where it was set, so that sums of 2^16 values near the largest number do not overflow before the
@@ -91,17 +93,15 @@ struct Cfg {
     static constexpr int bPFull = bSFull + 2;       // (L) [2] P written, its scores read, O rescaled
     static constexpr int bPvDone = bPFull + 2;      // [NS] O += P V done: the stage is free
     static constexpr int bEnd = bPvDone + NS;       // (L) [2] teardown: all MMAs issued by a warp are done
-    static constexpr int bQFree = bEnd + 2;         // the piece's scores are done: Q may be overwritten
-    static constexpr int kBars = bQFree + 1;
+    static constexpr int kBars = bEnd + 2;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;   // tensor-memory base, abort, issued counts, NaN flags
     static constexpr uint32_t kOkOff = kMiscOff + 64;           // [8] a bit per 8 tokens of a tile: behind the end, or on a valid page
-    static constexpr uint32_t kXOff = kOkOff + 32;              // [128] exchange between the two threads of a row
-    static constexpr uint32_t kPlanOff = (kXOff + 4 * 128 + 15) / 16 * 16;  // scan and plan
-    static constexpr uint32_t kSmem = kPlanOff + 128;
+    static constexpr uint32_t kXOff = kOkOff + 32;              // [kSoft] exchange between the four threads of a row
+    static constexpr uint32_t kPlanOff = (kXOff + 4 * kSoft + 15) / 16 * 16;  // scan and plan
+    static constexpr uint32_t kSmem = kPlanOff + 8 * (kThreads / 32 + 2);
     static constexpr uint32_t kTmS = 0, kTmO = 256;  // [2] 64 columns; DL / 2 columns
     static_assert(kSmem <= 232448, "shared memory");
 };
-constexpr int kThreads = 256;
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -160,8 +160,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
 __device__ __forceinline__ bool any_of_softmax(bool x)
 {
     uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, 128, q;\nselp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(x)), "n"(kSoft) : "memory");
     return r != 0;
 }
 
@@ -230,12 +230,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // misc[2..3] tiles and [4..5] Qs whose copies this and the other CTA issued; [6..7] NaN flags by a piece's parity
     volatile uint32_t *okmask = reinterpret_cast<volatile uint32_t *>(smem + C::kOkOff);
     float *xch = reinterpret_cast<float *>(smem + C::kXOff);
-    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff);  // [8] warps' sums; then x0, x1, a, u, total, shares
+    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff);  // warps' sums; then the first unit's first cost, and the unit
 
-    if (warp == 4) umma::tmem_alloc_pair(tmem_slot, 512);
+    if (warp == kSoftWarps) umma::tmem_alloc_pair(tmem_slot, 512);
     if (tid == 0) {
         umma::mbar_init(&mbar[C::bQFull], 2);
-        umma::mbar_init(&mbar[C::bQFree], 1);
         for (int i = 0; i < NS * NG; ++i) umma::mbar_init(&mbar[C::bKFull + i], 2);
         for (int i = 0; i < NS; ++i) {
             umma::mbar_init(&mbar[C::bVFull + i], 1);
@@ -243,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(&mbar[C::bSFull + i], 1);
-            umma::mbar_init(&mbar[C::bPFull + i], 8);
+            umma::mbar_init(&mbar[C::bPFull + i], 2 * kSoftWarps);
             umma::mbar_init(&mbar[C::bEnd + i], 1);
         }
         for (int i = 1; i < 8; ++i) misc[i] = 0;
@@ -276,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     umma::fence_after_sync();
     long long total = 0, before = upto - mine;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         const long long v = plan[w];
         if (w < warp) before += v;
         total += v;
@@ -293,12 +292,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (a + p.tiles + kUnitCost > share.x0) break;
             a += p.tiles + kUnitCost;
         }
-        plan[8] = a;
-        plan[9] = u;
+        plan[kThreads / 32] = a;
+        plan[kThreads / 32 + 1] = u;
     }
     umma::cluster_sync();
-    share.a = plan[8];
-    share.u = share.x0 < share.x1 ? static_cast<int>(plan[9]) : share.units;
+    share.a = plan[kThreads / 32];
+    share.u = share.x0 < share.x1 ? static_cast<int>(plan[kThreads / 32 + 1]) : share.units;
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
@@ -323,10 +322,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     };
 
-    if (warp < 4) {
-        // ================= a row's half of the tokens: softmax, P, output =================
-        const int r = tid & 63, h = tid >> 6;
-        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * warp) << 16);
+    if (warp < kSoftWarps) {
+        // ================= a quarter of a row's tokens: softmax, P, output =================
+        // row r, half h of the tile's tokens (and of the coordinates), columns 32 g .. of that half
+        const int r = tid & 63, h = (tid >> 6) & 1, g = tid >> 7;
+        const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const float c = fabsf(A.sm_scale) * kLog2e;
         const uint32_t flip = A.sm_scale < 0.f ? 0x80000000u : 0u;
         const int *table = nullptr;
@@ -352,26 +352,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = p.t0; i < p.t1 && !dead; ++i, ++it) {
                 bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
                 umma::fence_after_sync();
-                uint32_t s[64];
-                umma::ld64(lane_base + C::kTmS + 64 * (it & 1), s);
+                float sf[32];
+                umma::ld32(lane_base + C::kTmS + 64 * (it & 1) + 32 * g, sf);
                 umma::fence_before_sync();
-                const int rem = lim - i * kTile - h * kHalf;  // of this half's tokens, those that the row sees
-                const uint32_t ok8 = okmask[it & 7] >> (8 * h) & 255u;
-                const bool whole = __all_sync(0xffffffffu, rem >= kHalf && ok8 == 255u);
+                const int rem = lim - i * kTile - h * kHalf - 32 * g;  // of these tokens, those that the row sees
+                const uint32_t ok4 = okmask[it & 7] >> (8 * h + 4 * g) & 15u;
+                const bool whole = __all_sync(0xffffffffu, rem >= 32 && ok4 == 15u);
                 if (flip) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) s[k] ^= flip;
+                    for (int k = 0; k < 32; ++k) sf[k] = -sf[k];
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (k >= rem || !(ok8 >> (k >> 3) & 1u)) s[k] = 0xff800000u;  // -inf
+                    for (int k = 0; k < 32; ++k)
+                        if (k >= rem || !(ok4 >> (k >> 3) & 1u)) sf[k] = -INFINITY;
                 }
                 float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 64; k += 4) {
-                    m0 = max3(m0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                    m1 = max3(m1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                for (int k = 0; k < 32; k += 4) {
+                    m0 = max3(m0, sf[k], sf[k + 1]);
+                    m1 = max3(m1, sf[k + 2], sf[k + 3]);
                 }
                 float top = fmaxf(m0, m1);
                 top = top == -INFINITY ? top : top * c;
@@ -382,16 +382,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     xch[tid] = top;
                     any_of_softmax(false);
-                    top = fmaxf(top, xch[tid ^ 64]);
+                    top = fmaxf(fmaxf(top, xch[tid ^ 64]), fmaxf(xch[tid ^ 128], xch[tid ^ 192]));
                     const bool need = valid && m_run != -INFINITY && top > m_run;
                     const float al = need ? fast_exp2(m_run - (top + kMargin)) : 1.f;
                     if (top > m_run) m_run = top + kMargin;
                     if (__any_sync(0xffffffffu, need)) {  // need: there was a tile before
                         bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);  // O is at rest
                         umma::fence_after_sync();
-                        const uint32_t to = lane_base + C::kTmO;
+                        const uint32_t to = lane_base + C::kTmO + g * (DL / 4);
 #pragma unroll 1
-                        for (int ch = 0; ch < DL / 2; ch += 32) {
+                        for (int ch = 0; ch < DL / 4; ch += 32) {
                             float o[32];
                             umma::ld32(to + ch, o);
                             uint32_t w[32];
@@ -407,11 +407,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float ref = m_run == -INFINITY ? 0.f : m_run;
                 const uint64_t c2 = pack2(c, c), ref2 = pack2(-ref, -ref);
                 uint64_t sum0 = 0, sum1 = 0;
-                uint32_t w[32];
+                uint32_t w[16];
 #pragma unroll
-                for (int k = 0; k < 64; k += 4) {
-                    float2 x0 = unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, ref2));
-                    float2 x1 = unpack2(fma2(pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, ref2));
+                for (int k = 0; k < 32; k += 4) {
+                    float2 x0 = unpack2(fma2(pack2(sf[k], sf[k + 1]), c2, ref2));
+                    float2 x1 = unpack2(fma2(pack2(sf[k + 2], sf[k + 3]), c2, ref2));
                     x0.x = fast_exp2(x0.x);
                     x0.y = fast_exp2(x0.y);
                     x1.x = fast_exp2(x1.x);
@@ -421,11 +421,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!whole) {  // hidden: zero also where c is 0 or the reference infinite
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (k >= rem || !(ok8 >> (k >> 3) & 1u)) w[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+                    for (int k = 0; k < 32; ++k)
+                        if (k >= rem || !(ok4 >> (k >> 3) & 1u)) w[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
                 }
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
+                for (int k = 0; k < 16; k += 2) {
                     sum0 = add2(sum0, pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)));
                     sum1 = add2(sum1, pack2(__uint_as_float(w[k + 1] << 16), __uint_as_float(w[k + 1] & 0xffff0000u)));
                 }
@@ -439,8 +439,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t pd = h == 0 ? sbase + C::kPOff + (it % C::NP) * C::kBlk + r * 128
                                            : st + (r >> 3) * C::kOct + (NBLK - 1) * 1024 + (r & 7) * 128;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    sts128(pd + ((k ^ (r & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+                for (int k = 0; k < 4; ++k)
+                    sts128(pd + (((4 * g + k) ^ (r & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
                 bad |= !wait_bar(C::bVFull + it % NS, (it / NS) & 1);
                 const int rem_n = p.n - i * kTile, rem_0 = lim0 - i * kTile;
                 if (rem_n < kTile || rem_0 < min(rem_n, kTile)) {
@@ -448,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // become zeros.  Of those that only some rows see, what is not finite becomes zero, and the rows that
                     // see it get their NaN at the end.
                     const int f = max(rem_0, 0);
-                    for (int e = tid; e < (kTile - f) * 8 * NO; e += 128) {
+                    for (int e = tid; e < (kTile - f) * 8 * NO; e += kSoft) {
                         const int t = f + e / (8 * NO), x = e % (8 * NO);
                         const uint32_t ad = st + ((t & 63) >> 3) * C::kOct + ((t >> 6) * NO + (x >> 3)) * 1024 + (t & 7) * 128 + (((x & 7) ^ (t & 7)) << 4);
                         if (t >= rem_n) {
@@ -483,11 +483,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 xch[tid] = l_run;
                 dead = any_of_softmax(bad);
                 if (!dead) {
-                    l_run += xch[tid ^ 64];
+                    l_run = (l_run + xch[tid ^ 64]) + (xch[tid ^ 128] + xch[tid ^ 192]);
                     const bool nan = misc[6 + (sg & 1)] != 0;
                     const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll 1
-                    for (int ch = 0; ch < DL / 2; ch += 32) {
+                    for (int ch = g * (DL / 4); ch < (g + 1) * (DL / 4); ch += 32) {
                         __syncwarp();
                         // columns 128 x .. of the first lanes are coordinates 128 x .., of the last ones DL / 2 + 128 x ..
                         const int j0 = h * (DL / 2) + ch;
@@ -519,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     umma::fence_before_sync();
-                    if (!whole_unit && h == 0) A.ml[slot] = make_float2(m_run, l_run);
+                    if (!whole_unit && valid && tid < 64) A.ml[slot] = make_float2(m_run, l_run);
                     any_of_softmax(false);  // the exchange and the flag have been read
                     if (tid == 0) misc[6 + (sg & 1)] = 0;
                 }
@@ -527,15 +527,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (dead || p.tiles == 0) {  // nothing counts: zeros, or a piece without weight
                 it = it0 + p.t1 - p.t0;
                 if (valid && (p.tiles == 0 || whole_unit)) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + h * (DL / 2));
-                    for (int k = 0; k < DL / 16; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
-                } else if (valid && h == 0) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + (2 * h + g) * (DL / 4));
+                    for (int k = 0; k < DL / 32; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+                } else if (valid && tid < 64) {
                     A.ml[slot] = make_float2(-INFINITY, 0.f);
                 }
             }
             if (p.tiles) ++sg;
         }
-    } else if (warp == 4) {
+    } else if (warp == kSoftWarps) {
         // ================= issue of the scores, for both CTAs =================
         if (rank == 0 && umma::elect_one()) {
             constexpr uint32_t id = umma::idesc_bf16(128, kTile, false);
@@ -566,13 +566,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (ok) umma::commit_pair(&mbar[C::bSFull + (it & 1)]);
                 }
-                if (ok) umma::commit_pair(&mbar[C::bQFree]);
             }
             umma::commit_pair(&mbar[C::bEnd]);
             drain(C::bEnd, 0);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kSoftWarps + 1) {
         // ================= issue of P.V, for both CTAs =================
         if (rank == 0 && umma::elect_one()) {
             constexpr uint32_t id = umma::idesc_bf16(128, 256, true);
@@ -605,21 +604,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             drain(C::bEnd + 1, 0);
         }
         __syncwarp();
-    } else if (warp == 6) {
-        // ================= loads: Q, and the tiles' own tokens =================
+    } else if (warp == kSoftWarps + 2) {
+        // ================= loads: the tiles' own tokens =================
         // Eight tokens are a box (all their coordinates lie side by side in the pool): lane j looks up the tile's tokens
         // 8 j .. 8 j + 7.  Block ids are read a tile ahead, behind the copies, so that no release waits for them.
         const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;  // a row behind the pool: reads zeros
-        int it = 0, sg = 0;
+        int it = 0;
         bool ok = true;
-        const uint32_t q_full = leader(C::bQFull), k_full = leader(C::bKFull);
+        const uint32_t k_full = leader(C::bKFull);
         Piece p;
         while (ok && share.next(A, p)) {
             if (p.tiles == 0) continue;
             const int32_t *table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
             auto fetch_id = [&](int i) -> int {
                 const int pos = i * kTile + 8 * (lane & 15);
-                return pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
+                return i < p.t1 && pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
             };
             int blk = fetch_id(p.t0);
             for (int i = p.t0; i < p.t1; ++i, ++it) {
@@ -648,40 +647,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     misc[2] = it + 1;
                 }
                 __syncwarp();
-                if (i == p.t0) {
-                    // Q, once the scores of the piece before are done (a barrier by the piece: this warp may be several tiles
-                    // ahead, and a parity tells only a phase from the next)
-                    if (sg > 0 && !(ok = wait_bar(C::bQFree, (sg - 1) & 1))) break;
-                    const int first = p.rt * kTile + static_cast<int>(rank) * kHalf;
-                    const int qy = first < A.R ? p.b * A.R + first : A.B * A.R;
-                    if (umma::elect_one()) {
-                        umma::cluster_arrive_expect(q_full, NBLK * C::kBlk);
-                        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                                     ::"r"(sbase + C::kQOff), "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(0), "r"(qy), "r"(0), "r"(q_full)
-                                     : "memory");
-                        misc[4] = sg + 1;
-                    }
-                    __syncwarp();
-                }
-                blk = i + 1 < p.t1 ? fetch_id(i + 1) : -1;
+                blk = fetch_id(i + 1);
             }
-            ++sg;
         }
     } else {
-        // ================= loads: the other CTA's tokens of the own coordinates =================
+        // ================= loads: Q, and the other CTA's tokens of the own coordinates =================
         const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;
         const int other = 1 - static_cast<int>(rank);
+        const uint32_t q_full = leader(C::bQFull);
         int it = 0, issued = 0;
         bool ok = true;
         Piece p;
         while (ok && share.next(A, p)) {
+            if (p.tiles == 0) continue;
+            // Q: the scores of the piece before are done, this warp has waited for the last of them
+            const int first = p.rt * kTile + static_cast<int>(rank) * kHalf;
+            const int qy = first < A.R ? p.b * A.R + first : A.B * A.R;
+            if (umma::elect_one()) {
+                umma::cluster_arrive_expect(q_full, NBLK * C::kBlk);
+                asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                             ::"r"(sbase + C::kQOff), "l"(reinterpret_cast<uint64_t>(&tmQ)), "r"(0), "r"(qy), "r"(0), "r"(q_full)
+                             : "memory");
+                misc[4] = misc[4] + 1;
+            }
+            __syncwarp();
             const int32_t *table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
             auto fetch_row = [&](int i) -> int {  // lane: tokens 8 (lane % 8) .. of the other half
                 const int pos = i * kTile + other * kHalf + 8 * (lane & 7);
                 const int blk = pos < p.n ? __ldg(table + (pos >> A.pshift)) : -1;
                 return blk >= 0 && blk < A.num_blocks ? (blk << A.pshift) + (pos & (A.P - 1)) : nowhere;
             };
-            int y = p.t0 < p.t1 ? fetch_row(p.t0) : 0;
+            int y = fetch_row(p.t0);
             for (int i = p.t0; i < p.t1; ++i, ++it) {
                 int row[8];
 #pragma unroll
@@ -708,9 +704,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     // ---- teardown: what either CTA has in flight lands before the pair ends, also when a wait gave up ----
     __syncwarp();
-    if (warp == 6 && lane < 2) {  // tell the other CTA how far this one came
-        const uint32_t to = umma::peer_addr(sbase + C::kMiscOff + 4 * (lane ? 5 : 3), rank ^ 1u);
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(misc[lane ? 4 : 2]) : "memory");
+    if (warp >= kSoftWarps + 2 && lane == 0) {  // tell the other CTA how far this one came
+        const int w = warp == kSoftWarps + 2 ? 2 : 4;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(umma::peer_addr(sbase + C::kMiscOff + 4 * (w + 1), rank ^ 1u)), "r"(misc[w]) : "memory");
     }
     umma::fence_before_sync();
     umma::cluster_sync();
@@ -733,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     umma::cluster_sync();
-    if (warp == 4) umma::tmem_dealloc_pair(tbase, 512);
+    if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
 }
 
 // Joins the pieces of the units that several pairs shared: a block per row at a time, kGroups stretches of its pieces side by
