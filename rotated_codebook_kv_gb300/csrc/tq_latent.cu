@@ -732,75 +732,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
 }
 
-// Joins the pieces of the units that several pairs shared: a block per row at a time, kGroups stretches of its pieces side by
-// side, four coordinates a thread.
+// Joins the pieces of the units that several pairs shared.  A warp per row where the pieces are few, a block per row (a stretch of
+// the pieces a warp) where they are many.
+constexpr int kMergeWarps = 8, kFewPieces = 6;
 template <int DL>
-__global__ void __launch_bounds__(DL) latent_merge_kernel(const Args A)
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const Args A)
 {
-    constexpr int kLanes = DL / 4, kGroups = 4;
-    __shared__ int jobs[kMaxPairs];
+    constexpr int N = DL / 128;  // float4s of a row per lane
+    __shared__ int4 jobs[kMaxPairs];      // pair, pieces, first row of the unit in the outputs, rows
+    __shared__ int first[kMaxPairs + 1];  // first item of a job
+    __shared__ float4 part[kMergeWarps][DL / 4];
     __shared__ int num_jobs;
-    __shared__ float w[2 * kMaxPairs];
-    __shared__ float4 part[kGroups][kLanes];
-    const int tid = threadIdx.x, lane = tid & 31, j = tid % kLanes, grp = tid / kLanes;
-    if (tid < 32) {
-        int n = 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 0) {
+        int n = 0, items = 0;
         for (int p0 = 0; p0 < A.pairs; p0 += 32) {
-            const bool has = p0 + lane < A.pairs && A.rec[p0 + lane].z > 0;
-            const unsigned m = __ballot_sync(0xffffffffu, has);
-            if (has) jobs[n + __popc(m & ((1u << lane) - 1u))] = p0 + lane;
+            const int4 rec = p0 + lane < A.pairs ? A.rec[p0 + lane] : make_int4(0, 0, 0, 0);
+            const int rows = min(kTile, A.R - rec.y * kTile);
+            const int cnt = rec.z > 0 ? (rec.z > kFewPieces ? rows : (rows + kMergeWarps - 1) / kMergeWarps) : 0;
+            int upto = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
+            if (cnt > 0) {
+                const int at = n + __popc(m & ((1u << lane) - 1u));
+                jobs[at] = make_int4(p0 + lane, rec.z, rec.x * A.R + rec.y * kTile, rows);
+                first[at] = items + upto - cnt;
+            }
             n += __popc(m);
+            items += __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (lane == 0) num_jobs = n;
+        if (lane == 0) {
+            first[n] = items;
+            num_jobs = n;
+        }
     }
     __syncthreads();
-    for (int e = blockIdx.x; e < num_jobs * kTile; e += gridDim.x) {
-        const int pair = jobs[e / kTile], r = e % kTile;
-        const int4 rec = A.rec[pair];
-        const int row = rec.y * kTile + r, n = rec.z;
-        if (row >= A.R) continue;
+    int job = 0;
+    for (int e = blockIdx.x; e < first[num_jobs]; e += gridDim.x) {
+        while (e >= first[job + 1]) ++job;
+        const int4 J = jobs[job];
+        const int pair = J.x, n = J.y;
+        const bool many = n > kFewPieces;
+        const int r = many ? e - first[job] : (e - first[job]) * kMergeWarps + warp;
+        const bool mine = r < J.w;
         // piece 0 is the pair's last one, piece k the first one of pair + k
         auto slot = [&](int k) -> size_t { return (k == 0 ? 2 * pair + 1 : 2 * (pair + k)) * static_cast<size_t>(kTile) + r; };
-        __syncthreads();
-        if (tid < n) {
-            const float2 v = A.ml[slot(tid)];
-            w[tid] = v.x;
-            w[kMaxPairs + tid] = v.y;
-        }
-        __syncthreads();
-        float M = -INFINITY;
-        for (int k = 0; k < n; ++k) M = fmaxf(M, w[k]);
-        const float ref = M == -INFINITY ? 0.f : M;
+        float4 o[N] = {};
         float den = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < n; ++k) {
-            const float l = w[kMaxPairs + k];
-            if (l != 0.f) den = fmaf(fast_exp2(w[k] - ref), l, den);
-        }
-#pragma unroll 4
-        for (int k = grp; k < n; k += kGroups) {
-            if (w[kMaxPairs + k] == 0.f) continue;
-            const float a = fast_exp2(w[k] - ref);
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(A.acc + slot(k) * DL) + j);
-            o.x = fmaf(a, v.x, o.x);
-            o.y = fmaf(a, v.y, o.y);
-            o.z = fmaf(a, v.z, o.z);
-            o.w = fmaf(a, v.w, o.w);
-        }
-        part[grp][j] = o;
-        __syncthreads();
-        if (grp == 0) {
+        if (mine) {
+            float M = -INFINITY;
+            for (int k = lane; k < n; k += 32) M = fmaxf(M, A.ml[slot(k)].x);
+            M = warp_max(M);
+            const float ref = M == -INFINITY ? 0.f : M;
+            const int step = many ? kMergeWarps : 1;
+            const float4 *acc = reinterpret_cast<const float4 *>(A.acc) + lane;
+#pragma unroll 2
+            for (int k = many ? warp : 0; k < n; k += step) {
+                const float2 ml = A.ml[slot(k)];
+                float4 v[N];
 #pragma unroll
-            for (int k = 1; k < kGroups; ++k) {
-                const float4 v = part[k][j];
-                o.x += v.x;
-                o.y += v.y;
-                o.z += v.z;
-                o.w += v.w;
+                for (int i = 0; i < N; ++i) v[i] = __ldg(acc + slot(k) * (DL / 4) + 32 * i);
+                if (ml.y == 0.f) continue;  // no weight, nothing written
+                const float a = fast_exp2(ml.x - ref);
+                den = fmaf(a, ml.y, den);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    o[i].x = fmaf(a, v[i].x, o[i].x);
+                    o[i].y = fmaf(a, v[i].y, o[i].y);
+                    o[i].z = fmaf(a, v[i].z, o[i].z);
+                    o[i].w = fmaf(a, v[i].w, o[i].w);
+                }
+            }
+        }
+        uint2 *dst = reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(J.z) + r) * DL);
+        if (!many) {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            if (mine)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    dst[lane + 32 * i] = make_uint2(bf16x2_of(o[i].x * inv, o[i].y * inv), bf16x2_of(o[i].z * inv, o[i].w * inv));
+            continue;
+        }
+        __shared__ float dens[kMergeWarps];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[warp][lane + 32 * i] = o[i];
+        if (lane == 0) dens[warp] = den;
+        __syncthreads();
+        if (tid < DL / 4) {
+            float4 t = part[0][tid];
+            den = dens[0];
+#pragma unroll
+            for (int w = 1; w < kMergeWarps; ++w) {
+                const float4 v = part[w][tid];
+                t.x += v.x;
+                t.y += v.y;
+                t.z += v.z;
+                t.w += v.w;
+                den += dens[w];
             }
             const float inv = den == 0.f ? 0.f : 1.f / den;
-            reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(rec.x) * A.R + row) * DL)[j] =
-                make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
+            dst[tid] = make_uint2(bf16x2_of(t.x * inv, t.y * inv), bf16x2_of(t.z * inv, t.w * inv));
         }
     }
 }
@@ -822,7 +858,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorM
     latent_kernel<DL><<<2 * a.pairs, kThreads, Cfg<DL>::kSmem, st>>>(tk, tv, tq, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    latent_merge_kernel<DL><<<4 * num_sms, DL, 0, st>>>(a);
+    latent_merge_kernel<DL><<<4 * num_sms, 32 * kMergeWarps, 0, st>>>(a);
     return cudaGetLastError();
 }
 
