@@ -26,46 +26,16 @@
 #include <climits>
 #include <cmath>
 
-#include <cuda.h>
-#include <cuda_runtime.h>
-
-#include "tq_device.cuh"
-#include "tq_internal.h"
+#include "tq_latent.cuh"
 #include "tq_umma.cuh"
 
 namespace tq {
 namespace latent {
 namespace {
 
-constexpr int kRope = TQ_LATENT_ROPE_DIM;
 constexpr int kTile = 128;       // tokens of a tile, rows of a unit
 constexpr int kHalf = 64;        // a CTA's tokens and rows
-constexpr int kUnitCost = 1;     // what a unit costs beside its tiles, in tiles
-constexpr int kMinShare = 3;     // least cost of a pair's share
-constexpr int kMaxPairs = 128;
-constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 constexpr int kThreads = kSoft + 128;
-constexpr float kLog2e = 1.4426950408889634f;
-// The reference m stands 2^kMargin above the running maximum when it is set, and O is rescaled only when the maximum passes
-// it: P <= 1 always, and 2^-16 where it was set, so that sums of 2^16 values near the largest number do not overflow before the
-// division; bf16 has the exponents for what is smaller.
-constexpr float kMargin = 16.f;
-
-struct Args {
-    const uint16_t *pool;
-    const int32_t *block_table, *seq_lens;
-    int B, Tq, Hq, R, RT;  // R = Tq Hq rows of a sequence in RT blocks of 128
-    int P, pshift, max_blocks;
-    int64_t num_blocks;
-    int pairs;
-    float sm_scale;
-    int4 *rec;             // [pairs] unit whose first piece is this pair's: b, row block, pieces (0: none)
-    float2 *ml;            // [2 pairs][128] reference, denominator
-    float *acc;            // [2 pairs][128][DL]
-    uint16_t *out;
-    unsigned *status;
-    long long wait_limit;
-};
 
 template <int DL>
 struct Cfg {
@@ -101,114 +71,6 @@ struct Cfg {
     static constexpr uint32_t kSmem = kPlanOff + 8 * (kThreads / 32 + 2);
     static constexpr uint32_t kTmS = 0, kTmO = 256;  // [2] 64 columns; DL / 2 columns
     static_assert(kSmem <= 232448, "shared memory");
-};
-
-__device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-__device__ __forceinline__ float fast_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t pack2(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v)
-{
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
-// The softmax warps' barrier; whether any of their threads says so.
-__device__ __forceinline__ bool any_of_softmax(bool x)
-{
-    uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(r) : "r"(static_cast<uint32_t>(x)), "n"(kSoft) : "memory");
-    return r != 0;
-}
-
-// A unit's piece: tokens of tiles t0 .. t1 - 1 of `tiles`, rows of block rt of sequence b.
-struct Piece {
-    int b, rt, n, L, t0, t1, tiles;
-    long long end;  // the unit's last cost + 1
-};
-
-// The unit u's sequence, row block, tokens that its last row sees, and tiles.
-__device__ __forceinline__ void unit_of(const Args &A, int u, Piece &p)
-{
-    p.b = u / A.RT;
-    p.rt = u - p.b * A.RT;
-    const int L = min(max(__ldg(A.seq_lens + p.b), 0), A.max_blocks << A.pshift);
-    const int last = A.Tq == 1 ? 0 : (min((p.rt + 1) * kTile, A.R) - 1) / A.Hq;
-    p.L = L;
-    p.n = max(0, L - A.Tq + last + 1);
-    p.tiles = (p.n + kTile - 1) / kTile;
-}
-
-// The pair's share: costs x0 .. x1 - 1 of the units' costs laid end to end, from unit u, whose first cost is a.
-struct Share {
-    long long x0, x1, a;
-    int u, units;
-    // The next piece (t0 < t1), or a unit without a token (tiles 0).
-    __device__ __forceinline__ bool next(const Args &A, Piece &p)
-    {
-        while (u < units && a < x1) {
-            unit_of(A, u, p);
-            const long long first = a + kUnitCost;
-            a = first + p.tiles;
-            p.end = a;
-            ++u;
-            if (p.tiles == 0) {
-                if (first - kUnitCost >= x0) {
-                    p.t0 = p.t1 = 0;
-                    return true;
-                }
-                continue;
-            }
-            p.t0 = static_cast<int>(min(max(x0 - first, 0LL), static_cast<long long>(p.tiles)));
-            p.t1 = static_cast<int>(min(max(x1 - first, 0LL), static_cast<long long>(p.tiles)));
-            if (p.t0 < p.t1) return true;
-        }
-        return false;
-    }
 };
 
 template <int DL>
@@ -250,54 +112,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) A.rec[pair] = make_int4(0, 0, 0, 0);
     }
 
-    // ---- the pair's share: a scan of the units' costs, a stretch of units per thread ----
-    Share share;
-    share.units = A.B * A.RT;
-    const int per = (share.units + kThreads - 1) / kThreads;
-    const int u0 = min(tid * per, share.units), u1 = min(u0 + per, share.units);
-    long long mine = 0;
-    for (int u = u0; u < u1; ++u) {
-        Piece p;
-        unit_of(A, u, p);
-        mine += p.tiles + kUnitCost;
-        if (blockIdx.x == 0 && p.rt == 0 && __ldg(A.seq_lens + p.b) > (A.max_blocks << A.pshift))
-            atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
-    }
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) plan[warp] = upto;
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    long long total = 0, before = upto - mine;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const long long v = plan[w];
-        if (w < warp) before += v;
-        total += v;
-    }
-    const long long shares = min(static_cast<long long>(A.pairs), max(total / kMinShare, 1LL));
-    share.x0 = pair < shares ? pair * total / shares : total;
-    share.x1 = pair < shares ? (pair + 1) * total / shares : total;
-    if (before <= share.x0 && share.x0 < before + mine) {  // one thread
-        long long a = before;
-        int u = u0;
-        for (;; ++u) {
-            Piece p;
-            unit_of(A, u, p);
-            if (a + p.tiles + kUnitCost > share.x0) break;
-            a += p.tiles + kUnitCost;
-        }
-        plan[kThreads / 32] = a;
-        plan[kThreads / 32 + 1] = u;
-    }
+    long long total, shares;
+    Share<kTile, kTile> share = deal<kTile, kTile, kThreads>(A, pair, blockIdx.x == 0, plan, total, shares);
     umma::cluster_sync();
-    share.a = plan[kThreads / 32];
-    share.u = share.x0 < share.x1 ? static_cast<int>(plan[kThreads / 32 + 1]) : share.units;
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
@@ -735,20 +555,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Joins the pieces of the units that several pairs shared.  A warp per row where the pieces are few, a block per row (a stretch of
 // the pieces a warp) where they are many.
 constexpr int kMergeWarps = 8, kFewPieces = 6;
-template <int DL>
+template <int DL, int ROWS>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const Args A)
 {
     constexpr int N = DL / 128;  // float4s of a row per lane
-    __shared__ int4 jobs[kMaxPairs];      // pair, pieces, first row of the unit in the outputs, rows
-    __shared__ int first[kMaxPairs + 1];  // first item of a job
+    __shared__ int4 jobs[kMaxWorkers];      // pair, pieces, first row of the unit in the outputs, rows
+    __shared__ int first[kMaxWorkers + 1];  // first item of a job
     __shared__ float4 part[kMergeWarps][DL / 4];
     __shared__ int num_jobs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 0) {
         int n = 0, items = 0;
-        for (int p0 = 0; p0 < A.pairs; p0 += 32) {
-            const int4 rec = p0 + lane < A.pairs ? A.rec[p0 + lane] : make_int4(0, 0, 0, 0);
-            const int rows = min(kTile, A.R - rec.y * kTile);
+        for (int p0 = 0; p0 < A.workers; p0 += 32) {
+            const int4 rec = p0 + lane < A.workers ? A.rec[p0 + lane] : make_int4(0, 0, 0, 0);
+            const int rows = min(ROWS, A.R - rec.y * ROWS);
             const int cnt = rec.z > 0 ? (rec.z > kFewPieces ? rows : (rows + kMergeWarps - 1) / kMergeWarps) : 0;
             int upto = cnt;
 #pragma unroll
@@ -759,7 +579,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const Ar
             const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
             if (cnt > 0) {
                 const int at = n + __popc(m & ((1u << lane) - 1u));
-                jobs[at] = make_int4(p0 + lane, rec.z, rec.x * A.R + rec.y * kTile, rows);
+                jobs[at] = make_int4(p0 + lane, rec.z, rec.x * A.R + rec.y * ROWS, rows);
                 first[at] = items + upto - cnt;
             }
             n += __popc(m);
@@ -780,7 +600,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const Ar
         const int r = many ? e - first[job] : (e - first[job]) * kMergeWarps + warp;
         const bool mine = r < J.w;
         // piece 0 is the pair's last one, piece k the first one of pair + k
-        auto slot = [&](int k) -> size_t { return (k == 0 ? 2 * pair + 1 : 2 * (pair + k)) * static_cast<size_t>(kTile) + r; };
+        auto slot = [&](int k) -> size_t { return (k == 0 ? 2 * pair + 1 : 2 * (pair + k)) * static_cast<size_t>(ROWS) + r; };
         float4 o[N] = {};
         float den = 0.f;
         if (mine) {
@@ -842,23 +662,30 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const Ar
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-int pairs_of(int num_sms) { return num_sms / 2 < kMaxPairs ? num_sms / 2 : kMaxPairs; }
+// Pairs of CTAs, or CTAs: the pieces of either take the same room.
+int pairs_of(int num_sms) { return num_sms / 2 < kMaxWorkers / 2 ? num_sms / 2 : kMaxWorkers / 2; }
+static_assert(kTile == 2 * kNarrowRows, "rows of a pair's unit and of a CTA's");
 
 size_t workspace_bytes(int dl, int pairs)
 {
     const size_t rows = static_cast<size_t>(2) * pairs * kTile;
-    return align256(kMaxPairs * sizeof(int4)) + align256(rows * sizeof(float2)) + rows * dl * sizeof(float);
+    return align256(kMaxWorkers * sizeof(int4)) + align256(rows * sizeof(float2)) + rows * dl * sizeof(float);
 }
 
 template <int DL>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const Args &a, int num_sms, cudaStream_t st)
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const Args &a, cudaStream_t st)
 {
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_kernel<DL>), Cfg<DL>::kSmem);
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_kernel<DL>), Cfg<DL>::kSmem);
     if (e != cudaSuccess) return e;
-    latent_kernel<DL><<<2 * a.pairs, kThreads, Cfg<DL>::kSmem, st>>>(tk, tv, tq, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    latent_merge_kernel<DL><<<4 * num_sms, 32 * kMergeWarps, 0, st>>>(a);
+    latent_kernel<DL><<<2 * a.workers, kThreads, Cfg<DL>::kSmem, st>>>(tk, tv, tq, a);
+    return cudaGetLastError();
+}
+
+template <int DL>
+cudaError_t launch_merge(const Args &a, bool narrow, int num_sms, cudaStream_t st)
+{
+    if (narrow) latent_merge_kernel<DL, kNarrowRows><<<4 * num_sms, 32 * kMergeWarps, 0, st>>>(a);
+    else latent_merge_kernel<DL, kTile><<<4 * num_sms, 32 * kMergeWarps, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -888,15 +715,19 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
         !aligned(out, 16))
         return api_error(TQ_ERR_INVALID_ARG, "%s: misaligned pointer", who);
     Args a{};
-    a.pairs = pairs_of(c.num_sms);
-    if (a.pairs < 1) return api_error(TQ_ERR_UNSUPPORTED, "%s: no pair of SMs", who);
-    const size_t need = workspace_bytes(dl, a.pairs);
+    const int pairs = pairs_of(c.num_sms);
+    if (pairs < 1) return api_error(TQ_ERR_UNSUPPORTED, "%s: no pair of SMs", who);
+    const bool narrow = rows <= kNarrowRows;
+    a.workers = narrow ? 2 * pairs : pairs;
+    const size_t need = workspace_bytes(dl, pairs);
     if (ws_bytes < need || !workspace)
         return api_error(TQ_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace ? ws_bytes : 0, need);
     CUtensorMap tk, tv, tq;
     cudaError_t e = cudaSuccess;
     const int d = dl + kRope;
-    if (!encode_row_blocks_map(&tk, pool, d, num_blocks * P, 8, dl == 512 ? Cfg<512>::GB : Cfg<256>::GB, &e) || !encode_row_blocks_map(&tv, pool, d, num_blocks * P, 8, dl / 128, &e) ||
+    const int group = narrow ? narrow_group(dl) : dl == 512 ? Cfg<512>::GB : Cfg<256>::GB;
+    if (!encode_row_blocks_map(&tk, pool, d, num_blocks * P, 8, group, &e) ||
+        (!narrow && !encode_row_blocks_map(&tv, pool, d, num_blocks * P, 8, dl / 128, &e)) ||
         !encode_row_blocks_map(&tq, q, d, rows * batch, kHalf, d / 64, &e))
         return api_error(TQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled: %s", who, cudaGetErrorString(e));
     a.pool = pool;
@@ -906,20 +737,22 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     a.Tq = q_tokens;
     a.Hq = Hq;
     a.R = static_cast<int>(rows);
-    a.RT = static_cast<int>((rows + kTile - 1) / kTile);
+    a.RT = narrow ? 1 : static_cast<int>((rows + kTile - 1) / kTile);
     a.P = P;
     a.pshift = P == 16 ? 4 : P == 32 ? 5 : 6;
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
     a.sm_scale = sm_scale;
     a.rec = static_cast<int4 *>(workspace);
-    a.ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + align256(kMaxPairs * sizeof(int4)));
-    a.acc = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ml) + align256(static_cast<size_t>(2) * a.pairs * kTile * sizeof(float2)));
+    a.ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + align256(kMaxWorkers * sizeof(int4)));
+    a.acc = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ml) + align256(static_cast<size_t>(2) * pairs * kTile * sizeof(float2)));
     a.out = out;
     a.status = c.status;
     a.wait_limit = c.wait_limit;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    e = dl == 512 ? launch<512>(tk, tv, tq, a, c.num_sms, st) : launch<256>(tk, tv, tq, a, c.num_sms, st);
+    if (narrow) e = launch_narrow(tk, tq, dl, a, st);
+    else e = dl == 512 ? launch<512>(tk, tv, tq, a, st) : launch<256>(tk, tv, tq, a, st);
+    if (e == cudaSuccess) e = dl == 512 ? launch_merge<512>(a, narrow, c.num_sms, st) : launch_merge<256>(a, narrow, c.num_sms, st);
     if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return TQ_OK;
 }
