@@ -118,6 +118,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     long long total, shares;
     Share<kTile, kTile> share = deal<kTile, kTile, kThreads>(A, pair, blockIdx.x == 0, plan, total, shares);
     umma::cluster_sync();
+    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
@@ -552,111 +553,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
 }
 
-// Joins the pieces of the units that several pairs shared.  A warp per row where the pieces are few, a block per row (a stretch of
-// the pieces a warp) where they are many.
-constexpr int kMergeWarps = 8, kFewPieces = 6;
+// Joins the pieces of the units that several workers shared: a warp per row where the pieces are few, a block per 128 coordinates
+// of a row (a stretch of the pieces a warp) where they are many.
+constexpr int kMergeWarps = 8, kFewPieces = 16;
+static_assert(kMaxWorkers <= 32 * kMergeWarps, "a thread per worker");
 template <int DL, int ROWS>
-__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const Args A)
+__global__ void __launch_bounds__(32 * kMergeWarps, 2) latent_merge_kernel(const Args A)
 {
     constexpr int N = DL / 128;  // float4s of a row per lane
-    __shared__ int4 jobs[kMaxWorkers];      // pair, pieces, first row of the unit in the outputs, rows
+    __shared__ int4 jobs[kMaxWorkers];      // worker, pieces, first row of the unit in the outputs, rows
     __shared__ int first[kMaxWorkers + 1];  // first item of a job
-    __shared__ float4 part[kMergeWarps][DL / 4];
-    __shared__ int num_jobs;
+    __shared__ int2 sums[kMergeWarps];
+    __shared__ float4 part[kMergeWarps][32];
+    __shared__ float dens[kMergeWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == 0) {
-        int n = 0, items = 0;
-        for (int p0 = 0; p0 < A.workers; p0 += 32) {
-            const int4 rec = p0 + lane < A.workers ? A.rec[p0 + lane] : make_int4(0, 0, 0, 0);
-            const int rows = min(ROWS, A.R - rec.y * ROWS);
-            const int cnt = rec.z > 0 ? (rec.z > kFewPieces ? rows : (rows + kMergeWarps - 1) / kMergeWarps) : 0;
-            int upto = cnt;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the attention kernel runs
+    const int4 rec = tid < A.workers ? A.rec[tid] : make_int4(0, 0, 0, 0);
+    const int rows = min(ROWS, A.R - rec.y * ROWS);
+    const int cnt = rec.z > kFewPieces ? N * rows : rec.z > 0 ? (rows + kMergeWarps - 1) / kMergeWarps : 0;
+    int upto = cnt;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
-            if (cnt > 0) {
-                const int at = n + __popc(m & ((1u << lane) - 1u));
-                jobs[at] = make_int4(p0 + lane, rec.z, rec.x * A.R + rec.y * ROWS, rows);
-                first[at] = items + upto - cnt;
-            }
-            n += __popc(m);
-            items += __shfl_sync(0xffffffffu, upto, 31);
-        }
-        if (lane == 0) {
-            first[n] = items;
-            num_jobs = n;
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
     }
+    const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
+    if (lane == 31) sums[warp] = make_int2(__popc(m), upto);
+    __syncthreads();
+    int num_jobs = 0, items = 0, at = __popc(m & ((1u << lane) - 1u)), before = upto - cnt;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+        if (w < warp) {
+            at += sums[w].x;
+            before += sums[w].y;
+        }
+        num_jobs += sums[w].x;
+        items += sums[w].y;
+    }
+    if (cnt > 0) {
+        jobs[at] = make_int4(tid, rec.z, rec.x * A.R + rec.y * ROWS, rows);
+        first[at] = before;
+    }
+    if (tid == 0) first[num_jobs] = items;
     __syncthreads();
     int job = 0;
-    for (int e = blockIdx.x; e < first[num_jobs]; e += gridDim.x) {
+    for (int e = blockIdx.x; e < items; e += gridDim.x) {
         while (e >= first[job + 1]) ++job;
         const int4 J = jobs[job];
-        const int pair = J.x, n = J.y;
-        const bool many = n > kFewPieces;
-        const int r = many ? e - first[job] : (e - first[job]) * kMergeWarps + warp;
-        const bool mine = r < J.w;
-        // piece 0 is the pair's last one, piece k the first one of pair + k
-        auto slot = [&](int k) -> size_t { return (k == 0 ? 2 * pair + 1 : 2 * (pair + k)) * static_cast<size_t>(ROWS) + r; };
-        float4 o[N] = {};
-        float den = 0.f;
-        if (mine) {
-            float M = -INFINITY;
-            for (int k = lane; k < n; k += 32) M = fmaxf(M, A.ml[slot(k)].x);
-            M = warp_max(M);
-            const float ref = M == -INFINITY ? 0.f : M;
-            const int step = many ? kMergeWarps : 1;
-            const float4 *acc = reinterpret_cast<const float4 *>(A.acc) + lane;
-#pragma unroll 2
-            for (int k = many ? warp : 0; k < n; k += step) {
-                const float2 ml = A.ml[slot(k)];
-                float4 v[N];
+        const int n = J.y;
+        // piece 0 is the worker's last one, piece k the first one of worker + k
+        auto slot = [&](int k, int r) -> size_t { return (k == 0 ? 2 * J.x + 1 : 2 * (J.x + k)) * static_cast<size_t>(ROWS) + r; };
+        auto add = [&](float4 &o, float a, float4 v) {
+            o.x = fmaf(a, v.x, o.x);
+            o.y = fmaf(a, v.y, o.y);
+            o.z = fmaf(a, v.z, o.z);
+            o.w = fmaf(a, v.w, o.w);
+        };
+        auto put = [&](int r, int j4, float4 o, float den) {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(J.z) + r) * DL)[j4] =
+                make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
+        };
+        const float4 *acc = reinterpret_cast<const float4 *>(A.acc);
+        if (n <= kFewPieces) {
+            const int r = (e - first[job]) * kMergeWarps + warp;
+            if (r >= J.w) continue;
+            const float2 mine = lane < n ? A.ml[slot(lane, r)] : make_float2(-INFINITY, 0.f);
+            const float M = warp_max(mine.x), ref = M == -INFINITY ? 0.f : M;
+            // a piece without weight wrote nothing: its factor stays 0 and its sums are not taken
+            const float a = mine.y == 0.f ? 0.f : fast_exp2(mine.x - ref);
+            const unsigned some = __ballot_sync(0xffffffffu, mine.y != 0.f);
+            const float den = warp_sum(mine.y == 0.f ? 0.f : a * mine.y);
+            float4 o[N] = {};
+            for (int k0 = 0; k0 < n; k0 += 4) {
+                float4 v[4][N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = __ldg(acc + slot(k) * (DL / 4) + 32 * i);
-                if (ml.y == 0.f) continue;  // no weight, nothing written
-                const float a = fast_exp2(ml.x - ref);
-                den = fmaf(a, ml.y, den);
+                for (int k = 0; k < 4; ++k)
+                    if (some >> (k0 + k) & 1u)
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    o[i].x = fmaf(a, v[i].x, o[i].x);
-                    o[i].y = fmaf(a, v[i].y, o[i].y);
-                    o[i].z = fmaf(a, v[i].z, o[i].z);
-                    o[i].w = fmaf(a, v[i].w, o[i].w);
+                        for (int i = 0; i < N; ++i) v[k][i] = acc[slot(k0 + k, r) * (DL / 4) + lane + 32 * i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float ak = __shfl_sync(0xffffffffu, a, (k0 + k) & 31);
+                    if (some >> (k0 + k) & 1u)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) add(o[i], ak, v[k][i]);
                 }
             }
-        }
-        uint2 *dst = reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(J.z) + r) * DL);
-        if (!many) {
-            const float inv = den == 0.f ? 0.f : 1.f / den;
-            if (mine)
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    dst[lane + 32 * i] = make_uint2(bf16x2_of(o[i].x * inv, o[i].y * inv), bf16x2_of(o[i].z * inv, o[i].w * inv));
+            for (int i = 0; i < N; ++i) put(r, lane + 32 * i, o[i], den);
             continue;
         }
-        __shared__ float dens[kMergeWarps];
-        __syncthreads();
+        const int r = (e - first[job]) / N, i = (e - first[job]) % N;
+        float M = -INFINITY;
+        for (int k = lane; k < n; k += 32) M = fmaxf(M, A.ml[slot(k, r)].x);
+        M = warp_max(M);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float den = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kDeep = 8;
+        for (int k0 = warp; k0 < n; k0 += kDeep * kMergeWarps) {
+            float2 ml[kDeep];
+            float4 v[kDeep];
 #pragma unroll
-        for (int i = 0; i < N; ++i) part[warp][lane + 32 * i] = o[i];
+            for (int j = 0; j < kDeep; ++j) {
+                const int k = k0 + j * kMergeWarps;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                if (k < n) {
+                    ml[j] = A.ml[slot(k, r)];
+                    v[j] = acc[slot(k, r) * (DL / 4) + lane + 32 * i];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) {
+                if (ml[j].y == 0.f) continue;
+                const float a = fast_exp2(ml[j].x - ref);
+                den = fmaf(a, ml[j].y, den);
+                add(o, a, v[j]);
+            }
+        }
+        __syncthreads();
+        part[warp][lane] = o;
         if (lane == 0) dens[warp] = den;
         __syncthreads();
-        if (tid < DL / 4) {
-            float4 t = part[0][tid];
-            den = dens[0];
+        if (warp == 0) {
 #pragma unroll
             for (int w = 1; w < kMergeWarps; ++w) {
-                const float4 v = part[w][tid];
-                t.x += v.x;
-                t.y += v.y;
-                t.z += v.z;
-                t.w += v.w;
+                add(o, 1.f, part[w][lane]);
                 den += dens[w];
             }
-            const float inv = den == 0.f ? 0.f : 1.f / den;
-            dst[tid] = make_uint2(bf16x2_of(t.x * inv, t.y * inv), bf16x2_of(t.z * inv, t.w * inv));
+            put(r, lane + 32 * i, o, den);
         }
     }
 }
@@ -684,9 +710,17 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorM
 template <int DL>
 cudaError_t launch_merge(const Args &a, bool narrow, int num_sms, cudaStream_t st)
 {
-    if (narrow) latent_merge_kernel<DL, kNarrowRows><<<4 * num_sms, 32 * kMergeWarps, 0, st>>>(a);
-    else latent_merge_kernel<DL, kTile><<<4 * num_sms, 32 * kMergeWarps, 0, st>>>(a);
-    return cudaGetLastError();
+    // its blocks start as the attention's end, and wait for all of them
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * num_sms);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return narrow ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL, kNarrowRows>, a) : cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL, kTile>, a);
 }
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }

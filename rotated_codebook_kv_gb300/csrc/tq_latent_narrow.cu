@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Share<kNarrowRows, kTok> share = deal<kNarrowRows, kTok, kThreads>(A, worker, blockIdx.x == 0,
                                                                        reinterpret_cast<long long *>(smem + C::kPlanOff), total, shares);
     umma::fence_after_sync();
+    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, see tq_latent.cu
