@@ -433,6 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int it = 0;
         bool ok = true;
         const uint32_t k_full = leader(C::bKFull);
+        const bool far = NS == 2 && A.RT == 1;  // several row blocks read the same tiles, which are in L2 then
         Piece p;
         while (ok && share.next(A, p)) {
             if (p.tiles == 0) continue;
@@ -469,6 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 blk = fetch_id(i + 1);
+                if (far) prefetch_rows<C::D>(A, (i + NS) * kTile + 8 * (lane & 15), fetch_id(i + NS), lane < 16 && lane >> 3 == static_cast<int>(rank));
             }
         }
     } else {

@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= loads of tiles: boxes of eight tokens, a lane looks up one =================
         const int nowhere = static_cast<int>(A.num_blocks) << A.pshift;  // a row behind the pool: reads zeros
         const uint32_t k_full = saddr(&mbar[C::bKFull]);
+        constexpr bool kPrefetch = NS == 2;  // with four stages it costs 2 % (190 sequences of up to 900 tokens 32.5 -> 33 us)
         int it = 0, issued = 0;
         bool ok = true;
         Piece p;
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 issued = it + 1;
                 blk = fetch_id(i + 1);
+                if (kPrefetch) prefetch_rows<C::D>(A, i * kTok + NS * kTok + 8 * (lane & 7), fetch_id(i + NS), lane < 8);
             }
         }
         for (int t = max(0, issued - NS); t < issued; ++t)
