@@ -109,16 +109,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 1; i < 8; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (rank == 0) A.rec[pair] = make_int4(0, 0, 0, 0);
     }
 
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    long long total, shares;
-    Share<kTile, kTile> share = deal<kTile, kTile, kThreads>(A, pair, blockIdx.x == 0, plan, total, shares);
+    int shares;
+    Share<kTile, kTile> share = deal<kTile, kTile, kThreads>(A, pair, blockIdx.x == 0, rank == 0, plan, shares);
     umma::cluster_sync();
-    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
@@ -161,11 +159,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool whole_unit = p.t0 == 0 && p.t1 == p.tiles;
             const size_t slot = (2 * pair + (p.t0 == 0 ? 1 : 0)) * static_cast<size_t>(kTile) + rank * kHalf + r;
             table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
-            if (tid == 0 && rank == 0 && p.t0 == 0 && !whole_unit) {
-                // the last share with a part of this unit: the least s with (s + 1) total / shares >= end
-                const int last = static_cast<int>((p.end * shares + total - 1) / total) - 1;
-                A.rec[pair] = make_int4(p.b, p.rt, last - pair + 1, 0);
-            }
             const int lim0 = max(0, p.L - A.Tq + (A.Tq == 1 ? 0 : p.rt * kTile / A.Hq) + 1);  // tokens that every row sees
             const int lim = A.Tq == 1 || !valid ? p.n : max(0, p.L - A.Tq + row / A.Hq + 1);
             float m_run = -INFINITY, l_run = 0.f;
@@ -553,140 +546,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     umma::cluster_sync();
     if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
-}
-
-// Joins the pieces of the units that several workers shared: a warp per row where the pieces are few, a block per 128 coordinates
-// of a row (a stretch of the pieces a warp) where they are many.
-constexpr int kMergeWarps = 8, kFewPieces = 16;
-static_assert(kMaxWorkers <= 32 * kMergeWarps, "a thread per worker");
-template <int DL, int ROWS>
-__global__ void __launch_bounds__(32 * kMergeWarps, 2) latent_merge_kernel(const Args A)
-{
-    constexpr int N = DL / 128;  // float4s of a row per lane
-    __shared__ int4 jobs[kMaxWorkers];      // worker, pieces, first row of the unit in the outputs, rows
-    __shared__ int first[kMaxWorkers + 1];  // first item of a job
-    __shared__ int2 sums[kMergeWarps];
-    __shared__ float4 part[kMergeWarps][32];
-    __shared__ float dens[kMergeWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the attention kernel runs
-    const int4 rec = tid < A.workers ? A.rec[tid] : make_int4(0, 0, 0, 0);
-    const int rows = min(ROWS, A.R - rec.y * ROWS);
-    const int cnt = rec.z > kFewPieces ? N * rows : rec.z > 0 ? (rows + kMergeWarps - 1) / kMergeWarps : 0;
-    int upto = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
-    if (lane == 31) sums[warp] = make_int2(__popc(m), upto);
-    __syncthreads();
-    int num_jobs = 0, items = 0, at = __popc(m & ((1u << lane) - 1u)), before = upto - cnt;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-        if (w < warp) {
-            at += sums[w].x;
-            before += sums[w].y;
-        }
-        num_jobs += sums[w].x;
-        items += sums[w].y;
-    }
-    if (cnt > 0) {
-        jobs[at] = make_int4(tid, rec.z, rec.x * A.R + rec.y * ROWS, rows);
-        first[at] = before;
-    }
-    if (tid == 0) first[num_jobs] = items;
-    __syncthreads();
-    int job = 0;
-    for (int e = blockIdx.x; e < items; e += gridDim.x) {
-        while (e >= first[job + 1]) ++job;
-        const int4 J = jobs[job];
-        const int n = J.y;
-        // piece 0 is the worker's last one, piece k the first one of worker + k
-        auto slot = [&](int k, int r) -> size_t { return (k == 0 ? 2 * J.x + 1 : 2 * (J.x + k)) * static_cast<size_t>(ROWS) + r; };
-        auto add = [&](float4 &o, float a, float4 v) {
-            o.x = fmaf(a, v.x, o.x);
-            o.y = fmaf(a, v.y, o.y);
-            o.z = fmaf(a, v.z, o.z);
-            o.w = fmaf(a, v.w, o.w);
-        };
-        auto put = [&](int r, int j4, float4 o, float den) {
-            const float inv = den == 0.f ? 0.f : 1.f / den;
-            reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(J.z) + r) * DL)[j4] =
-                make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
-        };
-        const float4 *acc = reinterpret_cast<const float4 *>(A.acc);
-        if (n <= kFewPieces) {
-            const int r = (e - first[job]) * kMergeWarps + warp;
-            if (r >= J.w) continue;
-            const float2 mine = lane < n ? A.ml[slot(lane, r)] : make_float2(-INFINITY, 0.f);
-            const float M = warp_max(mine.x), ref = M == -INFINITY ? 0.f : M;
-            // a piece without weight wrote nothing: its factor stays 0 and its sums are not taken
-            const float a = mine.y == 0.f ? 0.f : fast_exp2(mine.x - ref);
-            const unsigned some = __ballot_sync(0xffffffffu, mine.y != 0.f);
-            const float den = warp_sum(mine.y == 0.f ? 0.f : a * mine.y);
-            float4 o[N] = {};
-            for (int k0 = 0; k0 < n; k0 += 4) {
-                float4 v[4][N];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (some >> (k0 + k) & 1u)
-#pragma unroll
-                        for (int i = 0; i < N; ++i) v[k][i] = acc[slot(k0 + k, r) * (DL / 4) + lane + 32 * i];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float ak = __shfl_sync(0xffffffffu, a, (k0 + k) & 31);
-                    if (some >> (k0 + k) & 1u)
-#pragma unroll
-                        for (int i = 0; i < N; ++i) add(o[i], ak, v[k][i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) put(r, lane + 32 * i, o[i], den);
-            continue;
-        }
-        const int r = (e - first[job]) / N, i = (e - first[job]) % N;
-        float M = -INFINITY;
-        for (int k = lane; k < n; k += 32) M = fmaxf(M, A.ml[slot(k, r)].x);
-        M = warp_max(M);
-        const float ref = M == -INFINITY ? 0.f : M;
-        float den = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kDeep = 8;
-        for (int k0 = warp; k0 < n; k0 += kDeep * kMergeWarps) {
-            float2 ml[kDeep];
-            float4 v[kDeep];
-#pragma unroll
-            for (int j = 0; j < kDeep; ++j) {
-                const int k = k0 + j * kMergeWarps;
-                ml[j] = make_float2(-INFINITY, 0.f);
-                if (k < n) {
-                    ml[j] = A.ml[slot(k, r)];
-                    v[j] = acc[slot(k, r) * (DL / 4) + lane + 32 * i];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kDeep; ++j) {
-                if (ml[j].y == 0.f) continue;
-                const float a = fast_exp2(ml[j].x - ref);
-                den = fmaf(a, ml[j].y, den);
-                add(o, a, v[j]);
-            }
-        }
-        __syncthreads();
-        part[warp][lane] = o;
-        if (lane == 0) dens[warp] = den;
-        __syncthreads();
-        if (warp == 0) {
-#pragma unroll
-            for (int w = 1; w < kMergeWarps; ++w) {
-                add(o, 1.f, part[w][lane]);
-                den += dens[w];
-            }
-            put(r, lane + 32 * i, o, den);
-        }
-    }
+    if (shares == 1) return;  // no unit is cut
+    cooperative_groups::this_grid().sync();
+    merge_pieces<DL, kTile, kThreads>(A, *reinterpret_cast<Merge<DL> *>(smem));
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -705,24 +567,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorM
 {
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_kernel<DL>), Cfg<DL>::kSmem);
     if (e != cudaSuccess) return e;
-    latent_kernel<DL><<<2 * a.workers, kThreads, Cfg<DL>::kSmem, st>>>(tk, tv, tq, a);
-    return cudaGetLastError();
-}
-
-template <int DL>
-cudaError_t launch_merge(const Args &a, bool narrow, int num_sms, cudaStream_t st)
-{
-    // its blocks start as the attention's end, and wait for all of them
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * num_sms);
-    cfg.blockDim = dim3(32 * kMergeWarps);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return narrow ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL, kNarrowRows>, a) : cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL, kTile>, a);
+    return launch_together(latent_kernel<DL>, 2 * a.workers, kThreads, Cfg<DL>::kSmem, st, tk, tv, tq, a);
 }
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -742,8 +587,10 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     if (num_blocks > ((int64_t(1) << 31) - 1) / P)
         return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who, static_cast<long long>(num_blocks));
     const int64_t rows = static_cast<int64_t>(q_tokens) * Hq;
-    if (rows >= (int64_t(1) << 31) - kTile || rows * batch >= (int64_t(1) << 31) ||
-        (rows + kTile - 1) / kTile * batch >= (int64_t(1) << 30))
+    const int64_t units = (rows + kTile - 1) / kTile * batch, tiles = static_cast<int64_t>(max_blocks) * P / kNarrowRows + 2;
+    // counted in 32 bits: rows, units, and the tiles of one worker's share
+    if (rows >= (int64_t(1) << 31) - kTile || rows * batch >= (int64_t(1) << 31) || units >= (int64_t(1) << 30) ||
+        units * tiles / (c.num_sms > 2 ? c.num_sms / 2 : 1) >= (int64_t(1) << 30))
         return api_error(TQ_ERR_UNSUPPORTED, "%s: too many sequences x query tokens in one call", who);
     if (batch == 0) return TQ_OK;
     if (!q || !pool || !block_table || !seq_lens || !out) return api_error(TQ_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -788,7 +635,6 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (narrow) e = launch_narrow(tk, tq, dl, a, st);
     else e = dl == 512 ? launch<512>(tk, tv, tq, a, st) : launch<256>(tk, tv, tq, a, st);
-    if (e == cudaSuccess) e = dl == 512 ? launch_merge<512>(a, narrow, c.num_sms, st) : launch_merge<256>(a, narrow, c.num_sms, st);
     if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return TQ_OK;
 }

@@ -1,6 +1,7 @@
 // tq_latent.cuh -- what the attention kernels over latent pages share: arguments, the dealing out of the work, small helpers.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -11,7 +12,7 @@ namespace tq {
 namespace latent {
 
 constexpr int kRope = TQ_LATENT_ROPE_DIM;
-constexpr int kUnitCost = 1;     // what a unit costs beside its tiles, in tiles
+constexpr int kUnitCost = 4;     // what a unit costs beside its tiles (Q, the first loads, its output), in tiles
 constexpr int kMinShare = 3;     // least cost of a worker's share
 constexpr int kMaxWorkers = 256;
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
@@ -102,14 +103,13 @@ __device__ __forceinline__ bool any_of_softmax(bool x)
 // A unit's piece: tokens of tiles t0 .. t1 - 1 of `tiles`, rows of block rt of sequence b.
 struct Piece {
     int b, rt, n, L, t0, t1, tiles;
-    long long end;  // the unit's last cost + 1
 };
 
 // The unit u's sequence, row block (of ROWS), tokens that its last row sees, and tiles (of TOKENS).
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ void unit_of(const Args &A, int u, Piece &p)
 {
-    p.b = u / A.RT;
+    p.b = A.RT == 1 ? u : u / A.RT;
     p.rt = u - p.b * A.RT;
     const int L = min(max(__ldg(A.seq_lens + p.b), 0), A.max_blocks << A.pshift);
     const int last = A.Tq == 1 ? 0 : (min((p.rt + 1) * ROWS, A.R) - 1) / A.Hq;
@@ -118,39 +118,44 @@ __device__ __forceinline__ void unit_of(const Args &A, int u, Piece &p)
     p.tiles = (p.n + TOKENS - 1) / TOKENS;
 }
 
-// A worker's share: costs x0 .. x1 - 1 of the units' costs laid end to end, from unit u, whose first cost is a.
+// A worker's share: `len` of the units' costs laid end to end, from unit u, whose first cost stands at a <= 0 against the share's
+// first.
 template <int ROWS, int TOKENS>
 struct Share {
-    long long x0, x1, a;
-    int u, units;
+    int a, len, u, units;
     // The next piece (t0 < t1), or a unit without a token (tiles 0).
     __device__ __forceinline__ bool next(const Args &A, Piece &p)
     {
-        while (u < units && a < x1) {
+        while (u < units && a < len) {
             unit_of<ROWS, TOKENS>(A, u, p);
-            const long long first = a + kUnitCost;
+            const int first = a + kUnitCost;
             a = first + p.tiles;
-            p.end = a;
             ++u;
             if (p.tiles == 0) {
-                if (first - kUnitCost >= x0) {
-                    p.t0 = p.t1 = 0;
-                    return true;
-                }
-                continue;
+                if (first < kUnitCost) continue;  // an earlier share's
+                p.t0 = p.t1 = 0;
+                return true;
             }
-            p.t0 = static_cast<int>(min(max(x0 - first, 0LL), static_cast<long long>(p.tiles)));
-            p.t1 = static_cast<int>(min(max(x1 - first, 0LL), static_cast<long long>(p.tiles)));
+            p.t0 = min(max(-first, 0), p.tiles);
+            p.t1 = min(max(len - first, 0), p.tiles);
             if (p.t0 < p.t1) return true;
         }
         return false;
     }
 };
 
-// The share of worker w: a scan of the units' costs, a stretch of units per thread of the block.  `sums` holds one number a
-// warp, then the first unit's first cost, and the unit; shared memory that nothing else uses.  Synchronises the block.
+// Where share w of n begins in `total` costs: quotients of 32 bits where they do.
+__device__ __forceinline__ long long share_start(int w, long long total, int n)
+{
+    if (total < (1 << 23)) return static_cast<unsigned>(w) * static_cast<unsigned>(total) / static_cast<unsigned>(n);
+    return w * total / n;
+}
+
+// The share of worker w: a scan of the units' costs, a stretch of units per thread of the block.  Tells the join (A.rec, by one
+// block of a worker) whether its last unit's first tile is its own and the last one a later worker's.  `sums` holds one number a warp, then the
+// first unit's place, and the unit; shared memory that nothing else uses.  Synchronises the block.
 template <int ROWS, int TOKENS, int THREADS>
-__device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w, bool report, long long *sums, long long &total, long long &shares)
+__device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w, bool report, bool first_block, long long *sums, int &shares)
 {
     constexpr int kWarps = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -173,33 +178,215 @@ __device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w, bool r
     }
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    long long before = upto - mine;
-    total = 0;
+    long long before = upto - mine, total = 0;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
         const long long v = sums[k];
         if (k < warp) before += v;
         total += v;
     }
-    shares = min(static_cast<long long>(A.workers), max(total / kMinShare, 1LL));
-    share.x0 = w < shares ? w * total / shares : total;
-    share.x1 = w < shares ? (w + 1) * total / shares : total;
-    if (before <= share.x0 && share.x0 < before + mine) {  // one thread
-        long long a = before;
-        int u = u0;
-        for (;; ++u) {
-            Piece p;
+    shares = static_cast<int>(min(static_cast<long long>(A.workers), max(total / kMinShare, 1LL)));
+    const bool active = w < shares;
+    const long long x0 = active ? share_start(w, total, shares) : 0, x1 = active ? share_start(w + 1, total, shares) : 0;
+    share.len = static_cast<int>(x1 - x0);
+    // the unit that a cost lies in, and its first cost, by the thread that counted it
+    auto find = [&](long long x, Piece &p, long long &a) -> int {
+        a = before;
+        for (int u = u0;; ++u) {
             unit_of<ROWS, TOKENS>(A, u, p);
-            if (a + p.tiles + kUnitCost > share.x0) break;
+            if (a + p.tiles + kUnitCost > x) return u;
             a += p.tiles + kUnitCost;
         }
-        sums[kWarps] = a;
+    };
+    Piece p;
+    long long a;
+    if (active && before <= x0 && x0 < before + mine) {
+        const int u = find(x0, p, a);
+        sums[kWarps] = a - x0;
         sums[kWarps + 1] = u;
     }
     __syncthreads();
-    share.a = sums[kWarps];
-    share.u = share.x0 < share.x1 ? static_cast<int>(sums[kWarps + 1]) : share.units;
+    share.a = static_cast<int>(sums[kWarps]);
+    share.u = active ? static_cast<int>(sums[kWarps + 1]) : share.units;
+    if (first_block) {
+        if (!active) {
+            if (tid == 0) A.rec[w] = make_int4(0, 0, 0, 0);
+        } else if (before < x1 && x1 <= before + mine) {
+            find(x1 - 1, p, a);
+            const long long end = a + kUnitCost + p.tiles;
+            int pieces = 0;
+            if (end > x1 && x0 <= a + kUnitCost && x1 > a + kUnitCost) {  // its first tile here, its last one not
+                // the last share with a part of this unit: the least s with (s + 1) total / shares >= end
+                const long long last = total < (1 << 23) ? (static_cast<unsigned>(end) * static_cast<unsigned>(shares) + static_cast<unsigned>(total) - 1u) / static_cast<unsigned>(total)
+                                                         : (end * shares + total - 1) / total;
+                pieces = static_cast<int>(last) - w;
+            }
+            A.rec[w] = make_int4(p.b, p.rt, pieces, 0);
+        }
+    }
     return share;
+}
+
+// Joins the pieces of the units that several workers shared, by all blocks of the grid once all have written theirs: a warp per
+// row where the pieces are few, a block per 256 coordinates of a row (a stretch of the pieces a warp) where they are many.  A
+// kernel of its own for it, launched as the attention's blocks ended, cost 5-10 us more (its start, and the end of the other).
+constexpr int kFewPieces = 16;
+template <int DL>
+struct Merge {
+    int4 jobs[kMaxWorkers];      // worker, pieces, first row of the unit in the outputs, rows
+    int first[kMaxWorkers + 1];  // first item of a job
+    int2 sums[32];
+    float4 part[32][2][32];
+    float2 dens[32];  // reference, denominator
+};
+template <int DL, int ROWS, int THREADS>
+__device__ __forceinline__ void merge_pieces(const Args &A, Merge<DL> &S)
+{
+    static_assert(kMaxWorkers <= THREADS, "a thread per worker");
+    constexpr int kMergeWarps = THREADS / 32;
+    constexpr int N = DL / 128;         // stretches of 128 coordinates of a row, a float4 per lane
+    constexpr int K = 16 / N;           // pieces of a row on their way together
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int4 rec = tid < A.workers ? __ldcg(A.rec + tid) : make_int4(0, 0, 0, 0);
+    const int rows = min(ROWS, A.R - rec.y * ROWS);
+    const int cnt = rec.z > kFewPieces ? N / 2 * rows : rec.z > 0 ? (rows + kMergeWarps - 1) / kMergeWarps : 0;
+    int upto = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
+    if (lane == 31) S.sums[warp] = make_int2(__popc(m), upto);
+    __syncthreads();
+    int num_jobs = 0, items = 0, at = __popc(m & ((1u << lane) - 1u)), before = upto - cnt;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+        if (w < warp) {
+            at += S.sums[w].x;
+            before += S.sums[w].y;
+        }
+        num_jobs += S.sums[w].x;
+        items += S.sums[w].y;
+    }
+    if (cnt > 0) {
+        S.jobs[at] = make_int4(tid, rec.z, rec.x * A.R + rec.y * ROWS, rows);
+        S.first[at] = before;
+    }
+    if (tid == 0) S.first[num_jobs] = items;
+    __syncthreads();
+    int job = 0;
+    for (int e = blockIdx.x; e < items; e += gridDim.x) {
+        while (e >= S.first[job + 1]) ++job;
+        const int4 J = S.jobs[job];
+        const int n = J.y;
+        // piece 0 is the worker's last one, piece k the first one of worker + k
+        auto slot = [&](int k, int r) -> size_t { return (k == 0 ? 2 * J.x + 1 : 2 * (J.x + k)) * static_cast<size_t>(ROWS) + r; };
+        auto add = [&](float4 &o, float a, float4 v) {
+            o.x = fmaf(a, v.x, o.x);
+            o.y = fmaf(a, v.y, o.y);
+            o.z = fmaf(a, v.z, o.z);
+            o.w = fmaf(a, v.w, o.w);
+        };
+        auto put = [&](int r, int j4, float4 o, float den) {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(J.z) + r) * DL)[j4] =
+                make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
+        };
+        // 2^(m - M), M the larger of them
+        auto scale_of = [](float m, float M) -> float { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
+        const float4 *acc = reinterpret_cast<const float4 *>(A.acc);
+        if (n <= kFewPieces) {
+            const int r = (e - S.first[job]) * kMergeWarps + warp;
+            if (r >= J.w) continue;
+            float m = -INFINITY, den = 0.f;
+            float4 o[N] = {};
+            for (int k0 = 0; k0 < n; k0 += K) {
+                float2 ml[K];
+                float4 v[K][N];
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    if (k0 + k < n) {
+                        ml[k] = __ldcg(A.ml + slot(k0 + k, r));
+#pragma unroll
+                        for (int i = 0; i < N; ++i) v[k][i] = __ldcg(acc + slot(k0 + k, r) * (DL / 4) + lane + 32 * i);
+                    }
+                }
+                const float m_old = m;
+#pragma unroll
+                for (int k = 0; k < K; ++k) m = fmaxf(m, ml[k].x);
+                const float al = scale_of(m_old, m);
+                den *= al;
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[i] = make_float4(al * o[i].x, al * o[i].y, al * o[i].z, al * o[i].w);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (ml[k].y == 0.f) continue;  // no piece, or one without weight (nothing written)
+                    const float a = scale_of(ml[k].x, m);
+                    den = fmaf(a, ml[k].y, den);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) add(o[i], a, v[k][i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) put(r, lane + 32 * i, o[i], den);
+            continue;
+        }
+        const int r = (e - S.first[job]) / (N / 2), i0 = (e - S.first[job]) % (N / 2) * 2;
+        float m = -INFINITY, den = 0.f;
+        float4 o[2] = {};
+        constexpr int kDeep = 4;
+        for (int k0 = warp; k0 < n; k0 += kDeep * kMergeWarps) {
+            float2 ml[kDeep];
+            float4 v[kDeep][2];
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) {
+                const int k = k0 + j * kMergeWarps;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                if (k < n) {
+                    ml[j] = __ldcg(A.ml + slot(k, r));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) v[j][i] = __ldcg(acc + slot(k, r) * (DL / 4) + lane + 32 * (i0 + i));
+                }
+            }
+            const float m_old = m;
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) m = fmaxf(m, ml[j].x);
+            const float al = scale_of(m_old, m);
+            den *= al;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) o[i] = make_float4(al * o[i].x, al * o[i].y, al * o[i].z, al * o[i].w);
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) {
+                if (ml[j].y == 0.f) continue;
+                const float a = scale_of(ml[j].x, m);
+                den = fmaf(a, ml[j].y, den);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) add(o[i], a, v[j][i]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) S.part[warp][i][lane] = o[i];
+        if (lane == 0) S.dens[warp] = make_float2(m, den);
+        __syncthreads();
+        if (warp < 2) {
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, S.dens[w].x);
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+            den = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) {
+                if (S.dens[w].y == 0.f) continue;
+                const float a = scale_of(S.dens[w].x, M);
+                den = fmaf(a, S.dens[w].y, den);
+                add(t, a, S.part[w][warp][lane]);
+            }
+            put(r, lane + 32 * (i0 + warp), t, den);
+        }
+    }
 }
 
 // Two stages do not quite cover HBM's latency: the tile behind them is asked into L2, 16 tokens (which lie on one page) by every
@@ -214,6 +401,23 @@ __device__ __forceinline__ void prefetch_rows(const Args &A, int pos, int blk, b
 
 // Rows of a sequence that the narrow kernel takes (one CTA, 64 rows); longer ones go to pairs of CTAs.
 constexpr int kNarrowRows = 64;
+// A launch whose blocks all run at once (they wait for one another before the pieces are joined).
+template <typename... P, typename... V>
+cudaError_t launch_together(void (*kernel)(P...), int blocks, int threads, size_t smem, cudaStream_t st, V... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The narrow kernel's launch, in its own translation unit; tk: boxes of a group's blocks (narrow_group), tq: 64 rows.
 int narrow_group(int dl);
 cudaError_t launch_narrow(const CUtensorMap &tk, const CUtensorMap &tq, int dl, const Args &a, cudaStream_t st);

@@ -106,14 +106,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 1; i < 4; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        A.rec[worker] = make_int4(0, 0, 0, 0);
     }
-    long long total, shares;
+    int shares;
     umma::fence_before_sync();
-    Share<kNarrowRows, kTok> share = deal<kNarrowRows, kTok, kThreads>(A, worker, blockIdx.x == 0,
-                                                                       reinterpret_cast<long long *>(smem + C::kPlanOff), total, shares);
+    Share<kNarrowRows, kTok> share = deal<kNarrowRows, kTok, kThreads>(A, worker, blockIdx.x == 0, true,
+                                                                       reinterpret_cast<long long *>(smem + C::kPlanOff), shares);
     umma::fence_after_sync();
-    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, see tq_latent.cu
@@ -152,11 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole_unit = p.t0 == 0 && p.t1 == p.tiles;
             const size_t at = static_cast<size_t>(p.b) * A.R;
             const size_t slot = (2 * worker + (p.t0 == 0 ? 1 : 0)) * static_cast<size_t>(kNarrowRows);
-            if (tid == 0 && p.t0 == 0 && !whole_unit) {
-                // the last share with a part of this unit: the least s with (s + 1) total / shares >= end
-                const int last = static_cast<int>((p.end * shares + total - 1) / total) - 1;
-                A.rec[worker] = make_int4(p.b, p.rt, last - worker + 1, 0);
-            }
             auto limit = [&](int row) -> int { return A.Tq == 1 || row >= A.R ? p.n : max(0, p.L - A.Tq + row / A.Hq + 1); };
             const int lim0 = limit(0);  // tokens that every row sees
             int lim[2];
@@ -501,6 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     umma::fence_after_sync();
     if (warp == kSoftWarps) umma::tmem_dealloc(tbase, 512);
+    if (shares == 1) return;  // no unit is cut
+    cooperative_groups::this_grid().sync();
+    merge_pieces<DL, kNarrowRows, kThreads>(A, *reinterpret_cast<Merge<DL> *>(smem));
 }
 
 template <int DL>
@@ -508,8 +504,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tq, const Args &a, 
 {
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_narrow_kernel<DL>), Cfg<DL>::kSmem);
     if (e != cudaSuccess) return e;
-    latent_narrow_kernel<DL><<<a.workers, kThreads, Cfg<DL>::kSmem, st>>>(tk, tq, a);
-    return cudaGetLastError();
+    return launch_together(latent_narrow_kernel<DL>, a.workers, kThreads, Cfg<DL>::kSmem, st, tk, tq, a);
 }
 
 }  // namespace
