@@ -336,19 +336,25 @@ class Codec:
         return torch.zeros(num_blocks, page_size, latent_dim + native.TQ_LATENT_ROPE_DIM, dtype=torch.bfloat16,
                            device=torch.device("cuda", self.device))
 
-    def _strided(self, x, shape, what: str):
-        """Address and strides of bf16 rows of this shape, the last dimension contiguous; a dimension of one counts as
-        packed."""
-        if x.dtype is not torch.bfloat16 or x.shape != shape or x.get_device() != self.device:
-            raise ValueError(f"{what} must be bf16 {list(shape)} on cuda:{self.device}; got {x.dtype} {tuple(x.shape)} on "
-                             f"{x.device}")
-        if x.numel() and x.stride(-1) != 1:
+    def _latent_rows(self, x, T: int, cols: int, what: str):
+        """Address and row stride of bf16 rows x [T, cols]."""
+        if x.dtype is not torch.bfloat16 or x.shape != (T, cols) or x.get_device() != self.device:
+            raise ValueError(f"{what} must be bf16 [{T}, {cols}] on cuda:{self.device}; got {x.dtype} {tuple(x.shape)} on {x.device}")
+        st, one = x.stride()
+        if one != 1 and T > 0:
             raise ValueError(f"{what}: the coordinates of a row must be contiguous")
-        st, packed = [], shape[-1]
-        for n, s in zip(reversed(shape[:-1]), reversed(x.stride()[:-1])):
-            st.append(s if n > 1 else packed)
-            packed *= n
-        return (x.data_ptr(), *reversed(st))
+        return x.data_ptr(), st if T > 1 else cols
+
+    def _latent_heads(self, x, T: int, heads: int, what: str):
+        """Address, token and head strides of bf16 rows x [T, heads, 64]."""
+        r = native.TQ_LATENT_ROPE_DIM
+        if x.dtype is not torch.bfloat16 or x.shape != (T, heads, r) or x.get_device() != self.device:
+            raise ValueError(f"{what} must be bf16 [{T}, {heads}, {r}] on cuda:{self.device}; got {x.dtype} {tuple(x.shape)} on "
+                             f"{x.device}")
+        st, sh, one = x.stride()
+        if one != 1 and T > 0 and heads > 0:
+            raise ValueError(f"{what}: the coordinates of a row must be contiguous")
+        return x.data_ptr(), st if T > 1 else heads * r, sh if heads > 1 else r
 
     def append_latent(self, latent, k_rope, slot_mapping, pool, page_size: int, num_blocks: int, q=None, q_out=None,
                       positions=None, rope=None, interleaved: bool = False, norm_weight=None, norm_eps: float = 1e-6,
@@ -367,8 +373,8 @@ class Codec:
             raise ValueError("latent must be [T, latent_dim]")
         r = native.TQ_LATENT_ROPE_DIM
         T, dl = latent.shape
-        lp, ls = self._strided(latent, (T, dl), "latent")
-        kp, ks = self._strided(k_rope, (T, r), "k_rope")
+        lp, ls = self._latent_rows(latent, T, dl, "latent")
+        kp, ks = self._latent_rows(k_rope, T, r, "k_rope")
         sp = self._flat(slot_mapping, torch.int64, T, "slot_mapping")
         pp = self._flat(pool, torch.bfloat16, num_blocks * page_size * (dl + r), "pool [num_blocks, page_size, latent_dim + 64]")
         wp = 0 if norm_weight is None else self._flat(norm_weight, torch.bfloat16, dl, "norm_weight")
@@ -383,10 +389,10 @@ class Codec:
             if q.dim() != 3:
                 raise ValueError("q must be [T, num_q_heads, 64]")
             Hq = q.shape[1]
-            qp, qs, qh = self._strided(q, (T, Hq, r), "q")
+            qp, qs, qh = self._latent_heads(q, T, Hq, "q")
             if q_out is None:  # zeros: rows of skipped tokens are not written
                 q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
-            op, os, oh = self._strided(q_out, (T, Hq, r), "q_out")
+            op, os, oh = self._latent_heads(q_out, T, Hq, "q_out")
         elif q_out is not None:
             raise ValueError("q_out without q")
         native.tq_append_latent(self.handle, lp, kp, qp, T, dl, Hq, ls, ks, qs, qh, wp, float(norm_eps), at, rp, rows,

@@ -4,9 +4,8 @@
 //   c' = c w / sqrt(mean(c^2) + eps), sums and products in fp32, rounded once
 //   (x, y) -> (x cos - y sin, y cos + x sin), every product and sum rounded once in fp32
 //
-// A block per token (several over the heads where tokens are few).  Its first warp takes the pool row: DL / 32 coordinates of
-// the latent a lane, one pass with the row in registers between the sum and the scaling.  A thread of the rest keeps one
-// unit (eight pairs) of the heads it takes, so the token's cosines and sines are loaded once.
+// Bound: HBM, in one pass.  Blocks for the pool rows (a warp each), then blocks for the query heads; everything that does not
+// depend on a token's slot and position is loaded with them.
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -37,6 +36,7 @@ struct LatentArgs {
     int64_t num_slots;
     uint16_t *pool, *q_out;
     unsigned *status;
+    bool small;  // (token, four heads) are counted in 32 bits
 };
 
 __device__ __forceinline__ uint4 ld_row(const void *p)  // plain: q may be rewritten in place
@@ -101,98 +101,118 @@ struct Turn {
     }
 };
 
-template <int DL>
-__global__ void __launch_bounds__(kThreads) append_latent_kernel(const LatentArgs A)
+// Whether a token is written: its slot lies in the pool and its position in the table.
+__device__ __forceinline__ bool token_ok(const LatentArgs &A, int64_t slot, int64_t pos, bool report)
 {
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t slot = ld_pinned_s64(A.slots + t);
-    const int64_t pos = A.rope ? ld_pinned_s64(A.positions + t) : 0;
-    const bool report = tid == 0 && blockIdx.y == 0;
-    if (slot < 0) return;
+    if (slot < 0) return false;
     if (slot >= A.num_slots) {
         if (report) atomicOr(A.status, TQ_DEVERR_SLOT_RANGE);
-        return;
+        return false;
     }
     if (A.rope && (pos < 0 || pos >= A.rope_rows)) {
         if (report) atomicOr(A.status, TQ_DEVERR_POSITION);
+        return false;
+    }
+    return true;
+}
+
+// A warp's pool row: DL / 32 coordinates of the latent a lane, in registers between the sum and the scaling.
+template <int DL>
+__device__ __forceinline__ void pool_row(const LatentArgs &A, int64_t t, int lane)
+{
+    constexpr int N = DL / 256;  // chunks of eight coordinates a lane
+    const int u = lane % kUnits;
+    const int j0 = A.interleaved ? 16 * u : 8 * u, j1 = A.interleaved ? 16 * u + 8 : kRope / 2 + 8 * u;
+    uint4 w[N], g[N], ka, kb;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        w[i] = ld_row(A.latent + t * A.ls + 8 * (lane + 32 * i));
+        if (A.weight) g[i] = ld_pinned(A.weight + 8 * (lane + 32 * i));
+    }
+    if (lane < kUnits) {
+        ka = ld_row(A.k + t * A.ks + j0);
+        kb = ld_row(A.k + t * A.ks + j1);
+    }
+    const int64_t slot = ld_pinned_s64(A.slots + t);
+    const int64_t pos = A.rope ? ld_pinned_s64(A.positions + t) : 0;
+    if (!token_ok(A, slot, pos, lane == 0)) return;
+    Turn tn{};
+    if (A.rope && lane < kUnits) tn.load(A.rope + pos * kRope, u);
+    uint16_t *dst = A.pool + slot * (DL + kRope);
+    if (A.weight) {
+        float x[N][8], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            unpack8(w[i], x[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum = fmaf(x[i][k], x[i][k], sum);
+        }
+        const float inv = 1.f / sqrtf(warp_sum(sum) * (1.f / DL) + A.eps);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float y[8];
+            unpack8(g[i], y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] *= x[i][k] * inv;
+            w[i] = pack8(y);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(dst + 8 * (lane + 32 * i)) = w[i];
+    if (lane < kUnits) {
+        if (A.rope) tn.turn(ka, kb, A.interleaved);
+        *reinterpret_cast<uint4 *>(dst + DL + j0) = ka;
+        *reinterpret_cast<uint4 *>(dst + DL + j1) = kb;
+    }
+}
+
+// row_blocks blocks for the pool rows, a warp each, then blocks for the queries: thread i's unit of heads r, r + n, r + 2 n and
+// r + 3 n of token i / n, r = i % n, n = ceil(Hq / 4), all of them on their way with the token's slot and position.
+constexpr int kHeads = 4;
+template <int DL>
+__global__ void __launch_bounds__(kThreads) append_latent_kernel(const LatentArgs A, const unsigned row_blocks)
+{
+    const int tid = threadIdx.x;
+    if (blockIdx.x < row_blocks) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + tid / 32;
+        if (t < A.T) pool_row<DL>(A, t, tid % 32);
         return;
     }
-    const int u = tid % kUnits;
+    const int n = (A.Hq + kHeads - 1) / kHeads, u = tid % kUnits;
+    const int64_t i = static_cast<int64_t>(blockIdx.x - row_blocks) * kLanes + tid / kUnits;
+    const int64_t t = A.small ? static_cast<uint32_t>(i) / static_cast<uint32_t>(n) : i / n;
+    if (t >= A.T) return;
+    const int r = static_cast<int>(i - t * n);
     const int j0 = A.interleaved ? 16 * u : 8 * u, j1 = A.interleaved ? 16 * u + 8 : kRope / 2 + 8 * u;
+    const uint16_t *src = A.q + t * A.qs;
+    uint4 a[kHeads], b[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k)
+        if (r + k * n < A.Hq) {
+            a[k] = ld_row(src + (r + k * n) * A.qh + j0);
+            b[k] = ld_row(src + (r + k * n) * A.qh + j1);
+        }
+    const int64_t slot = ld_pinned_s64(A.slots + t);
+    const int64_t pos = A.rope ? ld_pinned_s64(A.positions + t) : 0;
+    if (!token_ok(A, slot, pos, false)) return;  // what is wrong is reported with the pool row
     Turn tn{};
     if (A.rope) tn.load(A.rope + pos * kRope, u);
-    if (blockIdx.y == 0 && tid < 32) {
-        constexpr int N = DL / 256;  // chunks of eight coordinates a lane
-        uint16_t *dst = A.pool + slot * (DL + kRope);
-        const uint16_t *src = A.latent + t * A.ls;
-        uint4 w[N], ka, kb;
+    uint16_t *dst = A.q_out + t * A.os;
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = ld_row(src + 8 * (lane + 32 * i));
-        if (lane < kUnits) {
-            ka = ld_row(A.k + t * A.ks + j0);
-            kb = ld_row(A.k + t * A.ks + j1);
+    for (int k = 0; k < kHeads; ++k)
+        if (r + k * n < A.Hq) {
+            if (A.rope) tn.turn(a[k], b[k], A.interleaved);
+            *reinterpret_cast<uint4 *>(dst + (r + k * n) * A.oh + j0) = a[k];
+            *reinterpret_cast<uint4 *>(dst + (r + k * n) * A.oh + j1) = b[k];
         }
-        if (A.weight) {
-            uint4 g[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = ld_pinned(A.weight + 8 * (lane + 32 * i));
-            float x[N][8], sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                unpack8(w[i], x[i]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum = fmaf(x[i][k], x[i][k], sum);
-            }
-            const float inv = 1.f / sqrtf(warp_sum(sum) * (1.f / DL) + A.eps);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float y[8];
-                unpack8(g[i], y);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] *= x[i][k] * inv;
-                w[i] = pack8(y);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(dst + 8 * (lane + 32 * i)) = w[i];
-        if (lane < kUnits) {
-            if (A.rope) tn.turn(ka, kb, A.interleaved);
-            *reinterpret_cast<uint4 *>(dst + DL + j0) = ka;
-            *reinterpret_cast<uint4 *>(dst + DL + j1) = kb;
-        }
-    }
-    if (!A.q) return;
-    const uint16_t *q = A.q + t * A.qs;
-    uint16_t *o = A.q_out + t * A.os;
-    const int step = kLanes * gridDim.y;
-    for (int h = blockIdx.y * kLanes + tid / kUnits; h < A.Hq; h += 2 * step) {  // two heads on their way at a time
-        const bool two = h + step < A.Hq;
-        const uint16_t *s0 = q + h * A.qh, *s1 = q + (two ? h + step : h) * A.qh;
-        uint4 a0 = ld_row(s0 + j0), b0 = ld_row(s0 + j1), a1{}, b1{};
-        if (two) {
-            a1 = ld_row(s1 + j0);
-            b1 = ld_row(s1 + j1);
-        }
-        if (A.rope) {
-            tn.turn(a0, b0, A.interleaved);
-            tn.turn(a1, b1, A.interleaved);
-        }
-        *reinterpret_cast<uint4 *>(o + h * A.oh + j0) = a0;
-        *reinterpret_cast<uint4 *>(o + h * A.oh + j1) = b0;
-        if (two) {
-            *reinterpret_cast<uint4 *>(o + (h + step) * A.oh + j0) = a1;
-            *reinterpret_cast<uint4 *>(o + (h + step) * A.oh + j1) = b1;
-        }
-    }
 }
 
 template <int DL>
 cudaError_t launch(const LatentArgs &a, cudaStream_t st)
 {
-    // Few tokens: a block per 64 heads, for latency.  Many: all heads of a token in one block.
-    const unsigned gy = a.T < 1024 && a.q ? static_cast<unsigned>((a.Hq + kLanes - 1) / kLanes) : 1u;
-    append_latent_kernel<DL><<<dim3(static_cast<unsigned>(a.T), gy), kThreads, 0, st>>>(a);
+    const int64_t rows = (a.T + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t q = a.q ? (a.T * ((a.Hq + kHeads - 1) / kHeads) + kLanes - 1) / kLanes : 0;
+    append_latent_kernel<DL><<<static_cast<unsigned>(rows + q), kThreads, 0, st>>>(a, static_cast<unsigned>(rows));
     return cudaGetLastError();
 }
 
@@ -225,7 +245,7 @@ extern "C" tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const
     if ((q == nullptr) != (q_out == nullptr)) return api_error(TQ_ERR_INVALID_ARG, "%s: q and q_out go together", who);
     if (norm_weight && !(norm_eps >= 0.f && std::isfinite(norm_eps)))
         return api_error(TQ_ERR_INVALID_ARG, "%s: norm_eps must be finite and >= 0", who);
-    if (T >= (int64_t(1) << 31) || num_q_heads > (1 << 20)) return api_error(TQ_ERR_UNSUPPORTED, "%s: too many tokens or heads in one call", who);
+    if (T >= (int64_t(1) << 30) || num_q_heads > (1 << 18) || T * num_q_heads >= (int64_t(1) << 36)) return api_error(TQ_ERR_UNSUPPORTED, "%s: too many tokens or heads in one call", who);
     if (num_blocks > ((int64_t(1) << 31) - 1) / page_size)
         return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who, static_cast<long long>(num_blocks));
     if (T == 0) return TQ_OK;
@@ -244,7 +264,7 @@ extern "C" tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const
     const tq::Codec &c = tq::handle_codec(h);
     const tq::LatentArgs a{latent, k_rope, q, T, num_q_heads, latent_stride, k_stride, q_stride_tok, q_stride_head, qo_stride_tok,
                            qo_stride_head, norm_weight, norm_eps, positions, rope, rope_rows, style == TQ_ROPE_INTERLEAVED,
-                           slot_mapping, num_blocks * page_size, pool, q_out, c.status};
+                           slot_mapping, num_blocks * page_size, pool, q_out, c.status, T * num_q_heads < (int64_t(1) << 31)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = latent_dim == 512 ? tq::launch<512>(a, st) : tq::launch<256>(a, st);
     if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
