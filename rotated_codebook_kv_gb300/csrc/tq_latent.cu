@@ -114,9 +114,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    int shares;
-    Share<kTile, kTile> share = deal<kTile, kTile, kThreads>(A, pair, blockIdx.x == 0, rank == 0, plan, shares);
+    Dealer<kTile, kTile, kThreads> dealer;
+    Share<kTile, kTile> share = dealer.deal(A, pair, blockIdx.x == 0, plan);
     umma::cluster_sync();
+    if (rank == 0) dealer.record(A);
+    const int shares = dealer.shares;
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
@@ -149,6 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float c = fabsf(A.sm_scale) * kLog2e;
         const uint32_t flip = A.sm_scale < 0.f ? 0x80000000u : 0u;
         const int *table = nullptr;
+        const bool sectors = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0;  // rows begin on 32 bytes
         bool bad = false, dead = false;  // this warp's wait failed; all know
         int it = 0, sg = 0;
         Piece p;
@@ -318,18 +321,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             }
                         }
                         if (valid && whole_unit) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + j0);
+                            uint16_t *dst = A.out + at * DL + j0;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t w[4];
+                            for (int k = 0; k < 32; k += 16) {
+                                float v[8];
 #pragma unroll
-                                for (int m = 0; m < 4; ++m) w[m] = bf16x2_of(o[8 * k + 2 * m] * inv, o[8 * k + 2 * m + 1] * inv);
-                                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int m = 0; m < 8; ++m) v[m] = __uint_as_float(bf16x2_of(o[k + 2 * m] * inv, o[k + 2 * m + 1] * inv));
+                                if (sectors) {
+                                    stg256(reinterpret_cast<float *>(dst + k), v);
+                                } else {
+                                    reinterpret_cast<float4 *>(dst + k)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                                    reinterpret_cast<float4 *>(dst + k)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                                }
                             }
                         } else if (valid) {
-                            float4 *dst = reinterpret_cast<float4 *>(A.acc + slot * DL + j0);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            for (int k = 0; k < 32; k += 8) {
+                                const float v[8] = {o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5], o[k + 6], o[k + 7]};
+                                stg256(A.acc + slot * DL + j0 + k, v);
+                            }
                         }
                     }
                     umma::fence_before_sync();

@@ -84,6 +84,13 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
+// 32 bytes, a whole sector a lane.
+__device__ __forceinline__ void stg256(float *p, const float (&v)[8])
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]),
+                 "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
@@ -151,71 +158,93 @@ __device__ __forceinline__ long long share_start(int w, long long total, int n)
     return w * total / n;
 }
 
-// The share of worker w: a scan of the units' costs, a stretch of units per thread of the block.  Tells the join (A.rec, by one
-// block of a worker) whether its last unit's first tile is its own and the last one a later worker's.  `sums` holds one number a warp, then the
-// first unit's place, and the unit; shared memory that nothing else uses.  Synchronises the block.
+// Deals out the work: a scan of the units' costs, a stretch of units per thread of the block.  `sums` holds one number a warp,
+// then the first unit's place, and the unit; shared memory that nothing else uses.
 template <int ROWS, int TOKENS, int THREADS>
-__device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w, bool report, bool first_block, long long *sums, int &shares)
-{
-    constexpr int kWarps = THREADS / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Share<ROWS, TOKENS> share;
-    share.units = A.B * A.RT;
-    const int per = (share.units + THREADS - 1) / THREADS;
-    const int u0 = min(tid * per, share.units), u1 = min(u0 + per, share.units);
-    long long mine = 0;
-    for (int u = u0; u < u1; ++u) {
-        Piece p;
-        unit_of<ROWS, TOKENS>(A, u, p);
-        mine += p.tiles + kUnitCost;
-        if (report && p.rt == 0 && __ldg(A.seq_lens + p.b) > (A.max_blocks << A.pshift)) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
-    }
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    long long before = upto - mine, total = 0;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        const long long v = sums[k];
-        if (k < warp) before += v;
-        total += v;
-    }
-    shares = static_cast<int>(min(static_cast<long long>(A.workers), max(total / kMinShare, 1LL)));
-    const bool active = w < shares;
-    const long long x0 = active ? share_start(w, total, shares) : 0, x1 = active ? share_start(w + 1, total, shares) : 0;
-    share.len = static_cast<int>(x1 - x0);
-    // the unit that a cost lies in, and its first cost, by the thread that counted it
-    auto find = [&](long long x, Piece &p, long long &a) -> int {
+struct Dealer {
+    static constexpr int kWarps = THREADS / 32;
+    long long before, mine, total, x0, x1;
+    int u0, w, shares;
+    bool active;
+
+    // The unit that cost x lies in, and its first cost, by the thread that counted it.
+    __device__ __forceinline__ int find(const Args &A, long long x, Piece &p, long long &a) const
+    {
         a = before;
         for (int u = u0;; ++u) {
             unit_of<ROWS, TOKENS>(A, u, p);
             if (a + p.tiles + kUnitCost > x) return u;
             a += p.tiles + kUnitCost;
         }
-    };
-    Piece p;
-    long long a;
-    if (active && before <= x0 && x0 < before + mine) {
-        const int u = find(x0, p, a);
-        sums[kWarps] = a - x0;
-        sums[kWarps + 1] = u;
     }
-    __syncthreads();
-    share.a = static_cast<int>(sums[kWarps]);
-    share.u = active ? static_cast<int>(sums[kWarps + 1]) : share.units;
-    if (first_block) {
+
+    // The share of worker w_.  Synchronises the block.
+    __device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w_, bool report, long long *sums)
+    {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        Share<ROWS, TOKENS> share;
+        w = w_;
+        share.units = A.B * A.RT;
+        const int per = (share.units + THREADS - 1) / THREADS;
+        u0 = min(tid * per, share.units);
+        const int u1 = min(u0 + per, share.units);
+        mine = 0;
+        for (int u = u0; u < u1; ++u) {
+            Piece p;
+            unit_of<ROWS, TOKENS>(A, u, p);
+            mine += p.tiles + kUnitCost;
+            if (report && p.rt == 0 && __ldg(A.seq_lens + p.b) > (A.max_blocks << A.pshift)) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
+        }
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        before = upto - mine;
+        total = 0;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const long long v = sums[k];
+            if (k < warp) before += v;
+            total += v;
+        }
+        shares = static_cast<int>(min(static_cast<long long>(A.workers), max(total / kMinShare, 1LL)));
+        active = w < shares;
+        x0 = active ? share_start(w, total, shares) : 0;
+        x1 = active ? share_start(w + 1, total, shares) : 0;
+        share.len = static_cast<int>(x1 - x0);
+        if (active && before <= x0 && x0 < before + mine) {
+            Piece p;
+            long long a;
+            const int u = find(A, x0, p, a);
+            sums[kWarps] = a - x0;
+            sums[kWarps + 1] = u;
+            // the block ids that the first loads wait for
+            const int t0 = max(0, static_cast<int>(x0 - a) - kUnitCost);
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(A.block_table + static_cast<int64_t>(p.b) * A.max_blocks + min(t0 * TOKENS >> A.pshift, A.max_blocks - 1)));
+        }
+        __syncthreads();
+        share.a = static_cast<int>(sums[kWarps]);
+        share.u = active ? static_cast<int>(sums[kWarps + 1]) : share.units;
+        return share;
+    }
+
+    // Tells the join whether this worker has the first tile of a unit whose last one is a later worker's: by the thread that
+    // counted the share's last unit, while the first loads are on their way.
+    __device__ __forceinline__ void record(const Args &A) const
+    {
         if (!active) {
-            if (tid == 0) A.rec[w] = make_int4(0, 0, 0, 0);
+            if (threadIdx.x == 0) A.rec[w] = make_int4(0, 0, 0, 0);
         } else if (before < x1 && x1 <= before + mine) {
-            find(x1 - 1, p, a);
+            Piece p;
+            long long a;
+            find(A, x1 - 1, p, a);
             const long long end = a + kUnitCost + p.tiles;
             int pieces = 0;
-            if (end > x1 && x0 <= a + kUnitCost && x1 > a + kUnitCost) {  // its first tile here, its last one not
+            if (end > x1 && x0 <= a + kUnitCost && x1 > a + kUnitCost) {
                 // the last share with a part of this unit: the least s with (s + 1) total / shares >= end
                 const long long last = total < (1 << 23) ? (static_cast<unsigned>(end) * static_cast<unsigned>(shares) + static_cast<unsigned>(total) - 1u) / static_cast<unsigned>(total)
                                                          : (end * shares + total - 1) / total;
@@ -224,8 +253,7 @@ __device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w, bool r
             A.rec[w] = make_int4(p.b, p.rt, pieces, 0);
         }
     }
-    return share;
-}
+};
 
 // Joins the pieces of the units that several workers shared, by all blocks of the grid once all have written theirs: a warp per
 // row where the pieces are few, a block per 256 coordinates of a row (a stretch of the pieces a warp) where they are many.  A

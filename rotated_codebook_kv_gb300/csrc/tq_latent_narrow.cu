@@ -107,12 +107,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 1; i < 4; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    int shares;
     umma::fence_before_sync();
-    Share<kNarrowRows, kTok> share = deal<kNarrowRows, kTok, kThreads>(A, worker, blockIdx.x == 0, true,
-                                                                       reinterpret_cast<long long *>(smem + C::kPlanOff), shares);
+    Dealer<kNarrowRows, kTok, kThreads> dealer;
+    Share<kNarrowRows, kTok> share = dealer.deal(A, worker, blockIdx.x == 0, reinterpret_cast<long long *>(smem + C::kPlanOff));
     umma::fence_after_sync();
     const uint32_t tbase = *tmem_slot;
+    dealer.record(A);
+    const int shares = dealer.shares;
 
     // bounded waits, see tq_latent.cu
     auto wait_one = [&](int i, uint32_t par) -> bool {
