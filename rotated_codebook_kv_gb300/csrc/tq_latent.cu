@@ -154,8 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool sectors = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0;  // rows begin on 32 bytes
         bool bad = false, dead = false;  // this warp's wait failed; all know
         int it = 0, sg = 0;
-        Piece p;
-        while (share.next(A, p)) {
+        Piece p, next;
+        for (bool more = share.next(A, p); more; p = next) {
             const int row = p.rt * kTile + static_cast<int>(rank) * kHalf + r;
             const bool valid = row < A.R;
             const size_t at = static_cast<size_t>(p.b) * A.R + row;
@@ -294,6 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) umma::cluster_arrive(leader(C::bPFull + (it & 1)));
             }
+            more = share.next(A, next);  // while the last products run
             if (p.t0 < p.t1 && !dead) {
                 bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);
                 umma::fence_after_sync();

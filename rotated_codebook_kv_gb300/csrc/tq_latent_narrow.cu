@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool flip = A.sm_scale < 0.f;
         bool bad = false, dead = false;  // this warp's wait failed; all know
         int it = 0;
-        Piece p;
-        while (share.next(A, p)) {
+        Piece p, next;
+        for (bool more = share.next(A, p); more; p = next) {
             const bool whole_unit = p.t0 == 0 && p.t1 == p.tiles;
             const size_t at = static_cast<size_t>(p.b) * A.R;
             const size_t slot = (2 * worker + (p.t0 == 0 ? 1 : 0)) * static_cast<size_t>(kNarrowRows);
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(&mbar[C::bPFull + (it & 1)])) : "memory");
             }
+            more = share.next(A, next);  // while the last products run
             if (p.t0 < p.t1 && !dead) {
                 bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);
                 umma::fence_after_sync();
