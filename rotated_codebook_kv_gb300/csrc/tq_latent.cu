@@ -68,7 +68,7 @@ struct Cfg {
     static constexpr uint32_t kOkOff = kMiscOff + 64;           // [8] a bit per 8 tokens of a tile: behind the end, or on a valid page
     static constexpr uint32_t kXOff = kOkOff + 32;              // [kSoft] exchange between the four threads of a row
     static constexpr uint32_t kPlanOff = (kXOff + 4 * kSoft + 15) / 16 * 16;  // scan and plan
-    static constexpr uint32_t kSmem = kPlanOff + 8 * (kThreads / 32 + 2);
+    static constexpr uint32_t kSmem = kPlanOff + 32 + 8 * (kThreads / 32 + 2);
     static constexpr uint32_t kTmS = 0, kTmO = 256;  // [2] 64 columns; DL / 2 columns
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -92,7 +92,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // misc[2..3] tiles and [4..5] Qs whose copies this and the other CTA issued; [6..7] NaN flags by a piece's parity
     volatile uint32_t *okmask = reinterpret_cast<volatile uint32_t *>(smem + C::kOkOff);
     float *xch = reinterpret_cast<float *>(smem + C::kXOff);
-    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff);  // warps' sums; then the first unit's first cost, and the unit
+    int4 *jobs = reinterpret_cast<int4 *>(smem + C::kPlanOff);
+    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff + 32);  // warps' sums; then the first unit's first cost, and the unit
 
     if (warp == kSoftWarps) umma::tmem_alloc_pair(tmem_slot, 512);
     if (tid == 0) {
@@ -109,16 +110,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 1; i < 8; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (rank == 0) A.done[pair] = 0;
     }
 
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     Dealer<kTile, kTile, kThreads> dealer;
-    Share<kTile, kTile> share = dealer.deal(A, pair, blockIdx.x == 0, plan);
+    Share<kTile, kTile> share = dealer.deal(A, pair, blockIdx.x == 0, plan, jobs);
     umma::cluster_sync();
-    if (rank == 0) dealer.record(A);
-    const int shares = dealer.shares;
+    auto grid = cooperative_groups::this_grid();
+    auto zeroed = grid.barrier_arrive();  // waited for before the first count
+    dealer.find_jobs(A, jobs);
     const uint32_t tbase = *tmem_slot;
 
     // bounded waits, by a warp and by one thread: they give up on the CTA's abort flag or after the wait limit (then raising
@@ -557,9 +560,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     umma::cluster_sync();
     if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
-    if (shares == 1) return;  // no unit is cut
-    cooperative_groups::this_grid().sync();
-    merge_pieces<DL, kTile, kThreads>(A, *reinterpret_cast<Merge<DL> *>(smem));
+    grid.barrier_wait(std::move(zeroed));
+    join<DL, kTile, kThreads>(A, jobs, pair, static_cast<int>(rank), 2, *reinterpret_cast<Merge *>(smem));
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -570,7 +572,7 @@ static_assert(kTile == 2 * kNarrowRows, "rows of a pair's unit and of a CTA's");
 size_t workspace_bytes(int dl, int pairs)
 {
     const size_t rows = static_cast<size_t>(2) * pairs * kTile;
-    return align256(kMaxWorkers * sizeof(int4)) + align256(rows * sizeof(float2)) + rows * dl * sizeof(float);
+    return align256(kMaxWorkers * sizeof(int)) + align256(rows * sizeof(float2)) + rows * dl * sizeof(float);
 }
 
 template <int DL>
@@ -637,8 +639,8 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
     a.sm_scale = sm_scale;
-    a.rec = static_cast<int4 *>(workspace);
-    a.ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + align256(kMaxWorkers * sizeof(int4)));
+    a.done = static_cast<int *>(workspace);
+    a.ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + align256(kMaxWorkers * sizeof(int)));
     a.acc = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ml) + align256(static_cast<size_t>(2) * pairs * kTile * sizeof(float2)));
     a.out = out;
     a.status = c.status;

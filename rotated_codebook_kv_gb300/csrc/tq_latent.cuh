@@ -1,6 +1,8 @@
 // tq_latent.cuh -- what the attention kernels over latent pages share: arguments, the dealing out of the work, small helpers.
 #pragma once
 
+#include <utility>
+
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -30,7 +32,7 @@ struct Args {
     int64_t num_blocks;
     int workers;           // pairs of CTAs, or CTAs
     float sm_scale;
-    int4 *rec;             // [workers] unit whose first piece is this worker's: b, row block, pieces (0: none)
+    int *done;             // [workers] blocks that have written their pieces of the unit whose first piece is this worker's
     float2 *ml;            // [2 workers][rows of a unit] reference, denominator
     float *acc;            // [2 workers][rows of a unit][DL]
     uint16_t *out;
@@ -179,7 +181,7 @@ struct Dealer {
     }
 
     // The share of worker w_.  Synchronises the block.
-    __device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w_, bool report, long long *sums)
+    __device__ __forceinline__ Share<ROWS, TOKENS> deal(const Args &A, int w_, bool report, long long *sums, int4 *jobs)
     {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         Share<ROWS, TOKENS> share;
@@ -188,6 +190,7 @@ struct Dealer {
         const int per = (share.units + THREADS - 1) / THREADS;
         u0 = min(tid * per, share.units);
         const int u1 = min(u0 + per, share.units);
+        if (tid < 2) jobs[tid] = make_int4(0, 0, 0, 0);
         mine = 0;
         for (int u = u0; u < u1; ++u) {
             Piece p;
@@ -232,101 +235,68 @@ struct Dealer {
         return share;
     }
 
-    // Tells the join whether this worker has the first tile of a unit whose last one is a later worker's: by the thread that
-    // counted the share's last unit, while the first loads are on their way.
-    __device__ __forceinline__ void record(const Args &A) const
+    // The units that this worker shares with others, at most two, by the threads that counted them, while the first loads are on
+    // their way: the first worker with a tile of the unit, how many there are, the sequence and the row block.
+    __device__ __forceinline__ void find_jobs(const Args &A, int4 *jobs) const
     {
-        if (!active) {
-            if (threadIdx.x == 0) A.rec[w] = make_int4(0, 0, 0, 0);
-        } else if (before < x1 && x1 <= before + mine) {
+        if (!active) return;
+        // the least s with (s + 1) total / shares >= v, for v <= total
+        auto reaches = [&](long long v) -> int {
+            if (total < (1 << 23))
+                return (static_cast<unsigned>(v) * static_cast<unsigned>(shares) + static_cast<unsigned>(total) - 1u) / static_cast<unsigned>(total) - 1;
+            return static_cast<int>((v * shares + total - 1) / total) - 1;
+        };
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            const long long x = side == 0 ? x0 : x1 - 1;
+            if (!(before <= x && x < before + mine)) continue;
             Piece p;
             long long a;
-            find(A, x1 - 1, p, a);
-            const long long end = a + kUnitCost + p.tiles;
-            int pieces = 0;
-            if (end > x1 && x0 <= a + kUnitCost && x1 > a + kUnitCost) {
-                // the last share with a part of this unit: the least s with (s + 1) total / shares >= end
-                const long long last = total < (1 << 23) ? (static_cast<unsigned>(end) * static_cast<unsigned>(shares) + static_cast<unsigned>(total) - 1u) / static_cast<unsigned>(total)
-                                                         : (end * shares + total - 1) / total;
-                pieces = static_cast<int>(last) - w;
-            }
-            A.rec[w] = make_int4(p.b, p.rt, pieces, 0);
+            find(A, x, p, a);
+            if (side == 1 && a <= x0) continue;  // the first border's unit
+            // its tiles have the costs a + kUnitCost .. a + kUnitCost + tiles - 1
+            const int f = reaches(a + kUnitCost + 1), l = reaches(a + kUnitCost + p.tiles);
+            if (p.tiles > 0 && f < l && f <= w && w <= l) jobs[side] = make_int4(f, l - f + 1, p.b, p.rt);
         }
     }
 };
 
-// Joins the pieces of the units that several workers shared, by all blocks of the grid once all have written theirs: a warp per
-// row where the pieces are few, a block per 256 coordinates of a row (a stretch of the pieces a warp) where they are many.  A
-// kernel of its own for it, launched as the attention's blocks ended, cost 5-10 us more (its start, and the end of the other).
+// Joins the pieces of a unit that several workers shared, by all of their blocks (block q of Q), once every piece is there: a warp
+// per row where the pieces are few, a block per 256 coordinates of a row (a stretch of the pieces a warp) where they are many.
+// A kernel of its own for it, launched as the attention's blocks ended, took 5-10 us longer, and a barrier over the grid 3-8.
 constexpr int kFewPieces = 16;
-template <int DL>
 struct Merge {
-    int4 jobs[kMaxWorkers];      // worker, pieces, first row of the unit in the outputs, rows
-    int first[kMaxWorkers + 1];  // first item of a job
-    int2 sums[32];
-    float4 part[32][2][32];
-    float2 dens[32];  // reference, denominator
+    float4 part[16][2][32];
+    float2 dens[16];  // reference, denominator
+    int give_up;
 };
 template <int DL, int ROWS, int THREADS>
-__device__ __forceinline__ void merge_pieces(const Args &A, Merge<DL> &S)
+__device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q, int Q, Merge &S)
 {
-    static_assert(kMaxWorkers <= THREADS, "a thread per worker");
-    constexpr int kMergeWarps = THREADS / 32;
-    constexpr int N = DL / 128;         // stretches of 128 coordinates of a row, a float4 per lane
-    constexpr int K = 16 / N;           // pieces of a row on their way together
+    constexpr int kWarps = THREADS / 32;
+    constexpr int N = DL / 128;  // stretches of 128 coordinates of a row, a float4 per lane
+    constexpr int K = 16 / N;    // pieces of a row on their way together
+    static_assert(kWarps <= 16, "a row of partial sums per warp");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int4 rec = tid < A.workers ? __ldcg(A.rec + tid) : make_int4(0, 0, 0, 0);
-    const int rows = min(ROWS, A.R - rec.y * ROWS);
-    const int cnt = rec.z > kFewPieces ? N / 2 * rows : rec.z > 0 ? (rows + kMergeWarps - 1) / kMergeWarps : 0;
-    int upto = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, cnt > 0);
-    if (lane == 31) S.sums[warp] = make_int2(__popc(m), upto);
-    __syncthreads();
-    int num_jobs = 0, items = 0, at = __popc(m & ((1u << lane) - 1u)), before = upto - cnt;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-        if (w < warp) {
-            at += S.sums[w].x;
-            before += S.sums[w].y;
-        }
-        num_jobs += S.sums[w].x;
-        items += S.sums[w].y;
-    }
-    if (cnt > 0) {
-        S.jobs[at] = make_int4(tid, rec.z, rec.x * A.R + rec.y * ROWS, rows);
-        S.first[at] = before;
-    }
-    if (tid == 0) S.first[num_jobs] = items;
-    __syncthreads();
-    int job = 0;
-    for (int e = blockIdx.x; e < items; e += gridDim.x) {
-        while (e >= S.first[job + 1]) ++job;
-        const int4 J = S.jobs[job];
-        const int n = J.y;
-        // piece 0 is the worker's last one, piece k the first one of worker + k
-        auto slot = [&](int k, int r) -> size_t { return (k == 0 ? 2 * J.x + 1 : 2 * (J.x + k)) * static_cast<size_t>(ROWS) + r; };
-        auto add = [&](float4 &o, float a, float4 v) {
-            o.x = fmaf(a, v.x, o.x);
-            o.y = fmaf(a, v.y, o.y);
-            o.z = fmaf(a, v.z, o.z);
-            o.w = fmaf(a, v.w, o.w);
-        };
-        auto put = [&](int r, int j4, float4 o, float den) {
-            const float inv = den == 0.f ? 0.f : 1.f / den;
-            reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(J.z) + r) * DL)[j4] =
-                make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
-        };
-        // 2^(m - M), M the larger of them
-        auto scale_of = [](float m, float M) -> float { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
-        const float4 *acc = reinterpret_cast<const float4 *>(A.acc);
-        if (n <= kFewPieces) {
-            const int r = (e - S.first[job]) * kMergeWarps + warp;
-            if (r >= J.w) continue;
+    const int n = job.y, row0 = job.w * ROWS, rows = min(ROWS, A.R - row0);
+    // piece 0 is the first worker's last one, piece k the first one of the k-th after it
+    auto slot = [&](int k, int r) -> size_t { return (k == 0 ? 2 * job.x + 1 : 2 * (job.x + k)) * static_cast<size_t>(ROWS) + r; };
+    auto add = [&](float4 &o, float a, float4 v) {
+        o.x = fmaf(a, v.x, o.x);
+        o.y = fmaf(a, v.y, o.y);
+        o.z = fmaf(a, v.z, o.z);
+        o.w = fmaf(a, v.w, o.w);
+    };
+    auto put = [&](int r, int j4, float4 o, float den) {
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(job.z) * A.R + row0 + r) * DL)[j4] =
+            make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
+    };
+    // 2^(m - M), M the larger of them
+    auto scale_of = [](float m, float M) -> float { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
+    const float4 *acc = reinterpret_cast<const float4 *>(A.acc);
+    if (n <= kFewPieces) {
+        for (int r = warp * Q + q; r < rows; r += kWarps * Q) {
             float m = -INFINITY, den = 0.f;
             float4 o[N] = {};
             for (int k0 = 0; k0 < n; k0 += K) {
@@ -359,18 +329,20 @@ __device__ __forceinline__ void merge_pieces(const Args &A, Merge<DL> &S)
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) put(r, lane + 32 * i, o[i], den);
-            continue;
         }
-        const int r = (e - S.first[job]) / (N / 2), i0 = (e - S.first[job]) % (N / 2) * 2;
+        return;
+    }
+    for (int e = q; e < rows * (N / 2); e += Q) {
+        const int r = e / (N / 2), i0 = e % (N / 2) * 2;
         float m = -INFINITY, den = 0.f;
         float4 o[2] = {};
         constexpr int kDeep = 4;
-        for (int k0 = warp; k0 < n; k0 += kDeep * kMergeWarps) {
+        for (int k0 = warp; k0 < n; k0 += kDeep * kWarps) {
             float2 ml[kDeep];
             float4 v[kDeep][2];
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
-                const int k = k0 + j * kMergeWarps;
+                const int k = k0 + j * kWarps;
                 ml[j] = make_float2(-INFINITY, 0.f);
                 if (k < n) {
                     ml[j] = __ldcg(A.ml + slot(k, r));
@@ -402,11 +374,11 @@ __device__ __forceinline__ void merge_pieces(const Args &A, Merge<DL> &S)
         if (warp < 2) {
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, S.dens[w].x);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, S.dens[w].x);
             float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
             den = 0.f;
 #pragma unroll
-            for (int w = 0; w < kMergeWarps; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 if (S.dens[w].y == 0.f) continue;
                 const float a = scale_of(S.dens[w].x, M);
                 den = fmaf(a, S.dens[w].y, den);
@@ -414,6 +386,40 @@ __device__ __forceinline__ void merge_pieces(const Args &A, Merge<DL> &S)
             }
             put(r, lane + 32 * (i0 + warp), t, den);
         }
+    }
+}
+
+// The end of a block (part of `parts` of worker w) whose pieces are all written: says so to the workers that it shares units
+// with, waits for theirs, and joins its part of them.  The wait is for blocks of the same launch, which all run at once
+// (launch_together), and whose own waits are bounded; its limit, some 30 s, is only reached where one of them has failed.
+template <int DL, int ROWS, int THREADS>
+__device__ __forceinline__ void join(const Args &A, const int4 *jobs, int w, int part, int parts, Merge &S)
+{
+    constexpr long long kJoinLimit = 60000000000LL;
+    if (threadIdx.x == 0) {
+        S.give_up = 0;
+        __threadfence();
+        for (int i = 0; i < 2; ++i)
+            if (jobs[i].y > 1) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(A.done + jobs[i].x) : "memory");
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int4 job = jobs[i];
+        if (job.y < 2) continue;
+        if (threadIdx.x == 0) {
+            const long long t0 = clock64();
+            for (int have = 0; have < job.y * parts;) {
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(have) : "l"(A.done + job.x) : "memory");
+                if (have < job.y * parts && clock64() - t0 > kJoinLimit) {
+                    S.give_up = 1;
+                    atomicOr(A.status, TQ_DEVERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
+        __syncthreads();
+        if (S.give_up) return;
+        merge_unit<DL, ROWS, THREADS>(A, job, (w - job.x) * parts + part, job.y * parts, S);
     }
 }
 

@@ -52,7 +52,7 @@ struct Cfg {
     static constexpr uint32_t kXOff = (kOkOff + 32 + 15) / 16 * 16;  // [2][64] exchange between the halves of a row
     static constexpr uint32_t kFacOff = kXOff + 4 * 128;       // [64] factors of the rows
     static constexpr uint32_t kPlanOff = kFacOff + 4 * 64;
-    static constexpr uint32_t kSmem = kPlanOff + 8 * (kThreads / 32 + 2);
+    static constexpr uint32_t kSmem = kPlanOff + 32 + 8 * (kThreads / 32 + 2);
     static constexpr uint32_t kTmS = 0, kTmO = 128;  // [2] 64 columns; [NX] 64 columns
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -106,14 +106,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 1; i < 4; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        A.done[worker] = 0;
     }
     umma::fence_before_sync();
+    int4 *jobs = reinterpret_cast<int4 *>(smem + C::kPlanOff);
     Dealer<kNarrowRows, kTok, kThreads> dealer;
-    Share<kNarrowRows, kTok> share = dealer.deal(A, worker, blockIdx.x == 0, reinterpret_cast<long long *>(smem + C::kPlanOff));
+    Share<kNarrowRows, kTok> share = dealer.deal(A, worker, blockIdx.x == 0, reinterpret_cast<long long *>(smem + C::kPlanOff + 32), jobs);
     umma::fence_after_sync();
     const uint32_t tbase = *tmem_slot;
-    dealer.record(A);
-    const int shares = dealer.shares;
+    auto grid = cooperative_groups::this_grid();
+    auto zeroed = grid.barrier_arrive();  // waited for before the first count
+    dealer.find_jobs(A, jobs);
 
     // bounded waits, see tq_latent.cu
     auto wait_one = [&](int i, uint32_t par) -> bool {
@@ -496,9 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     umma::fence_after_sync();
     if (warp == kSoftWarps) umma::tmem_dealloc(tbase, 512);
-    if (shares == 1) return;  // no unit is cut
-    cooperative_groups::this_grid().sync();
-    merge_pieces<DL, kNarrowRows, kThreads>(A, *reinterpret_cast<Merge<DL> *>(smem));
+    grid.barrier_wait(std::move(zeroed));
+    join<DL, kNarrowRows, kThreads>(A, jobs, worker, 0, 1, *reinterpret_cast<Merge *>(smem));
 }
 
 template <int DL>
