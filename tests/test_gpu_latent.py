@@ -120,6 +120,40 @@ def test_a_long_sequence_cut_into_many_pieces(dl, Hq, n):
     check(run(c), ref, bound)
 
 
+@pytest.mark.parametrize("dl,Hq", [(512, 64), (512, 128), (256, 20), (256, 90)])
+def test_sequences_cut_into_several_pieces(dl, Hq):
+    """Some ten pieces a sequence, joined row by row; the same call gives the same bits."""
+    c = case(dl, 64, Hq, [2500, 2300, 64 * 36, 700, 2501, 2047, 1, 2499], seed=Hq)
+    ref, bound = reference(c)
+    out = run(c)
+    check(out, ref, bound)
+    for _ in range(5):
+        assert torch.equal(run(c), out)
+
+
+def test_more_units_than_threads():
+    """Row blocks of a few sequences, several of them counted by one thread; lengths below the chunk's."""
+    c = case(256, 32, 100, [310, 20, 400], Tq=260, seed=4)
+    q, lens = c["q"], c["lens"]
+    rows = [0, 1, 100, 239, 240, 258, 259]
+    out = run(c)
+    for i in rows:  # each query token as the last one of shorter sequences
+        one = dict(c, q=q[:, i].contiguous(), lens=(lens - 259 + i).clamp(min=0))
+        ref, bound = reference(one)
+        check(out[:, i], ref, bound)
+    assert codec().get_status() == 0
+
+
+@pytest.mark.parametrize("Hq,Tq", [(8, None), (70, None), (70, 3)])
+def test_outputs_on_16_bytes(Hq, Tq):
+    c = case(512, 16, Hq, [500, 77], Tq=Tq, seed=2)
+    ref = run(c)
+    buf = torch.full((ref.numel() + 16,), 9.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[8: 8 + ref.numel()].view(ref.shape)
+    assert out.data_ptr() % 32 == 16 and run(c, out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, ref) and torch.all(buf[:8] == 9) and torch.all(buf[-8:] == 9)
+
+
 @pytest.mark.parametrize("dl", [256, 512])
 def test_decode_of_many_sequences(dl):
     """More sequences than a block has threads, lengths from 0 on."""
@@ -233,6 +267,20 @@ def test_what_is_not_finite_in_a_later_token_stays_hidden(dl, Hq, Tq, j, bits):
     assert codec().get_status() == 0
 
 
+@pytest.mark.parametrize("dl,Hq,Tq", [(512, 20, 40), (256, 1, 50)])
+def test_what_is_not_finite_reaches_across_pieces(dl, Hq, Tq):
+    """A long sequence cut into many pieces, NaN early (every row sees it) or among its last tokens."""
+    n = 6000
+    clean = case(dl, 16, Hq, [n], Tq=Tq, seed=13)
+    ref = run(clean)
+    for pos, first in ((17, 0), (n - 5, Tq - 5), (n - Tq // 2, Tq - Tq // 2)):
+        c = dict(clean, pool=clean["pool"].clone())
+        c["pool"][int(c["table"][0, pos // 16]), pos % 16, 9] = float("nan")
+        out = run(c)
+        assert bool(torch.isnan(out[0, first:]).all())
+        assert torch.equal(out[0, :first], ref[0, :first])
+
+
 def test_nan_in_a_query_stays_in_its_row():
     c = case(512, 16, 4, [100, 50], seed=6)
     c["q"][0, 1, 5] = float("nan")
@@ -275,11 +323,12 @@ def test_pool_offsets_past_32_bits():
     assert codec().get_status() == 0
 
 
-@pytest.mark.parametrize("dl,Tq", [(512, None), (256, None), (512, 40), (256, 40)])
-def test_wait_timeout_reports_and_recovers(dl, Tq):
+@pytest.mark.parametrize("dl,Hq,Tq", [(512, 4, None), (256, 4, None), (512, 100, None), (256, 100, None), (512, 4, 40), (256, 4, 40),
+                                      (512, 4, 9), (256, 4, 9)])
+def test_wait_timeout_reports_and_recovers(dl, Hq, Tq):
     """With a wait limit of 0 every wait tests its barrier once, the first one as its copies are issued."""
     own = Codec(128, 4, 4, 64)
-    c = case(dl, 16, 4, [3000] * 30, Tq=Tq, seed=7)
+    c = case(dl, 16, Hq, [3000] * 30, Tq=Tq, seed=7)
 
     def go():
         call = own.decode_attention_latent if Tq is None else own.prefill_attention_latent
