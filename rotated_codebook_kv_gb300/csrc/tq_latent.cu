@@ -637,6 +637,7 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     a.P = P;
     a.pshift = P == 16 ? 4 : P == 32 ? 5 : 6;
     a.max_blocks = max_blocks;
+    a.few = (narrow ? batch : units) <= 32 && units * tiles < (1 << 23);
     a.num_blocks = num_blocks;
     a.sm_scale = sm_scale;
     a.done = static_cast<int *>(workspace);

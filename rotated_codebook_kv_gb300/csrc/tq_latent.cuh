@@ -29,6 +29,7 @@ struct Args {
     const int32_t *block_table, *seq_lens;
     int B, Tq, Hq, R, RT;  // R = Tq Hq rows of a sequence, in RT blocks (of 128, or of 64 in the narrow kernel)
     int P, pshift, max_blocks;
+    bool few;              // a warp's lanes are enough to count the units
     int64_t num_blocks;
     int workers;           // pairs of CTAs, or CTAs
     float sm_scale;
@@ -187,10 +188,43 @@ struct Dealer {
         Share<ROWS, TOKENS> share;
         w = w_;
         share.units = A.B * A.RT;
+        if (tid < 2) jobs[tid] = make_int4(0, 0, 0, 0);
+        if (A.few) {
+            // a unit per lane: every warp counts them for itself and meets no other (0.5 us less than the way below, which 65 units
+            // on 32 lanes lose again)
+            u0 = min(lane, share.units);
+            int m = 0;
+            if (lane < share.units) {
+                Piece p;
+                unit_of<ROWS, TOKENS>(A, lane, p);
+                m = p.tiles + kUnitCost;
+                if (report && warp == 0 && p.rt == 0 && __ldg(A.seq_lens + p.b) > (A.max_blocks << A.pshift)) atomicOr(A.status, TQ_DEVERR_SEQ_RANGE);
+            }
+            int upto = m;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const int all = __shfl_sync(0xffffffffu, upto, 31), b = upto - m;
+            before = b;
+            mine = m;
+            total = all;
+            shares = min(A.workers, max(all / kMinShare, 1));
+            active = w < shares;
+            const int y0 = active ? static_cast<int>(share_start(w, all, shares)) : 0, y1 = active ? static_cast<int>(share_start(w + 1, all, shares)) : 0;
+            x0 = y0;
+            x1 = y1;
+            const int src = __ffs(__ballot_sync(0xffffffffu, b <= y0 && y0 < b + m)) - 1;  // the lane of the unit that y0 lies in
+            share.len = y1 - y0;
+            share.a = __shfl_sync(0xffffffffu, b, src) - y0;
+            share.u = active ? src : share.units;
+            __syncthreads();
+            return share;
+        }
         const int per = (share.units + THREADS - 1) / THREADS;
         u0 = min(tid * per, share.units);
         const int u1 = min(u0 + per, share.units);
-        if (tid < 2) jobs[tid] = make_int4(0, 0, 0, 0);
         mine = 0;
         for (int u = u0; u < u1; ++u) {
             Piece p;
@@ -239,7 +273,7 @@ struct Dealer {
     // their way: the first worker with a tile of the unit, how many there are, the sequence and the row block.
     __device__ __forceinline__ void find_jobs(const Args &A, int4 *jobs) const
     {
-        if (!active) return;
+        if (!active || (A.few && threadIdx.x >= 32)) return;
         // the least s with (s + 1) total / shares >= v, for v <= total
         auto reaches = [&](long long v) -> int {
             if (total < (1 << 23))
@@ -275,7 +309,7 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
 {
     constexpr int kWarps = THREADS / 32;
     constexpr int N = DL / 128;  // stretches of 128 coordinates of a row, a float4 per lane
-    constexpr int K = 16 / N;    // pieces of a row on their way together
+    constexpr int K = 8 / N;     // pieces of a row on their way together
     static_assert(kWarps <= 16, "a row of partial sums per warp");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = job.y, row0 = job.w * ROWS, rows = min(ROWS, A.R - row0);

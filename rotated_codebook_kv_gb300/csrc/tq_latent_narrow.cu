@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait_one(C::bPFull + (it & 1), (it >> 1) & 1))) break;
                     umma::fence_after_sync();
                     const uint32_t st = (it % NS) * (C::kStage / 16);
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < NX; ++x)
 #pragma unroll
                         for (int t = 0; t < kTok / 16; ++t)
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     okmask[it & 7] = valid;
                     const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
                     const uint32_t full = k_full + 8 * NG * (it % NS);
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < NG; ++x) {
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * x), "r"(8 * 1024 * C::GB) : "memory");
 #pragma unroll
