@@ -34,7 +34,8 @@
  *     never trap.
  *
  * Supported parameters: head_dim in {128, 256}; k_bits, v_bits in {2, 3, 4};
- * group in {32, 64, 128} dividing head_dim; page_size in {16, 32}.  QJL is on
+ * group in {32, 64, 128} dividing head_dim; page_size in {16, 32} (of latent
+ * pages, whose sizes are given there, also 64).  QJL is on
  * exactly when k_bits <= 3 (m = head_dim projection rows, one bit each).
  */
 #ifndef TQ_H_
@@ -423,15 +424,16 @@ tq_status tq_prefill_attention_fp8(tq_handle h, const uint16_t *q, const uint8_t
  *       projection can be passed).  q, q_out: device bf16, token t / head h at ptr +
  *       t * stride_tok + h * stride_head, the heads' TQ_LATENT_ROPE_DIM coordinates that take part
  *       in the rotation: q_out may be the last columns of the attention's queries.  q may
- *       be NULL (then so is q_out, and their sizes are ignored); q_out may be q itself, else
- *       it does not overlap the inputs.  Strides are multiples of 8 and no less than a row,
- *       pointers 16-byte aligned.
+ *       be NULL (then so is q_out, and their sizes are ignored); q_out may be q itself (with
+ *       q's strides), else it does not overlap the inputs; all heads of a q_out token lie before
+ *       the next token's, or all tokens of a head before the next head's.  Strides are
+ *       multiples of 8 and no less than a row, pointers 16-byte aligned.
  * norm_weight: device bf16 [latent_dim], or NULL: c w / sqrt(mean(c^2) + norm_eps) in fp32,
  *       rounded once to bf16; without it c passes through.
  * rope, rope_rows, positions, style: as in tq_append_kv_bf16 with rot_dim
  *       TQ_LATENT_ROPE_DIM, for k_rope and q; rope NULL: no rotation (positions ignored).
  * slot_mapping: as in tq_append_kv_bf16; a skipped token leaves its row and its q_out
- *       rows as they were.
+ *       rows as they were.  A slot given twice in a call holds one of its tokens or parts of both.
  * One launch on `stream`; T == 0 launches nothing.
  */
 #define TQ_LATENT_ROPE_DIM 64
@@ -456,7 +458,10 @@ tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const uint16_t *
  * workspace: ws_bytes >= tq_workspace_bytes_latent(...), 256-byte aligned; its contents after
  *   the call are not specified, and calls that may overlap need one each.  Work is cut on
  *   the GPU, from the lengths of all sequences, so results depend on the batch, within rounding.
- * Two launches (attention, and what joins the pieces).
+ * out overlaps no input and not the workspace.
+ * One cooperative launch: its blocks, one per SM, wait for the pieces of one another, so that it
+ *   starts when all SMs are free of other launches' blocks; TQ_ERR_CUDA where they cannot
+ *   all run at once (a context that is limited to some of the SMs).
  *
  * tq_prefill_attention_latent -- the last q_tokens positions of every sequence attend
  * causally to its latent pages, their own rows included (tq_prefill_attention's contract).

@@ -261,6 +261,8 @@ extern "C" tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const
     if (bad(latent_stride, latent_dim) || bad(k_stride, r) ||
         (q && (bad(q_stride_tok, r) || bad(q_stride_head, r) || bad(qo_stride_tok, r) || bad(qo_stride_head, r))))
         return api_error(TQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, no less than a row", who);
+    if (q && T > 1 && num_q_heads > 1 && qo_stride_tok < (num_q_heads - 1) * qo_stride_head + r && qo_stride_head < (T - 1) * qo_stride_tok + r)
+        return api_error(TQ_ERR_INVALID_ARG, "%s: rows of q_out overlap", who);
     const tq::Codec &c = tq::handle_codec(h);
     const tq::LatentArgs a{latent, k_rope, q, T, num_q_heads, latent_stride, k_stride, q_stride_tok, q_stride_head, qo_stride_tok,
                            qo_stride_head, norm_weight, norm_eps, positions, rope, rope_rows, style == TQ_ROPE_INTERLEAVED,

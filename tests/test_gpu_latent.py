@@ -388,6 +388,23 @@ def test_two_graphs_with_a_workspace_each_and_another_stream():
     check(od, ref, bound)
 
 
+def test_two_calls_at_once():
+    cases = [case(512, 64, 20, [3000, 70, 511], seed=21), case(256, 32, 100, [900, 1, 2049], seed=22), case(512, 32, 6, [700, 40], Tq=30, seed=23)]
+    refs = [run(c) for c in cases]
+    spaces = [codec().workspace_latent(len(c["lens"]), 1 if c["q"].dim() == 3 else c["q"].shape[1], c["q"].shape[-2], c["dl"]) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(8):
+        for c, w, s in zip(cases, spaces, streams):
+            with torch.cuda.stream(s):
+                call = codec().decode_attention_latent if c["q"].dim() == 3 else codec().prefill_attention_latent
+                outs.append(call(c["q"], c["pool"], c["table"], c["lens"], c["P"], c["nb"], scale(c), workspace=w))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, refs[i % len(cases)])
+
+
 # ---- append ------------------------------------------------------------------------------------------------
 
 APPEND = [
@@ -557,6 +574,22 @@ def test_append_refusals():
                dict(rope=x.data_ptr(), pos=slots.data_ptr()), dict(lat=x.data_ptr() + 2), dict(ls=248), dict(ls=324), dict(ks=56), dict(qs=56),
                dict(qh=0), dict(os=4), dict(oh=-64), dict(w=x.data_ptr(), eps=-1.0), dict(w=x.data_ptr(), eps=float("nan"))):
         refused(I, "tq_append_latent", **kw)
+
+
+def test_append_into_rows_that_overlap_is_refused():
+    k = codec()
+    T, Hq = 5, 3
+    x, q = torch.randn(T, 320, device=DEV).bfloat16(), torch.randn(T, Hq, 64, device=DEV).bfloat16()
+    pool, slots = k.alloc_pool_latent(1, 16, 256), torch.arange(T, device=DEV)
+    room = torch.zeros(T * Hq * 64, dtype=torch.bfloat16, device=DEV)
+    for st, sh, ok in ((64, 64, False), (64 * Hq - 8, 64, False), (64, 64 * T - 8, False), (64 * Hq, 64, True), (64, 64 * T, True)):
+        out = torch.as_strided(room, (T, Hq, 64), (st, sh, 1))
+        if ok:
+            k.append_latent(x[:, :256], x[:, 256:], slots, pool, 16, 1, q=q, q_out=out)
+            assert torch.equal(out, q)
+        else:
+            with pytest.raises(native.TQError, match="overlap"):
+                k.append_latent(x[:, :256], x[:, 256:], slots, pool, 16, 1, q=q, q_out=out)
 
 
 @pytest.mark.parametrize("dl,P,Hq", [(512, 64, 20), (256, 16, 5)])
