@@ -55,6 +55,7 @@ struct Cfg {
     static constexpr int GB = DL == 512 ? 3 : 5;  // blocks of a group, which has a barrier of its own
     static constexpr int NG = NBLK / GB;
     static_assert(NG * GB == NBLK, "whole groups");
+    static constexpr int kHalfGroups = NO / GB;  // groups of the first half of the tokens' values alone
     static constexpr uint32_t kBlk = 64 * 128;
     static constexpr uint32_t kOct = NBLK * 1024; // eight tokens of a stage: NBLK blocks of 8 x 128 bytes
     static constexpr uint32_t kStage = NBLK * kBlk;
@@ -69,7 +70,8 @@ struct Cfg {
     static constexpr int bSFull = bVFull + NS;      // [2] scores in tensor memory
     static constexpr int bPFull = bSFull + 2;       // (L) [2] P written, its scores read, O rescaled
     static constexpr int bPvDone = bPFull + 2;      // [NS] O += P V done: the stage is free
-    static constexpr int bEnd = bPvDone + NS;       // (L) [2] teardown: all MMAs issued by a warp are done
+    static constexpr int bPvHalf = bPvDone + NS;    // [NS] and those of the first half of its tokens
+    static constexpr int bEnd = bPvHalf + NS;       // (L) [2] teardown: all MMAs issued by a warp are done
     static constexpr int kBars = bEnd + 2;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * kBars;   // tensor-memory base, abort, issued counts, NaN flags
     static constexpr uint32_t kOkOff = kMiscOff + 64;           // [8] a bit per 8 tokens of a tile: behind the end, or on a valid page
@@ -96,7 +98,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     volatile int *misc = reinterpret_cast<volatile int *>(smem + C::kMiscOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
     volatile int *abort_flag = misc + 1;
-    // misc[2..3] tiles and [4..5] Qs whose copies this and the other CTA issued; [6..7] NaN flags by a piece's parity
+    // misc[2..3] groups of tiles and [4..5] Qs whose copies this and the other CTA issued; [6..7] NaN flags by a piece's parity
     volatile uint32_t *okmask = reinterpret_cast<volatile uint32_t *>(smem + C::kOkOff);
     float *xch = reinterpret_cast<float *>(smem + C::kXOff);
     int4 *jobs = reinterpret_cast<int4 *>(smem + C::kPlanOff);
@@ -109,6 +111,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NS; ++i) {
             umma::mbar_init(&mbar[C::bVFull + i], 1);
             umma::mbar_init(&mbar[C::bPvDone + i], 1);
+            umma::mbar_init(&mbar[C::bPvHalf + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(&mbar[C::bSFull + i], 1);
@@ -259,9 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float2 sum = unpack2(add2(sum0, sum1));
                 l_run += sum.x + sum.y;
                 // P: the first half's buffer is free when an earlier tile's P.V is done, the rotated part with these scores
-                if (h == 0 && it >= C::NP) {
-                    bad |= !wait_bar(C::bPvDone + (it - C::NP) % NS, ((it - C::NP) / NS) & 1);
-                }
+                if (h == 0 && it >= C::NP) bad |= !wait_bar(C::bPvHalf + (it - C::NP) % NS, ((it - C::NP) / NS) & 1);
                 const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
                 const uint32_t pd = h == 0 ? sbase + C::kPOff + (it % C::NP) * C::kBlk + r * 128
                                            : st + (r >> 3) * C::kOct + (NBLK - 1) * 1024 + (r & 7) * 128;
@@ -424,13 +425,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     umma::fence_after_sync();
                     const uint32_t st = (C::kKOff + (it % NS) * C::kStage) / 16;
 #pragma unroll
-                    for (int x = 0; x < C::NX; ++x)
+                    for (int t = 0; t < 8; ++t)  // 16 tokens
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) {  // 16 tokens
+                        for (int x = 0; x < C::NX; ++x) {
                             const uint32_t pa = 2 * (t & 3) + (t < 4 ? lo_p + (C::kPOff + (it % C::NP) * C::kBlk) / 16
                                                                      : lo_r + st + (NBLK - 1) * 64);
                             const uint32_t va = lo_v + st + (t & 3) * (2 * C::kOct / 16) + ((t >> 2) * NO + 2 * x) * 64;
                             umma::mma_f16_pair(tbase + C::kTmO + 128 * x, pa, t < 4 ? hi_p : hi_r, va, hi_v, id, i > p.t0 || t > 0);
+                            if (t == 3 && x == C::NX - 1) umma::commit_pair(&mbar[C::bPvHalf + it % NS]);
                         }
                     umma::commit_pair(&mbar[C::bPvDone + it % NS]);
                 }
@@ -466,23 +468,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 int row[8];
 #pragma unroll
                 for (int g = 0; g < 8; ++g) row[g] = __shfl_sync(0xffffffffu, y, 8 * static_cast<int>(rank) + g);
-                if (it >= NS && !(ok = wait_bar(C::bPvDone + it % NS, (it / NS - 1) & 1))) break;
-                if (umma::elect_one()) {
-                    okmask[it & 7] = valid;
-                    const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
-                    const uint32_t full = k_full + 8 * NG * (it % NS);
+                const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
+                const uint32_t full = k_full + 8 * NG * (it % NS);
 #pragma unroll
-                    for (int x = 0; x < NG; ++x) {
+                for (int x = 0; x < NG; ++x) {
+                    if (it >= NS && (x == 0 || x == C::kHalfGroups) && !(ok = wait_bar((x < C::kHalfGroups ? C::bPvHalf : C::bPvDone) + it % NS, (it / NS - 1) & 1))) break;
+                    if (umma::elect_one()) {
+                        if (x == 0) okmask[it & 7] = valid;
                         umma::cluster_arrive_expect(full + 8 * x, 8 * 1024 * C::GB);
 #pragma unroll
                         for (int g = 0; g < 8; ++g)
                             asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                                          ::"r"(st + g * C::kOct + x * (C::GB * 1024)), "l"(reinterpret_cast<uint64_t>(&tmK)), "r"(0), "r"(row[g]), "r"(C::GB * x), "r"(full + 8 * x)
                                          : "memory");
+                        misc[2] = it * NG + x + 1;
                     }
-                    misc[2] = it + 1;
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
                 blk = fetch_id(i + 1);
                 if (far) prefetch_rows<C::D>(A, (i + NS) * kTile + 8 * (lane & 15), fetch_id(i + NS), lane < 16 && lane >> 3 == static_cast<int>(rank));
             }
@@ -550,13 +553,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     umma::fence_after_sync();
     if (tid == 0) {
         // a barrier that only the other CTA has announced copies on gets this CTA's arrival, so that its phase ends with them
-        for (int t = misc[2]; t < misc[3]; ++t)
-            for (int g = 0; g < NG; ++g) umma::cluster_arrive(leader(C::bKFull + (t % NS) * NG + g));
+        for (int t = misc[2]; t < misc[3]; ++t) umma::cluster_arrive(leader(C::bKFull + t % (NS * NG)));
         for (int t = misc[4]; t < misc[5]; ++t) umma::cluster_arrive(leader(C::bQFull));
         if (rank == 0) {
-            const int tiles = max(misc[2], misc[3]), qs = max(misc[4], misc[5]);
-            for (int t = max(0, tiles - NS); t < tiles; ++t)
-                for (int g = 0; g < NG; ++g) drain(C::bKFull + (t % NS) * NG + g, (t / NS) & 1);
+            const int groups = max(misc[2], misc[3]), qs = max(misc[4], misc[5]);
+            for (int t = max(0, groups - NS * NG); t < groups; ++t) drain(C::bKFull + t % (NS * NG), t / (NS * NG) & 1);
             if (qs > 0) drain(C::bQFull, (qs - 1) & 1);
         } else {
             // the first CTA's commits arrive here too, and none may find this CTA gone: its last ones, on these
