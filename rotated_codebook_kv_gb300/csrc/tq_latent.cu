@@ -223,6 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int ch = 0; ch < DL / 4; ch += 32) {
                             float o[32];
+                            __syncwarp();
                             umma::ld32(to + ch, o);
                             uint32_t w[32];
 #pragma unroll

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                             for (int ch = 0; ch < rows16; ch += 16) {
                                 float o[16];
+                                __syncwarp();
                                 umma::ld16(lane_base + C::kTmO + 64 * x + ch, o);
                                 uint32_t w[16];
 #pragma unroll
