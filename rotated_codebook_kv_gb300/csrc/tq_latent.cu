@@ -19,12 +19,15 @@
 // every CTA finds its share from the lengths.  The pairs that share a unit leave their sums in the workspace and join them at
 // their ends, each a part of the rows.
 //
-// Measured (a call in a graph): 1024 tokens behind 15k of 128 heads, DL = 512: 2.90 ms, 1.56 PFLOP/s, 82% of the measured bf16
-// rate; 256 tokens of 4 sequences of 2k to 8k, 64 heads: 570 us, 1.51 PFLOP/s.  A tile's products take ~2180 cycles of the tensor
-// pipe, but read 2875 cycles' worth of shared memory: that bounds a tile, ~3150 cycles.  Decode of 8 x 32k tokens of 128 heads:
-// 75 us, 4.1 TB/s; 4 tokens of 24 sequences of 1k to 9k, 32 heads: 50 us; there start (~7.5 us to the first tile), the chain load
+// P.V goes through the tokens, and at the middle hands back the blocks and the half of P that only the first 64 of them use (with
+// all at the end 571 instead of 551 us in the second case below).
+//
+// Measured (a call in a graph): 1024 tokens behind 15k of 128 heads, DL = 512: 2.82 ms, 1.61 PFLOP/s, 84% of the measured bf16
+// rate; 256 tokens of 4 sequences of 2k to 8k, 64 heads: 551 us, 1.56 PFLOP/s.  A tile's products take ~2180 cycles of the tensor
+// pipe, but read 2875 cycles' worth of shared memory: that bounds a tile, ~3050 cycles.  Decode of 8 x 32k tokens of 128 heads:
+// 73 us, 4.2 TB/s; 4 tokens of 24 sequences of 1k to 9k, 32 heads: 50 us; there start (~7 us to the first scores), the chain load
 // - scores - softmax - P.V through two stages, and the join take what is above HBM's time.  At DL = 256 the softmax warps bound a
-// tile: ~2000 cycles against 1150 of the products.
+// tile: ~1900 cycles against 1150 of the products.
 //
 // Warps (one CTA per SM): 8, a thread per row and quarter of the tile's tokens: softmax, P, output; 1 issue of the scores and 1
 // of P.V (in the pair's first CTA, for both); 1 loads of the tiles; 1 loads of Q and over the dead blocks.

@@ -12,10 +12,10 @@
 // another CTA and its chain from the last byte to the stage's release is shorter, so the two stages (four at DL = 256) keep
 // more in flight.  Measured against the pairs for every call: 32 sequences of 1k to 8k of 64 heads 48.7 us instead of 52.0, 2 x
 // 131k of 32 heads 60.3 instead of 66.9 (5.0 TB/s, 74% of the measured copy rate), 190 of up to 900 of 40 heads at DL = 256 26.4
-// instead of 32.6, one of 500 of 8 heads 10.7 instead of 12.5 (a call in a graph).
+// instead of 32.6, one of 500 of 8 heads 9.8 instead of 12.5 (a call in a graph).
 //
-// What bounds it: a stage is taken from its load's start to its P.V's end, ~7400 cycles, so that two of them give a tile every
-// ~3700 (HBM alone: ~3030); and beside the tiles ~7.5 us from the launch to the first tile and 3 to 6 for output and join.
+// What bounds it: a tile takes 1.88 us between start and end where all SMs stream (HBM alone: 1.65); and beside the tiles ~7 us
+// from the launch to the first scores and 3 to 6 for output and join.
 // The loops over a tile's groups are not unrolled: the shorter code is worth 0.5 us (49.3 -> 48.7); the pairs' kernel, unrolled,
 // is the faster one (568 against 574 us for chunks of 256 tokens).
 //
