@@ -186,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
                 umma::fence_after_sync();
                 float sf[32];
+                __syncwarp();
                 umma::ld32(lane_base + C::kTmS + 64 * (it & 1) + 32 * g, sf);
                 umma::fence_before_sync();
                 const int rem = lim - i * kTile - h * kHalf - 32 * g;  // of these tokens, those that the row sees
@@ -571,6 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     umma::cluster_sync();
+    __syncwarp();
     if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
     grid.barrier_wait(std::move(zeroed));
     join<DL, kTile, kThreads>(A, jobs, pair, static_cast<int>(rank), 2, *reinterpret_cast<Merge *>(smem));

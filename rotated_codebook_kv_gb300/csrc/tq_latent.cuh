@@ -103,11 +103,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
     return v;
 }
 
-// The softmax warps' barrier; whether any of their threads says so.
+// The softmax warps' barrier; whether any of their threads says so.  The warp is gathered for it, and behind it: accesses to
+// tensor memory want whole warps.
 __device__ __forceinline__ bool any_of_softmax(bool x)
 {
     uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+    __syncwarp();
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred.aligned p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}\n"
                  : "=r"(r) : "r"(static_cast<uint32_t>(x)), "n"(kSoft) : "memory");
     return r != 0;
 }

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
                 umma::fence_after_sync();
                 float s[16];
+                __syncwarp();
                 ld_rows(lane_base + C::kTmS + 64 * (it & 1) + 32 * g, s);
                 umma::fence_before_sync();
                 const uint32_t ok4 = okmask[it & 7] >> (4 * g) & 15u;
@@ -506,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
+    __syncwarp();
     if (warp == kSoftWarps) umma::tmem_dealloc(tbase, 512);
     grid.barrier_wait(std::move(zeroed));
     join<DL, kNarrowRows, kThreads>(A, jobs, worker, 0, 1, *reinterpret_cast<Merge *>(smem));
