@@ -19,6 +19,8 @@ constexpr int kRope = TQ_LATENT_ROPE_DIM;
 constexpr int kUnitCost = 4;
 constexpr int kMinShare = 3;     // least cost of a worker's share: 6 to 16 leave SMs idle in small calls (11.5 -> 13.8 us at 16)
 constexpr int kMaxWorkers = 256;
+// Rows of a sequence that the narrow kernel takes (one CTA, 64 rows); longer ones go to pairs of CTAs.
+constexpr int kNarrowRows = 64;
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference m stands 2^kMargin above the running maximum when it is set, and O is rescaled only when the maximum passes
@@ -123,12 +125,15 @@ struct Piece {
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ void unit_of(const Args &A, int u, Piece &p)
 {
-    p.b = A.RT == 1 ? u : u / A.RT;
-    p.rt = u - p.b * A.RT;
+    const bool one = ROWS == kNarrowRows || A.RT == 1;  // a unit a sequence, whose last row is of the last token
+    p.b = one ? u : u / A.RT;
+    p.rt = one ? 0 : u - p.b * A.RT;
     const int L = min(max(__ldg(A.seq_lens + p.b), 0), A.max_blocks << A.pshift);
-    const int last = A.Tq == 1 ? 0 : (min((p.rt + 1) * ROWS, A.R) - 1) / A.Hq;
-    p.L = L;
-    p.n = max(0, L - A.Tq + last + 1);
+    p.L = p.n = L;
+    if (!one) {
+        const int last = (min((p.rt + 1) * ROWS, A.R) - 1) / A.Hq;
+        p.n = max(0, L - A.Tq + last + 1);
+    }
     p.tiles = (p.n + TOKENS - 1) / TOKENS;
 }
 
@@ -216,7 +221,8 @@ struct Dealer {
             total = all;
             shares = min(A.workers, max(all / kMinShare, 1));
             active = w < shares;
-            const int y0 = active ? static_cast<int>(share_start(w, all, shares)) : 0, y1 = active ? static_cast<int>(share_start(w + 1, all, shares)) : 0;
+            auto start = [&](int s) -> int { return static_cast<int>(static_cast<unsigned>(s) * static_cast<unsigned>(all) / static_cast<unsigned>(shares)); };
+            const int y0 = active ? start(w) : 0, y1 = active ? start(w + 1) : 0;  // all < 2^23 + 2^8, s <= 2^8
             x0 = y0;
             x1 = y1;
             const int src = __ffs(__ballot_sync(0xffffffffu, b <= y0 && y0 < b + m)) - 1;  // the lane of the unit that y0 lies in
@@ -430,13 +436,13 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
 // The end of a block (part of `parts` of worker w) whose pieces are all written: says so to the workers that it shares units
 // with, waits for theirs, and joins its part of them.  The wait is for blocks of the same launch, which all run at once
 // (launch_together), and whose own waits are bounded; its limit, some 30 s, is only reached where one of them has failed.
+// The caller has synchronised the block behind its last writes, so that the release covers them all.
 template <int DL, int ROWS, int THREADS>
 __device__ __forceinline__ void join(const Args &A, const int4 *jobs, int w, int part, int parts, Merge &S)
 {
     constexpr long long kJoinLimit = 60000000000LL;
     if (threadIdx.x == 0) {
         S.give_up = 0;
-        __threadfence();
         for (int i = 0; i < 2; ++i)
             if (jobs[i].y > 1) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(A.done + jobs[i].x) : "memory");
     }
@@ -471,8 +477,6 @@ __device__ __forceinline__ void prefetch_rows(const Args &A, int pos, int blk, b
         l2_prefetch_bulk(A.pool + ((static_cast<int64_t>(blk) << A.pshift) + (pos & (A.P - 1))) * D, 16 * D * 2);
 }
 
-// Rows of a sequence that the narrow kernel takes (one CTA, 64 rows); longer ones go to pairs of CTAs.
-constexpr int kNarrowRows = 64;
 // A launch whose blocks all run at once (they wait for one another before the pieces are joined).
 template <typename... P, typename... V>
 cudaError_t launch_together(void (*kernel)(P...), int blocks, int threads, size_t smem, cudaStream_t st, V... args)
