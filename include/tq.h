@@ -484,10 +484,13 @@ tq_status tq_prefill_attention_latent(tq_handle h, const uint16_t *q, const uint
  * polls one barrier (a tensor-core completion, a page copy, a hand-off between
  * warps) before it gives up, sets TQ_DEVERR_TIMEOUT and winds its CTA down.
  * The default, TQ_DEFAULT_WAIT_LIMIT, is about one second at the maximum
- * clock; no correct run comes near it.  A limit of 0 makes every wait test its
- * barrier once without blocking and give up if it has not completed, so that
- * the error path can be exercised on purpose without any real hang (the waits
- * for work already in flight keep a fixed bound of their own).  Host-only;
+ * clock; no correct run comes near it.  (Where the attention over latent pages
+ * waits for other blocks' pieces, the limit grows in proportion to what the call
+ * has taken so far over that default; a block that gives up there writes zeros.)
+ * A limit of 0 makes every wait test its barrier once without blocking and give
+ * up if it has not completed, so that the error path can be exercised on purpose
+ * without any real hang (the waits for work already in flight keep a fixed bound
+ * of their own).  Host-only;
  * affects later launches of this handle.
  */
 #define TQ_DEFAULT_WAIT_LIMIT 2000000000LL

@@ -31,8 +31,10 @@
 //
 // Warps (one CTA per SM): 8, a thread per row and quarter of the tile's tokens: softmax, P, output; 1 issue of the scores and 1
 // of P.V (in the pair's first CTA, for both); 1 loads of the tiles; 1 loads of Q and over the dead blocks.
-// Every wait is bounded by the handle's wait limit; a timeout sets TQ_DEVERR_TIMEOUT and stops the CTA, whose rows then
-// carry no weight; copies and MMAs in flight finish before the pair ends.
+// Every wait on a barrier in shared memory, and the join's for other workers' pieces, is bounded by the handle's wait limit (see
+// join); a timeout sets TQ_DEVERR_TIMEOUT and stops the CTA, whose rows then carry no weight, or are zeros where the join gave
+// up; copies and MMAs in flight finish before the pair ends.  The barrier over the grid has no limit and needs none: a block
+// arrives at it before it waits for anything but its own threads and its cluster's start, and all blocks run at once.
 #include <climits>
 #include <cmath>
 
@@ -80,7 +82,7 @@ struct Cfg {
     static constexpr uint32_t kOkOff = kMiscOff + 64;           // [8] a bit per 8 tokens of a tile: behind the end, or on a valid page
     static constexpr uint32_t kXOff = kOkOff + 32;              // [kSoft] exchange between the four threads of a row
     static constexpr uint32_t kPlanOff = (kXOff + 4 * kSoft + 15) / 16 * 16;  // scan and plan
-    static constexpr uint32_t kSmem = kPlanOff + 32 + 8 * (kThreads / 32 + 2);
+    static constexpr uint32_t kSmem = kPlanOff + 32 + 8 * (kThreads / 32 + 3);
     static constexpr uint32_t kTmS = 0, kTmO = 256;  // [2] 64 columns; DL / 2 columns
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -105,7 +107,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     volatile uint32_t *okmask = reinterpret_cast<volatile uint32_t *>(smem + C::kOkOff);
     float *xch = reinterpret_cast<float *>(smem + C::kXOff);
     int4 *jobs = reinterpret_cast<int4 *>(smem + C::kPlanOff);
-    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff + 32);  // warps' sums; then the first unit's first cost, and the unit
+    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff + 32);  // warps' sums; then the first unit's first cost, and the unit; when the block began
 
     if (warp == kSoftWarps) umma::tmem_alloc_pair(tmem_slot, 512);
     if (tid == 0) {
@@ -124,6 +126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 1; i < 8; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (rank == 0) A.done[pair] = 0;
+        plan[kThreads / 32 + 2] = clock64();
     }
 
     umma::fence_before_sync();
@@ -575,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (warp == kSoftWarps) umma::tmem_dealloc_pair(tbase, 512);
     grid.barrier_wait(std::move(zeroed));
-    join<DL, kTile, kThreads>(A, jobs, pair, static_cast<int>(rank), 2, *reinterpret_cast<Merge *>(smem));
+    join<DL, kTile, kThreads>(A, jobs, pair, static_cast<int>(rank), 2, plan[kThreads / 32 + 2], *reinterpret_cast<Merge *>(smem));
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }

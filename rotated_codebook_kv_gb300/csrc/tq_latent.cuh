@@ -312,7 +312,6 @@ constexpr int kFewPieces = 16;
 struct Merge {
     float4 part[16][2][32];
     float2 dens[16];  // reference, denominator
-    int give_up;
 };
 template <int DL, int ROWS, int THREADS>
 __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q, int Q, Merge &S)
@@ -433,37 +432,54 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
     }
 }
 
+// Zeros in the rows that merge_unit would have written.
+template <int DL, int ROWS, int THREADS>
+__device__ __forceinline__ void clear_unit(const Args &A, const int4 job, int q, int Q)
+{
+    constexpr int kWarps = THREADS / 32, N = DL / 256;  // stretches of 256 coordinates of a row, a uint4 per lane
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row0 = job.w * ROWS, rows = min(ROWS, A.R - row0);
+    uint4 *out = reinterpret_cast<uint4 *>(A.out + (static_cast<size_t>(job.z) * A.R + row0) * DL) + lane;
+    const bool few = job.y <= kFewPieces;
+    for (int e = few ? (warp * Q + q) * N : q; e < rows * N; e += few ? kWarps * Q * N : Q)
+        if (few || warp == 0)
+            for (int i = 0; i < (few ? N : 1); ++i) out[(e + i) * 32] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // The end of a block (part of `parts` of worker w) whose pieces are all written: says so to the workers that it shares units
 // with, waits for theirs, and joins its part of them.  The wait is for blocks of the same launch, which all run at once
-// (launch_together), and whose own waits are bounded; its limit, some 30 s, is only reached where one of them has failed.
-// The caller has synchronised the block behind its last writes, so that the release covers them all.
+// (launch_together), and whose own waits are bounded.  Shares are equal, so what another block may still need grows with what
+// this one took since `born`: the handle's wait limit, and as much again for each time that the default limit has passed
+// meanwhile.  A block that gives up reports it and writes zeros.  The caller has synchronised the block behind its last
+// writes, so that the release covers them all.
 template <int DL, int ROWS, int THREADS>
-__device__ __forceinline__ void join(const Args &A, const int4 *jobs, int w, int part, int parts, Merge &S)
+__device__ __forceinline__ void join(const Args &A, const int4 *jobs, int w, int part, int parts, long long born, Merge &S)
 {
-    constexpr long long kJoinLimit = 60000000000LL;
-    if (threadIdx.x == 0) {
-        S.give_up = 0;
+    if (threadIdx.x == 0)
         for (int i = 0; i < 2; ++i)
             if (jobs[i].y > 1) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(A.done + jobs[i].x) : "memory");
-    }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const int4 job = jobs[i];
         if (job.y < 2) continue;
+        bool late = false;
         if (threadIdx.x == 0) {
             const long long t0 = clock64();
-            for (int have = 0; have < job.y * parts;) {
+            const float limit = static_cast<float>(A.wait_limit) * (1.f + static_cast<float>(t0 - born) * (1.f / kDefaultWaitLimit));
+            for (;;) {
+                int have;
                 asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(have) : "l"(A.done + job.x) : "memory");
-                if (have < job.y * parts && clock64() - t0 > kJoinLimit) {
-                    S.give_up = 1;
+                if (have >= job.y * parts) break;
+                if (static_cast<float>(clock64() - t0) >= limit) {
+                    late = true;
                     atomicOr(A.status, TQ_DEVERR_TIMEOUT);
                     break;
                 }
             }
         }
-        __syncthreads();
-        if (S.give_up) return;
-        merge_unit<DL, ROWS, THREADS>(A, job, (w - job.x) * parts + part, job.y * parts, S);
+        const int q = (w - job.x) * parts + part, Q = job.y * parts;
+        if (__syncthreads_or(late)) clear_unit<DL, ROWS, THREADS>(A, job, q, Q);
+        else merge_unit<DL, ROWS, THREADS>(A, job, q, Q, S);
     }
 }
 

@@ -59,7 +59,7 @@ struct Cfg {
     static constexpr uint32_t kXOff = (kOkOff + 32 + 15) / 16 * 16;  // [2][64] exchange between the halves of a row
     static constexpr uint32_t kFacOff = kXOff + 4 * 128;       // [64] factors of the rows
     static constexpr uint32_t kPlanOff = kFacOff + 4 * 64;
-    static constexpr uint32_t kSmem = kPlanOff + 32 + 8 * (kThreads / 32 + 2);
+    static constexpr uint32_t kSmem = kPlanOff + 32 + 8 * (kThreads / 32 + 3);
     static constexpr uint32_t kTmS = 0, kTmO = 128;  // [2] 64 columns; [NX] 64 columns
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = misc + 1;  // misc[2]: something not finite was hidden
     volatile uint32_t *okmask = reinterpret_cast<volatile uint32_t *>(smem + C::kOkOff);
     float *xch = reinterpret_cast<float *>(smem + C::kXOff), *fac = reinterpret_cast<float *>(smem + C::kFacOff);
+    int4 *jobs = reinterpret_cast<int4 *>(smem + C::kPlanOff);
+    long long *plan = reinterpret_cast<long long *>(smem + C::kPlanOff + 32);  // see tq_latent.cu
 
     if (warp == kSoftWarps) umma::tmem_alloc(tmem_slot, 512);
     if (tid == 0) {
@@ -114,11 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 1; i < 4; ++i) misc[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         A.done[worker] = 0;
+        plan[kThreads / 32 + 2] = clock64();
     }
     umma::fence_before_sync();
-    int4 *jobs = reinterpret_cast<int4 *>(smem + C::kPlanOff);
     Dealer<kNarrowRows, kTok, kThreads> dealer;
-    Share<kNarrowRows, kTok> share = dealer.deal(A, worker, blockIdx.x == 0, reinterpret_cast<long long *>(smem + C::kPlanOff + 32), jobs);
+    Share<kNarrowRows, kTok> share = dealer.deal(A, worker, blockIdx.x == 0, plan, jobs);
     umma::fence_after_sync();
     const uint32_t tbase = *tmem_slot;
     auto grid = cooperative_groups::this_grid();
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (warp == kSoftWarps) umma::tmem_dealloc(tbase, 512);
     grid.barrier_wait(std::move(zeroed));
-    join<DL, kNarrowRows, kThreads>(A, jobs, worker, 0, 1, *reinterpret_cast<Merge *>(smem));
+    join<DL, kNarrowRows, kThreads>(A, jobs, worker, 0, 1, plan[kThreads / 32 + 2], *reinterpret_cast<Merge *>(smem));
 }
 
 template <int DL>
