@@ -212,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 float top = fmaxf(m0, m1);
                 top = top == -INFINITY ? top : top * c;
-                if (any_of_softmax(bad || top > m_run)) {
+                if (any_of_softmax(bad || top > m_run - kLeast)) {
                     if (any_of_softmax(bad)) {
                         dead = true;
                         break;
@@ -220,9 +220,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     xch[tid] = top;
                     any_of_softmax(false);
                     top = fmaxf(fmaxf(top, xch[tid ^ 64]), fmaxf(xch[tid ^ 128], xch[tid ^ 192]));
-                    const bool need = valid && m_run != -INFINITY && top > m_run;
+                    const bool moves = top > m_run - kLeast, need = valid && m_run != -INFINITY && moves;
                     const float al = need ? fast_exp2(m_run - (top + kMargin)) : 1.f;
-                    if (top > m_run) m_run = top + kMargin;
+                    if (moves) m_run = top + kMargin;
                     if (__any_sync(0xffffffffu, need)) {  // need: there was a tile before
                         bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);  // O is at rest
                         umma::fence_after_sync();

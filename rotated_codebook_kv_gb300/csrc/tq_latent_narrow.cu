@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   max3(s[2 * e + 9], s[2 * e + 12], s[2 * e + 13]), -INFINITY);
                     top[e] = top[e] == -INFINITY ? top[e] : top[e] * c;
                 }
-                if (any_of_softmax(bad || top[0] > m_run[0] || top[1] > m_run[1])) {
+                if (any_of_softmax(bad || top[0] > m_run[0] - kLeast || top[1] > m_run[1] - kLeast)) {
                     if (any_of_softmax(bad)) {
                         dead = true;
                         break;
@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         top[e] = fmaxf(top[e], xch[64 * (g ^ 1) + r0 + 8 * e]);
-                        const bool moves = m_run[e] != -INFINITY && top[e] > m_run[e];
+                        const bool above = top[e] > m_run[e] - kLeast, moves = m_run[e] != -INFINITY && above;
                         const float al = moves ? fast_exp2(m_run[e] - (top[e] + kMargin)) : 1.f;
-                        if (top[e] > m_run[e]) m_run[e] = top[e] + kMargin;
+                        if (above) m_run[e] = top[e] + kMargin;
                         l_run[e] *= al;
                         need |= moves && r0 + 8 * e < A.R;
                         if (g == 0 && (lane & 3) == 0) fac[r0 + 8 * e] = al;

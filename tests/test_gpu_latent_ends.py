@@ -3,9 +3,12 @@ import pytest
 import torch
 
 from rotated_codebook_kv_gb300 import Codec, native
-from test_gpu_latent import DEV, case
+from test_gpu_latent import DEV, case, check, reference, run
 
 pytestmark = pytest.mark.gpu
+
+# the kernel of up to 64 rows a sequence and that of more, one query token and several
+SHAPES = [(512, 4, None), (256, 4, None), (512, 100, None), (256, 100, None), (512, 4, 5), (256, 30, 7)]
 
 
 @pytest.mark.parametrize("dl,Tq", [(512, 64), (256, 64), (512, 128), (256, 128)])
@@ -39,3 +42,31 @@ def test_the_join_waits_no_longer_than_the_wait_limit(dl, Tq):
         assert bool((right | zero).all()) and bool(zero.any())
     own.set_wait_limit(native.TQ_DEFAULT_WAIT_LIMIT)
     assert torch.equal(go()[:-1], ref[:-1]) and own.get_status() == 0
+
+
+def rising(c, rise, first):
+    """Scores (in powers of two) of 0 for the first tokens and of `rise` from token `first` on, latents near bf16's largest."""
+    dl, P = c["dl"], c["P"]
+    c["q"].zero_()
+    c["q"][..., dl] = 1
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for b, n in enumerate(c["lens"].tolist()):
+        for i, blk in enumerate(c["table"][b].tolist()):
+            m = min(P, n - i * P)
+            if m <= 0:
+                break
+            c["pool"][blk, :m, :dl] = torch.where(torch.rand(m, dl, device=DEV, generator=g) < 0.5, 2.9e38, 3.0e38).to(torch.bfloat16)
+            c["pool"][blk, :m, dl:] = 0
+            t = torch.arange(i * P, i * P + m, device=DEV)
+            c["pool"][blk, :m, dl] = torch.where(t < first, 0.0, rise).to(torch.bfloat16)
+    return c
+
+
+@pytest.mark.parametrize("rise", [7.5, 15.875, 16.5, 31.75, 40.0])
+@pytest.mark.parametrize("dl,Hq,Tq", SHAPES)
+def test_values_near_the_largest_under_rising_scores(dl, Hq, Tq, rise):
+    """Later scores above the first ones: sums of probabilities times values stay finite before the division."""
+    c = rising(case(dl, 16, Hq, [700, 9000], Tq=Tq, seed=7), rise, 130)
+    sm = 0.6931471805599453  # a score is a power of two
+    ref, bound = reference(c, sm)
+    check(run(c, sm), ref, bound)
