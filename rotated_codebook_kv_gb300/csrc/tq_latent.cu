@@ -2,7 +2,7 @@
 //
 //   S[r][t] = <q_r, [c_t | r_t]>    r: (query token, head) rows of a sequence, D = DL + 64 coordinates
 //   O[r][j] = sum_t P[r][t] c_t[j]  j < DL
-// with y = sm_scale log2(e) S, P = 2^(y - m) rounded to bf16, the denominator the fp32 sum of the rounded P.
+// with y = sm_scale log2(e) S, P = 2^(y - m) rounded to bf16 (m as kMargin says), the denominator the fp32 sum of the rounded P.
 //
 // All heads read the same rows, so a tile of 128 tokens serves 128 rows: 2 (D + DL) 128 flops against 2 D bytes a token,
 // 242 flop/B at DL = 512.  O is 128 x 512 in fp32, all of an SM's tensor memory; so a pair of CTAs (a cluster of two)
@@ -168,6 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int r = tid & 63, h = (tid >> 6) & 1, g = tid >> 7;
         const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const float c = fabsf(A.sm_scale) * kLog2e;
+        const float slack = kSlack / c;
         const uint32_t flip = A.sm_scale < 0.f ? 0x80000000u : 0u;
         const int *table = nullptr;
         const bool sectors = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0;  // rows begin on 32 bytes
@@ -183,7 +184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             table = A.block_table + static_cast<int64_t>(p.b) * A.max_blocks;
             const int lim0 = max(0, p.L - A.Tq + (A.Tq == 1 ? 0 : p.rt * kTile / A.Hq) + 1);  // tokens that every row sees
             const int lim = A.Tq == 1 || !valid ? p.n : max(0, p.L - A.Tq + row / A.Hq + 1);
-            float m_run = -INFINITY, l_run = 0.f;
+            float m_run = -INFINITY, m_most = -INFINITY, l_run = 0.f;  // reference; what does not move it yet
+            bool far_ref = false;
+            float base = -kMargin;
             const int it0 = it;
             for (int i = p.t0; i < p.t1 && !dead; ++i, ++it) {
                 bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
@@ -211,8 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     m1 = max3(m1, sf[k + 2], sf[k + 3]);
                 }
                 float top = fmaxf(m0, m1);
-                top = top == -INFINITY ? top : top * c;
-                if (any_of_softmax(bad || top > m_run - kLeast)) {
+                if (any_of_softmax(bad || top > m_most)) {
                     if (any_of_softmax(bad)) {
                         dead = true;
                         break;
@@ -220,9 +222,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     xch[tid] = top;
                     any_of_softmax(false);
                     top = fmaxf(fmaxf(top, xch[tid ^ 64]), fmaxf(xch[tid ^ 128], xch[tid ^ 192]));
-                    const bool moves = top > m_run - kLeast, need = valid && m_run != -INFINITY && moves;
-                    const float al = need ? fast_exp2(m_run - (top + kMargin)) : 1.f;
-                    if (moves) m_run = top + kMargin;
+                    const bool moves = top > m_most, need = valid && m_run != -INFINITY && moves;
+                    const float al = need ? fast_exp2((m_run - top) * c) : 1.f;
+                    if (moves) m_run = top, m_most = __fadd_rd(top, slack);
+                    far_ref = __any_sync(0xffffffffu, m_run != -INFINITY && fabsf(m_run) * c > kFar);
+                    base = far_ref || m_run == -INFINITY ? -kMargin : fmaf(-m_run, c, -kMargin);
                     if (__any_sync(0xffffffffu, need)) {  // need: there was a tile before
                         bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);  // O is at rest
                         umma::fence_after_sync();
@@ -242,14 +246,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         l_run *= al;
                     }
                 }
-                const float ref = m_run == -INFINITY ? 0.f : m_run;
-                const uint64_t c2 = pack2(c, c), ref2 = pack2(-ref, -ref);
+                if (far_ref) {
+                    const float ref = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float2 d = unpack2(add2(pack2(sf[k], sf[k + 1]), pack2(-ref, -ref)));
+                        sf[k] = d.x;
+                        sf[k + 1] = d.y;
+                    }
+                }
+                const uint64_t c2 = pack2(c, c), base2 = pack2(base, base);
                 uint64_t sum0 = 0, sum1 = 0;
                 uint32_t w[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    float2 x0 = unpack2(fma2(pack2(sf[k], sf[k + 1]), c2, ref2));
-                    float2 x1 = unpack2(fma2(pack2(sf[k + 2], sf[k + 3]), c2, ref2));
+                    float2 x0 = unpack2(fma2(pack2(sf[k], sf[k + 1]), c2, base2));
+                    float2 x1 = unpack2(fma2(pack2(sf[k + 2], sf[k + 3]), c2, base2));
                     x0.x = fast_exp2(x0.x);
                     x0.y = fast_exp2(x0.y);
                     x1.x = fast_exp2(x1.x);

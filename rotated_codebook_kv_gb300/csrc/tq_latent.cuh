@@ -23,11 +23,14 @@ constexpr int kMaxWorkers = 256;
 constexpr int kNarrowRows = 64;
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
 constexpr float kLog2e = 1.4426950408889634f;
-// The reference m stands kMargin (powers of two) above the running maximum when it is set, and O is rescaled when a score comes
-// nearer to it than kLeast: P is 2^-32 where the maximum was set and 2^-16 at most, so that no sum of 2^16 values, however large
-// each is, overflows before the division.  At the other end O keeps steps of 2^-149, of 2^-117 after the division.  (8 between
-// the two instead of 16: more rescaling, a long prompt's chunk 2.86 -> 2.96 ms.)
-constexpr float kMargin = 32.f, kLeast = 16.f;
+// P = 2^(c (s - r) - kMargin), c = |sm_scale| log2(e), r the largest score when it was set (the reference).  It moves, and O is
+// rescaled, when a score passes it by more than kSlack powers of two: P is 2^-32 at r and 2^-16 at most, so that no sum of 2^16
+// values, however large each is, overflows before the division.  At the other end O keeps steps of 2^-149, of 2^-117 after the
+// division.  (A slack of 8: more rescaling, a long prompt's chunk 2.86 -> 2.96 ms.)
+// c s - (c r + kMargin), one operation, is off by the rounding of c r: 2^-14 at kFar.  Where a reference lies beyond, the
+// difference s - r comes first, so that scores of any size keep P in its range (for every tile: 1.5% of a long chunk; the branch
+// itself 0.4%).
+constexpr float kMargin = 32.f, kSlack = 16.f, kFar = 1024.f;
 
 struct Args {
     const uint16_t *pool;
@@ -336,8 +339,9 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
         reinterpret_cast<uint2 *>(A.out + (static_cast<size_t>(job.z) * A.R + row0 + r) * DL)[j4] =
             make_uint2(bf16x2_of(o.x * inv, o.y * inv), bf16x2_of(o.z * inv, o.w * inv));
     };
-    // 2^(m - M), M the larger of them
-    auto scale_of = [](float m, float M) -> float { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
+    // 2^(c (m - M)), M the larger of two references
+    const float c = fabsf(A.sm_scale) * kLog2e;
+    auto scale_of = [c](float m, float M) -> float { return m == -INFINITY ? 0.f : fast_exp2((m - M) * c); };
     const float4 *acc = reinterpret_cast<const float4 *>(A.acc);
     if (n <= kFewPieces) {
         for (int r = warp * Q + q; r < rows; r += kWarps * Q) {

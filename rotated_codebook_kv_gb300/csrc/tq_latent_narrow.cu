@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3, g = warp >> 2, r0 = 16 * quad + (lane >> 2);
         const uint32_t lane_base = tbase + (static_cast<uint32_t>(32 * quad) << 16);
         const float c = fabsf(A.sm_scale) * kLog2e;
+        const float slack = kSlack / c;
         const bool flip = A.sm_scale < 0.f;
         bool bad = false, dead = false;  // this warp's wait failed; all know
         int it = 0;
@@ -166,13 +167,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto limit = [&](int row) -> int { return A.Tq == 1 || row >= A.R ? p.n : max(0, p.L - A.Tq + row / A.Hq + 1); };
             const int lim0 = limit(0);  // tokens that every row sees
             int lim[2];
-            float m_run[2], l_run[2];
+            float m_run[2], m_most[2], l_run[2];  // reference; what does not move it yet; denominator
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 lim[e] = limit(r0 + 8 * e);
-                m_run[e] = -INFINITY;
+                m_run[e] = m_most[e] = -INFINITY;
                 l_run[e] = 0.f;
             }
+            bool far_ref = false;
+            float shift[2] = {-kMargin, -kMargin};
             const int it0 = it;
             for (int i = p.t0; i < p.t1 && !dead; ++i, ++it) {
                 bad |= !wait_bar(C::bSFull + (it & 1), (it >> 1) & 1);
@@ -201,9 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 2; ++e) {
                     top[e] = max3(max3(max3(s[2 * e], s[2 * e + 1], s[2 * e + 4]), s[2 * e + 5], s[2 * e + 8]),
                                   max3(s[2 * e + 9], s[2 * e + 12], s[2 * e + 13]), -INFINITY);
-                    top[e] = top[e] == -INFINITY ? top[e] : top[e] * c;
                 }
-                if (any_of_softmax(bad || top[0] > m_run[0] - kLeast || top[1] > m_run[1] - kLeast)) {
+                if (any_of_softmax(bad || top[0] > m_most[0] || top[1] > m_most[1])) {
                     if (any_of_softmax(bad)) {
                         dead = true;
                         break;
@@ -219,13 +221,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         top[e] = fmaxf(top[e], xch[64 * (g ^ 1) + r0 + 8 * e]);
-                        const bool above = top[e] > m_run[e] - kLeast, moves = m_run[e] != -INFINITY && above;
-                        const float al = moves ? fast_exp2(m_run[e] - (top[e] + kMargin)) : 1.f;
-                        if (above) m_run[e] = top[e] + kMargin;
+                        const bool above = top[e] > m_most[e], moves = m_run[e] != -INFINITY && above;
+                        const float al = moves ? fast_exp2((m_run[e] - top[e]) * c) : 1.f;
+                        if (above) m_run[e] = top[e], m_most[e] = __fadd_rd(top[e], slack);
                         l_run[e] *= al;
                         need |= moves && r0 + 8 * e < A.R;
                         if (g == 0 && (lane & 3) == 0) fac[r0 + 8 * e] = al;
                     }
+                    far_ref = __any_sync(0xffffffffu, (m_run[0] != -INFINITY && fabsf(m_run[0]) * c > kFar) ||
+                                                          (m_run[1] != -INFINITY && fabsf(m_run[1]) * c > kFar));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) shift[e] = far_ref || m_run[e] == -INFINITY ? -kMargin : fmaf(-m_run[e], c, -kMargin);
                     if (any_of_softmax(need)) {  // there was a tile before
                         bad |= !wait_bar(C::bPvDone + (it - 1) % NS, ((it - 1) / NS) & 1);  // O is at rest
                         umma::fence_after_sync();
@@ -246,15 +252,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const uint32_t st = sbase + C::kKOff + (it % NS) * C::kStage;
-                float ref[2];
+                if (__builtin_expect(far_ref, 0)) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) ref[e] = m_run[e] == -INFINITY ? 0.f : m_run[e];
+                    for (int k = 0; k < 16; ++k) s[k] -= m_run[k >> 1 & 1] == -INFINITY ? 0.f : m_run[k >> 1 & 1];
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int k = 4 * j + 2 * e;
-                        uint32_t w = bf16x2_of(fast_exp2(fmaf(s[k], c, -ref[e])), fast_exp2(fmaf(s[k + 1], c, -ref[e])));
+                        uint32_t w = bf16x2_of(fast_exp2(fmaf(s[k], c, shift[e])), fast_exp2(fmaf(s[k + 1], c, shift[e])));
                         if (!whole) {  // hidden: zero also where c is 0 or the reference infinite
                             if (hidden(k)) w &= 0xffff0000u;
                             if (hidden(k + 1)) w &= 0x0000ffffu;

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from rotated_codebook_kv_gb300 import Codec, native
-from test_gpu_latent import DEV, case, check, reference, run
+from test_gpu_latent import DEV, case, check, codec, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,42 @@ def test_values_near_the_largest_under_rising_scores(dl, Hq, Tq, rise):
     sm = 0.6931471805599453  # a score is a power of two
     ref, bound = reference(c, sm)
     check(run(c, sm), ref, bound)
+
+
+def onehot(c, q, lo):
+    """Queries of one coordinate each, of size q and both signs; latents from size lo on, so that scores are single products."""
+    dl = c["dl"]
+    g = torch.Generator(device=DEV).manual_seed(2)
+    flat = c["q"].view(-1, dl + 64)
+    flat.zero_()
+    j = torch.randint(0, dl + 64, (flat.shape[0],), generator=g, device=DEV)
+    s = torch.randint(0, 2, (flat.shape[0],), generator=g, device=DEV) * 2.0 - 1
+    flat[torch.arange(flat.shape[0], device=DEV), j] = (s * q).to(torch.bfloat16)
+    x = torch.randn(c["pool"].shape, device=DEV, generator=g)
+    c["pool"].copy_(torch.where(torch.isfinite(c["pool"]), x * lo, c["pool"].float()))
+    return c
+
+
+@pytest.mark.parametrize("sm", [0.07, -0.07])
+@pytest.mark.parametrize("power", [22, 26, 30, 33, 40, 80])
+@pytest.mark.parametrize("dl,Hq,Tq", SHAPES)
+def test_scores_of_any_size(dl, Hq, Tq, power, sm):
+    """Scores of up to 2^82 times the scale, each a single product: the token with the largest takes all, ties share."""
+    c = onehot(case(dl, 16, Hq, [40, 700, 5000], Tq=Tq, seed=9), 2.0 ** (power // 2), 2.0 ** (power - power // 2))
+    out = run(c, sm).double()
+    q4 = c["q"].view(3, -1, Hq, dl + 64).double()
+    o4 = out.view(3, -1, Hq, dl)
+    tq = q4.shape[1]
+    for b, L in enumerate(c["lens"].tolist()):
+        k = c["pool"][c["table"][b, : -(-L // 16)].long()].double().flatten(0, 1)[:L]
+        for i in range(tq):
+            n = L - tq + 1 + i
+            x = (q4[b, i] @ k[:n].T) * sm
+            w = torch.softmax(x, -1)
+            top2 = x.topk(2, -1).values
+            sure = (top2[:, 0] - top2[:, 1] > 64) | (top2[:, 0] == top2[:, 1])  # what is between 0 and 64 keeps some weight
+            ref = w @ k[:n, :dl]
+            assert int(sure.sum()) > 0
+            tol = 2.0 ** -8 * ref.abs() + 2.0 ** -20 * k[:n, :dl].abs().amax(0)
+            assert bool(((o4[b, i] - ref).abs() <= tol)[sure].all())
+    assert bool(torch.isfinite(out).all()) and codec().get_status() == 0
