@@ -386,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL + (2 * h + g) * (DL / 4));
                     for (int k = 0; k < DL / 32; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
                 } else if (valid && tid < 64) {
-                    A.ml[slot] = make_float2(-INFINITY, 0.f);
+                    A.ml[slot] = make_float2(-INFINITY, kNothing);
                 }
             }
             if (p.tiles) ++sg;

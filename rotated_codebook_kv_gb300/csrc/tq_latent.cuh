@@ -42,7 +42,7 @@ struct Args {
     int workers;           // pairs of CTAs, or CTAs
     float sm_scale;
     int *done;             // [workers] blocks that have written their pieces of the unit whose first piece is this worker's
-    float2 *ml;            // [2 workers][rows of a unit] reference, denominator
+    float2 *ml;            // [2 workers][rows of a unit] reference, denominator (kNothing: the piece has no sums)
     float *acc;            // [2 workers][rows of a unit][DL]
     uint16_t *out;
     unsigned *status;
@@ -312,7 +312,9 @@ struct Dealer {
 // Joins the pieces of a unit that several workers shared, by all of their blocks (block q of Q), once every piece is there: a warp
 // per row where the pieces are few, a block per 256 coordinates of a row (a stretch of the pieces a warp) where they are many.
 // A kernel of its own for it, launched as the attention's blocks ended, took 5-10 us longer, and a barrier over the grid 3-8.
+// A piece whose scores are all -inf has the denominator 0 and counts all the same: its sums hold 0 times what is infinite.
 constexpr int kFewPieces = 16;
+constexpr float kNothing = -1.f;
 struct Merge {
     float4 part[16][2][32];
     float2 dens[16];  // reference, denominator
@@ -352,7 +354,7 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
                 float4 v[K][N];
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    ml[k] = make_float2(-INFINITY, 0.f);
+                    ml[k] = make_float2(-INFINITY, kNothing);
                     if (k0 + k < n) {
                         ml[k] = __ldcg(A.ml + slot(k0 + k, r));
 #pragma unroll
@@ -368,7 +370,7 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
                 for (int i = 0; i < N; ++i) o[i] = make_float4(al * o[i].x, al * o[i].y, al * o[i].z, al * o[i].w);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    if (ml[k].y == 0.f) continue;  // no piece, or one without weight (nothing written)
+                    if (ml[k].y == kNothing) continue;
                     const float a = scale_of(ml[k].x, m);
                     den = fmaf(a, ml[k].y, den);
 #pragma unroll
@@ -391,7 +393,7 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
                 const int k = k0 + j * kWarps;
-                ml[j] = make_float2(-INFINITY, 0.f);
+                ml[j] = make_float2(-INFINITY, kNothing);
                 if (k < n) {
                     ml[j] = __ldcg(A.ml + slot(k, r));
 #pragma unroll
@@ -407,7 +409,7 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
             for (int i = 0; i < 2; ++i) o[i] = make_float4(al * o[i].x, al * o[i].y, al * o[i].z, al * o[i].w);
 #pragma unroll
             for (int j = 0; j < kDeep; ++j) {
-                if (ml[j].y == 0.f) continue;
+                if (ml[j].y == kNothing) continue;
                 const float a = scale_of(ml[j].x, m);
                 den = fmaf(a, ml[j].y, den);
 #pragma unroll
@@ -427,7 +429,6 @@ __device__ __forceinline__ void merge_unit(const Args &A, const int4 job, int q,
             den = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                if (S.dens[w].y == 0.f) continue;
                 const float a = scale_of(S.dens[w].x, M);
                 den = fmaf(a, S.dens[w].y, den);
                 add(t, a, S.part[w][warp][lane]);

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 *dst = reinterpret_cast<uint4 *>(A.out + at * DL);
                     for (int k = tid; k < A.R * (DL / 8); k += kSoft) dst[k] = make_uint4(0u, 0u, 0u, 0u);
                 } else if (tid < A.R) {
-                    A.ml[slot + tid] = make_float2(-INFINITY, 0.f);
+                    A.ml[slot + tid] = make_float2(-INFINITY, kNothing);
                 }
             }
         }

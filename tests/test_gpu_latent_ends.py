@@ -109,3 +109,23 @@ def test_scores_of_any_size(dl, Hq, Tq, power, sm):
             tol = 2.0 ** -8 * ref.abs() + 2.0 ** -20 * k[:n, :dl].abs().amax(0)
             assert bool(((o4[b, i] - ref).abs() <= tol)[sure].all())
     assert bool(torch.isfinite(out).all()) and codec().get_status() == 0
+
+
+@pytest.mark.parametrize("dl,Hq,Tq", SHAPES)
+def test_tokens_of_an_infinite_negative_score_across_pieces(dl, Hq, Tq):
+    """An infinite coordinate whose score is -inf has no weight, and the coordinate itself is 0 times infinity, however the
+    sequence is cut."""
+    n, j = 6000, 9
+    for first in (0, 64, 128, 192, 256, 320, 384, 448, 512, 640, 768, 1024, 5990):
+        c = case(dl, 16, Hq, [n], Tq=Tq, seed=15)
+        c["q"][..., j] = c["q"][..., j].abs() + 0.5
+        ok = torch.ones(1, n, dtype=torch.bool, device=DEV)
+        ok[0, first:] = False
+        ref, bound = reference(c, ok=ok)
+        t = torch.arange(first, n, device=DEV)
+        c["pool"][c["table"][0, t // 16].long(), t % 16, j] = float("-inf")
+        out = run(c)
+        seen = out if Tq is None else out[:, max(0, Tq - (n - first)):]
+        assert bool(torch.isnan(seen[..., j]).all()), first
+        rest = torch.arange(dl, device=DEV) != j
+        check(out[..., rest], ref[..., rest], bound[..., rest])
