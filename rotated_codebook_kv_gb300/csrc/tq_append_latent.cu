@@ -258,11 +258,15 @@ extern "C" tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const
         !aligned(q_out, 16) || !aligned(rope, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 8))
         return api_error(TQ_ERR_INVALID_ARG, "%s: misaligned pointer", who);
     const int r = TQ_LATENT_ROPE_DIM;
-    const int64_t most = int64_t(1) << 40;  // no offset passes 64 bits
+    const int64_t most = int64_t(1) << 40;
     auto bad = [&](int64_t s, int64_t least) { return s < least || s > most || s % 8; };
     if (bad(latent_stride, latent_dim) || bad(k_stride, r) ||
         (q && (bad(q_stride_tok, r) || bad(q_stride_head, r) || bad(qo_stride_tok, r) || bad(qo_stride_head, r))))
         return api_error(TQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, no less than a row", who);
+    // no offset passes 2^60 elements: T - 1 tokens of a stride up to 2^59, and fewer than 2^18 heads of a stride up to 2^40
+    const int64_t widest = T > 1 ? (int64_t(1) << 59) / (T - 1) : most;
+    if (latent_stride > widest || k_stride > widest || (q && (q_stride_tok > widest || qo_stride_tok > widest)))
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: rows too far apart", who);
     if (q && T > 1 && num_q_heads > 1 && qo_stride_tok < (num_q_heads - 1) * qo_stride_head + r && qo_stride_head < (T - 1) * qo_stride_tok + r)
         return api_error(TQ_ERR_INVALID_ARG, "%s: rows of q_out overlap", who);
     const tq::Codec &c = tq::handle_codec(h);

@@ -129,3 +129,17 @@ def test_tokens_of_an_infinite_negative_score_across_pieces(dl, Hq, Tq):
         assert bool(torch.isnan(seen[..., j]).all()), first
         rest = torch.arange(dl, device=DEV) != j
         check(out[..., rest], ref[..., rest], bound[..., rest])
+
+
+def refused(status, word, T=4, Hq=2, ls=320, ks=320, qs=128, qh=64, q=1 << 20, o=1 << 21, os=128, oh=64):
+    """An append that is refused before anything is launched; its pointers lead nowhere."""
+    at = 1 << 22
+    with pytest.raises(native.TQError, match=word) as e:
+        native.tq_append_latent(codec().handle, at, at, q, T, 256, Hq, ls, ks, qs, qh, 0, 0.0, 0, 0, 0, 0, at, at, 16, 2, o, os, oh, 0)
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("T,stride", [((1 << 29) + 1, 1 << 35), ((1 << 29) + 1, 1 << 34), ((1 << 30) - 1, 1 << 40), ((1 << 20) + 1, 1 << 40)])
+@pytest.mark.parametrize("which", ["ls", "ks", "qs", "os"])
+def test_append_of_rows_whose_offsets_pass_64_bits_is_refused(T, stride, which):
+    refused(native.TQ_ERR_UNSUPPORTED, "too far apart", T=T, **{which: stride})
