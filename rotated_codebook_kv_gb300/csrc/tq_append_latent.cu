@@ -269,6 +269,9 @@ extern "C" tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const
         return api_error(TQ_ERR_UNSUPPORTED, "%s: rows too far apart", who);
     if (q && T > 1 && num_q_heads > 1 && qo_stride_tok < (num_q_heads - 1) * qo_stride_head + r && qo_stride_head < (T - 1) * qo_stride_tok + r)
         return api_error(TQ_ERR_INVALID_ARG, "%s: rows of q_out overlap", who);
+    // in place: a thread rewrites what it has read itself, not what another one is still to read
+    if (q && q_out == q && ((T > 1 && qo_stride_tok != q_stride_tok) || (num_q_heads > 1 && qo_stride_head != q_stride_head)))
+        return api_error(TQ_ERR_INVALID_ARG, "%s: q_out is q with other strides", who);
     const tq::Codec &c = tq::handle_codec(h);
     const tq::LatentArgs a{latent, k_rope, q, T, num_q_heads, latent_stride, k_stride, q_stride_tok, q_stride_head, qo_stride_tok,
                            qo_stride_head, norm_weight, norm_eps, positions, rope, rope_rows, style == TQ_ROPE_INTERLEAVED,

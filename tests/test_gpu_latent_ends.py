@@ -143,3 +143,21 @@ def refused(status, word, T=4, Hq=2, ls=320, ks=320, qs=128, qh=64, q=1 << 20, o
 @pytest.mark.parametrize("which", ["ls", "ks", "qs", "os"])
 def test_append_of_rows_whose_offsets_pass_64_bits_is_refused(T, stride, which):
     refused(native.TQ_ERR_UNSUPPORTED, "too far apart", T=T, **{which: stride})
+
+
+def test_outputs_over_the_queries_with_other_strides_are_refused():
+    k = codec()
+    T, Hq = 6, 4
+    x, pool, slots = torch.randn(T, 320, device=DEV).bfloat16(), k.alloc_pool_latent(1, 16, 256), torch.arange(T, device=DEV)
+    room = torch.randn(2 * T * Hq * 64, device=DEV).bfloat16()
+    q = room[: T * Hq * 64].view(T, Hq, 64)
+
+    def call(q, q_out):
+        return k.append_latent(x[: q.shape[0], :256], x[: q.shape[0], 256:], slots[: q.shape[0]], pool, 16, 1, q=q, q_out=q_out)
+
+    for st, sh in ((64, 64 * T), (64 * Hq * 2, 64), (64 * Hq + 8, 64)):
+        with pytest.raises(native.TQError, match="strides"):
+            call(q, torch.as_strided(room, (T, Hq, 64), (st, sh, 1)))
+    for a, b in ((q[:1], torch.as_strided(room, (1, Hq, 64), (64 * 99, 64, 1))), (q[:, :1], torch.as_strided(room, (T, 1, 64), (64 * Hq, 64 * 99, 1))), (q, q)):
+        want = a.clone()
+        assert torch.equal(call(a, b), want)
