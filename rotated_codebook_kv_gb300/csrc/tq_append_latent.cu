@@ -149,7 +149,23 @@ __device__ __forceinline__ void pool_row(const LatentArgs &A, int64_t t, int lan
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum = fmaf(x[i][k], x[i][k], sum);
         }
-        const float inv = 1.f / sqrtf(warp_sum(sum) * (1.f / DL) + A.eps);
+        float total = warp_sum(sum), eps = A.eps;
+        // Squares past fp32's range, or in its lowest part with no eps above them: the same with c times a power of two (all
+        // lanes agree).
+        const float s = !(total < INFINITY) ? 0x1p-80f : total < 0x1p-100f && eps < 0x1p-80f ? 0x1p100f : 1.f;
+        if (s != 1.f) {
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    x[i][k] *= s;
+                    sum = fmaf(x[i][k], x[i][k], sum);
+                }
+            total = warp_sum(sum);
+            eps = eps * s * s;
+        }
+        const float inv = 1.f / sqrtf(total * (1.f / DL) + eps);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float y[8];

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import latent as R
 from rotated_codebook_kv_gb300 import Codec, native
 from test_gpu_latent import DEV, case, check, codec, reference, run
 
@@ -161,3 +162,21 @@ def test_outputs_over_the_queries_with_other_strides_are_refused():
     for a, b in ((q[:1], torch.as_strided(room, (1, Hq, 64), (64 * 99, 64, 1))), (q[:, :1], torch.as_strided(room, (T, 1, 64), (64 * Hq, 64 * 99, 1))), (q, q)):
         want = a.clone()
         assert torch.equal(call(a, b), want)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("power", [-120, -100, -70, -40, 58, 64, 100, 124])
+@pytest.mark.parametrize("dl", [256, 512])
+def test_norm_of_latents_of_any_size(dl, power, eps):
+    k = codec()
+    g = torch.Generator().manual_seed(dl)
+    x = (torch.randn(9, dl, generator=g).clamp(-4, 4) * 2.0 ** power).to(torch.bfloat16)
+    x[3] = 0
+    x[3, 7] = 2.0 ** power
+    w = (torch.randn(dl, generator=g).abs() + 0.5).to(torch.bfloat16)
+    key = torch.zeros(9, 64, dtype=torch.bfloat16, device=DEV)
+    pool = k.alloc_pool_latent(1, 16, dl)
+    k.append_latent(x.to(DEV), key, torch.arange(9, device=DEV), pool, 16, 1, norm_weight=w.to(DEV), norm_eps=eps)
+    y = R.norm(x, w, eps if eps == 0 else float(torch.tensor(eps, dtype=torch.float32)))
+    got = pool[0, :9, :dl].cpu().double()
+    assert bool(((got - y).abs() <= R.norm_bound(y, dl)).all())
