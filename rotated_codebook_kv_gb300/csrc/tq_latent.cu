@@ -647,6 +647,11 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     const size_t need = workspace_bytes(dl, pairs);
     if (ws_bytes < need || !workspace)
         return api_error(TQ_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace ? ws_bytes : 0, need);
+    // the runtime keeps an error until it is asked for: left there, the library's next launch would report it as its own
+    auto failed = [who](const char *what, cudaError_t e) -> tq_status {
+        cudaGetLastError();
+        return api_error(TQ_ERR_CUDA, "%s: %s: %s", who, what, cudaGetErrorString(e));
+    };
     CUtensorMap tk, tv, tq;
     cudaError_t e = cudaSuccess;
     const int d = dl + kRope;
@@ -654,7 +659,7 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     if (!encode_row_blocks_map(&tk, pool, d, num_blocks * P, 8, group, &e) ||
         (!narrow && !encode_row_blocks_map(&tv, pool, d, num_blocks * P, 8, dl / 128, &e)) ||
         !encode_row_blocks_map(&tq, q, d, rows * batch, kHalf, d / 64, &e))
-        return api_error(TQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled: %s", who, cudaGetErrorString(e));
+        return failed("cuTensorMapEncodeTiled", e);
     a.pool = pool;
     a.block_table = block_table;
     a.seq_lens = seq_lens;
@@ -678,7 +683,7 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (narrow) e = launch_narrow(tk, tq, dl, a, st);
     else e = dl == 512 ? launch<512>(tk, tv, tq, a, st) : launch<256>(tk, tv, tq, a, st);
-    if (e != cudaSuccess) return api_error(TQ_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+    if (e != cudaSuccess) return failed("launch", e);
     return TQ_OK;
 }
 

@@ -1,4 +1,6 @@
 """Latent pages at the ends of their ranges, on both of the attention's kernels."""
+import ctypes
+
 import pytest
 import torch
 
@@ -180,3 +182,27 @@ def test_norm_of_latents_of_any_size(dl, power, eps):
     y = R.norm(x, w, eps if eps == 0 else float(torch.tensor(eps, dtype=torch.float32)))
     got = pool[0, :9, :dl].cpu().double()
     assert bool(((got - y).abs() <= R.norm_bound(y, dl)).all())
+
+
+@pytest.mark.parametrize("Hq", [4, 100])
+def test_a_launch_that_fails_fails_alone(Hq):
+    """A launch into a capture that has become invalid is refused by the runtime; the next call does not report it again."""
+    c = case(512, 16, Hq, [100], seed=1)
+    ref = run(c)
+    k = codec()
+    ws, out = k.workspace_latent(1, 1, Hq, 512), torch.zeros_like(ref)
+    x, slots, pool = torch.randn(3, 576, device=DEV).bfloat16(), torch.arange(3, device=DEV), k.alloc_pool_latent(1, 16, 512)
+    cuda, s = ctypes.CDLL("libcuda.so.1"), torch.cuda.Stream()
+    at = ctypes.c_void_p(s.cuda_stream)
+    torch.cuda.synchronize()
+    assert cuda.cuStreamBeginCapture_v2(at, 2) == 0  # relaxed
+    assert cuda.cuStreamSynchronize(at) != 0         # not allowed: the capture is invalid from here on
+    with pytest.raises(native.TQError) as e:
+        native.tq_decode_attention_latent(k.handle, c["q"].data_ptr(), c["pool"].data_ptr(), c["table"].data_ptr(), c["lens"].data_ptr(), 1, Hq,
+                                          512, 16, c["table"].shape[1], c["nb"], 0.07, ws.data_ptr(), ws.numel(), out.data_ptr(), s.cuda_stream)
+    assert e.value.status == native.TQ_ERR_CUDA
+    graph = ctypes.c_void_p()
+    assert cuda.cuStreamEndCapture(at, ctypes.byref(graph)) != 0 and not graph.value
+    k.append_latent(x[:, :512], x[:, 512:], slots, pool, 16, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(pool[0, :3], x) and torch.equal(run(c), ref) and torch.all(out == 0)
