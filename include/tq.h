@@ -460,8 +460,7 @@ tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const uint16_t *
  *   the GPU, from the lengths of all sequences, so results depend on the batch, within rounding.
  * out overlaps no input and not the workspace.
  * One cooperative launch: its blocks, one per SM, wait for the pieces of one another, so that it
- *   starts when all SMs are free of other launches' blocks; TQ_ERR_CUDA where they cannot
- *   all run at once (a context that is limited to some of the SMs).
+ *   starts when all SMs that the stream's context may use are free of other launches' blocks.
  *
  * tq_prefill_attention_latent -- the last q_tokens positions of every sequence attend
  * causally to its latent pages, their own rows included (tq_prefill_attention's contract).

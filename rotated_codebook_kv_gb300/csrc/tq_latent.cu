@@ -607,9 +607,7 @@ size_t workspace_bytes(int dl, int pairs)
 template <int DL>
 cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq, const Args &a, cudaStream_t st)
 {
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_kernel<DL>), Cfg<DL>::kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_together(latent_kernel<DL>, 2 * a.workers, kThreads, Cfg<DL>::kSmem, st, tk, tv, tq, a);
+    return launch_together(latent_kernel<DL>, 2, kThreads, Cfg<DL>::kSmem, st, a, tk, tv, tq);
 }
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -644,6 +642,7 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     if (pairs < 1) return api_error(TQ_ERR_UNSUPPORTED, "%s: no pair of SMs", who);
     const bool narrow = rows <= kNarrowRows;
     a.workers = narrow ? 2 * pairs : pairs;
+    a.least_workers = static_cast<int>(units * (tiles + kUnitCost) / (3 << 29)) + 1;
     const size_t need = workspace_bytes(dl, pairs);
     if (ws_bytes < need || !workspace)
         return api_error(TQ_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace ? ws_bytes : 0, need);

@@ -40,6 +40,7 @@ struct Args {
     bool few;              // a warp's lanes are enough to count the units
     int64_t num_blocks;
     int workers;           // pairs of CTAs, or CTAs
+    int least_workers;     // a share's costs could pass 1.5 x 2^30 with fewer
     float sm_scale;
     int *done;             // [workers] blocks that have written their pieces of the unit whose first piece is this worker's
     float2 *ml;            // [2 workers][rows of a unit] reference, denominator (kNothing: the piece has no sums)
@@ -499,21 +500,35 @@ __device__ __forceinline__ void prefetch_rows(const Args &A, int pos, int blk, b
         l2_prefetch_bulk(A.pool + ((static_cast<int64_t>(blk) << A.pshift) + (pos & (A.P - 1))) * D, 16 * D * 2);
 }
 
-// A launch whose blocks all run at once (they wait for one another before the pieces are joined).
+// Launches `workers` workers of `size` blocks (a cluster), or as many as fit on the SMs that the stream may use where those are
+// fewer (a limited context): they all run at once, for they wait for one another before the pieces are joined.  The query takes
+// 0.15 us.
 template <typename... P, typename... V>
-cudaError_t launch_together(void (*kernel)(P...), int blocks, int threads, size_t smem, cudaStream_t st, V... args)
+cudaError_t launch_together(void (*kernel)(P...), int size, int threads, size_t smem, cudaStream_t st, Args a, V... maps)
 {
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kernel), smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeCooperative;
-    attr.val.cooperative = 1;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(size);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = dim3(size * a.workers);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    int fit = 0;
+    e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (fit < a.least_workers) return cudaErrorCooperativeLaunchTooLarge;
+    if (fit < a.workers) a.workers = fit;
+    cfg.gridDim = dim3(size * a.workers);
+    attr = {};
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps..., a);
 }
 
 // The narrow kernel's launch, in its own translation unit; tk: boxes of a group's blocks (narrow_group), tq: 64 rows.

@@ -525,9 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DL>
 cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tq, const Args &a, cudaStream_t st)
 {
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(latent_narrow_kernel<DL>), Cfg<DL>::kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_together(latent_narrow_kernel<DL>, a.workers, kThreads, Cfg<DL>::kSmem, st, tk, tq, a);
+    return launch_together(latent_narrow_kernel<DL>, 1, kThreads, Cfg<DL>::kSmem, st, a, tk, tq);
 }
 
 }  // namespace

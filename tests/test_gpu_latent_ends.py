@@ -206,3 +206,36 @@ def test_a_launch_that_fails_fails_alone(Hq):
     k.append_latent(x[:, :512], x[:, 512:], slots, pool, 16, 1)
     torch.cuda.synchronize()
     assert torch.equal(pool[0, :3], x) and torch.equal(run(c), ref) and torch.all(out == 0)
+
+
+@pytest.fixture
+def limited_stream():
+    """A stream of a context that may use some 16 SMs."""
+    cuda = ctypes.CDLL("libcuda.so.1")
+    torch.zeros(1, device=DEV)
+    SM, everything, part, rest = 1, *(ctypes.create_string_buffer(512) for _ in range(3))
+    count, desc, ctx, stream = ctypes.c_uint(1), ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_void_p()
+    for call in (lambda: cuda.cuDeviceGetDevResource(0, everything, SM),
+                 lambda: cuda.cuDevSmResourceSplitByCount(part, ctypes.byref(count), everything, rest, 0, 16),
+                 lambda: cuda.cuDevResourceGenerateDesc(ctypes.byref(desc), part, 1),
+                 lambda: cuda.cuGreenCtxCreate(ctypes.byref(ctx), desc, 0, 1),
+                 lambda: cuda.cuGreenCtxStreamCreate(ctypes.byref(stream), ctx, 1, 0)):
+        if call() != 0:
+            pytest.skip("no contexts of some of the SMs here")
+    yield stream.value
+    torch.cuda.synchronize()
+    assert cuda.cuStreamDestroy_v2(stream) == 0 and cuda.cuGreenCtxDestroy(ctx) == 0
+
+
+@pytest.mark.parametrize("dl,Hq,Tq", SHAPES)
+def test_on_some_of_the_sms(limited_stream, dl, Hq, Tq):
+    for lens in ([9], [3000, 1, 0, 777], [100] * 40):
+        c = case(dl, 16, Hq, lens, Tq=Tq, seed=3)
+        ref, bound = reference(c)
+        whole = run(c)
+        ws, out = codec().workspace_latent(len(lens), Tq or 1, Hq, dl), torch.full_like(whole, 7.0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            run(c, workspace=ws, out=out, stream=limited_stream)
+        check(out, ref, bound)
+    assert codec().get_status() == 0
