@@ -455,9 +455,10 @@ tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const uint16_t *
  * Scores are exact bf16 products summed in fp32; the probabilities enter the value product
  * rounded to bf16 (off by 2^-8 of themselves at most) and the denominator sums what
  * enters; sums are fp32.
- * workspace: ws_bytes >= tq_workspace_bytes_latent(...), 256-byte aligned; its contents after
- *   the call are not specified, and calls that may overlap need one each.  Work is cut on
- *   the GPU, from the lengths of all sequences, so results depend on the batch, within rounding.
+ * workspace: ws_bytes >= tq_workspace_bytes_latent(...), 256-byte aligned (on 152 SMs 20 MB for
+ *   latent_dim 256, 40 for 512, whatever the other sizes); its contents after the call are not
+ *   specified, and calls that may overlap need one each.  Work is cut on the GPU, from the
+ *   lengths of all sequences, so results depend on the batch, within rounding.
  * out overlaps no input and not the workspace.
  * One cooperative launch: its blocks, one per SM, wait for the pieces of one another, so that it
  *   starts when all SMs that the stream's context may use are free of other launches' blocks.

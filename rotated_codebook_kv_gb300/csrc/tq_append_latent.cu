@@ -6,8 +6,8 @@
 //
 // Bound: HBM, in one pass.  Blocks for the pool rows (a warp each), then blocks for the query heads; everything that does not
 // depend on a token's slot and position is loaded with them.  Measured (a call in a graph): 8192 tokens of 128 heads, DL = 512:
-// 52 us, 5.6 TB/s (82% of the measured copy rate; a block a token, its row first: 66); 4,687 ragged tokens of 20 heads at
-// DL = 256: 7.3 us; 8 tokens of 64 heads: 2.9 us, which is the launch and three latencies (slot, cosines, store).
+// 53 us, 5.5 TB/s (80% of the measured copy rate; a block a token, its row first: 66); 4,687 ragged tokens of 20 heads at
+// DL = 256: 8.9 us; 8 tokens of 64 heads: 2.7 us, which is the launch and three latencies (slot, cosines, store).
 #include <cmath>
 #include <cuda_runtime.h>
 

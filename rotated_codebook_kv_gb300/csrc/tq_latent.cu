@@ -22,10 +22,14 @@
 // P.V goes through the tokens, and at the middle hands back the blocks and the half of P that only the first 64 of them use (with
 // all at the end 571 instead of 551 us in the second case below).
 //
-// Measured (a call in a graph): 1024 tokens behind 15k of 128 heads, DL = 512: 2.82 ms, 1.61 PFLOP/s, 84% of the measured bf16
-// rate; 256 tokens of 4 sequences of 2k to 8k, 64 heads: 551 us, 1.56 PFLOP/s.  A tile's products take ~2180 cycles of the tensor
+// P is one bf16 term: a second one for its remainder would be a second value product, half of a tile's tensor work again, and its
+// buffers have no room beside the stages.  It adds 4 to 9% to the error that the output's own rounding leaves (16% for a few
+// hundred tokens).
+//
+// Measured (a call in a graph): 1024 tokens behind 15k of 128 heads, DL = 512: 2.85 ms, 1.59 PFLOP/s, 83% of the measured bf16
+// rate; 256 tokens of 4 sequences of 2k to 8k, 64 heads: 552 us, 1.55 PFLOP/s.  A tile's products take ~2180 cycles of the tensor
 // pipe, but read 2875 cycles' worth of shared memory: that bounds a tile, ~3050 cycles.  Decode of 8 x 32k tokens of 128 heads:
-// 73 us, 4.2 TB/s; 4 tokens of 24 sequences of 1k to 9k, 32 heads: 50 us; there start (~7 us to the first scores), the chain load
+// 74.5 us, 4.1 TB/s; 4 tokens of 24 sequences of 1k to 9k, 32 heads: 51 us; there start (~7 us to the first scores), the chain load
 // - scores - softmax - P.V through two stages, and the join take what is above HBM's time.  At DL = 256 the softmax warps bound a
 // tile: ~1900 cycles against 1150 of the products.
 //

@@ -10,9 +10,10 @@
 // Few rows leave a tile bound by HBM: 64 x D x 2 bytes at an SM's share take ~3000 cycles, the products ~2100 (M = 64 runs at
 // half the rate).  Against the pairs of tq_latent.cu (where half of the 128 rows would be idle) a tile needs nothing of
 // another CTA and its chain from the last byte to the stage's release is shorter, so the two stages (four at DL = 256) keep
-// more in flight.  Measured against the pairs for every call: 32 sequences of 1k to 8k of 64 heads 48.3 us instead of 49.5, 2 x
-// 131k of 32 heads 60.2 instead of 63.0 (5.0 TB/s, 74% of the measured copy rate), 190 of up to 900 of 40 heads at DL = 256 25.6
-// instead of 32.3, one of 500 of 8 heads 9.6 instead of 11.5 (a call in a graph).
+// more in flight.  Measured against the pairs for every call: 32 sequences of 1k to 8k of 64 heads 50.4 us instead of 50.7, 2 x
+// 131k of 32 heads 61.5 instead of 64.5 (4.9 TB/s, 72% of the measured copy rate), 190 of up to 900 of 40 heads at DL = 256 26.5
+// instead of 32.7, one of 500 of 8 heads 9.6 instead of 10.9 (a call in a graph, inputs that together pass L2).  P in one bf16
+// term as there, so that a row's accuracy does not hang on how many there are.
 //
 // What bounds it: a tile takes 1.88 us between start and end where all SMs stream (HBM alone: 1.65); and beside the tiles ~7 us
 // from the launch to the first scores and 3 to 6 for output and join.

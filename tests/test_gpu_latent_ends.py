@@ -17,7 +17,7 @@ SHAPES = [(512, 4, None), (256, 4, None), (512, 100, None), (256, 100, None), (5
 @pytest.mark.parametrize("dl,Tq", [(512, 64), (256, 64), (512, 128), (256, 128)])
 def test_the_join_waits_no_longer_than_the_wait_limit(dl, Tq):
     """A long sequence cut into many pieces; a NaN in its last token keeps the worker of the last piece for some 50 to 200 us
-    (it looks for the rows that see it), while the others wait for it to join them: longer than a limit of 20 us, which the
+    (it looks for the rows that see it), while the others wait for it to join them: longer than a limit of 30 us, which the
     barriers of a tile stay below."""
     own = Codec(128, 4, 4, 64)
     n = 20000
@@ -34,7 +34,7 @@ def test_the_join_waits_no_longer_than_the_wait_limit(dl, Tq):
     ref = go()
     assert own.get_status() == 0
     assert bool(torch.isfinite(ref[:-1].float()).all()) and bool(torch.isnan(ref[-1]).all())
-    own.set_wait_limit(40000)
+    own.set_wait_limit(60000)
     for _ in range(3):
         out = go()
         assert own.get_status() == native.TQ_DEVERR_TIMEOUT
