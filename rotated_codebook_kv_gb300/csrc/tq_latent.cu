@@ -627,6 +627,8 @@ tq_status attend(const char *who, tq_handle h, const uint16_t *q, const uint16_t
     if (batch < 0 || q_tokens < 1 || Hq < 1 || max_blocks < 1 || num_blocks < 1)
         return api_error(TQ_ERR_INVALID_ARG, "%s: bad sizes", who);
     if (!std::isfinite(sm_scale)) return api_error(TQ_ERR_INVALID_ARG, "%s: sm_scale not finite", who);
+    if (!std::isfinite(sm_scale * kLog2e))  // scores are taken in powers of two
+        return api_error(TQ_ERR_UNSUPPORTED, "%s: sm_scale out of range", who);
     if (max_blocks > (1 << 30) / P) return api_error(TQ_ERR_UNSUPPORTED, "%s: more than 2^30 positions", who);
     if (num_blocks > ((int64_t(1) << 31) - 1) / P)
         return api_error(TQ_ERR_UNSUPPORTED, "%s: pool of %lld blocks is too large", who, static_cast<long long>(num_blocks));

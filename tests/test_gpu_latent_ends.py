@@ -239,3 +239,15 @@ def test_on_some_of_the_sms(limited_stream, dl, Hq, Tq):
             run(c, workspace=ws, out=out, stream=limited_stream)
         check(out, ref, bound)
     assert codec().get_status() == 0
+
+
+@pytest.mark.parametrize("Tq", [None, 2])
+def test_a_scale_that_leaves_fp32_in_powers_of_two_is_refused(Tq):
+    c = case(256, 16, 2, [40], Tq=Tq, seed=1)
+    for sm in (2.4e38, -3.0e38):
+        with pytest.raises(native.TQError, match="sm_scale") as e:
+            run(c, sm)
+        assert e.value.status == native.TQ_ERR_UNSUPPORTED
+    c["q"].mul_(1e-38)
+    ref, bound = reference(c, 2.3e38)
+    check(run(c, 2.3e38), ref, bound)
