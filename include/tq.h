@@ -454,7 +454,8 @@ tq_status tq_append_latent(tq_handle h, const uint16_t *latent, const uint16_t *
  *   a sequence of length 0 gives zeros.
  * Scores are exact bf16 products summed in fp32; the probabilities enter the value product
  * rounded to bf16 (off by 2^-8 of themselves at most) and the denominator sums what
- * enters; sums are fp32.
+ * enters; sums are fp32.  Probabilities are kept at 2^-16 and less, so that sums of large latents
+ * stay finite; latents below about 2^-105 are rounded to steps of 2^-117.
  * workspace: ws_bytes >= tq_workspace_bytes_latent(...), 256-byte aligned (on 152 SMs 20 MB for
  *   latent_dim 256, 40 for 512, whatever the other sizes); its contents after the call are not
  *   specified, and calls that may overlap need one each.  Work is cut on the GPU, from the

@@ -26,7 +26,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // P = 2^(c (s - r) - kMargin), c = |sm_scale| log2(e), r the largest score when it was set (the reference).  It moves, and O is
 // rescaled, when a score passes it by more than kSlack powers of two: P is 2^-32 at r and 2^-16 at most, so that no sum of 2^16
 // values, however large each is, overflows before the division.  At the other end O keeps steps of 2^-149, of 2^-117 after the
-// division.  (A slack of 8: more rescaling, a long prompt's chunk 2.86 -> 2.96 ms.)
+// division (latents of 2^-104 are still right to bf16's last bit, of 2^-110 to 1 - 5%).  (A slack of 8: more rescaling, a long
+// prompt's chunk 2.86 -> 2.96 ms.)
 // c s - (c r + kMargin), one operation, is off by the rounding of c r: 2^-14 at kFar.  Where a reference lies beyond, the
 // difference s - r comes first, so that scores of any size keep P in its range (for every tile: 1.5% of a long chunk; the branch
 // itself 0.4%).
